@@ -25,6 +25,8 @@ __all__ = [
     "lb_gemm_trit_planes_grouped_tiles", "lb_dequantize_q1_0",
     "lb_dequantize_q2_0_g64", "lb_dequantize_trit_planes", "OUT_F32", "OUT_BF16",
     "lb_pack_base3", "lb_gemv_base3", "base3_row_bytes", "lb_test_inject_wait_timeout",
+    "lb_kv_plan", "lb_kv4_append", "lb_dequantize_kv4", "lb_attn_kv4_workspace_bytes",
+    "lb_attn_kv4", "lb_logits_adjust", "kv4_cache_bytes",
 ]
 
 LB_STATUS = {0: "LB_OK", -1: "LB_ERR_NULL", -2: "LB_ERR_ALIGN", -3: "LB_ERR_SHAPE",
@@ -60,6 +62,13 @@ class lb_trit_matrix(ctypes.Structure):
 
 class lb_gemm_matrix(ctypes.Structure):
     _fields_ = [("bits", P), ("scales", P), ("y", P), ("N", I64)]
+
+
+class lb_logit_rules(ctypes.Structure):
+    _fields_ = [("prompt_ids", P), ("prompt_start", P), ("output_ids", P), ("output_start", P),
+                ("repetition", P), ("presence", P), ("frequency", P), ("bias_ids", P),
+                ("bias_values", P), ("bias_start", P), ("mask", P), ("mask_stride", I64),
+                ("mask_rows", I64), ("mask_row_opt", P)]
 
 
 GEMM_MAX_GROUP = 8
@@ -104,6 +113,13 @@ SIGNATURES = {
     "lb_dequantize_trit_planes": (I32, [P, F32, I64, I64, I32, P, P]),
     "lb_pack_base3": (I32, [P, I64, I64, P, P]),
     "lb_gemv_base3": (I32, [P, F32, P, P, P, P, I64, I64, I32, P]),
+    "lb_kv_plan": (I32, [P, P, I64, P, I64, P, I32, P, I64, I64, P, P, P, P, P, P]),
+    "lb_kv4_append": (I32, [P, P, I32, I64, I64, P, I64, P, I64, I32, I32, I32, P]),
+    "lb_dequantize_kv4": (I32, [P, I64, I32, I32, I32, P, I64, I32, P, P, P]),
+    "lb_attn_kv4_workspace_bytes": (ctypes.c_size_t, [I32, I32, I32, I64]),
+    "lb_attn_kv4": (I32, [P, I32, I64, P, I64, I32, I32, I32, I32, P, I64, P, P, I64, I64, I64,
+                          F32, I32, I64, P, I64, P, P, ctypes.c_size_t, P]),
+    "lb_logits_adjust": (I32, [P, I32, I64, P, I64, I64, I64, ctypes.POINTER(lb_logit_rules), P]),
 }
 
 OUT_F32 = 0
@@ -156,6 +172,21 @@ def _ptr(t):
             raise ValueError("lb_* entry points take contiguous tensors")
         return t.data_ptr()
     raise TypeError(f"cannot pass {type(t)} as a device pointer")
+
+
+def _rows(t):
+    """Pointer of a tensor whose first dimension may be strided (a slice of a wider buffer); what
+    follows it lies together."""
+    if not hasattr(t, "data_ptr"):
+        return _ptr(t)
+    if not t.is_cuda:
+        raise ValueError("lb_* entry points take device tensors")
+    dense = 1
+    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
+        if n != 1 and s != dense:
+            raise ValueError("only the first dimension may be strided")
+        dense *= n
+    return t.data_ptr()
 
 
 def _stream(stream):
@@ -423,3 +454,75 @@ def lb_gemv_base3(packed, w_scale: float, q, x_scale, y, acc, N: int, K: int, B:
     _check("lb_gemv_base3", load().lb_gemv_base3(
         _ptr(packed), float(w_scale), _ptr(q), _ptr(x_scale), _ptr(y), _ptr(acc), int(N),
         int(K), int(B), _stream(stream)))
+
+
+def kv4_cache_bytes(pages: int, kv_heads: int, page_size: int, head_dim: int) -> int:
+    """Bytes of a 4-bit key/value cache (LB_KV4_CACHE_BYTES)."""
+    return int(pages) * int(kv_heads) * int(page_size) * (int(head_dim) + 8)
+
+
+def lb_kv_plan(past, fresh, R: int, free_pages, n_free: int, free_from, page_size: int,
+               block_table, table_width: int, T: int, q_start, kv_len, position, slot, counts,
+               stream=None):
+    """Pages and slots of a step's new tokens.  free_from: None or a one-element tensor."""
+    _check("lb_kv_plan", load().lb_kv_plan(
+        _ptr(past), _ptr(fresh), int(R), _ptr(free_pages), int(n_free), _ptr(free_from),
+        int(page_size), _ptr(block_table), int(table_width), int(T), _ptr(q_start), _ptr(kv_len),
+        _ptr(position), _ptr(slot), _ptr(counts), _stream(stream)))
+
+
+def lb_kv4_append(k, v, type: int, k_stride: int, v_stride: int, slot, T: int, cache, pages: int,
+                  page_size: int, kv_heads: int, head_dim: int, stream=None):
+    """New keys and values [T][kv_heads][head_dim] (OUT_F32 or OUT_BF16, tokens strided) -> cache."""
+    _check("lb_kv4_append", load().lb_kv4_append(
+        _rows(k), _rows(v), int(type), int(k_stride), int(v_stride), _ptr(slot), int(T),
+        _ptr(cache), int(pages), int(page_size), int(kv_heads), int(head_dim), _stream(stream)))
+
+
+def lb_dequantize_kv4(cache, pages: int, page_size: int, kv_heads: int, head_dim: int, slot,
+                      T: int, out_format: int, k, v, stream=None):
+    """Cache rows of T slots -> keys and values [T][kv_heads][head_dim]."""
+    _check("lb_dequantize_kv4", load().lb_dequantize_kv4(
+        _ptr(cache), int(pages), int(page_size), int(kv_heads), int(head_dim), _ptr(slot), int(T),
+        int(out_format), _ptr(k), _ptr(v), _stream(stream)))
+
+
+def lb_attn_kv4_workspace_bytes(heads: int, kv_heads: int, head_dim: int, max_q: int) -> int:
+    """Bytes of device scratch lb_attn_kv4 needs."""
+    return int(load().lb_attn_kv4_workspace_bytes(int(heads), int(kv_heads), int(head_dim),
+                                                  int(max_q)))
+
+
+def lb_attn_kv4(q, type: int, q_stride: int, cache, pages: int, page_size: int, heads: int,
+                kv_heads: int, head_dim: int, block_table, table_width: int, q_start, kv_len,
+                R: int, T: int, max_q: int, scale: float, causal: bool, window: int, out,
+                out_stride: int, lse, workspace, workspace_bytes=None, stream=None):
+    """Attention of T new tokens over the cache; q and out [T][heads][head_dim] of one type, tokens
+    strided; lse None or [T][heads] fp32; workspace a device tensor (its size is passed) or a
+    pointer with workspace_bytes."""
+    if workspace_bytes is None:
+        workspace_bytes = workspace.numel() * workspace.element_size()
+    _check("lb_attn_kv4", load().lb_attn_kv4(
+        _rows(q), int(type), int(q_stride), _ptr(cache), int(pages), int(page_size), int(heads),
+        int(kv_heads), int(head_dim), _ptr(block_table), int(table_width), _ptr(q_start),
+        _ptr(kv_len), int(R), int(T), int(max_q), float(scale), int(bool(causal)), int(window),
+        _rows(out), int(out_stride), _ptr(lse), _ptr(workspace), int(workspace_bytes),
+        _stream(stream)))
+
+
+def lb_logits_adjust(logits, type: int, stride: int, out, out_stride: int, B: int, V: int, *,
+                     prompt_ids=None, prompt_start=None, output_ids=None, output_start=None,
+                     repetition=None, presence=None, frequency=None, bias_ids=None,
+                     bias_values=None, bias_start=None, mask=None, mask_stride: int = 0,
+                     mask_rows=None, mask_row=None, stream=None):
+    """Penalties, biases and grammar masks on logits [B][V] (OUT_F32 or OUT_BF16, rows strided);
+    out may be logits.  What is None is left out; mask_rows defaults to mask's rows."""
+    if mask is not None and mask_rows is None:
+        mask_rows = mask.numel() // int(mask_stride)
+    rules = lb_logit_rules(
+        _ptr(prompt_ids), _ptr(prompt_start), _ptr(output_ids), _ptr(output_start),
+        _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_ids), _ptr(bias_values),
+        _ptr(bias_start), _ptr(mask), int(mask_stride), int(mask_rows or 0), _ptr(mask_row))
+    _check("lb_logits_adjust", load().lb_logits_adjust(
+        _rows(logits), int(type), int(stride), _rows(out), int(out_stride), int(B), int(V),
+        ctypes.byref(rules), _stream(stream)))

@@ -384,6 +384,146 @@ int lb_gemm_q2_0_g64_noalloc(const uint8_t *codes, const uint16_t *scales, const
                              const uint16_t *d, float *y, int64_t M, int64_t N, int64_t K,
                              void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * Serving step: what stands between the products of one decoder layer and after its head.  No
+ * counterpart in the source pages; conveniences of this library for a server that keeps its
+ * keys and values in a paged cache of 4-bit codes:
+ *   lb_kv_plan        pages and slots of a step's new tokens from the requests' lengths
+ *   lb_kv4_append     new keys and values -> cache;  lb_dequantize_kv4: cache -> values
+ *   lb_attn_kv4       attention of the new tokens over the cache
+ *   lb_logits_adjust  penalties, biases and grammar masks on the head's logits
+ *
+ * Cache: one byte buffer [pages][kv_heads][page_size / 16][16 * (head_dim + 8)], page_size in
+ * {16, 32, 64, 128, 256}, head_dim in {64, 128}.  The innermost piece, a chunk, holds 16
+ * consecutive tokens of one head:
+ *   16 key rows of head_dim/2 bytes, 16 value rows of head_dim/2 bytes (the code of dimension 2j
+ *   in the low half of byte j, of 2j + 1 in the high half),
+ *   16 key pairs {d, z}, 16 value pairs {d, z}, each two fp16.
+ * A code c in 0..15 stands for d * (c - z); z is a whole number in 0..15.  A token's slot is
+ * page * page_size + its place in the page.
+ * ------------------------------------------------------------------------------------- */
+#define LB_KV4_CHUNK 16
+#define LB_KV4_CACHE_BYTES(pages, kv_heads, page_size, head_dim) \
+    ((size_t)(pages) * (size_t)(kv_heads) * (size_t)(page_size) * ((size_t)(head_dim) + 8))
+#define LB_KV_MAX_REQUESTS 8192
+
+/* Page plan of one step.  Request r holds past[r] tokens in the cache and brings fresh[r] new
+ * ones (0 allowed; a negative length counts as 0).  With P = page_size,
+ *   have[r] = ceil(past[r] / P),  take[r] = ceil((past[r] + fresh[r]) / P) - have[r],
+ *   first[r] = sum of take[0..r-1]:
+ *   block_table[r][have[r] + i] = free_pages[from + first[r] + i], i < take[r]  (other entries
+ *               stay; from = free_from_opt ? *free_from_opt : 0)
+ *   q_start[r]  = sum of fresh[0..r-1], r = 0..R
+ *   kv_len[r]   = past[r] + fresh[r]
+ *   position[t] = past[r] + (t - q_start[r]) of the request r that new token t belongs to
+ *   slot[t]     = block_table[r][position / P] * P + position % P
+ *   counts      = {q_start[R], from + first[R]}: the new tokens, and the first entry of
+ *               free_pages that is still free (the next step's free_from).
+ *   past, fresh : [R] int32.   free_pages : [n_free] int32.   block_table : [R][table_width]
+ *   int32, read and written.   q_start : [R + 1] int32.   kv_len : [R] int32.
+ *   position : [T] int32, slot : [T] int64; entries past q_start[R] are set to -1.
+ *   counts : [2] int32, not the memory that free_from_opt points to.
+ * Where free_pages runs out or a row of the table is full, the entries without a page are -1
+ * and the slots of their tokens are -1 (lb_kv4_append skips them and lb_attn_kv4 does not see
+ * them); counts[1] > n_free tells of the first case, counts[0] > T that tokens were left out.
+ * The pages of one call are different if those of free_pages are.
+ * 1 <= R <= LB_KV_MAX_REQUESTS; 0 <= n_free, T < 2^31; 1 <= table_width < 2^31; sums of lengths
+ * below 2^31.  4-byte alignment (slot: 8).  free_pages may be NULL if n_free is 0; position and
+ * slot if T is 0. */
+int lb_kv_plan(const int32_t *past, const int32_t *fresh, int64_t R, const int32_t *free_pages,
+               int64_t n_free, const int32_t *free_from_opt, int page_size,
+               int32_t *block_table, int64_t table_width, int64_t T, int32_t *q_start,
+               int32_t *kv_len, int32_t *position, int64_t *slot, int32_t *counts, void *stream);
+
+/* New keys and values -> cache.  For each token t, head h and each of its two rows x of head_dim
+ * values, in binary32 arithmetic with IEEE division and round-half-even:
+ *   lo = min(min x, 0), hi = max(max x, 0), d = fp16_rne(min((hi - lo) / 15, 65504)),
+ *   id = d != 0 ? 1 / d : 0,  z = clamp(rne(-lo * id), 0, 15),
+ *   c_i = clamp(rne(x_i * id) + z, 0, 15).
+ *   k, v : [T][kv_heads][head_dim], fp32 (type LB_OUT_F32) or bf16 (LB_OUT_BF16); a token's heads
+ *          lie together, tokens k_stride / v_stride elements apart (slices of one q|k|v buffer).
+ *   slot : [T] int64; a token whose slot is not in [0, pages * page_size) is skipped.  Tokens of
+ *          one call have different slots.
+ *   cache: LB_KV4_CACHE_BYTES(pages, kv_heads, page_size, head_dim) bytes.
+ * Rows with NaN or infinite values store unspecified codes and scales of their own row.
+ * 0 <= T < 2^31 (0: nothing is done); strides >= kv_heads * head_dim; k, v, cache and the strides
+ * in bytes 16-byte aligned, slot 8-byte. */
+int lb_kv4_append(const void *k, const void *v, int type, int64_t k_stride, int64_t v_stride,
+                  const int64_t *slot, int64_t T, uint8_t *cache, int64_t pages, int page_size,
+                  int kv_heads, int head_dim, void *stream);
+
+/* Cache -> values: k[t][h][i] = d * (c - z) of slot[t]'s key row of head h, v likewise (the exact
+ * binary32 product; out_format LB_OUT_BF16 rounds it to nearest even).  A token whose slot is not in
+ * [0, pages * page_size) gives zeros.  k, v : [T][kv_heads][head_dim], 16-byte aligned. */
+int lb_dequantize_kv4(const uint8_t *cache, int64_t pages, int page_size, int kv_heads,
+                      int head_dim, const int64_t *slot, int64_t T, int out_format, void *k,
+                      void *v, void *stream);
+
+/* Attention over the cache.  Request r's queries are the rows t in [q_start[r], q_start[r + 1])
+ * of q; row t is token kv_len[r] - n + i of its request (n its rows, i = t - q_start[r]) and head
+ * h reads key/value head h / (heads / kv_heads):
+ *   visible(t) = { j : 0 <= j < kv_len[r], j <= position(t) if causal,
+ *                  j > position(t) - window if window > 0 }
+ *   s_j = scale * sum_i q[t][h][i] * k_j[i],
+ *   out[t][h] = sum_j softmax_j(s) * v_j over visible(t), lse[t][h] = ln sum_j exp(s_j).
+ * A row that sees nothing (kv_len[r] = 0, or fewer tokens than queries) gives out = 0 and
+ * lse = -inf.  Tokens on a page whose block_table entry is not in [0, pages) are not seen.
+ *   q, out : [T][heads][head_dim], both fp32 (type LB_OUT_F32) or both bf16 (LB_OUT_BF16); tokens
+ *            q_stride / out_stride elements apart.  out may not overlap q.
+ *   block_table : [R][table_width] int32.   q_start : [R + 1] int32, not falling, within [0, T].
+ *   kv_len : [R] int32, at most table_width * page_size (more is not read).
+ *   lse_opt: NULL, or [T][heads] fp32.
+ *   workspace : at least lb_attn_kv4_workspace_bytes(heads, kv_heads, head_dim, max_q) bytes, owned
+ *            by the caller, not used by another call that may run at the same time; its contents
+ *            need no initialization.
+ *   max_q  : an upper bound of every request's number of queries, read on the host to choose the
+ *            kernels (a request with more is computed all the same, on slower ones).
+ * Sums, softmax statistics and outputs accumulate in binary32.  Weights and queries enter the
+ * tensor cores as fp16: with bf16 tensors one part (weights round to 11 bits, queries are exact),
+ * with fp32 tensors two (22 bits).
+ * heads % kv_heads == 0, heads / kv_heads <= 64; 1 <= R <= LB_KV_MAX_REQUESTS; 0 <= T < 2^31 (0:
+ * nothing is done); 1 <= table_width, table_width * page_size < 2^31; max_q >= 1; 0 < scale
+ * finite; window >= 0, and 0 without causal; 16-byte alignment of q, out, cache, workspace and the
+ * two strides in bytes, 4-byte of the others. */
+size_t lb_attn_kv4_workspace_bytes(int heads, int kv_heads, int head_dim, int64_t max_q);
+int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8_t *cache, int64_t pages,
+                int page_size, int heads, int kv_heads, int head_dim, const int32_t *block_table,
+                int64_t table_width, const int32_t *q_start, const int32_t *kv_len, int64_t R,
+                int64_t T, int64_t max_q, float scale, int causal, int64_t window, void *out,
+                int64_t out_stride, float *lse_opt, void *workspace, size_t workspace_bytes,
+                void *stream);
+
+/* Penalties, biases and grammar masks on logits.  Row b, token v, in binary32:
+ *   x = logits[b][v]
+ *   v in b's prompt or output:  x = x > 0 ? x / repetition[b] : x * repetition[b]
+ *   v n > 0 times in b's output: x = (x - n * frequency[b]) - presence[b]
+ *   v in b's bias list:         x = x + its value (the later entry's if v stands there twice)
+ *   v not allowed by b's mask:  x = -inf, whatever it was
+ *   out[b][v] = x
+ * The lists are rows of one array: list b is ids[start[b] .. start[b + 1] - 1], start int32
+ * [B + 1], not falling; ids int32; an id outside [0, V) is skipped.  NULL ids, values of [B] or mask
+ * leave a step out (repetition without lists does nothing).  mask : uint32 words, bit
+ * v % 32 of word v / 32 allows v; row mask_row_opt[b] of mask_rows rows, mask_stride words apart, or
+ * row b if mask_row_opt is NULL (mask_rows >= B then); a row outside [0, mask_rows) means no mask.
+ *   logits, out : [B][V] fp32 (type LB_OUT_F32) or bf16 (LB_OUT_BF16), rows `stride` elements
+ *                 apart; out may be logits itself (same stride).
+ * 1 <= B <= 65535; 1 <= V <= LB_LOGITS_MAX_V; strides >= V; mask_stride >= ceil(V / 32).
+ * Pointers aligned to their elements (16-byte rows are fastest). */
+#define LB_LOGITS_MAX_V 400000
+typedef struct lb_logit_rules {
+    const int32_t *prompt_ids, *prompt_start;
+    const int32_t *output_ids, *output_start;
+    const float *repetition, *presence, *frequency;  /* [B] each, or NULL */
+    const int32_t *bias_ids;
+    const float *bias_values;
+    const int32_t *bias_start;
+    const uint32_t *mask;
+    int64_t mask_stride, mask_rows;
+    const int32_t *mask_row_opt;
+} lb_logit_rules;
+int lb_logits_adjust(const void *logits, int type, int64_t stride, void *out, int64_t out_stride,
+                     int64_t B, int64_t V, const lb_logit_rules *rules, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
