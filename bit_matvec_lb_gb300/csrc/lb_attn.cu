@@ -1,78 +1,585 @@
-// lb_attn.cu -- attention over the paged 4-bit key/value cache.
-#include "lb_kv4.cuh"
+// lb_attn.cu -- attention over the paged 4-bit key/value cache for requests with few query rows
+// (decode, verification of drafted tokens), and the entry point.
+#include "lb_attn.cuh"
 
 #include <math.h>
 
 namespace lb {
 
-struct AttnParams {
-    const void *q;
-    void *out;
-    float *lse;
-    const uint8_t *cache;
-    const int32_t *table, *q_start, *kv_len;
-    int64_t q_stride, out_stride, pages, width, T;
-    int R, heads, kv_heads, shift, causal, window;
-    float scale;
+// ------------------------------------------------------------------------------------------
+// Mathematics.  For one key/value head, the rows that read it (queries x heads of the group) are
+// the columns of two products with the code matrices: with k_t = kd_t (kc_t - kz_t),
+//   s_t = scale * kd_t * (sum_i q_i kc_ti - kz_t sum_i q_i),
+//   out = sum_t p_t vd_t (vc_t - vz_t) / sum_t p_t,   p_t = 2^(s_t log2 e - R),
+// so codes enter the tensor cores as they are, whole numbers 0..15, exact in fp16, and the scales
+// act on the scores and weights.  R runs over max_t(s_t + e_t) with 2^e_t >= vd_t, which bounds the
+// weights w_t = p_t vd_t themselves (not the p_t): they enter the second product as fp16 in
+// [0, 2^15], whatever the sizes of the scales.
+//
+// Bound: reading the cache (D + 8 bytes per token and head).  A code costs 5/8 (keys) or 3/4
+// (values) of an integer operation to become fp16: masked in place, 4-bit fields at bits 0 and 16
+// of a word are the fp16 pair c * 2^-24 (subnormal, exact), at bits 4 and 20 it is 16 c * 2^-24; q
+// and the outputs carry the 16 and 2^24.  Two neighbouring tokens' words are interleaved by 16 bits
+// to pair tokens for the second product.  mma.sync serves here: rows are 8 to 16 wide, the products
+// are a third of the issue slots at full bandwidth, and tcgen05 would need the fp16 codes written
+// to shared memory, four times the cache's bytes.
+// ------------------------------------------------------------------------------------------
+constexpr int kWarps = 4;
+constexpr int kThreads = kWarps * 32;
+constexpr int kTile = 32;            // tokens of one warp step (two chunks)
+constexpr int kStages = 4;           // tiles in flight per warp
+constexpr int kWhole = 16;           // items of at most this many tiles are never split
+constexpr int kMinRun = 8;           // tiles per CTA below which no more CTAs are used
+constexpr int kMaxCtas = 608;
+constexpr float kLift = 256.f;       // weights are lifted by 2^8 ...
+constexpr float kSlack = 7.f;        // ... and may pass the reference by 2^7 before it moves
+
+__device__ __forceinline__ void mma16816(float (&c)[4], uint32_t a0, uint32_t a1, uint32_t a2,
+                                         uint32_t a3, uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
+        "{%0,%1,%2,%3};"
+        : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
+    uint32_t d;
+    asm("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(d) : "r"(a));
+    return d;
+}
+
+// Four fp16 pairs of a word of eight codes: {0,4} * 1, {1,5} * 16, {2,6} * 1, {3,7} * 16 (* 2^-24).
+__device__ __forceinline__ void spread_codes(uint32_t w, uint32_t (&x)[4]) {
+    x[0] = and_imm<0x000F000Fu>(w);
+    x[1] = and_imm<0x00F000F0u>(w);
+    const uint32_t h = w >> 8;
+    x[2] = and_imm<0x000F000Fu>(h);
+    x[3] = and_imm<0x00F000F0u>(h);
+}
+
+template <int D, int SPLIT, int NT>
+struct Decode {
+    static constexpr int kCols = 8 * NT / SPLIT;   // query rows of one item
+    static constexpr int kChunk = kv4_chunk_bytes(D);
+    static constexpr int kStage = 2 * kChunk;
+    static constexpr int kRing = kWarps * kStages * kStage;
+    static constexpr int kMerge = kWarps * kCols * (D + 4) * 4;
+    static constexpr size_t kSmem = kRing > kMerge ? kRing : kMerge;
 };
 
-// One warp per query row and head: D / 32 dimensions a lane, one key at a time, running maximum
-// and sum.
-template <int D, typename T>
-__global__ void __launch_bounds__(128) attn_simple_kernel(const AttnParams p) {
-    constexpr int E = D / 32;
-    const int lane = threadIdx.x & 31;
+// Work of one request in units of one tile of one item (an item: one key/value head and up to
+// kCols rows); at least one tile, so that rows that see nothing are visited and written.
+struct Units {
+    int lo, hi;    // visible tokens
+    int t0, tiles; // first tile, tiles
+    int groups;    // items per head
+};
+
+template <int COLS>
+__device__ __forceinline__ int64_t request_units(const AttnParams &p, const Request &q, Units &u) {
+    visible_range(p, q, 0, q.n, u.lo, u.hi);
+    u.t0 = u.lo / kTile;
+    u.tiles = max((u.hi + kTile - 1) / kTile - u.t0, 1);
+    u.groups = (q.n * p.group + COLS - 1) / COLS;
+    return (int64_t)u.tiles * u.groups * p.kv_heads;
+}
+
+template <int D, typename T, int SPLIT, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(const AttnParams p) {
+    using C = Decode<D, SPLIT, NT>;
+    constexpr int COLS = C::kCols;
+    constexpr int W = D / 32;             // words of eight codes per thread and key row
+    constexpr int VW = D / 64;            // words of eight codes per thread and value row
+    extern __shared__ __align__(128) uint8_t smem[];
+    __shared__ uint64_t full[kWarps][kStages];
+    __shared__ int64_t scan[kWarps];
+    __shared__ int64_t s_start;
+    __shared__ int s_r;
+    __shared__ float m_ref[kWarps][COLS], m_sum[kWarps][COLS], m_zero[kWarps][COLS];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int g = lane >> 2, tg = lane & 3;
+
+    if (lane < kStages) mbar_init(&full[warp][lane], 1);
+    fence_mbar_init();
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t w = (int64_t)blockIdx.x * 4 + (threadIdx.x >> 5);
-    const int64_t t = w / p.heads;
-    const int h = (int)(w % p.heads);
-    if (t >= p.T) return;
-    int r = 0;
-    while (r < p.R && !(t >= p.q_start[r] && t < p.q_start[r + 1])) r++;
-    if (r == p.R) return;
-    const int len = (int)min((int64_t)max(p.kv_len[r], 0), p.width << p.shift);
-    const int pos = p.kv_len[r] - (p.q_start[r + 1] - (int)t);
-    const int hi = p.causal ? min(len, pos + 1) : len;
-    const int lo = p.window ? max(0, pos - p.window + 1) : 0;
-    const int kvh = h / (p.heads / p.kv_heads);
-    float q[E], o[E] = {}, m = -INFINITY, l = 0.f;
-    const T *qr = static_cast<const T *>(p.q) + t * p.q_stride + (int64_t)h * D + lane * E;
-    for (int e = 0; e < E; e++) q[e] = (float)qr[e];
-    for (int j = lo; j < hi; j++) {
-        const int page = p.table[r * p.width + (j >> p.shift)];
-        if (page < 0 || page >= p.pages) continue;
-        const int in = j & ((1 << p.shift) - 1);
-        const uint8_t *c = p.cache + kv4_chunk_offset(page, kvh, in, p.kv_heads, p.shift, D);
-        const uint8_t *kc = c + (in & 15) * (D / 2), *vc = kc + kv4_codes_bytes(D);
-        const __half2 kd = reinterpret_cast<const __half2 *>(c + 2 * kv4_codes_bytes(D))[in & 15];
-        const __half2 vd =
-            reinterpret_cast<const __half2 *>(c + 2 * kv4_codes_bytes(D) + kKv4PairBytes)[in & 15];
-        float s = 0.f;
-        for (int e = 0; e < E; e++) {
-            const int i = lane * E + e;
-            s += q[e] * (__low2float(kd) * ((float)((kc[i / 2] >> (i % 2 * 4)) & 15) - __high2float(kd)));
-        }
-        for (int k = 16; k > 0; k >>= 1) s += __shfl_xor_sync(0xffffffffu, s, k);
-        s *= p.scale;
-        const float mn = fmaxf(m, s), f = m == -INFINITY ? 0.f : expf(m - mn), w1 = expf(s - mn);
-        m = mn;
-        l = l * f + w1;
-        for (int e = 0; e < E; e++) {
-            const int i = lane * E + e;
-            const float v = __low2float(vd) * ((float)((vc[i / 2] >> (i % 2 * 4)) & 15) - __high2float(vd));
-            o[e] = o[e] * f + w1 * v;
+
+    // ---- this CTA's run of units [u0, u1) and the request it begins in ----
+    int64_t mine = 0;
+    const int run = (p.R + kThreads - 1) / kThreads;
+    const int ra = min(tid * run, p.R), rb = min(ra + run, p.R);
+    Units un;
+    for (int r = ra; r < rb; r++) mine += request_units<COLS>(p, load_request(p, r), un);
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += a;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kWarps; w++) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    const int64_t ctas = min((int64_t)gridDim.x, (total + kMinRun - 1) / kMinRun);
+    int4 *record = p.record + 2 * blockIdx.x;
+    if (tid < 2) record[tid] = make_int4(-1, 0, 0, 0);
+    if (blockIdx.x >= ctas) return;
+    const int64_t u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
+    if (before <= u0 && u0 < before + mine) {
+        int64_t at = before;
+        for (int r = ra; r < rb; r++) {
+            const int64_t n = request_units<COLS>(p, load_request(p, r), un);
+            if (u0 < at + n) {
+                s_r = r, s_start = at;
+                break;
+            }
+            at += n;
         }
     }
-    T *orow = static_cast<T *>(p.out) + t * p.out_stride + (int64_t)h * D + lane * E;
-    for (int e = 0; e < E; e++) orow[e] = (T)(l > 0.f ? o[e] / l : 0.f);
-    if (p.lse && lane == 0) p.lse[t * p.heads + h] = l > 0.f ? m + logf(l) : -INFINITY;
+    __syncthreads();
+
+    uint32_t count = 0;        // tiles this warp has taken from its ring, over all items
+    uint64_t limit = 2000000000ull;
+    uint8_t *ring = smem + warp * (kStages * C::kStage);
+    int r = s_r;
+    Request rq = load_request(p, r);
+    int64_t r_units = request_units<COLS>(p, rq, un), r_begin = s_start;
+
+    for (int64_t u = u0; u < u1;) {
+        while (u >= r_begin + r_units) {  // requests without work have no units
+            r_begin += r_units;
+            rq = load_request(p, ++r);
+            r_units = request_units<COLS>(p, rq, un);
+        }
+        const int item = (int)((u - r_begin) / un.tiles);
+        const int first = (int)((u - r_begin) - (int64_t)item * un.tiles);  // tile within the item
+        int last = (int)min((int64_t)un.tiles, first + (u1 - u));
+        u += last - first;
+        if (un.tiles <= kWhole) {  // never split: the CTA in whose run it begins takes it
+            if (first > 0) continue;
+            last = un.tiles;
+        }
+        const int h = item / un.groups, col0 = item % un.groups * COLS;
+        const int ncol = min(COLS, rq.n * p.group - col0);
+
+        // ---- pages and first copies ----
+        const int n = last - first - warp;                  // this warp: tiles first + warp + 4 i
+        const int tiles = n > 0 ? (n + kWarps - 1) / kWarps : 0;
+        int pg0 = -1, pg1 = -1, pg_base = -32;
+        uint32_t valid = 0;                                 // two bits per stage
+        auto tile_token = [&](int i) { return (un.t0 + first + warp + kWarps * i) * kTile; };
+        auto load_pages = [&](int base) {
+            pg_base = base;
+            const int j = tile_token(base + lane);
+            const int64_t c0 = j >> p.shift, c1 = (j + 16) >> p.shift;
+            const int32_t *row = p.table + (int64_t)r * p.width;
+            pg0 = base + lane < tiles && c0 < p.width ? row[c0] : -1;
+            pg1 = c1 == c0 ? pg0 : base + lane < tiles && c1 < p.width ? row[c1] : -1;
+        };
+        auto issue = [&](int i) {  // tile i of this warp into stage (count + i) % kStages
+            const uint32_t slot = count + i;
+            const int stage = slot % kStages, j = tile_token(i);
+            const int a = __shfl_sync(0xffffffffu, pg0, i - pg_base);
+            const int b = __shfl_sync(0xffffffffu, pg1, i - pg_base);
+            const bool va = a >= 0 && a < p.pages && j < un.hi && j + 16 > un.lo;
+            const bool vb = b >= 0 && b < p.pages && j + 16 < un.hi && j + 32 > un.lo;
+            valid = (valid & ~(3u << (2 * stage))) | ((uint32_t)va | (uint32_t)vb << 1) << (2 * stage);
+            if (lane == 0) {
+                uint8_t *dst = ring + stage * C::kStage;
+                uint64_t *bar = &full[warp][stage];
+                const int in = j & ((1 << p.shift) - 1);
+                mbar_arrive_expect_tx(bar, ((int)va + (int)vb) * C::kChunk);
+                if (va) {
+                    const uint8_t *src =
+                        p.cache + kv4_chunk_offset(a, h, in, p.kv_heads, p.shift, D);
+                    bulk_g2s(dst, src, vb && p.shift > 4 ? 2 * C::kChunk : C::kChunk, bar);
+                }
+                if (vb && !(va && p.shift > 4))
+                    bulk_g2s(dst + C::kChunk,
+                             p.cache + kv4_chunk_offset(b, h, p.shift > 4 ? in + 16 : 0, p.kv_heads,
+                                                        p.shift, D),
+                             C::kChunk, bar);
+            }
+        };
+        if (tiles > 0) load_pages(0);
+        for (int i = 0; i < min(tiles, kStages); i++) issue(i);
+
+        // ---- query columns: fp16 parts of this thread's D / 4 dimensions of column g ----
+        uint32_t qb[NT][2 * W][2];
+        float col_a[NT][2], col_sum[NT][2];  // of the columns 2 tg, 2 tg + 1 (SPLIT: parts of one)
+        int col_hi[NT][2], col_lo[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            const int part = SPLIT == 2 ? g & 1 : 0;
+            const int c = SPLIT == 2 ? nt * 4 + g / 2 : nt * 8 + g;
+            float x[8 * W];
+            const bool live = c < ncol;
+            const int cc = col0 + (live ? c : 0);
+            const int qi = cc / p.group, head = h * p.group + cc % p.group;
+            const T *src = static_cast<const T *>(p.q) + (int64_t)(rq.q0 + qi) * p.q_stride +
+                           (int64_t)head * D + tg * (D / 4);
+#pragma unroll
+            for (int i = 0; i < W; i++) {
+                float y[8];
+                load8(src + 8 * i, y);
+#pragma unroll
+                for (int e = 0; e < 8; e++) x[8 * i + e] = live ? y[e] : 0.f;
+            }
+            float amax = 0.f;
+#pragma unroll
+            for (int i = 0; i < 8 * W; i++) amax = fmaxf(amax, fabsf(x[i]));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 1));
+            amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 2));
+            float up, down, sum = 0.f;
+            row_power(amax, up, down);
+#pragma unroll
+            for (int i = 0; i < 8 * W; i++) {
+                x[i] *= up;
+                sum += x[i];
+                if (part) x[i] -= __half2float(__float2half_rn(x[i]));
+            }
+            sum += __shfl_xor_sync(0xffffffffu, sum, 1);
+            sum += __shfl_xor_sync(0xffffffffu, sum, 2);
+#pragma unroll
+            for (int i = 0; i < W; i++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) {
+                    const float s = e & 1 ? 0.0625f : 1.f;
+                    qb[nt][2 * i + e / 2][e & 1] = half2_bits(x[8 * i + e] * s, x[8 * i + e + 4] * s);
+                }
+            const float a = p.scale * kLog2e * down * 16777216.f;
+            sum *= 1.f / 16777216.f;
+            int hi = un.hi, lo = 0;
+            if (p.causal) hi = min(hi, rq.base + qi + 1);
+            if (p.window) lo = rq.base + qi - p.window + 1;
+#pragma unroll
+            for (int e = 0; e < 2; e++) {
+                const int from = (2 * tg + e) * 4;
+                col_a[nt][e] = __shfl_sync(0xffffffffu, a, from);
+                col_sum[nt][e] = __shfl_sync(0xffffffffu, sum, from);
+                col_hi[nt][e] = __shfl_sync(0xffffffffu, hi, from);
+                col_lo[nt][e] = __shfl_sync(0xffffffffu, lo, from);
+            }
+        }
+        // Tokens that every column sees: no mask in a tile inside them.
+        int all_hi = un.hi, all_lo = 0;
+        if (p.causal) all_hi = min(all_hi, rq.base + col0 / p.group + 1);
+        if (p.window) all_lo = rq.base + (col0 + ncol - 1) / p.group - p.window + 1;
+
+        float o[D / 16][NT][4];
+        float ref[NT][2], sum[NT][2], zero[NT][2];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+#pragma unroll
+            for (int m = 0; m < D / 16; m++)
+#pragma unroll
+                for (int e = 0; e < 4; e++) o[m][nt][e] = 0.f;
+#pragma unroll
+            for (int e = 0; e < 2; e++) ref[nt][e] = -INFINITY, sum[nt][e] = 0.f, zero[nt][e] = 0.f;
+        }
+
+        for (int i = 0; i < tiles; i++) {
+            const int stage = count % kStages;
+            if (!mbar_wait(&full[warp][stage], (count / kStages) & 1, limit)) {
+                *p.error = 1;
+                limit = 1000000ull;
+            }
+            const int j0 = tile_token(i);
+            const uint32_t bits = (valid >> (2 * stage)) & 3u;
+            const bool inside = j0 >= all_lo && j0 + kTile <= all_hi;
+#pragma unroll 1
+            for (int half = 0; half < 2; half++) {
+                if (!(bits >> half & 1)) continue;
+                const uint8_t *chunk = ring + stage * C::kStage + half * C::kChunk;
+                // Row g of the first product is token g ^ (bit 1 of g), so that both the key rows
+                // of eight lanes and the value rows of 16 lanes lie in different banks (or two).
+                const int tok = g ^ ((g >> 1) & 1);
+                const int ja = j0 + 16 * half + tok, jb = ja + 8;
+                const __half2 *kp = reinterpret_cast<const __half2 *>(chunk + 2 * kv4_codes_bytes(D));
+                const __half2 *vp = kp + LB_KV4_CHUNK;
+                float2 ka = __half22float2(kp[tok]), kb = __half22float2(kp[tok + 8]);
+                float2 va = __half22float2(vp[tok]), vb = __half22float2(vp[tok + 8]);
+                if (!inside) {  // what lies behind the request's end is not read as a number
+                    const float2 none = make_float2(0.f, 0.f);
+                    if (ja >= un.hi) ka = none, va = none;
+                    if (jb >= un.hi) kb = none, vb = none;
+                }
+                float acc[NT][4];
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) acc[nt][e] = 0.f;
+                uint32_t wa[W], wb[W];
+                const uint8_t *ra_ = chunk + tok * (D / 2) + tg * (D / 8);
+                if (D == 128) {
+                    const uint4 a = *reinterpret_cast<const uint4 *>(ra_);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(ra_ + 8 * (D / 2));
+                    wa[0] = a.x, wa[1] = a.y, wa[W - 2] = a.z, wa[W - 1] = a.w;
+                    wb[0] = b.x, wb[1] = b.y, wb[W - 2] = b.z, wb[W - 1] = b.w;
+                } else {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(ra_);
+                    const uint2 b = *reinterpret_cast<const uint2 *>(ra_ + 8 * (D / 2));
+                    wa[0] = a.x, wa[1] = a.y, wb[0] = b.x, wb[1] = b.y;
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < W; i2++) {
+                    uint32_t xa[4], xb[4];
+                    spread_codes(wa[i2], xa);
+                    spread_codes(wb[i2], xb);
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++) {
+                        mma16816(acc[nt], xa[0], xb[0], xa[1], xb[1], qb[nt][2 * i2][0],
+                                 qb[nt][2 * i2][1]);
+                        mma16816(acc[nt], xa[2], xb[2], xa[3], xb[3], qb[nt][2 * i2 + 1][0],
+                                 qb[nt][2 * i2 + 1][1]);
+                    }
+                }
+                // Scores in powers of two; s[..][0..1] token a, [2..3] token b.
+                constexpr int E = SPLIT == 2 ? 1 : 2;
+                float s[NT][E][2];
+                const float ea = scale_exponent(va.x), eb = scale_exponent(vb.x);
+                bool move = false;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                    for (int e = 0; e < E; e++) {
+                        const float xa = SPLIT == 2 ? acc[nt][0] + acc[nt][1] : acc[nt][e];
+                        const float xb = SPLIT == 2 ? acc[nt][2] + acc[nt][3] : acc[nt][2 + e];
+                        float sa = (ka.x * col_a[nt][e]) * fmaf(-ka.y, col_sum[nt][e], xa);
+                        float sb = (kb.x * col_a[nt][e]) * fmaf(-kb.y, col_sum[nt][e], xb);
+                        if (!inside) {
+                            if (ja >= col_hi[nt][e] || ja < col_lo[nt][e]) sa = -INFINITY;
+                            if (jb >= col_hi[nt][e] || jb < col_lo[nt][e]) sb = -INFINITY;
+                        }
+                        s[nt][e][0] = sa, s[nt][e][1] = sb;
+                        move |= fmaxf(sa + ea, sb + eb) > ref[nt][e] + kSlack;
+                    }
+                if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                    for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                        for (int e = 0; e < E; e++) {
+                            float m = fmaxf(s[nt][e][0] + ea, s[nt][e][1] + eb);
+#pragma unroll
+                            for (int k = 4; k < 32; k <<= 1)
+                                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+                            m = fmaxf(m, ref[nt][e]);
+                            const float f = m == ref[nt][e] ? 1.f : ex2(ref[nt][e] - m);
+                            ref[nt][e] = m;
+                            sum[nt][e] *= f, zero[nt][e] *= f;
+#pragma unroll
+                            for (int d = 0; d < D / 16; d++) {
+                                o[d][nt][e] *= f, o[d][nt][2 + e] *= f;
+                                if (SPLIT == 2) o[d][nt][1] *= f, o[d][nt][3] *= f;
+                            }
+                        }
+                }
+                uint32_t pb[NT][2];
+                const float la = va.x * kLift, lb = vb.x * kLift;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    float w[2][2];
+#pragma unroll
+                    for (int e = 0; e < E; e++) {
+                        const float base = ref[nt][e] == -INFINITY ? 0.f : ref[nt][e];
+                        const float pa = ex2(s[nt][e][0] - base), pc = ex2(s[nt][e][1] - base);
+                        sum[nt][e] += pa + pc;
+                        w[e][0] = pa * la, w[e][1] = pc * lb;
+                    }
+                    if (SPLIT == 2) {
+                        // Two parts: the second holds what rounding to fp16 took from the first.
+                        const __half ha = __float2half_rn(w[0][0]), hb = __float2half_rn(w[0][1]);
+                        zero[nt][0] += w[0][0] * va.y + w[0][1] * vb.y;
+                        const __half2 qa = __halves2half2(ha, __float2half_rn(w[0][0] - __half2float(ha)));
+                        const __half2 qc = __halves2half2(hb, __float2half_rn(w[0][1] - __half2float(hb)));
+                        pb[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&qa));
+                        pb[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&qc));
+                    } else {
+                        // The zero's share uses the weights as rounded, so that an error of a
+                        // weight acts on d (c - z), not on d c and d z apart.
+                        const __half2 qa = __floats2half2_rn(w[0][0], w[1][0]);
+                        const __half2 qc = __floats2half2_rn(w[0][1], w[1][1]);
+                        const float2 fa = __half22float2(qa), fc = __half22float2(qc);
+                        zero[nt][0] += fa.x * va.y + fc.x * vb.y;
+                        zero[nt][1] += fa.y * va.y + fc.y * vb.y;
+                        pb[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&qa));
+                        pb[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&qc));
+                    }
+                }
+                // Second product: this thread's dimensions g * D/8 .. of tokens (k order) 2 tg,
+                // 2 tg + 1, 2 tg + 8, 2 tg + 9.
+                const int t0 = (2 * tg) ^ (tg & 1), t1 = (2 * tg + 1) ^ (tg & 1);
+                const uint8_t *vr = chunk + kv4_codes_bytes(D) + g * (D / 16);
+                uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
+                if (D == 128) {
+                    const uint2 a = *reinterpret_cast<const uint2 *>(vr + t0 * (D / 2));
+                    const uint2 b = *reinterpret_cast<const uint2 *>(vr + t1 * (D / 2));
+                    const uint2 c = *reinterpret_cast<const uint2 *>(vr + (t0 + 8) * (D / 2));
+                    const uint2 d = *reinterpret_cast<const uint2 *>(vr + (t1 + 8) * (D / 2));
+                    v0[0] = a.x, v0[VW - 1] = a.y, v1[0] = b.x, v1[VW - 1] = b.y;
+                    v2[0] = c.x, v2[VW - 1] = c.y, v3[0] = d.x, v3[VW - 1] = d.y;
+                } else {
+                    v0[0] = *reinterpret_cast<const uint32_t *>(vr + t0 * (D / 2));
+                    v1[0] = *reinterpret_cast<const uint32_t *>(vr + t1 * (D / 2));
+                    v2[0] = *reinterpret_cast<const uint32_t *>(vr + (t0 + 8) * (D / 2));
+                    v3[0] = *reinterpret_cast<const uint32_t *>(vr + (t1 + 8) * (D / 2));
+                }
+#pragma unroll
+                for (int i2 = 0; i2 < VW; i2++)
+#pragma unroll
+                    for (int hw = 0; hw < 2; hw++) {
+                        uint32_t x[4], y[4];
+                        spread_codes(prmt(v0[i2], v1[i2], hw ? 0x7632 : 0x5410), x);
+                        spread_codes(prmt(v2[i2], v3[i2], hw ? 0x7632 : 0x5410), y);
+#pragma unroll
+                        for (int nt = 0; nt < NT; nt++) {
+                            mma16816(o[i2 * 4 + hw * 2][nt], x[0], x[1], y[0], y[1], pb[nt][0], pb[nt][1]);
+                            mma16816(o[i2 * 4 + hw * 2 + 1][nt], x[2], x[3], y[2], y[3], pb[nt][0],
+                                     pb[nt][1]);
+                        }
+                    }
+            }
+            __syncwarp();
+            count++;
+            const int nx = i + kStages;
+            if (nx < tiles) {
+                if (nx >= pg_base + 32) load_pages(nx);
+                // issue() counts from this item's first tile
+                count -= i + 1;
+                issue(nx);
+                count += i + 1;
+            }
+        }
+
+        // ---- merge the warps ----
+        float *mo = reinterpret_cast<float *>(smem);  // [warp][COLS][D + 4], over the idle ring
+        constexpr int MS = D + 4;
+        __syncthreads();                              // every warp's ring is empty
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            constexpr int E = SPLIT == 2 ? 1 : 2;
+#pragma unroll
+            for (int e = 0; e < E; e++) {
+#pragma unroll
+                for (int k = 4; k < 32; k <<= 1) {
+                    sum[nt][e] += __shfl_xor_sync(0xffffffffu, sum[nt][e], k);
+                    zero[nt][e] += __shfl_xor_sync(0xffffffffu, zero[nt][e], k);
+                }
+                const int c = SPLIT == 2 ? nt * 4 + tg : nt * 8 + 2 * tg + e;
+                if (g == 0) m_ref[warp][c] = ref[nt][e], m_sum[warp][c] = sum[nt][e], m_zero[warp][c] = zero[nt][e];
+                float *dst = mo + (warp * COLS + c) * MS + g * (D / 8);
+#pragma unroll
+                for (int m = 0; m < D / 16; m++) {
+                    const float a = SPLIT == 2 ? o[m][nt][0] + o[m][nt][1] : o[m][nt][e];
+                    const float b = SPLIT == 2 ? o[m][nt][2] + o[m][nt][3] : o[m][nt][2 + e];
+                    // m-tile m: dimensions 2 m (times 1) and 2 m + 1 (times 16) of this thread's D / 8
+                    *reinterpret_cast<float2 *>(dst + 2 * m) = make_float2(a * 16777216.f, b * 1048576.f);
+                }
+            }
+        }
+        __syncthreads();
+        const bool whole = first == 0 && last == un.tiles;
+        const int slot = 2 * blockIdx.x + (first == 0 ? 1 : 0);
+        for (int c = tid / (D / 4); c < ncol; c += kThreads / (D / 4)) {
+            const int d = tid % (D / 4) * 4;
+            float m = -INFINITY;
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) m = fmaxf(m, m_ref[w][c]);
+            float l = 0.f, z = 0.f, x[4] = {};
+#pragma unroll
+            for (int w = 0; w < kWarps; w++) {
+                const float f = m_ref[w][c] == -INFINITY ? 0.f : ex2(m_ref[w][c] - m);
+                l += f * m_sum[w][c], z += f * m_zero[w][c];
+                const float4 v = *reinterpret_cast<const float4 *>(mo + (w * COLS + c) * MS + d);
+                x[0] += f * v.x, x[1] += f * v.y, x[2] += f * v.z, x[3] += f * v.w;
+            }
+#pragma unroll
+            for (int e = 0; e < 4; e++) x[e] = (x[e] - z) * (1.f / kLift);
+            if (whole) {
+                const int cc = col0 + c, head = h * p.group + cc % p.group;
+                const int64_t t = rq.q0 + cc / p.group;
+                const float inv = l > 0.f ? 1.f / l : 0.f;
+                T *dst = static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + d;
+#pragma unroll
+                for (int e = 0; e < 4; e++) store_value(dst + e, l > 0.f ? x[e] * inv : 0.f);
+                if (p.lse && d == 0) p.lse[t * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+            } else {
+                *reinterpret_cast<float4 *>(p.part + ((int64_t)slot * COLS + c) * D + d) =
+                    make_float4(x[0], x[1], x[2], x[3]);
+                if (d == 0) p.stat[slot * COLS + c] = make_float2(m, l);
+            }
+        }
+        if (!whole && tid == 0)
+            record[first == 0 ? 1 : 0] = make_int4(r, item, last == un.tiles, ncol);
+        fence_proxy_async_shared();  // the merge's writes come before the next item's copies
+        __syncthreads();
+    }
+}
+
+// Joins the parts of items that several CTAs shared: the CTA that took an item's last part is
+// found by its record; the parts before it lie in the CTAs before it.  One block per CTA record
+// and row, D threads.
+template <int D, typename T, int COLS>
+__global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x, c = blockIdx.y, d = threadIdx.x;
+    const int4 rec = p.record[2 * b];
+    if (rec.x < 0 || !rec.z || c >= rec.w) return;
+    // parts: slots 2 b, 2 (b - 1), ... (continued), then the one that began the item
+    int first = b - 1;
+    while (first > 0 && p.record[2 * first].x == rec.x && p.record[2 * first].y == rec.y) first--;
+    auto slot_of = [&](int i) { return i == first ? 2 * first + 1 : 2 * i; };
+    float m = -INFINITY;
+    for (int i = first; i <= b; i++) m = fmaxf(m, p.stat[slot_of(i) * COLS + c].x);
+    float l = 0.f, x = 0.f;
+#pragma unroll 4
+    for (int i = first; i <= b; i++) {
+        const float2 s = p.stat[slot_of(i) * COLS + c];
+        const float v = p.part[((int64_t)slot_of(i) * COLS + c) * D + d];
+        const float f = s.x == -INFINITY ? 0.f : ex2(s.x - m);
+        l += f * s.y, x += f * v;
+    }
+    const Request q = load_request(p, rec.x);
+    const int groups = (q.n * p.group + COLS - 1) / COLS;
+    const int cc = rec.y % groups * COLS + c, head = rec.y / groups * p.group + cc % p.group;
+    const int64_t t = q.q0 + cc / p.group;
+    store_value(static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + d, l > 0.f ? x / l : 0.f);
+    if (p.lse && d == 0) p.lse[t * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+}
+
+template <int D, typename T, int NT>
+static int launch_decode(AttnParams p, uint8_t *workspace, int sms, cudaStream_t st) {
+    constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
+    using C = Decode<D, SPLIT, NT>;
+    p.record = reinterpret_cast<int4 *>(workspace);
+    p.stat = reinterpret_cast<float2 *>(p.record + 2 * kMaxCtas);
+    p.part = reinterpret_cast<float *>(p.stat + 2 * kMaxCtas * C::kCols);
+    auto kernel = attn_decode_kernel<D, T, SPLIT, NT>;
+    int per_sm;
+    if (int e = prepare_kernel((const void *)kernel, kThreads, C::kSmem, &per_sm)) return e;
+    const int ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
+    if (int e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), C::kSmem, st, p)) return e;
+    if ((p.width << p.shift) <= kWhole * kTile) return LB_OK;  // no item can have been split
+    return launch_pdl(attn_join_kernel<D, T, C::kCols>, dim3(ctas, C::kCols), dim3(D), 0, st, p);
+}
+
+template <int D, typename T>
+static int dispatch_decode(const AttnParams &p, int64_t max_q, uint8_t *workspace, int sms,
+                           cudaStream_t st) {
+    constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
+    return max_q * p.group * SPLIT <= 8 ? launch_decode<D, T, 1>(p, workspace, sms, st)
+                                        : launch_decode<D, T, 2>(p, workspace, sms, st);
 }
 
 }  // namespace lb
 
 LB_EXPORT size_t lb_attn_kv4_workspace_bytes(int heads, int kv_heads, int head_dim, int64_t max_q) {
-    return heads < 1 || kv_heads < 1 || head_dim < 1 || max_q < 1 ? 0 : 16;
+    if (heads < 1 || kv_heads < 1 || head_dim < 1 || max_q < 1) return 0;
+    return (size_t)lb::kMaxCtas * 2 * (16 + 16 * (8 + (size_t)head_dim * 4));
 }
 
 LB_EXPORT int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8_t *cache,
@@ -87,7 +594,8 @@ LB_EXPORT int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8
     if ((type != LB_OUT_F32 && type != LB_OUT_BF16) ||
         !kv4_shape_ok(pages, page_size, kv_heads, head_dim) || heads < kv_heads ||
         heads % kv_heads || heads / kv_heads > 64 || R < 1 || R > LB_KV_MAX_REQUESTS || T < 0 ||
-        T >= lim || table_width < 1 || table_width >= lim / page_size || max_q < 1 || max_q >= lim ||
+        T * (heads / kv_heads) >= lim || table_width < 1 ||
+        table_width > (lim >> 1) / page_size || max_q < 1 || max_q >= lim ||
         !(scale > 0.f) || !(scale < INFINITY) || window < 0 || window >= lim || (window && !causal) ||
         q_stride < (int64_t)heads * head_dim || out_stride < (int64_t)heads * head_dim ||
         workspace_bytes < lb_attn_kv4_workspace_bytes(heads, kv_heads, head_dim, max_q))
@@ -100,15 +608,20 @@ LB_EXPORT int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8
     DeviceInfo di;
     if (int e = current_device_info(&di)) return e;
     if (T == 0) return LB_OK;
-    const AttnParams p{q, out, lse_opt, cache, block_table, q_start, kv_len, q_stride, out_stride,
-                       pages, table_width, T, (int)R, heads, kv_heads, page_shift_of(page_size),
-                       causal, (int)window, scale};
-    const dim3 grid((unsigned)((T * heads + 3) / 4));
+    AttnParams p{};
+    p.q = q, p.out = out, p.lse = lse_opt, p.cache = cache, p.table = block_table;
+    p.q_start = q_start, p.kv_len = kv_len, p.q_stride = q_stride, p.out_stride = out_stride;
+    p.pages = pages, p.width = table_width, p.T = T, p.R = (int)R, p.heads = heads;
+    p.kv_heads = kv_heads, p.group = heads / kv_heads, p.shift = page_shift_of(page_size);
+    p.causal = causal != 0, p.window = (int)window, p.scale = scale;
+    p.rows_lo = 0, p.rows_hi = 0x7fffffff;
+    p.error = device_error_word();
+    if (!p.error) return LB_ERR_LAUNCH;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
     cudaStream_t st = as_stream(stream);
     if (type == LB_OUT_F32)
-        return head_dim == 64 ? launch_pdl(attn_simple_kernel<64, float>, grid, dim3(128), 0, st, p)
-                              : launch_pdl(attn_simple_kernel<128, float>, grid, dim3(128), 0, st, p);
-    return head_dim == 64
-               ? launch_pdl(attn_simple_kernel<64, __nv_bfloat16>, grid, dim3(128), 0, st, p)
-               : launch_pdl(attn_simple_kernel<128, __nv_bfloat16>, grid, dim3(128), 0, st, p);
+        return head_dim == 64 ? dispatch_decode<64, float>(p, max_q, ws, di.sms, st)
+                              : dispatch_decode<128, float>(p, max_q, ws, di.sms, st);
+    return head_dim == 64 ? dispatch_decode<64, __nv_bfloat16>(p, max_q, ws, di.sms, st)
+                          : dispatch_decode<128, __nv_bfloat16>(p, max_q, ws, di.sms, st);
 }

@@ -481,8 +481,8 @@ int lb_dequantize_kv4(const uint8_t *cache, int64_t pages, int page_size, int kv
  * Sums, softmax statistics and outputs accumulate in binary32.  Weights and queries enter the
  * tensor cores as fp16: with bf16 tensors one part (weights round to 11 bits, queries are exact),
  * with fp32 tensors two (22 bits).
- * heads % kv_heads == 0, heads / kv_heads <= 64; 1 <= R <= LB_KV_MAX_REQUESTS; 0 <= T < 2^31 (0:
- * nothing is done); 1 <= table_width, table_width * page_size < 2^31; max_q >= 1; 0 < scale
+ * heads % kv_heads == 0, heads / kv_heads <= 64; 1 <= R <= LB_KV_MAX_REQUESTS; 0 <= T (0: nothing
+ * is done), T * heads / kv_heads < 2^31; 1 <= table_width, table_width * page_size <= 2^30; max_q >= 1; 0 < scale
  * finite; window >= 0, and 0 without causal; 16-byte alignment of q, out, cache, workspace and the
  * two strides in bytes, 4-byte of the others. */
 size_t lb_attn_kv4_workspace_bytes(int heads, int kv_heads, int head_dim, int64_t max_q);
