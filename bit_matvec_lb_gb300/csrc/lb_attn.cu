@@ -12,7 +12,7 @@ namespace lb {
 //   s_t = scale * kd_t * (sum_i q_i kc_ti - kz_t sum_i q_i),
 //   out = sum_t p_t vd_t (vc_t - vz_t) / sum_t p_t,   p_t = 2^(s_t log2 e - R),
 // so codes enter the tensor cores as they are, whole numbers 0..15, exact in fp16, and the scales
-// act on the scores and weights.  R runs over max_t(s_t + e_t) with 2^e_t >= vd_t, which bounds the
+// act on the scores and weights.  R runs over max_t(s_t + log2 vd_t), which bounds the
 // weights w_t = p_t vd_t themselves (not the p_t): they enter the second product as fp16 in
 // [0, 2^15], whatever the sizes of the scales.
 //
@@ -165,11 +165,32 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
         const int h = item / un.groups, col0 = item % un.groups * COLS;
         const int ncol = min(COLS, rq.n * p.group - col0);
 
+        // ---- query columns: this thread's D / 4 dimensions of column g, asked for before the
+        // copies, behind which they would wait in the memory's queues ----
+        float qx[NT][8 * W];
+#pragma unroll
+        for (int nt = 0; nt < NT; nt++) {
+            const int c = SPLIT == 2 ? nt * 4 + g / 2 : nt * 8 + g;
+            const int cc = col0 + (c < ncol ? c : 0);
+            const int qi = cc / p.group, head = h * p.group + cc % p.group;
+            const T *src = static_cast<const T *>(p.q) + (int64_t)(rq.q0 + qi) * p.q_stride +
+                           (int64_t)head * D + tg * (D / 4);
+#pragma unroll
+            for (int i = 0; i < W; i++) {
+                float y[8];
+                load8(src + 8 * i, y);
+#pragma unroll
+                for (int e = 0; e < 8; e++) qx[nt][8 * i + e] = c < ncol ? y[e] : 0.f;
+            }
+        }
+
         // ---- pages and first copies ----
         const int n = last - first - warp;                  // this warp: tiles first + warp + 4 i
         const int tiles = n > 0 ? (n + kWarps - 1) / kWarps : 0;
         int pg0 = -1, pg1 = -1, pg_base = -32;
         uint32_t valid = 0;                                 // two bits per stage
+        const int64_t page_bytes = ((int64_t)p.kv_heads << (p.shift - 4)) * C::kChunk;
+        const uint8_t *head_base = p.cache + ((int64_t)h << (p.shift - 4)) * C::kChunk;
         auto tile_token = [&](int i) { return (un.t0 + first + warp + kWarps * i) * kTile; };
         auto load_pages = [&](int base) {
             pg_base = base;
@@ -193,21 +214,19 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
                 const int in = j & ((1 << p.shift) - 1);
                 mbar_arrive_expect_tx(bar, ((int)va + (int)vb) * C::kChunk);
                 if (va) {
-                    const uint8_t *src =
-                        p.cache + kv4_chunk_offset(a, h, in, p.kv_heads, p.shift, D);
-                    bulk_g2s(dst, src, vb && p.shift > 4 ? 2 * C::kChunk : C::kChunk, bar);
+                    bulk_g2s(dst, head_base + a * page_bytes + (in >> 4) * C::kChunk,
+                             vb && p.shift > 4 ? 2 * C::kChunk : C::kChunk, bar);
                 }
                 if (vb && !(va && p.shift > 4))
                     bulk_g2s(dst + C::kChunk,
-                             p.cache + kv4_chunk_offset(b, h, p.shift > 4 ? in + 16 : 0, p.kv_heads,
-                                                        p.shift, D),
+                             head_base + b * page_bytes + (p.shift > 4 ? (in >> 4) + 1 : 0) * C::kChunk,
                              C::kChunk, bar);
             }
         };
         if (tiles > 0) load_pages(0);
         for (int i = 0; i < min(tiles, kStages); i++) issue(i);
 
-        // ---- query columns: fp16 parts of this thread's D / 4 dimensions of column g ----
+        // ---- fp16 parts of the queries, and the columns' constants ----
         uint32_t qb[NT][2 * W][2];
         float col_a[NT][2], col_sum[NT][2];  // of the columns 2 tg, 2 tg + 1 (SPLIT: parts of one)
         int col_hi[NT][2], col_lo[NT][2];
@@ -215,19 +234,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
         for (int nt = 0; nt < NT; nt++) {
             const int part = SPLIT == 2 ? g & 1 : 0;
             const int c = SPLIT == 2 ? nt * 4 + g / 2 : nt * 8 + g;
-            float x[8 * W];
-            const bool live = c < ncol;
-            const int cc = col0 + (live ? c : 0);
-            const int qi = cc / p.group, head = h * p.group + cc % p.group;
-            const T *src = static_cast<const T *>(p.q) + (int64_t)(rq.q0 + qi) * p.q_stride +
-                           (int64_t)head * D + tg * (D / 4);
-#pragma unroll
-            for (int i = 0; i < W; i++) {
-                float y[8];
-                load8(src + 8 * i, y);
-#pragma unroll
-                for (int e = 0; e < 8; e++) x[8 * i + e] = live ? y[e] : 0.f;
-            }
+            const int qi = (col0 + (c < ncol ? c : 0)) / p.group;
+            float(&x)[8 * W] = qx[nt];
             float amax = 0.f;
 #pragma unroll
             for (int i = 0; i < 8 * W; i++) amax = fmaxf(amax, fabsf(x[i]));
@@ -270,7 +278,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
         if (p.window) all_lo = rq.base + (col0 + ncol - 1) / p.group - p.window + 1;
 
         float o[D / 16][NT][4];
-        float ref[NT][2], sum[NT][2], zero[NT][2];
+        float ref[NT][2], base[NT][2], sum[NT][2], zero[NT][2];
 #pragma unroll
         for (int nt = 0; nt < NT; nt++) {
 #pragma unroll
@@ -278,7 +286,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
 #pragma unroll
                 for (int e = 0; e < 4; e++) o[m][nt][e] = 0.f;
 #pragma unroll
-            for (int e = 0; e < 2; e++) ref[nt][e] = -INFINITY, sum[nt][e] = 0.f, zero[nt][e] = 0.f;
+            for (int e = 0; e < 2; e++) ref[nt][e] = -INFINITY, base[nt][e] = sum[nt][e] = zero[nt][e] = 0.f;
         }
 
         for (int i = 0; i < tiles; i++) {
@@ -289,23 +297,23 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
             }
             const int j0 = tile_token(i);
             const uint32_t bits = (valid >> (2 * stage)) & 3u;
-            const bool inside = j0 >= all_lo && j0 + kTile <= all_hi;
-#pragma unroll 1
+            const bool inside = bits == 3u && j0 >= all_lo && j0 + kTile <= all_hi;
+            const uint8_t *tile = ring + stage * C::kStage;
+            // Row g of the first product is token g ^ (bit 1 of g) of a chunk, so that both the key
+            // rows of eight lanes and the value rows of 16 lanes lie in different banks (or two).
+            const int tok = g ^ ((g >> 1) & 1);
+            constexpr int E = SPLIT == 2 ? 1 : 2;
+            // Tokens of this thread: 2 * half and 2 * half + 1 are tok and tok + 8 of a chunk.
+            float2 kd[4], vd[4];
+            float s[NT][E][4];
+#pragma unroll
             for (int half = 0; half < 2; half++) {
-                if (!(bits >> half & 1)) continue;
-                const uint8_t *chunk = ring + stage * C::kStage + half * C::kChunk;
-                // Row g of the first product is token g ^ (bit 1 of g), so that both the key rows
-                // of eight lanes and the value rows of 16 lanes lie in different banks (or two).
-                const int tok = g ^ ((g >> 1) & 1);
-                const int ja = j0 + 16 * half + tok, jb = ja + 8;
+                const uint8_t *chunk = tile + half * C::kChunk;
                 const __half2 *kp = reinterpret_cast<const __half2 *>(chunk + 2 * kv4_codes_bytes(D));
-                const __half2 *vp = kp + LB_KV4_CHUNK;
-                float2 ka = __half22float2(kp[tok]), kb = __half22float2(kp[tok + 8]);
-                float2 va = __half22float2(vp[tok]), vb = __half22float2(vp[tok + 8]);
-                if (!inside) {  // what lies behind the request's end is not read as a number
-                    const float2 none = make_float2(0.f, 0.f);
-                    if (ja >= un.hi) ka = none, va = none;
-                    if (jb >= un.hi) kb = none, vb = none;
+#pragma unroll
+                for (int e = 0; e < 2; e++) {
+                    kd[2 * half + e] = __half22float2(kp[tok + 8 * e]);
+                    vd[2 * half + e] = __half22float2(kp[LB_KV4_CHUNK + tok + 8 * e]);
                 }
                 float acc[NT][4];
 #pragma unroll
@@ -313,106 +321,122 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
 #pragma unroll
                     for (int e = 0; e < 4; e++) acc[nt][e] = 0.f;
                 uint32_t wa[W], wb[W];
-                const uint8_t *ra_ = chunk + tok * (D / 2) + tg * (D / 8);
+                const uint8_t *row = chunk + tok * (D / 2) + tg * (D / 8);
                 if (D == 128) {
-                    const uint4 a = *reinterpret_cast<const uint4 *>(ra_);
-                    const uint4 b = *reinterpret_cast<const uint4 *>(ra_ + 8 * (D / 2));
+                    const uint4 a = *reinterpret_cast<const uint4 *>(row);
+                    const uint4 b = *reinterpret_cast<const uint4 *>(row + 8 * (D / 2));
                     wa[0] = a.x, wa[1] = a.y, wa[W - 2] = a.z, wa[W - 1] = a.w;
                     wb[0] = b.x, wb[1] = b.y, wb[W - 2] = b.z, wb[W - 1] = b.w;
                 } else {
-                    const uint2 a = *reinterpret_cast<const uint2 *>(ra_);
-                    const uint2 b = *reinterpret_cast<const uint2 *>(ra_ + 8 * (D / 2));
+                    const uint2 a = *reinterpret_cast<const uint2 *>(row);
+                    const uint2 b = *reinterpret_cast<const uint2 *>(row + 8 * (D / 2));
                     wa[0] = a.x, wa[1] = a.y, wb[0] = b.x, wb[1] = b.y;
                 }
 #pragma unroll
-                for (int i2 = 0; i2 < W; i2++) {
+                for (int k = 0; k < W; k++) {
                     uint32_t xa[4], xb[4];
-                    spread_codes(wa[i2], xa);
-                    spread_codes(wb[i2], xb);
+                    spread_codes(wa[k], xa);
+                    spread_codes(wb[k], xb);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
-                        mma16816(acc[nt], xa[0], xb[0], xa[1], xb[1], qb[nt][2 * i2][0],
-                                 qb[nt][2 * i2][1]);
-                        mma16816(acc[nt], xa[2], xb[2], xa[3], xb[3], qb[nt][2 * i2 + 1][0],
-                                 qb[nt][2 * i2 + 1][1]);
+                        mma16816(acc[nt], xa[0], xb[0], xa[1], xb[1], qb[nt][2 * k][0], qb[nt][2 * k][1]);
+                        mma16816(acc[nt], xa[2], xb[2], xa[3], xb[3], qb[nt][2 * k + 1][0],
+                                 qb[nt][2 * k + 1][1]);
                     }
                 }
-                // Scores in powers of two; s[..][0..1] token a, [2..3] token b.
-                constexpr int E = SPLIT == 2 ? 1 : 2;
-                float s[NT][E][2];
-                const float ea = scale_exponent(va.x), eb = scale_exponent(vb.x);
-                bool move = false;
 #pragma unroll
                 for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int e = 0; e < E; e++) {
-                        const float xa = SPLIT == 2 ? acc[nt][0] + acc[nt][1] : acc[nt][e];
-                        const float xb = SPLIT == 2 ? acc[nt][2] + acc[nt][3] : acc[nt][2 + e];
-                        float sa = (ka.x * col_a[nt][e]) * fmaf(-ka.y, col_sum[nt][e], xa);
-                        float sb = (kb.x * col_a[nt][e]) * fmaf(-kb.y, col_sum[nt][e], xb);
-                        if (!inside) {
-                            if (ja >= col_hi[nt][e] || ja < col_lo[nt][e]) sa = -INFINITY;
-                            if (jb >= col_hi[nt][e] || jb < col_lo[nt][e]) sb = -INFINITY;
-                        }
-                        s[nt][e][0] = sa, s[nt][e][1] = sb;
-                        move |= fmaxf(sa + ea, sb + eb) > ref[nt][e] + kSlack;
+                        s[nt][e][2 * half] = SPLIT == 2 ? acc[nt][0] + acc[nt][1] : acc[nt][e];
+                        s[nt][e][2 * half + 1] = SPLIT == 2 ? acc[nt][2] + acc[nt][3] : acc[nt][2 + e];
                     }
-                if (__any_sync(0xffffffffu, move)) {
+            }
+            int tj[4];
+            if (!inside) {  // what lies behind the request's end is not read as a number
 #pragma unroll
-                    for (int nt = 0; nt < NT; nt++)
-#pragma unroll
-                        for (int e = 0; e < E; e++) {
-                            float m = fmaxf(s[nt][e][0] + ea, s[nt][e][1] + eb);
-#pragma unroll
-                            for (int k = 4; k < 32; k <<= 1)
-                                m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
-                            m = fmaxf(m, ref[nt][e]);
-                            const float f = m == ref[nt][e] ? 1.f : ex2(ref[nt][e] - m);
-                            ref[nt][e] = m;
-                            sum[nt][e] *= f, zero[nt][e] *= f;
-#pragma unroll
-                            for (int d = 0; d < D / 16; d++) {
-                                o[d][nt][e] *= f, o[d][nt][2 + e] *= f;
-                                if (SPLIT == 2) o[d][nt][1] *= f, o[d][nt][3] *= f;
-                            }
-                        }
+                for (int x = 0; x < 4; x++) {
+                    tj[x] = bits >> (x / 2) & 1 ? j0 + 16 * (x / 2) + 8 * (x & 1) + tok : 0x7fffffff;
+                    if (tj[x] >= un.hi) kd[x] = vd[x] = make_float2(0.f, 0.f);
                 }
-                uint32_t pb[NT][2];
-                const float la = va.x * kLift, lb = vb.x * kLift;
+            }
+            // Scores in powers of two, and the bound of the weights' size.
+            float vl[4];
+            bool move = false;
 #pragma unroll
-                for (int nt = 0; nt < NT; nt++) {
-                    float w[2][2];
+            for (int x = 0; x < 4; x++) vl[x] = scale_log2(vd[x].x);
+#pragma unroll
+            for (int nt = 0; nt < NT; nt++)
+#pragma unroll
+                for (int e = 0; e < E; e++) {
+                    float top = -INFINITY;
+#pragma unroll
+                    for (int x = 0; x < 4; x++) {
+                        float y = (kd[x].x * col_a[nt][e]) * fmaf(-kd[x].y, col_sum[nt][e], s[nt][e][x]);
+                        if (!inside && (tj[x] >= col_hi[nt][e] || tj[x] < col_lo[nt][e])) y = -INFINITY;
+                        s[nt][e][x] = y;
+                        top = fmaxf(top, y + vl[x]);
+                    }
+                    move |= top > ref[nt][e] + kSlack;
+                }
+            if (__any_sync(0xffffffffu, move)) {
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++)
 #pragma unroll
                     for (int e = 0; e < E; e++) {
-                        const float base = ref[nt][e] == -INFINITY ? 0.f : ref[nt][e];
-                        const float pa = ex2(s[nt][e][0] - base), pc = ex2(s[nt][e][1] - base);
-                        sum[nt][e] += pa + pc;
-                        w[e][0] = pa * la, w[e][1] = pc * lb;
+                        float m = ref[nt][e];
+#pragma unroll
+                        for (int x = 0; x < 4; x++) m = fmaxf(m, s[nt][e][x] + vl[x]);
+#pragma unroll
+                        for (int k = 4; k < 32; k <<= 1)
+                            m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, k));
+                        const float f = m == ref[nt][e] ? 1.f : ex2(ref[nt][e] - m);
+                        ref[nt][e] = m;
+                        // a column that has seen nothing yet: any finite base gives weights of 0
+                        base[nt][e] = m == -INFINITY ? 0.f : m;
+                        sum[nt][e] *= f, zero[nt][e] *= f;
+#pragma unroll
+                        for (int d = 0; d < D / 16; d++) {
+                            o[d][nt][e] *= f, o[d][nt][2 + e] *= f;
+                            if (SPLIT == 2) o[d][nt][1] *= f, o[d][nt][3] *= f;
+                        }
                     }
-                    if (SPLIT == 2) {
-                        // Two parts: the second holds what rounding to fp16 took from the first.
-                        const __half ha = __float2half_rn(w[0][0]), hb = __float2half_rn(w[0][1]);
-                        zero[nt][0] += w[0][0] * va.y + w[0][1] * vb.y;
-                        const __half2 qa = __halves2half2(ha, __float2half_rn(w[0][0] - __half2float(ha)));
-                        const __half2 qc = __halves2half2(hb, __float2half_rn(w[0][1] - __half2float(hb)));
-                        pb[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&qa));
-                        pb[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&qc));
+            }
+            uint32_t pb[NT][4];
+#pragma unroll
+            for (int x = 0; x < 4; x++) {
+                const float lift = vd[x].x * kLift;
+#pragma unroll
+                for (int nt = 0; nt < NT; nt++) {
+                    float w[2];
+#pragma unroll
+                    for (int e = 0; e < E; e++) {
+                        const float pr = ex2(s[nt][e][x] - base[nt][e]);
+                        sum[nt][e] += pr;
+                        w[e] = pr * lift;
+                    }
+                    __half2 q2;
+                    if (SPLIT == 2) {  // two parts: the second holds what rounding took from the first
+                        const __half hi = __float2half_rn(w[0]);
+                        q2 = __halves2half2(hi, __float2half_rn(w[0] - __half2float(hi)));
+                        zero[nt][0] = fmaf(w[0], vd[x].y, zero[nt][0]);
                     } else {
                         // The zero's share uses the weights as rounded, so that an error of a
                         // weight acts on d (c - z), not on d c and d z apart.
-                        const __half2 qa = __floats2half2_rn(w[0][0], w[1][0]);
-                        const __half2 qc = __floats2half2_rn(w[0][1], w[1][1]);
-                        const float2 fa = __half22float2(qa), fc = __half22float2(qc);
-                        zero[nt][0] += fa.x * va.y + fc.x * vb.y;
-                        zero[nt][1] += fa.y * va.y + fc.y * vb.y;
-                        pb[nt][0] = transpose8x8(*reinterpret_cast<const uint32_t *>(&qa));
-                        pb[nt][1] = transpose8x8(*reinterpret_cast<const uint32_t *>(&qc));
+                        q2 = __floats2half2_rn(w[0], w[1]);
+                        const float2 f = __half22float2(q2);
+                        zero[nt][0] = fmaf(f.x, vd[x].y, zero[nt][0]);
+                        zero[nt][E - 1] = fmaf(f.y, vd[x].y, zero[nt][E - 1]);
                     }
+                    pb[nt][x] = transpose8x8(*reinterpret_cast<const uint32_t *>(&q2));
                 }
-                // Second product: this thread's dimensions g * D/8 .. of tokens (k order) 2 tg,
-                // 2 tg + 1, 2 tg + 8, 2 tg + 9.
-                const int t0 = (2 * tg) ^ (tg & 1), t1 = (2 * tg + 1) ^ (tg & 1);
-                const uint8_t *vr = chunk + kv4_codes_bytes(D) + g * (D / 16);
+            }
+            // Second product: this thread's dimensions g * D/8 .. of tokens (k order) 2 tg,
+            // 2 tg + 1, 2 tg + 8, 2 tg + 9 of each chunk.
+            const int t0 = (2 * tg) ^ (tg & 1), t1 = (2 * tg + 1) ^ (tg & 1);
+#pragma unroll
+            for (int half = 0; half < 2; half++) {
+                const uint8_t *vr = tile + half * C::kChunk + kv4_codes_bytes(D) + g * (D / 16);
                 uint32_t v0[VW], v1[VW], v2[VW], v3[VW];
                 if (D == 128) {
                     const uint2 a = *reinterpret_cast<const uint2 *>(vr + t0 * (D / 2));
@@ -428,17 +452,18 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
                     v3[0] = *reinterpret_cast<const uint32_t *>(vr + (t1 + 8) * (D / 2));
                 }
 #pragma unroll
-                for (int i2 = 0; i2 < VW; i2++)
+                for (int k = 0; k < VW; k++)
 #pragma unroll
                     for (int hw = 0; hw < 2; hw++) {
                         uint32_t x[4], y[4];
-                        spread_codes(prmt(v0[i2], v1[i2], hw ? 0x7632 : 0x5410), x);
-                        spread_codes(prmt(v2[i2], v3[i2], hw ? 0x7632 : 0x5410), y);
+                        spread_codes(prmt(v0[k], v1[k], hw ? 0x7632 : 0x5410), x);
+                        spread_codes(prmt(v2[k], v3[k], hw ? 0x7632 : 0x5410), y);
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++) {
-                            mma16816(o[i2 * 4 + hw * 2][nt], x[0], x[1], y[0], y[1], pb[nt][0], pb[nt][1]);
-                            mma16816(o[i2 * 4 + hw * 2 + 1][nt], x[2], x[3], y[2], y[3], pb[nt][0],
-                                     pb[nt][1]);
+                            mma16816(o[k * 4 + hw * 2][nt], x[0], x[1], y[0], y[1], pb[nt][2 * half],
+                                     pb[nt][2 * half + 1]);
+                            mma16816(o[k * 4 + hw * 2 + 1][nt], x[2], x[3], y[2], y[3], pb[nt][2 * half],
+                                     pb[nt][2 * half + 1]);
                         }
                     }
             }
@@ -512,48 +537,83 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
                 if (d == 0) p.stat[slot * COLS + c] = make_float2(m, l);
             }
         }
-        if (!whole && tid == 0)
-            record[first == 0 ? 1 : 0] = make_int4(r, item, last == un.tiles, ncol);
+        if (!whole && tid == 0) {
+            // The CTA the item begins in: the last one whose run starts at or before its first unit.
+            const int64_t begin = r_begin + (int64_t)item * un.tiles;
+            const int owner = (int)(((begin + 1) * ctas - 1) / total);
+            record[first == 0 ? 1 : 0] = make_int4(r, item, last == un.tiles ? owner + 1 : 0, ncol);
+        }
         fence_proxy_async_shared();  // the merge's writes come before the next item's copies
         __syncthreads();
     }
 }
 
-// Joins the parts of items that several CTAs shared: the CTA that took an item's last part is
-// found by its record; the parts before it lie in the CTAs before it.  One block per CTA record
-// and row, D threads.
+// Joins the parts of items that several CTAs shared.  The record of the CTA that took an item's
+// last part names the CTA that began it; the parts in between are the CTAs' between them.  One
+// block per CTA record and row: the parts' weights first, one part per thread, then their sum with
+// D / 4 threads per part.
+constexpr int kJoin = 128;
 template <int D, typename T, int COLS>
-__global__ void __launch_bounds__(D) attn_join_kernel(const AttnParams p) {
+__global__ void __launch_bounds__(kJoin) attn_join_kernel(const AttnParams p) {
+    constexpr int L = D / 4, GROUPS = kJoin / L;
+    __shared__ float weight[kMaxCtas];
+    __shared__ float red[kJoin / 32], acc[GROUPS][D];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     pdl_wait();
     pdl_launch_dependents();
-    const int b = blockIdx.x, c = blockIdx.y, d = threadIdx.x;
+    const int b = blockIdx.x, c = blockIdx.y;
     const int4 rec = p.record[2 * b];
-    if (rec.x < 0 || !rec.z || c >= rec.w) return;
-    // parts: slots 2 b, 2 (b - 1), ... (continued), then the one that began the item
-    int first = b - 1;
-    while (first > 0 && p.record[2 * first].x == rec.x && p.record[2 * first].y == rec.y) first--;
-    auto slot_of = [&](int i) { return i == first ? 2 * first + 1 : 2 * i; };
-    float m = -INFINITY;
-    for (int i = first; i <= b; i++) m = fmaxf(m, p.stat[slot_of(i) * COLS + c].x);
-    float l = 0.f, x = 0.f;
-#pragma unroll 4
-    for (int i = first; i <= b; i++) {
+    if (rec.x < 0 || rec.z == 0 || c >= rec.w) return;
+    const int first = rec.z - 1, n = b - first + 1;
+    auto slot_of = [&](int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); };
+    float m = -INFINITY, l = 0.f;
+    for (int i = tid; i < n; i += kJoin) m = fmaxf(m, p.stat[slot_of(i) * COLS + c].x);
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if (lane == 0) red[warp] = m;
+    __syncthreads();
+#pragma unroll
+    for (int w = 0; w < kJoin / 32; w++) m = fmaxf(m, red[w]);
+    for (int i = tid; i < n; i += kJoin) {
         const float2 s = p.stat[slot_of(i) * COLS + c];
-        const float v = p.part[((int64_t)slot_of(i) * COLS + c) * D + d];
         const float f = s.x == -INFINITY ? 0.f : ex2(s.x - m);
-        l += f * s.y, x += f * v;
+        weight[i] = f;
+        l = fmaf(f, s.y, l);
     }
+    __syncthreads();
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
+    if (lane == 0) red[warp] = l;
+    float x[4] = {};
+#pragma unroll 4
+    for (int i = tid / L; i < n; i += GROUPS) {
+        const float4 v = *reinterpret_cast<const float4 *>(
+            p.part + ((int64_t)slot_of(i) * COLS + c) * D + tid % L * 4);
+        const float f = weight[i];
+        x[0] = fmaf(f, v.x, x[0]), x[1] = fmaf(f, v.y, x[1]);
+        x[2] = fmaf(f, v.z, x[2]), x[3] = fmaf(f, v.w, x[3]);
+    }
+    *reinterpret_cast<float4 *>(&acc[tid / L][tid % L * 4]) = make_float4(x[0], x[1], x[2], x[3]);
+    __syncthreads();
+    l = 0.f;
+#pragma unroll
+    for (int w = 0; w < kJoin / 32; w++) l += red[w];
     const Request q = load_request(p, rec.x);
     const int groups = (q.n * p.group + COLS - 1) / COLS;
     const int cc = rec.y % groups * COLS + c, head = rec.y / groups * p.group + cc % p.group;
     const int64_t t = q.q0 + cc / p.group;
-    store_value(static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + d, l > 0.f ? x / l : 0.f);
-    if (p.lse && d == 0) p.lse[t * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (tid < D) {
+        float y = 0.f;
+#pragma unroll
+        for (int i = 0; i < GROUPS; i++) y += acc[i][tid];
+        store_value(static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + tid,
+                    l > 0.f ? y / l : 0.f);
+    }
+    if (p.lse && tid == 0) p.lse[t * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
 }
 
-template <int D, typename T, int NT>
+template <int D, typename T, int SPLIT, int NT>
 static int launch_decode(AttnParams p, uint8_t *workspace, int sms, cudaStream_t st) {
-    constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
     using C = Decode<D, SPLIT, NT>;
     p.record = reinterpret_cast<int4 *>(workspace);
     p.stat = reinterpret_cast<float2 *>(p.record + 2 * kMaxCtas);
@@ -564,15 +624,23 @@ static int launch_decode(AttnParams p, uint8_t *workspace, int sms, cudaStream_t
     const int ctas = sms * per_sm < kMaxCtas ? sms * per_sm : kMaxCtas;
     if (int e = launch_pdl(kernel, dim3(ctas), dim3(kThreads), C::kSmem, st, p)) return e;
     if ((p.width << p.shift) <= kWhole * kTile) return LB_OK;  // no item can have been split
-    return launch_pdl(attn_join_kernel<D, T, C::kCols>, dim3(ctas, C::kCols), dim3(D), 0, st, p);
+    return launch_pdl(attn_join_kernel<D, T, C::kCols>, dim3(ctas, C::kCols), dim3(kJoin), 0, st,
+                      p);
 }
 
-template <int D, typename T>
-static int dispatch_decode(const AttnParams &p, int64_t max_q, uint8_t *workspace, int sms,
-                           cudaStream_t st) {
-    constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
-    return max_q * p.group * SPLIT <= 8 ? launch_decode<D, T, 1>(p, workspace, sms, st)
-                                        : launch_decode<D, T, 2>(p, workspace, sms, st);
+// One fp16 part needs 11 bits (bf16 tensors); fp32 tensors take two.  Up to four rows per head
+// take two parts in either type: the eight columns of a product hold them anyway, and a thread
+// then has one row's scores instead of two, half of them of empty columns.
+template <int D>
+static int dispatch_decode(const AttnParams &p, int type, int64_t max_q, uint8_t *workspace,
+                           int sms, cudaStream_t st) {
+    const int64_t rows = max_q * p.group;
+    if (type == LB_OUT_F32)
+        return rows <= 4 ? launch_decode<D, float, 2, 1>(p, workspace, sms, st)
+                         : launch_decode<D, float, 2, 2>(p, workspace, sms, st);
+    if (rows <= 4) return launch_decode<D, __nv_bfloat16, 2, 1>(p, workspace, sms, st);
+    return rows <= 8 ? launch_decode<D, __nv_bfloat16, 1, 1>(p, workspace, sms, st)
+                     : launch_decode<D, __nv_bfloat16, 1, 2>(p, workspace, sms, st);
 }
 
 }  // namespace lb
@@ -619,9 +687,6 @@ LB_EXPORT int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8
     if (!p.error) return LB_ERR_LAUNCH;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     cudaStream_t st = as_stream(stream);
-    if (type == LB_OUT_F32)
-        return head_dim == 64 ? dispatch_decode<64, float>(p, max_q, ws, di.sms, st)
-                              : dispatch_decode<128, float>(p, max_q, ws, di.sms, st);
-    return head_dim == 64 ? dispatch_decode<64, __nv_bfloat16>(p, max_q, ws, di.sms, st)
-                          : dispatch_decode<128, __nv_bfloat16>(p, max_q, ws, di.sms, st);
+    return head_dim == 64 ? dispatch_decode<64>(p, type, max_q, ws, di.sms, st)
+                          : dispatch_decode<128>(p, type, max_q, ws, di.sms, st);
 }

@@ -18,7 +18,8 @@ struct AttnParams {
     int *error;
     float *part;     // partial sums: [slot][row][D], slot = 2 * CTA + (0: continued, 1: begun)
     float2 *stat;    // [slot][row] {reference exponent, sum of weights}
-    int4 *record;    // [slot] {request, item of the request, 1 = the item's last part, rows}; x < 0: none
+    int4 *record;    // [slot] {request, item of the request, 1 + the CTA that began the item if
+                     // this is its last part else 0, rows}; x < 0: none
 };
 
 // A request as the kernels see it; everything is clamped so that no access leaves its buffer.
@@ -74,9 +75,12 @@ __device__ __forceinline__ void row_power(float amax, float &up, float &down) {
     down = __uint_as_float((uint32_t)(127 - x) << 23);
 }
 
-// Smallest exponent e with d <= 2^e for an fp16 scale widened to binary32 (at least -24).
-__device__ __forceinline__ float scale_exponent(float d) {
-    return (float)max((int)(__float_as_uint(d) >> 23) - 126, -24);
+// log2 of an fp16 scale, to a small error and at least -24 (a scale of 0 gives weights of 0 whatever
+// its score).
+__device__ __forceinline__ float scale_log2(float d) {
+    float y;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(y) : "f"(fmaxf(d, 5.9604645e-8f)));
+    return y;
 }
 
 __device__ __forceinline__ void store_value(float *p, float x) { *p = x; }
