@@ -31,6 +31,8 @@ constexpr int kStages = 4;           // tiles in flight per warp
 constexpr int kWhole = 16;           // items of at most this many tiles are never split
 constexpr int kMinRun = 8;           // tiles per CTA below which no more CTAs are used
 constexpr int kMaxCtas = 608;
+constexpr int kFewRows = 32;         // query rows per head up to which this file's kernel is used
+constexpr int kFewRequests = 8;      // batches this small run as one launch
 constexpr float kLift = 256.f;       // weights are lifted by 2^8 ...
 constexpr float kSlack = 7.f;        // ... and may pass the reference by 2^7 before it moves
 
@@ -647,7 +649,9 @@ static int dispatch_decode(const AttnParams &p, int type, int64_t max_q, uint8_t
 
 LB_EXPORT size_t lb_attn_kv4_workspace_bytes(int heads, int kv_heads, int head_dim, int64_t max_q) {
     if (heads < 1 || kv_heads < 1 || head_dim < 1 || max_q < 1) return 0;
-    return (size_t)lb::kMaxCtas * 2 * (16 + 16 * (8 + (size_t)head_dim * 4));
+    const size_t few = (size_t)lb::kMaxCtas * 2 * (16 + 16 * (8 + (size_t)head_dim * 4));
+    const size_t many = lb::attn_prompt_workspace(head_dim);
+    return max_q * (heads / kv_heads) <= lb::kFewRows || few > many ? few : many;
 }
 
 LB_EXPORT int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8_t *cache,
@@ -687,6 +691,15 @@ LB_EXPORT int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8
     if (!p.error) return LB_ERR_LAUNCH;
     uint8_t *ws = static_cast<uint8_t *>(workspace);
     cudaStream_t st = as_stream(stream);
+    if (max_q * p.group > kFewRows) {
+        // A few requests go together; in a larger batch those with few rows (decode steps beside
+        // prompts) take the other kernel.
+        if (R > kFewRequests) p.rows_lo = kFewRows;
+        if (int e = attn_prompt(p, type, head_dim, ws, di.sms, st)) return e;
+        if (R <= kFewRequests) return LB_OK;
+        p.rows_lo = 0, p.rows_hi = kFewRows;
+        max_q = kFewRows / p.group > 1 ? kFewRows / p.group : 1;
+    }
     return head_dim == 64 ? dispatch_decode<64>(p, type, max_q, ws, di.sms, st)
                           : dispatch_decode<128>(p, type, max_q, ws, di.sms, st);
 }

@@ -22,6 +22,11 @@ struct AttnParams {
                      // this is its last part else 0, rows}; x < 0: none
 };
 
+// Many-row requests (lb_attn_tc.cu): scratch bytes and launches.
+size_t attn_prompt_workspace(int head_dim);
+int attn_prompt(const AttnParams &p, int type, int head_dim, uint8_t *workspace, int sms,
+                cudaStream_t st);
+
 // A request as the kernels see it; everything is clamped so that no access leaves its buffer.
 struct Request {
     int q0, n;       // first query row, queries

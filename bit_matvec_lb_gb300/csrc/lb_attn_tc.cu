@@ -1,0 +1,793 @@
+// lb_attn_tc.cu -- attention over the paged 4-bit key/value cache for requests with many query rows
+// (prompts, chunks of them) on the 5th-generation tensor cores.
+#include "lb_attn.cuh"
+#include "lb_tc.cuh"
+
+namespace lb {
+
+// ------------------------------------------------------------------------------------------
+// Mathematics.  A key/value head's rows (queries x heads of the group, packed) times 128 keys at a
+// time: S = Q K'^T and O += P V', K' and V' the codes less their zero, whole numbers in -15..15 and
+// exact in fp16.  The keys' scales act on the scores, x = S kd_t a_r - R_r in powers of two (a_r
+// holds the row's own power of two, scale and log2 e), the values' scales on the weights,
+// P = 2^x vd_t, which enter the second product as fp16 bounded by the reference R_r (see below).
+// fp32 tensors take two fp16 parts of Q and of P: each product twice.
+//
+// One CTA per SM, 14 warps: two times four for the softmax of two tiles of 128 rows (a thread per
+// row), four that turn codes into fp16 operands, one that issues the tensor-core operations and
+// one that copies cache chunks in.  S of both tiles and O of both fill tensor memory (4 x 128
+// columns); P overwrites S.  The operations are issued PV0(j) QK0(j+1) PV1(j) QK1(j+1), so each
+// tile's softmax runs under the other tile's products.
+//
+// The reference moves only when it must: weights may grow until a tile's sum times the tile's
+// largest value scale would leave fp16's range; only then are the scores read a second time for
+// their maximum and O rescaled.  Work is split into equal runs of key tiles over the CTAs, parts of
+// an item that several CTAs share are joined by a second kernel.
+// ------------------------------------------------------------------------------------------
+constexpr int kKeys = 128;           // keys per tile
+constexpr int kRows = 128;           // query rows per tile, two tiles per item
+constexpr int kPiece = 64;           // keys per copy stage (four chunks)
+constexpr int kPieces = 3;           // copy stages
+constexpr int kScales = 4;           // tiles of scales kept
+constexpr int kTcThreads = 448;
+constexpr int kTcMaxCtas = 160;
+constexpr int kTcWhole = 4;          // items of at most this many tiles are never split
+constexpr int kTcMinRun = 4;
+constexpr float kTcLift = 16.f;      // weights at the reference: 2^4
+constexpr float kTcMost = 60000.f;   // largest weight a tile may hold
+
+template <int D, int SPLIT>
+struct Prompt {
+    static constexpr int kBuf = 2 / SPLIT;             // fp16 key and value tiles
+    static constexpr int kQ = kRows * D * 2;           // bytes of one part of one row tile
+    static constexpr int kTileB = kKeys * D * 2;
+    static constexpr int kRaw = kPiece / 16 * kv4_chunk_bytes(D);
+    static constexpr int oQ = 0;                       // [2 tiles][SPLIT]
+    static constexpr int oK = oQ + 2 * SPLIT * kQ;     // [kBuf]
+    static constexpr int oV = oK + kBuf * kTileB;
+    static constexpr int oRaw = oV + kBuf * kTileB;    // [kPieces]
+    static constexpr int oScale = oRaw + kPieces * kRaw;  // [kScales][2][kKeys] floats
+    static constexpr int kSmem = oScale + kScales * 2 * kKeys * 4;
+};
+
+struct TcBars {
+    uint64_t raw_full[kPieces], raw_empty[kPieces];
+    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t sc_full[kScales];
+    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+};
+
+// D[tmem] (+)= A[tmem] * B[desc]^T, cta_group::1, kind::f16.
+__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
+                                           uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(tmem_d),
+        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+// Shared-memory matrix descriptor, K-major, no swizzle: core matrices of 8 rows x 16 bytes, 128 B
+// apart along K, `sbo` bytes between groups of 8 rows.
+__device__ __forceinline__ uint64_t kmajor_desc(uint32_t saddr, uint32_t sbo) {
+    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(128 >> 4) << 16 |
+           (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46;
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void tmem_wait_st() {
+    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+}
+__device__ __forceinline__ uint64_t pair_of(float a, float b) {
+    return (uint64_t)__float_as_uint(a) | (uint64_t)__float_as_uint(b) << 32;
+}
+__device__ __forceinline__ float lo_of(uint64_t v) { return __uint_as_float((uint32_t)v); }
+__device__ __forceinline__ float hi_of(uint64_t v) { return __uint_as_float((uint32_t)(v >> 32)); }
+__device__ __forceinline__ uint64_t mul2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("mul.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t add2(uint64_t a, uint64_t b) {
+    uint64_t d;
+    asm("add.rn.f32x2 %0, %1, %2;" : "=l"(d) : "l"(a), "l"(b));
+    return d;
+}
+__device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
+    uint64_t d;
+    asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
+    return d;
+}
+
+// Rows [256 b, 256 b + 256) of a request: their visible key tiles.
+struct Pair {
+    int lo, hi, t0, tiles, rows;
+};
+__device__ __forceinline__ Pair pair_of_rows(const AttnParams &p, const Request &q, int b) {
+    Pair x;
+    const int total = q.n * p.group, r0 = b * 2 * kRows;
+    x.rows = min(2 * kRows, total - r0);
+    visible_range(p, q, r0 / p.group, (r0 + x.rows - 1) / p.group + 1, x.lo, x.hi);
+    x.t0 = x.lo / kKeys;
+    x.tiles = max((x.hi + kKeys - 1) / kKeys - x.t0, 1);
+    return x;
+}
+__device__ __forceinline__ int pairs_of(const AttnParams &p, const Request &q) {
+    return (q.n * p.group + 2 * kRows - 1) / (2 * kRows);
+}
+
+// A CTA's items in order; every warp walks them by itself.
+struct Walk {
+    Request q;
+    Pair x;
+    int r, b, h;            // request, pair of row tiles, head
+    int64_t u, end, begin;  // next unit, end of the run, first unit of the item
+    int first, last;        // this CTA's tiles of the item
+
+    __device__ __forceinline__ void set(const AttnParams &p) {
+        q = load_request(p, r);
+        x = pair_of_rows(p, q, b);
+    }
+    // The next item this CTA takes part in; false at the end of its run.
+    __device__ __forceinline__ bool next(const AttnParams &p) {
+        while (u < end) {
+            while (u >= begin + x.tiles) {
+                begin += x.tiles;
+                if (++h < p.kv_heads) continue;
+                h = 0;
+                if (++b >= pairs_of(p, q)) {
+                    b = 0;
+                    do q = load_request(p, ++r);
+                    while (q.n == 0);
+                }
+                x = pair_of_rows(p, q, b);
+            }
+            first = (int)(u - begin);
+            last = (int)min((int64_t)x.tiles, first + (end - u));
+            u += last - first;
+            if (x.tiles > kTcWhole) return true;
+            if (first == 0) {  // never split: the CTA in whose run it begins takes it
+                last = x.tiles;
+                return true;
+            }
+        }
+        return false;
+    }
+};
+
+template <int D, typename T, int SPLIT>
+__global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnParams p) {
+    using C = Prompt<D, SPLIT>;
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ TcBars bar;
+    __shared__ uint32_t s_tmem, raw_valid[kPieces], sc_valid[kScales][2];
+    __shared__ float sc_max[kScales][8], row_a[2][kRows];
+    __shared__ int64_t scan[kTcThreads / 32], s_begin;
+    __shared__ int s_r, s_b, s_h;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+
+    if (tid == 0) {
+        for (int i = 0; i < kPieces; i++) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], 4);
+        for (int i = 0; i < 2; i++) {
+            mbar_init(&bar.k_full[i], 4), mbar_init(&bar.k_empty[i], 1);
+            mbar_init(&bar.v_full[i], 4), mbar_init(&bar.v_empty[i], 1);
+            mbar_init(&bar.q_full[i], 4), mbar_init(&bar.s_full[i], 1);
+            mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
+        }
+        for (int i = 0; i < kScales; i++) mbar_init(&bar.sc_full[i], 4);
+        fence_mbar_init();
+    }
+    pdl_wait();
+
+    // ---- this CTA's run of units ----
+    const int run = (p.R + kTcThreads - 1) / kTcThreads;
+    const int ra = min(tid * run, p.R), rb = min(ra + run, p.R);
+    int64_t mine = 0;
+    for (int r = ra; r < rb; r++) {
+        const Request q = load_request(p, r);
+        for (int b = 0, n = pairs_of(p, q); b < n; b++)
+            mine += (int64_t)pair_of_rows(p, q, b).tiles * p.kv_heads;
+    }
+    int64_t incl = mine;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int64_t a = __shfl_up_sync(0xffffffffu, incl, o);
+        if (lane >= o) incl += a;
+    }
+    if (lane == 31) scan[warp] = incl;
+    __syncthreads();
+    int64_t total = 0, before = incl - mine;
+#pragma unroll
+    for (int w = 0; w < kTcThreads / 32; w++) {
+        if (w < warp) before += scan[w];
+        total += scan[w];
+    }
+    const int64_t ctas = min((int64_t)gridDim.x, (total + kTcMinRun - 1) / kTcMinRun);
+    int4 *record = p.record + 2 * blockIdx.x;
+    if (tid < 2) record[tid] = make_int4(-1, 0, 0, 0);
+    if (blockIdx.x >= ctas) {
+        pdl_launch_dependents();
+        return;
+    }
+    Walk it;
+    it.u = total * blockIdx.x / ctas, it.end = total * (blockIdx.x + 1) / ctas;
+    if (before <= it.u && it.u < before + mine) {
+        int64_t at = before;
+        for (int r = ra; r < rb; r++) {
+            const Request q = load_request(p, r);
+            for (int b = 0, n = pairs_of(p, q); b < n; b++) {
+                const int64_t t = pair_of_rows(p, q, b).tiles;
+                if (it.u < at + t * p.kv_heads) {
+                    const int h = (int)((it.u - at) / t);
+                    s_r = r, s_b = b, s_h = h, s_begin = at + h * t;
+                    r = rb;
+                    break;
+                }
+                at += t * p.kv_heads;
+            }
+        }
+    }
+    // Tensor memory is taken only now, when the kernels before this one have ended, and the next
+    // kernel may start only after it: neither waits for the other's columns.
+    if (warp == 12) tmem_alloc(&s_tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = s_tmem;
+    const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + D};
+    it.r = s_r, it.b = s_b, it.h = s_h, it.begin = s_begin;
+    it.set(p);
+
+    uint64_t limit = 2000000000ull;
+    auto wait = [&](uint64_t &b, uint32_t parity) {
+        if (!mbar_wait(&b, parity & 1, limit)) {
+            *p.error = 1;
+            limit = 1000000ull;
+        }
+        __syncwarp();
+    };
+    float *kd_s = reinterpret_cast<float *>(smem + C::oScale);   // [kScales][kKeys]
+    float *vd_s = kd_s + kScales * kKeys;
+    uint32_t gt = 0;  // tiles so far, over all items
+
+    if (warp < 8) {
+        // =================== softmax: one row per thread ===================
+        const int w = warp >> 2, row = tid & 127;
+        const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane quarter in the address' upper half
+        const uint32_t S = tS[w] + lanes, O = tO[w] + lanes;
+        uint32_t cw = 0;
+        while (it.next(p)) {
+            const int n = it.last - it.first;
+            const int ncol = it.x.rows - w * kRows;  // rows of this tile
+            if (ncol <= 0) {
+                gt += n;
+                continue;
+            }
+            const int row0 = it.b * 2 * kRows + w * kRows;
+            // ---- queries: a warp's 32 rows, 8 rows x 32 dimensions at a time ----
+#pragma unroll 1
+            for (int g = 0; g < 4; g++) {
+                const int rr = (warp & 3) * 32 + g * 8 + (lane & 7);
+                const int cc = row0 + min(rr, ncol - 1);
+                const T *src = static_cast<const T *>(p.q) +
+                               (int64_t)(it.q.q0 + cc / p.group) * p.q_stride +
+                               (int64_t)(it.h * p.group + cc % p.group) * D + (lane >> 3) * 8;
+                float x[D / 32][8], amax = 0.f;
+#pragma unroll
+                for (int k = 0; k < D / 32; k++) {
+                    load8(src + 32 * k, x[k]);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(x[k][e]));
+                }
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+                float up, down;
+                row_power(amax, up, down);
+                if (lane < 8) row_a[w][rr] = p.scale * kLog2e * down;
+#pragma unroll
+                for (int k = 0; k < D / 32; k++) {
+                    // order 0 4 1 5 2 6 3 7, as the codes of a word unfold
+                    const uint32_t at = (rr >> 3) * (D * 16) + (4 * k + (lane >> 3)) * 128 + (rr & 7) * 16;
+                    uint32_t hi[4], lo[4];
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const float a = x[k][e] * up, b = x[k][e + 4] * up;
+                        const __half2 h2 = __floats2half2_rn(a, b);
+                        hi[e] = *reinterpret_cast<const uint32_t *>(&h2);
+                        lo[e] = half2_bits(a - __low2float(h2), b - __high2float(h2));
+                    }
+                    uint8_t *dst = smem + C::oQ + w * SPLIT * C::kQ + at;
+                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                    if (SPLIT == 2)
+                        *reinterpret_cast<uint4 *>(dst + C::kQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+                }
+            }
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.q_full[w]);
+            const float a = row_a[w][row];
+            const uint64_t a2 = pair_of(a, a);
+            // Keys this row sees, and those all rows of the tile see.
+            const int qi = (row0 + min(row, ncol - 1)) / p.group;
+            int hi = it.x.hi, lo = 0, all_hi = hi, all_lo = 0;
+            if (p.causal) {
+                hi = min(hi, it.q.base + qi + 1);
+                all_hi = min(all_hi, it.q.base + row0 / p.group + 1);
+            }
+            if (p.window) {
+                lo = it.q.base + qi - p.window + 1;
+                all_lo = it.q.base + (row0 + ncol - 1) / p.group - p.window + 1;
+            }
+            float ref = -INFINITY, l = 0.f;
+
+            for (int j = 0; j < n; j++, gt++, cw++) {
+                const int slot = gt % kScales, j0 = (it.x.t0 + it.first + j) * kKeys;
+                wait(bar.sc_full[slot], gt / kScales);
+                const uint32_t ok = sc_valid[slot][0] | sc_valid[slot][1] << 4;
+                const bool inside = ok == 0xFFu && j0 >= all_lo && j0 + kKeys <= all_hi;
+                float vmax = 0.f;
+#pragma unroll
+                for (int e = 0; e < 8; e++) vmax = fmaxf(vmax, sc_max[slot][e]);
+                const ulonglong2 *kd = reinterpret_cast<const ulonglong2 *>(kd_s + slot * kKeys);
+                const ulonglong2 *vd = reinterpret_cast<const ulonglong2 *>(vd_s + slot * kKeys);
+                wait(bar.s_full[w], cw);
+                tc_fence_after();
+
+                // Scores of 32 keys (c) as pairs, masked if need be.
+                auto scores = [&](int c, uint64_t (&s)[16]) {
+                    tmem_ld32_pairs(S + 32 * c, s);
+#pragma unroll
+                    for (int e = 0; e < 8; e++) {
+                        const ulonglong2 k = kd[8 * c + e];
+                        s[2 * e] = mul2(mul2(s[2 * e], k.x), a2);
+                        s[2 * e + 1] = mul2(mul2(s[2 * e + 1], k.y), a2);
+                    }
+                    if (!inside) {
+#pragma unroll
+                        for (int e = 0; e < 16; e++) {
+                            const int t = j0 + 32 * c + 2 * e;
+                            const bool there = ok >> (2 * c + (e >> 3)) & 1;
+                            s[e] = pair_of(there && t >= lo && t < hi ? lo_of(s[e]) : -INFINITY,
+                                           there && t + 1 >= lo && t + 1 < hi ? hi_of(s[e]) : -INFINITY);
+                        }
+                    }
+                };
+                // The row's maximum, a new reference, and O under it.
+                auto move = [&]() {
+                    float m = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; c++) {
+                        uint64_t s[16];
+                        scores(c, s);
+#pragma unroll
+                        for (int e = 0; e < 16; e++) m = fmaxf(m, fmaxf(lo_of(s[e]), hi_of(s[e])));
+                    }
+                    m = fmaxf(ref, m + scale_log2(vmax * (1.f / kTcLift)));
+                    const float f = m == ref ? 1.f : ex2(ref - m);
+                    ref = m;
+                    l *= f;
+                    if (j > 0) {
+                        wait(bar.o_full[w], cw - 1);
+                        tc_fence_after();
+#pragma unroll 1
+                        for (int c = 0; c < D; c += 32) {
+                            uint32_t o[32];
+                            tmem_ld32(O + c, o);
+#pragma unroll
+                            for (int e = 0; e < 32; e++)
+                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
+                            tmem_st16(O + c, o);
+                            tmem_st16(O + c + 16, o + 16);
+                        }
+                        tmem_wait_st();
+                    }
+                };
+                if (SPLIT == 2) {
+                    // Two passes: the maximum first (the products take twice as long here).
+                    float m = -INFINITY;
+#pragma unroll 1
+                    for (int c = 0; c < 4; c++) {
+                        uint64_t s[16];
+                        scores(c, s);
+#pragma unroll
+                        for (int e = 0; e < 16; e++) m = fmaxf(m, fmaxf(lo_of(s[e]), hi_of(s[e])));
+                    }
+                    if (__any_sync(0xffffffffu, m + scale_log2(vmax * (1.f / kTcLift)) > ref + 8.f)) move();
+                    const float b = ref == -INFINITY ? 0.f : ref;
+                    const uint64_t nr = pair_of(-b, -b);
+                    uint64_t sum = 0;
+#pragma unroll 1
+                    for (int c = 0; c < 4; c++) {
+                        uint64_t s[16];
+                        uint32_t ph[16], pl[16];
+                        scores(c, s);
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            const ulonglong2 v = vd[8 * c + e];
+#pragma unroll
+                            for (int k = 0; k < 2; k++) {
+                                const uint64_t x = add2(s[2 * e + k], nr);
+                                const uint64_t pr = pair_of(ex2(lo_of(x)), ex2(hi_of(x)));
+                                sum = add2(sum, pr);
+                                const uint64_t wv = mul2(pr, k ? v.y : v.x);
+                                const __half2 h2 = __floats2half2_rn(lo_of(wv), hi_of(wv));
+                                ph[2 * e + k] = *reinterpret_cast<const uint32_t *>(&h2);
+                                pl[2 * e + k] = half2_bits(lo_of(wv) - __low2float(h2), hi_of(wv) - __high2float(h2));
+                            }
+                        }
+                        tmem_st16(S + 32 * c, ph);
+                        tmem_st16(S + 32 * c + 16, pl);
+                    }
+                    l += lo_of(sum) + hi_of(sum);
+                } else {
+                    uint32_t ph[64];
+                    float part;
+                    auto weights = [&]() {
+                        const float b = ref == -INFINITY ? 0.f : ref;
+                        const uint64_t nr = pair_of(-b, -b);
+                        uint64_t sum = 0;
+#pragma unroll
+                        for (int c = 0; c < 4; c++) {
+                            uint64_t s[16];
+                            scores(c, s);
+#pragma unroll
+                            for (int e = 0; e < 8; e++) {
+                                const ulonglong2 v = vd[8 * c + e];
+#pragma unroll
+                                for (int k = 0; k < 2; k++) {
+                                    const uint64_t x = add2(s[2 * e + k], nr);
+                                    const uint64_t pr = pair_of(ex2(lo_of(x)), ex2(hi_of(x)));
+                                    sum = add2(sum, pr);
+                                    const uint64_t wv = mul2(pr, k ? v.y : v.x);
+                                    ph[16 * c + 2 * e + k] = half2_bits(lo_of(wv), hi_of(wv));
+                                }
+                            }
+                        }
+                        part = lo_of(sum) + hi_of(sum);
+                    };
+                    weights();
+                    if (__any_sync(0xffffffffu, ref == -INFINITY || !(part * vmax <= kTcMost))) {
+                        move();
+                        weights();
+                    }
+                    l += part;
+#pragma unroll
+                    for (int c = 0; c < 4; c++) tmem_st16(S + 16 * c, ph + 16 * c);
+                }
+                tmem_wait_st();
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.p_full[w]);
+            }
+
+            // ---- outputs, or this CTA's part of them ----
+            wait(bar.o_full[w], cw - 1);
+            tc_fence_after();
+            const bool whole = it.first == 0 && it.last == it.x.tiles;
+            const int part = 2 * blockIdx.x + (it.first == 0 ? 1 : 0);
+            const int cc = row0 + row, head = it.h * p.group + cc % p.group;
+            const int64_t t = it.q.q0 + cc / p.group;
+            const float f = (whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f) * (1.f / kTcLift);
+#pragma unroll 1
+            for (int c = 0; c < D; c += 64) {
+                // column 8 e + k of these 64 is dimension 8 k + e
+                uint32_t o0[32], o1[32];
+                tmem_ld32(O + c, o0);
+                tmem_ld32(O + c + 32, o1);
+                if (row < ncol) {
+#pragma unroll
+                    for (int k = 0; k < 8; k++) {
+                        float y[8];
+#pragma unroll
+                        for (int e = 0; e < 8; e++) {
+                            y[e] = __uint_as_float(e < 4 ? o0[8 * e + k] : o1[8 * (e - 4) + k]) * f;
+                            if (whole && !(l > 0.f)) y[e] = 0.f;
+                        }
+                        if (whole)
+                            store8(static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + c + 8 * k, y);
+                        else
+                            store8(p.part + ((int64_t)part * (2 * kRows) + w * kRows + row) * D + c + 8 * k, y);
+                    }
+                }
+                __syncwarp();
+            }
+            if (row < ncol) {
+                if (!whole)
+                    p.stat[part * 2 * kRows + w * kRows + row] = make_float2(ref, l);
+                else if (p.lse)
+                    p.lse[t * p.heads + head] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+            }
+            if (!whole && tid == 0) {
+                const int owner = (int)(((it.begin + 1) * ctas - 1) / total);
+                record[it.first == 0 ? 1 : 0] = make_int4(
+                    it.r, it.b * p.kv_heads + it.h, it.last == it.x.tiles ? owner + 1 : 0, it.x.rows);
+            }
+            tc_fence_before();  // O is read before the next item's products write it
+        }
+    } else if (warp < 12) {
+        // =================== codes to fp16 operands: one chunk per warp and piece ===================
+        const int q = warp - 8;
+        uint32_t piece = 0;
+        const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k64 = __half2half2(__ushort_as_half(0x5400));
+        // 8 codes less their zeros: pairs (0,4) (1,5) (2,6) (3,7); z1024 = 1024 + z, z64 = 64 + z.
+        auto unfold = [&](uint32_t w, __half2 z1024, __half2 z64, uint32_t (&x)[4]) {
+            const uint32_t h = w >> 8;
+            uint32_t y[4];
+            asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(y[0]) : "r"(w));
+            asm("lop3.b32 %0, %1, 0x00F000F0, 0x54005400, 0xEA;" : "=r"(y[1]) : "r"(w));
+            asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(y[2]) : "r"(h));
+            asm("lop3.b32 %0, %1, 0x00F000F0, 0x54005400, 0xEA;" : "=r"(y[3]) : "r"(h));
+#pragma unroll
+            for (int e = 0; e < 4; e++) {
+                const __half2 v = __hsub2(*reinterpret_cast<__half2 *>(&y[e]), e & 1 ? z64 : z1024);
+                x[e] = *reinterpret_cast<const uint32_t *>(&v);
+            }
+        };
+        while (it.next(p)) {
+            const int n = it.last - it.first;
+            for (int j = 0; j < n; j++, gt++) {
+                const int buf = gt % C::kBuf, slot = gt % kScales;
+                const uint32_t turn = gt / C::kBuf;
+                uint8_t *K = smem + C::oK + buf * C::kTileB, *V = smem + C::oV + buf * C::kTileB;
+                // All keys before any values: with one buffer of each, the values of the tile before
+                // are free only after the products with these keys.
+                wait(bar.k_empty[buf], turn + 1);
+#pragma unroll 1
+                for (int half = 0; half < 2; half++) {
+                    const int st = (piece + half) % kPieces;
+                    wait(bar.raw_full[st], (piece + half) / kPieces);
+                    const uint8_t *chunk = smem + C::oRaw + st * C::kRaw + q * kv4_chunk_bytes(D);
+                    const uint32_t valid = raw_valid[st];
+                    const int j0 = (it.x.t0 + it.first + j) * kKeys + half * kPiece + q * 16;
+                    const int live = valid >> q & 1 ? min(16, it.x.hi - j0) : 0;  // tokens that exist
+                    const __half2 *pairs = reinterpret_cast<const __half2 *>(chunk + 2 * kv4_codes_bytes(D));
+                    {  // scales: lane t < 16 keys, the others values
+                        const int t = lane & 15;
+                        const float d = t < live ? __low2float(pairs[lane]) : 0.f;
+                        const int at = slot * kKeys + half * kPiece + q * 16 + t;
+                        if (lane < 16) kd_s[at] = d;
+                        else vd_s[at] = d * kTcLift;
+                        float m = lane < 16 ? 0.f : d * kTcLift;
+#pragma unroll
+                        for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+                        if (lane == 16) sc_max[slot][half * 4 + q] = m;
+                        if (lane == 0 && q == 0) sc_valid[slot][half] = valid;
+                    }
+                    // ---- keys ----
+                    constexpr int QN = D / 32;              // 16-byte quarters of a key row
+                    constexpr int TN = 32 / QN;             // tokens per step
+#pragma unroll
+                    for (int s = 0; s < 16 / TN; s++) {
+                        const int t8 = lane & 7, t = s * TN + (lane >> 3) / QN * 8 + t8;
+                        // rotated so that both the reads and the writes of 8 lanes miss each other
+                        const int kq = ((lane >> 3) % QN + (D == 128 ? t8 >> 1 : t8 >> 2)) % QN;
+                        const uint4 wv = *reinterpret_cast<const uint4 *>(chunk + t * (D / 2) + kq * 16);
+                        const uint32_t w4[4] = {wv.x, wv.y, wv.z, wv.w};
+                        const __half2 z = __half2half2(t < live ? __high2half(pairs[t]) : __ushort_as_half(0));
+                        const __half2 za = __hadd2(k1024, z), zb = __hadd2(k64, z);
+                        const int tt = half * kPiece + q * 16 + t;
+                        uint8_t *dst = K + (tt >> 3) * (D * 16) + (kq * 4) * 128 + (tt & 7) * 16;
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            uint32_t x[4];
+                            unfold(w4[i], za, zb, x);
+                            *reinterpret_cast<uint4 *>(dst + i * 128) = make_uint4(x[0], x[1], x[2], x[3]);
+                        }
+                    }
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.k_full[buf]), mbar_arrive(&bar.sc_full[slot]);
+                wait(bar.v_empty[buf], turn + 1);
+#pragma unroll 1
+                for (int half = 0; half < 2; half++, piece++) {
+                    const int st = piece % kPieces;
+                    const uint8_t *chunk = smem + C::oRaw + st * C::kRaw + q * kv4_chunk_bytes(D);
+                    const int j0 = (it.x.t0 + it.first + j) * kKeys + half * kPiece + q * 16;
+                    const int live = raw_valid[st] >> q & 1 ? min(16, it.x.hi - j0) : 0;
+                    const __half2 *pairs = reinterpret_cast<const __half2 *>(chunk + 2 * kv4_codes_bytes(D));
+                    // ---- values: 8 tokens x 8 dimensions per lane, transposed ----
+                    constexpr int WN = D / 8;
+                    if (lane < 2 * WN) {
+                        const int wi = lane % WN, gr = lane / WN;
+                        const uint8_t *src = chunk + kv4_codes_bytes(D) + gr * 8 * (D / 2) + wi * 4;
+                        uint32_t x[4][8];  // token pair, dimension
+#pragma unroll
+                        for (int i = 0; i < 4; i++) {
+                            // the second half warp reads a pair's tokens in the other order (banks)
+                            const uint32_t a = *reinterpret_cast<const uint32_t *>(src + (2 * i + gr) * (D / 2));
+                            const uint32_t b = *reinterpret_cast<const uint32_t *>(src + (2 * i + 1 - gr) * (D / 2));
+                            const int t = gr * 8 + 2 * i;
+                            const __half z0 = t < live ? __high2half(pairs[16 + t]) : __ushort_as_half(0);
+                            const __half z1 = t + 1 < live ? __high2half(pairs[16 + t + 1]) : __ushort_as_half(0);
+                            const __half2 z = __halves2half2(z0, z1);
+                            const __half2 za = __hadd2(k1024, z), zb = __hadd2(k64, z);
+                            uint32_t lo[4], hi[4];
+                            unfold(prmt(a, b, gr ? 0x1054 : 0x5410), za, zb, lo);
+                            unfold(prmt(a, b, gr ? 0x3276 : 0x7632), za, zb, hi);
+#pragma unroll
+                            for (int e = 0; e < 4; e++) x[i][e] = lo[e], x[i][4 + e] = hi[e];
+                        }
+                        // dimension 8 wi + e is row 64 (wi / 8) + 8 e + wi % 8 of the operand
+                        uint8_t *dst = V + (wi >> 3) * (8 * 2048) + (half * 8 + q * 2 + gr) * 128 + (wi & 7) * 16;
+#pragma unroll
+                        for (int e = 0; e < 8; e++)
+                            *reinterpret_cast<uint4 *>(dst + e * 2048) =
+                                make_uint4(x[0][e], x[1][e], x[2][e], x[3][e]);
+                    }
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.raw_empty[st]);
+                }
+                fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.v_full[buf]);
+            }
+        }
+    } else if (warp == 12) {
+        // =================== tensor-core operations ===================
+        const uint32_t sb = smem_u32(smem);
+        constexpr uint32_t idS = idesc_f16(128, kKeys), idO = idesc_f16(128, D);
+        uint32_t cw[2] = {0, 0}, nq[2] = {0, 0};
+        auto qk = [&](int w, int buf) {
+            if (lane == 0) {
+#pragma unroll
+                for (int s = 0; s < SPLIT; s++)
+#pragma unroll
+                    for (int k = 0; k < D / 16; k++)
+                        mma_f16(tS[w], kmajor_desc(sb + C::oQ + (w * SPLIT + s) * C::kQ + k * 256, D * 16),
+                                kmajor_desc(sb + C::oK + buf * C::kTileB + k * 256, D * 16), idS, s + k > 0);
+                mma_commit(&bar.s_full[w]);
+            }
+            __syncwarp();
+        };
+        while (it.next(p)) {
+            const int n = it.last - it.first, tiles = it.x.rows > kRows ? 2 : 1;
+            for (int w = 0; w < tiles; w++) wait(bar.q_full[w], nq[w]++);
+            wait(bar.k_full[gt % C::kBuf], gt / C::kBuf);
+            tc_fence_after();
+            for (int w = 0; w < tiles; w++) qk(w, gt % C::kBuf);
+            if (lane == 0) mma_commit(&bar.k_empty[gt % C::kBuf]);
+            for (int j = 0; j < n; j++, gt++) {
+                const int buf = gt % C::kBuf, nb = (gt + 1) % C::kBuf;
+                wait(bar.v_full[buf], gt / C::kBuf);
+                for (int w = 0; w < tiles; w++) {
+                    wait(bar.p_full[w], cw[w]++);
+                    tc_fence_after();
+                    if (lane == 0) {
+#pragma unroll
+                        for (int s = 0; s < SPLIT; s++)
+#pragma unroll
+                            for (int k = 0; k < kKeys / 16; k++)
+                                mma_f16_ts(tO[w], tS[w] + (SPLIT == 2 ? 32 * (k / 2) + 16 * s + 8 * (k % 2) : 8 * k),
+                                           kmajor_desc(sb + C::oV + buf * C::kTileB + k * 256, 2048), idO,
+                                           j > 0 || s + k > 0);
+                        mma_commit(&bar.o_full[w]);
+                        if (w == tiles - 1) mma_commit(&bar.v_empty[buf]);
+                    }
+                    __syncwarp();
+                    if (j + 1 < n) {
+                        if (w == 0) {
+                            wait(bar.k_full[nb], (gt + 1) / C::kBuf);
+                            tc_fence_after();
+                        }
+                        qk(w, nb);
+                        if (w == tiles - 1 && lane == 0) mma_commit(&bar.k_empty[nb]);
+                    }
+                }
+            }
+        }
+        // The last arrivals of the tensor core must not outlive the CTA's shared memory.
+        if (gt > 0) {
+            wait(bar.k_empty[(gt - 1) % C::kBuf], (gt - 1) / C::kBuf);
+            wait(bar.v_empty[(gt - 1) % C::kBuf], (gt - 1) / C::kBuf);
+        }
+    } else {
+        // =================== cache chunks into shared memory ===================
+        uint32_t piece = 0;
+        const int64_t page_bytes = ((int64_t)p.kv_heads << (p.shift - 4)) * kv4_chunk_bytes(D);
+        while (it.next(p)) {
+            const int n = 2 * (it.last - it.first);
+            const uint8_t *base = p.cache + ((int64_t)it.h << (p.shift - 4)) * kv4_chunk_bytes(D);
+            const int32_t *row = p.table + (int64_t)it.r * p.width;
+            int page = -1;
+            for (int i = 0; i < n; i++, piece++) {
+                const int tok0 = (it.x.t0 + it.first) * kKeys + i * kPiece;
+                if ((i & 7) == 0) {  // the pages of the next 32 chunks, one per lane
+                    const int j = tok0 + 16 * lane;
+                    const int64_t c = j >> p.shift;
+                    page = i + (lane >> 2) < n && j < it.x.hi && c < p.width ? row[c] : -1;
+                }
+                const int pg = __shfl_sync(0xffffffffu, page, (i & 7) * 4 + (lane & 3));
+                const int j = tok0 + 16 * (lane & 3), st = piece % kPieces;
+                const bool ok = lane < 4 && pg >= 0 && pg < p.pages && j < it.x.hi && j + 16 > it.x.lo;
+                const uint32_t valid = __ballot_sync(0xffffffffu, ok);
+                wait(bar.raw_empty[st], piece / kPieces + 1);
+                if (lane == 0) {
+                    raw_valid[st] = valid;
+                    mbar_arrive_expect_tx(&bar.raw_full[st], __popc(valid) * kv4_chunk_bytes(D));
+                }
+                __syncwarp();
+                if (ok)
+                    bulk_g2s(smem + C::oRaw + st * C::kRaw + lane * kv4_chunk_bytes(D),
+                             base + pg * page_bytes + ((j & ((1 << p.shift) - 1)) >> 4) * kv4_chunk_bytes(D),
+                             kv4_chunk_bytes(D), &bar.raw_full[st]);
+            }
+        }
+    }
+    tc_fence_before();
+    __syncthreads();
+    if (warp == 12) {
+        tc_fence_after();
+        tmem_dealloc(tmem, 512);
+    }
+}
+
+// Joins the parts of items that several CTAs shared, a warp per row (see attn_join_kernel).
+template <int D, typename T>
+__global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnParams p) {
+    pdl_wait();
+    pdl_launch_dependents();
+    const int b = blockIdx.x, lane = threadIdx.x & 31;
+    const int row = blockIdx.y * 8 + (threadIdx.x >> 5);
+    const int4 rec = p.record[2 * b];
+    if (rec.x < 0 || rec.z == 0 || row >= rec.w) return;
+    const int first = rec.z - 1, n = b - first + 1;
+    auto at_of = [&](int i) { return (int64_t)(i == 0 ? 2 * first + 1 : 2 * (first + i)) * (2 * kRows) + row; };
+    float m = -INFINITY, l = 0.f, x[4] = {};
+    for (int i = 0; i < n; i++) m = fmaxf(m, p.stat[at_of(i)].x);
+    if (lane * 4 < D) {
+        for (int i = 0; i < n; i++) {
+            const float2 s = p.stat[at_of(i)];
+            const float4 v = *reinterpret_cast<const float4 *>(p.part + at_of(i) * D + lane * 4);
+            const float f = s.x == -INFINITY ? 0.f : ex2(s.x - m);
+            l = fmaf(f, s.y, l);
+            x[0] = fmaf(f, v.x, x[0]), x[1] = fmaf(f, v.y, x[1]);
+            x[2] = fmaf(f, v.z, x[2]), x[3] = fmaf(f, v.w, x[3]);
+        }
+        const Request q = load_request(p, rec.x);
+        const int cc = rec.y / p.kv_heads * 2 * kRows + row;
+        const int head = rec.y % p.kv_heads * p.group + cc % p.group;
+        const int64_t t = q.q0 + cc / p.group;
+        T *dst = static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + lane * 4;
+#pragma unroll
+        for (int e = 0; e < 4; e++) store_value(dst + e, l > 0.f ? x[e] / l : 0.f);
+        if (p.lse && lane == 0) p.lse[t * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    }
+}
+
+size_t attn_prompt_workspace(int head_dim) {
+    return (size_t)kTcMaxCtas * 2 * (16 + 2 * kRows * (8 + (size_t)head_dim * 4));
+}
+
+template <int D, typename T>
+static int launch_prompt(AttnParams p, uint8_t *workspace, int sms, cudaStream_t st) {
+    constexpr int SPLIT = sizeof(T) == 4 ? 2 : 1;
+    using C = Prompt<D, SPLIT>;
+    p.record = reinterpret_cast<int4 *>(workspace);
+    p.stat = reinterpret_cast<float2 *>(p.record + 2 * kTcMaxCtas);
+    p.part = reinterpret_cast<float *>(p.stat + 2 * kTcMaxCtas * 2 * kRows);
+    auto kernel = attn_prompt_kernel<D, T, SPLIT>;
+    int per_sm;
+    if (int e = prepare_kernel((const void *)kernel, kTcThreads, C::kSmem, &per_sm)) return e;
+    const int ctas = sms < kTcMaxCtas ? sms : kTcMaxCtas;
+    if (int e = launch_pdl(kernel, dim3(ctas), dim3(kTcThreads), C::kSmem, st, p)) return e;
+    if ((p.width << p.shift) <= kTcWhole * kKeys) return LB_OK;  // no item can have been split
+    return launch_pdl(attn_join_rows_kernel<D, T>, dim3(ctas, 2 * kRows / 8), dim3(256), 0, st, p);
+}
+
+int attn_prompt(const AttnParams &p, int type, int head_dim, uint8_t *workspace, int sms,
+                cudaStream_t st) {
+    if (type == LB_OUT_F32)
+        return head_dim == 64 ? launch_prompt<64, float>(p, workspace, sms, st)
+                              : launch_prompt<128, float>(p, workspace, sms, st);
+    return head_dim == 64 ? launch_prompt<64, __nv_bfloat16>(p, workspace, sms, st)
+                          : launch_prompt<128, __nv_bfloat16>(p, workspace, sms, st);
+}
+
+}  // namespace lb
