@@ -528,11 +528,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
             if (whole) {
                 const int cc = col0 + c, head = h * p.group + cc % p.group;
                 const int64_t t = rq.q0 + cc / p.group;
-                const float inv = l > 0.f ? 1.f / l : 0.f;
+                const float inv = l == 0.f ? 0.f : 1.f / l;
                 T *dst = static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + d;
 #pragma unroll
-                for (int e = 0; e < 4; e++) store_value(dst + e, l > 0.f ? x[e] * inv : 0.f);
-                if (p.lse && d == 0) p.lse[t * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+                for (int e = 0; e < 4; e++) store_value(dst + e, l == 0.f ? 0.f : x[e] * inv);
+                if (p.lse && d == 0) p.lse[t * p.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
             } else {
                 *reinterpret_cast<float4 *>(p.part + ((int64_t)slot * COLS + c) * D + d) =
                     make_float4(x[0], x[1], x[2], x[3]);
@@ -609,9 +609,9 @@ __global__ void __launch_bounds__(kJoin) attn_join_kernel(const AttnParams p) {
 #pragma unroll
         for (int i = 0; i < GROUPS; i++) y += acc[i][tid];
         store_value(static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + tid,
-                    l > 0.f ? y / l : 0.f);
+                    l == 0.f ? 0.f : y / l);
     }
-    if (p.lse && tid == 0) p.lse[t * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+    if (p.lse && tid == 0) p.lse[t * p.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
 }
 
 template <int D, typename T, int SPLIT, int NT>

@@ -19,9 +19,10 @@ namespace lb {
 // columns); P overwrites S.  The operations are issued PV0(j) QK0(j+1) PV1(j) QK1(j+1), so each
 // tile's softmax runs under the other tile's products.
 //
-// The reference moves only when it must: weights may grow until a tile's sum times the tile's
-// largest value scale would leave fp16's range; only then are the scores read a second time for
-// their maximum and O rescaled.  Work is split into equal runs of key tiles over the CTAs, parts of
+// One pass over the scores: the reference is the first tile's maximum and moves only when it must,
+// when the weights of 32 keys could leave fp16's range.  Then those 32 scores are read again for
+// their maximum, and what is already there under the old reference (the tile's earlier weights, O
+// and the sum) is scaled by a power of two.  Work is split into equal runs of key tiles over the CTAs, parts of
 // an item that several CTAs share are joined by a second kernel.
 // ------------------------------------------------------------------------------------------
 constexpr int kKeys = 128;           // keys per tile
@@ -30,6 +31,7 @@ constexpr int kPiece = 64;           // keys per copy stage (four chunks)
 constexpr int kPieces = 3;           // copy stages
 constexpr int kScales = 4;           // tiles of scales kept
 constexpr int kTcThreads = 448;
+constexpr int kItemCost = 3;         // an item's queries and outputs take about as long as 3 tiles
 constexpr int kTcMaxCtas = 160;
 constexpr int kTcWhole = 4;          // items of at most this many tiles are never split
 constexpr int kTcMinRun = 4;
@@ -80,6 +82,25 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// 16 columns asked for; they are there after tmem_ld16_wait.
+__device__ __forceinline__ void tmem_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15}, [%16];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void tmem_ld16_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
+}
 __device__ __forceinline__ void tmem_wait_st() {
     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
 }
@@ -102,6 +123,25 @@ __device__ __forceinline__ uint64_t fma2(uint64_t a, uint64_t b, uint64_t c) {
     uint64_t d;
     asm("fma.rn.f32x2 %0, %1, %2, %3;" : "=l"(d) : "l"(a), "l"(b), "l"(c));
     return d;
+}
+
+__device__ __forceinline__ void pairs_of(const uint32_t (&r)[16], uint64_t (&s)[8]) {
+#pragma unroll
+    for (int e = 0; e < 8; e++) s[e] = (uint64_t)r[2 * e] | (uint64_t)r[2 * e + 1] << 32;
+}
+// A chunk's weights: 8 columns (one part) or 16.
+__device__ __forceinline__ void tmem_st_weights(uint32_t taddr, const uint32_t (&r)[16]) {
+    tmem_st16(taddr, r);
+}
+__device__ __forceinline__ void tmem_st_weights(uint32_t taddr, const uint32_t (&r)[8]) {
+    asm volatile("tcgen05.st.sync.aligned.32x32b.x8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"r"(taddr),
+                 "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7])
+                 : "memory");
+}
+// A pair of -ref: what is added to a row's scores; 0 for a row that has seen nothing yet.
+__device__ __forceinline__ uint64_t minus_base(float ref) {
+    const float b = ref == -INFINITY ? 0.f : -ref;
+    return pair_of(b, b);
 }
 
 // Rows [256 b, 256 b + 256) of a request: their visible key tiles.
@@ -136,8 +176,8 @@ struct Walk {
     // The next item this CTA takes part in; false at the end of its run.
     __device__ __forceinline__ bool next(const AttnParams &p) {
         while (u < end) {
-            while (u >= begin + x.tiles) {
-                begin += x.tiles;
+            while (u >= begin + x.tiles + kItemCost) {
+                begin += x.tiles + kItemCost;
                 if (++h < p.kv_heads) continue;
                 h = 0;
                 if (++b >= pairs_of(p, q)) {
@@ -147,14 +187,15 @@ struct Walk {
                 }
                 x = pair_of_rows(p, q, b);
             }
-            first = (int)(u - begin);
-            last = (int)min((int64_t)x.tiles, first + (end - u));
-            u += last - first;
-            if (x.tiles > kTcWhole) return true;
-            if (first == 0) {  // never split: the CTA in whose run it begins takes it
-                last = x.tiles;
-                return true;
+            const bool starts = u == begin;
+            first = max((int)(u - begin) - kItemCost, 0);
+            const int64_t stop = min(end, begin + x.tiles + kItemCost);
+            last = max((int)(stop - begin) - kItemCost, 0);
+            u = stop;
+            if (x.tiles <= kTcWhole) {  // never split: the CTA in whose run it begins takes it
+                first = 0, last = starts ? x.tiles : 0;
             }
+            if (last > first) return true;
         }
         return false;
     }
@@ -191,7 +232,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
     for (int r = ra; r < rb; r++) {
         const Request q = load_request(p, r);
         for (int b = 0, n = pairs_of(p, q); b < n; b++)
-            mine += (int64_t)pair_of_rows(p, q, b).tiles * p.kv_heads;
+            mine += (int64_t)(pair_of_rows(p, q, b).tiles + kItemCost) * p.kv_heads;
     }
     int64_t incl = mine;
 #pragma unroll
@@ -221,7 +262,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
         for (int r = ra; r < rb; r++) {
             const Request q = load_request(p, r);
             for (int b = 0, n = pairs_of(p, q); b < n; b++) {
-                const int64_t t = pair_of_rows(p, q, b).tiles;
+                const int64_t t = pair_of_rows(p, q, b).tiles + kItemCost;
                 if (it.u < at + t * p.kv_heads) {
                     const int h = (int)((it.u - at) / t);
                     s_r = r, s_b = b, s_h = h, s_begin = at + h * t;
@@ -244,11 +285,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
     it.r = s_r, it.b = s_b, it.h = s_h, it.begin = s_begin;
     it.set(p);
 
-    uint64_t limit = 2000000000ull;
+    // Bounded: about 2 s (2000 tries of up to a millisecond), after the first that ran out a few tries.
+    int tries = 2000;
     auto wait = [&](uint64_t &b, uint32_t parity) {
-        if (!mbar_wait(&b, parity & 1, limit)) {
+        int i = 0;
+        while (!mbar_try_wait_hint(&b, parity & 1, 1000000u) && i < tries) i++;
+        if (i >= tries) {
             *p.error = 1;
-            limit = 1000000ull;
+            tries = 4;
         }
         __syncwarp();
     };
@@ -270,42 +314,52 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 continue;
             }
             const int row0 = it.b * 2 * kRows + w * kRows;
-            // ---- queries: a warp's 32 rows, 8 rows x 32 dimensions at a time ----
+            // ---- queries: a warp's 32 rows, 8 rows x 32 dimensions per step; the loads of
+            // several groups of 8 rows first ----
+            constexpr int BATCH = sizeof(T) == 2 ? 4 : 2;
 #pragma unroll 1
-            for (int g = 0; g < 4; g++) {
-                const int rr = (warp & 3) * 32 + g * 8 + (lane & 7);
-                const int cc = row0 + min(rr, ncol - 1);
-                const T *src = static_cast<const T *>(p.q) +
-                               (int64_t)(it.q.q0 + cc / p.group) * p.q_stride +
-                               (int64_t)(it.h * p.group + cc % p.group) * D + (lane >> 3) * 8;
-                float x[D / 32][8], amax = 0.f;
+            for (int g0 = 0; g0 < 4; g0 += BATCH) {
+                float x[BATCH][D / 32][8];
 #pragma unroll
-                for (int k = 0; k < D / 32; k++) {
-                    load8(src + 32 * k, x[k]);
+                for (int g = 0; g < BATCH; g++) {
+                    const int cc = row0 + min((warp & 3) * 32 + (g0 + g) * 8 + (lane & 7), ncol - 1);
+                    const T *src = static_cast<const T *>(p.q) +
+                                   (int64_t)(it.q.q0 + cc / p.group) * p.q_stride +
+                                   (int64_t)(it.h * p.group + cc % p.group) * D + (lane >> 3) * 8;
 #pragma unroll
-                    for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(x[k][e]));
+                    for (int k = 0; k < D / 32; k++) load8(src + 32 * k, x[g][k]);
                 }
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
-                amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
-                float up, down;
-                row_power(amax, up, down);
-                if (lane < 8) row_a[w][rr] = p.scale * kLog2e * down;
 #pragma unroll
-                for (int k = 0; k < D / 32; k++) {
-                    // order 0 4 1 5 2 6 3 7, as the codes of a word unfold
-                    const uint32_t at = (rr >> 3) * (D * 16) + (4 * k + (lane >> 3)) * 128 + (rr & 7) * 16;
-                    uint32_t hi[4], lo[4];
+                for (int g = 0; g < BATCH; g++) {
+                    const int rr = (warp & 3) * 32 + (g0 + g) * 8 + (lane & 7);
+                    float amax = 0.f;
 #pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const float a = x[k][e] * up, b = x[k][e + 4] * up;
-                        const __half2 h2 = __floats2half2_rn(a, b);
-                        hi[e] = *reinterpret_cast<const uint32_t *>(&h2);
-                        lo[e] = half2_bits(a - __low2float(h2), b - __high2float(h2));
+                    for (int k = 0; k < D / 32; k++)
+#pragma unroll
+                        for (int e = 0; e < 8; e++) amax = fmaxf(amax, fabsf(x[g][k][e]));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 8));
+                    amax = fmaxf(amax, __shfl_xor_sync(0xffffffffu, amax, 16));
+                    float up, down;
+                    row_power(amax, up, down);
+                    if (lane < 8) row_a[w][rr] = p.scale * kLog2e * down;
+#pragma unroll
+                    for (int k = 0; k < D / 32; k++) {
+                        // order 0 4 1 5 2 6 3 7, as the codes of a word unfold
+                        const uint32_t at =
+                            (rr >> 3) * (D * 16) + (4 * k + (lane >> 3)) * 128 + (rr & 7) * 16;
+                        uint32_t hi[4], lo[4];
+#pragma unroll
+                        for (int e = 0; e < 4; e++) {
+                            const float a = x[g][k][e] * up, b = x[g][k][e + 4] * up;
+                            const __half2 h2 = __floats2half2_rn(a, b);
+                            hi[e] = *reinterpret_cast<const uint32_t *>(&h2);
+                            lo[e] = half2_bits(a - __low2float(h2), b - __high2float(h2));
+                        }
+                        uint8_t *dst = smem + C::oQ + w * SPLIT * C::kQ + at;
+                        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+                        if (SPLIT == 2)
+                            *reinterpret_cast<uint4 *>(dst + C::kQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                     }
-                    uint8_t *dst = smem + C::oQ + w * SPLIT * C::kQ + at;
-                    *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-                    if (SPLIT == 2)
-                        *reinterpret_cast<uint4 *>(dst + C::kQ) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
                 }
             }
             fence_proxy_async_smem();
@@ -339,126 +393,139 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 wait(bar.s_full[w], cw);
                 tc_fence_after();
 
-                // Scores of 32 keys (c) as pairs, masked if need be.
-                auto scores = [&](int c, uint64_t (&s)[16]) {
-                    tmem_ld32_pairs(S + 32 * c, s);
+                // Scores of 16 keys (c), plus nb, as pairs, from the raw products in s.
+                auto scores = [&](int c, uint64_t (&s)[8], uint64_t nb) {
 #pragma unroll
-                    for (int e = 0; e < 8; e++) {
-                        const ulonglong2 k = kd[8 * c + e];
-                        s[2 * e] = mul2(mul2(s[2 * e], k.x), a2);
-                        s[2 * e + 1] = mul2(mul2(s[2 * e + 1], k.y), a2);
+                    for (int e = 0; e < 4; e++) {
+                        const ulonglong2 k = kd[4 * c + e];
+                        s[2 * e] = fma2(mul2(s[2 * e], k.x), a2, nb);
+                        s[2 * e + 1] = fma2(mul2(s[2 * e + 1], k.y), a2, nb);
                     }
                     if (!inside) {
+                        const bool there = ok >> c & 1;
 #pragma unroll
-                        for (int e = 0; e < 16; e++) {
-                            const int t = j0 + 32 * c + 2 * e;
-                            const bool there = ok >> (2 * c + (e >> 3)) & 1;
+                        for (int e = 0; e < 8; e++) {
+                            const int t = j0 + 16 * c + 2 * e;
                             s[e] = pair_of(there && t >= lo && t < hi ? lo_of(s[e]) : -INFINITY,
                                            there && t + 1 >= lo && t + 1 < hi ? hi_of(s[e]) : -INFINITY);
                         }
                     }
                 };
-                // The row's maximum, a new reference, and O under it.
-                auto move = [&]() {
-                    float m = -INFINITY;
-#pragma unroll 1
-                    for (int c = 0; c < 4; c++) {
-                        uint64_t s[16];
-                        scores(c, s);
+                // The weights of chunk c as fp16 (and, second, what rounding took from them).
+                auto weights = [&](int c, uint64_t(&s)[8], uint64_t &sum, uint32_t *ph) {
 #pragma unroll
-                        for (int e = 0; e < 16; e++) m = fmaxf(m, fmaxf(lo_of(s[e]), hi_of(s[e])));
-                    }
-                    m = fmaxf(ref, m + scale_log2(vmax * (1.f / kTcLift)));
-                    const float f = m == ref ? 1.f : ex2(ref - m);
-                    ref = m;
-                    l *= f;
-                    if (j > 0) {
-                        wait(bar.o_full[w], cw - 1);
-                        tc_fence_after();
-#pragma unroll 1
-                        for (int c = 0; c < D; c += 32) {
-                            uint32_t o[32];
-                            tmem_ld32(O + c, o);
-#pragma unroll
-                            for (int e = 0; e < 32; e++)
-                                o[e] = __float_as_uint(__uint_as_float(o[e]) * f);
-                            tmem_st16(O + c, o);
-                            tmem_st16(O + c + 16, o + 16);
-                        }
-                        tmem_wait_st();
+                    for (int e = 0; e < 8; e++) {
+                        const ulonglong2 v = vd[4 * c + e / 2];
+                        const uint64_t pr = pair_of(ex2(lo_of(s[e])), ex2(hi_of(s[e])));
+                        sum = add2(sum, pr);
+                        const uint64_t wv = mul2(pr, e & 1 ? v.y : v.x);
+                        const __half2 h2 = __floats2half2_rn(lo_of(wv), hi_of(wv));
+                        ph[e] = *reinterpret_cast<const uint32_t *>(&h2);
+                        if (SPLIT == 2)
+                            ph[8 * (SPLIT - 1) + e] =
+                                half2_bits(lo_of(wv) - __low2float(h2), hi_of(wv) - __high2float(h2));
                     }
                 };
-                if (SPLIT == 2) {
-                    // Two passes: the maximum first (the products take twice as long here).
+                const float vlog = scale_log2(vmax * (1.f / kTcLift));
+                uint32_t r0[16], r1[16];
+                tmem_ld16_start(S, r0);
+                if (j == 0) {  // the first reference: this tile's maximum
                     float m = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 4; c++) {
-                        uint64_t s[16];
-                        scores(c, s);
+                    for (int c = 0; c < 8; c++) {
+                        tmem_ld16_wait(r0);
+                        uint64_t s[8];
+                        pairs_of(r0, s);
+                        tmem_ld16_start(S + 16 * ((c + 1) & 7), r0);
+                        scores(c, s, 0);
 #pragma unroll
-                        for (int e = 0; e < 16; e++) m = fmaxf(m, fmaxf(lo_of(s[e]), hi_of(s[e])));
+                        for (int e = 0; e < 8; e++) m = fmaxf(m, fmaxf(lo_of(s[e]), hi_of(s[e])));
                     }
-                    if (__any_sync(0xffffffffu, m + scale_log2(vmax * (1.f / kTcLift)) > ref + 8.f)) move();
-                    const float b = ref == -INFINITY ? 0.f : ref;
-                    const uint64_t nr = pair_of(-b, -b);
+                    ref = m == -INFINITY ? m : m + vlog;  // the last load, of chunk 0, is in flight
+                }
+                // A chunk's weights as fp16 (and what rounding took from them), 8 columns each, over
+                // its 16 scores: P of chunk c lies at columns 16 c.
+                uint64_t nb = minus_base(ref);
+#pragma unroll
+                for (int c2 = 0; c2 < 4; c2++) {
+                    uint32_t ph[2][8 * SPLIT];
                     uint64_t sum = 0;
-#pragma unroll 1
-                    for (int c = 0; c < 4; c++) {
-                        uint64_t s[16];
-                        uint32_t ph[16], pl[16];
-                        scores(c, s);
+#pragma unroll
+                    for (int k = 0; k < 2; k++) {
+                        const int c = 2 * c2 + k;
+                        uint32_t(&r)[16] = k ? r1 : r0;
+                        tmem_ld16_wait(r);
+                        if (c < 7) tmem_ld16_start(S + 16 * (c + 1), k ? r0 : r1);
+                        uint64_t s[8];
+                        pairs_of(r, s);
+                        scores(c, s, nb);
+                        weights(c, s, sum, ph[k]);
+                    }
+                    float part = lo_of(sum) + hi_of(sum);
+                    if (__any_sync(0xffffffffu, ref == -INFINITY || !(part * vmax <= kTcMost))) {
+                        // (r0 holds the next chunk's scores, or is in flight: it stays.)
+                        float m = -INFINITY;
+                        uint32_t t0[16], t1[16];
+                        tmem_ld16_start(S + 32 * c2, t0);
+                        tmem_ld16_start(S + 32 * c2 + 16, t1);
+                        tmem_ld16_wait(t0);
+                        tmem_ld16_wait(t1);
+                        uint64_t s0[8], s1[8];
+                        pairs_of(t0, s0);
+                        pairs_of(t1, s1);
+                        scores(2 * c2, s0, nb);
+                        scores(2 * c2 + 1, s1, nb);
 #pragma unroll
                         for (int e = 0; e < 8; e++) {
-                            const ulonglong2 v = vd[8 * c + e];
+                            m = fmaxf(m, fmaxf(lo_of(s0[e]), hi_of(s0[e])));
+                            m = fmaxf(m, fmaxf(lo_of(s1[e]), hi_of(s1[e])));
+                        }
+                        float f = 1.f, d = 0.f;  // 2^-d, d a whole number
+                        if (ref == -INFINITY) {
+                            if (m > -INFINITY) d = m + vlog, ref = d;  // nothing is there to scale
+                        } else if (m + vlog > 0.f) {
+                            d = ceilf(m + vlog), ref += d;
+                            f = ex2(-d);
+                        }
+                        nb = minus_base(ref);
+                        l *= f;
+                        const __half2 fh = __float2half2_rn(f);
+#pragma unroll 1
+                        for (int c = 0; c < 2 * c2; c++) {
+                            tmem_ld16_start(S + 16 * c, t0);
+                            tmem_ld16_wait(t0);
 #pragma unroll
-                            for (int k = 0; k < 2; k++) {
-                                const uint64_t x = add2(s[2 * e + k], nr);
-                                const uint64_t pr = pair_of(ex2(lo_of(x)), ex2(hi_of(x)));
-                                sum = add2(sum, pr);
-                                const uint64_t wv = mul2(pr, k ? v.y : v.x);
-                                const __half2 h2 = __floats2half2_rn(lo_of(wv), hi_of(wv));
-                                ph[2 * e + k] = *reinterpret_cast<const uint32_t *>(&h2);
-                                pl[2 * e + k] = half2_bits(lo_of(wv) - __low2float(h2), hi_of(wv) - __high2float(h2));
+                            for (int e = 0; e < 8 * SPLIT; e++) {
+                                const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&t0[e]), fh);
+                                t0[e] = *reinterpret_cast<const uint32_t *>(&v);
+                            }
+                            tmem_st16(S + 16 * c, t0);
+                        }
+                        if (j > 0) {
+                            wait(bar.o_full[w], cw - 1);
+                            tc_fence_after();
+#pragma unroll 1
+                            for (int c = 0; c < D; c += 16) {
+                                tmem_ld16_start(O + c, t0);
+                                tmem_ld16_wait(t0);
+#pragma unroll
+                                for (int e = 0; e < 16; e++)
+                                    t0[e] = __float_as_uint(__uint_as_float(t0[e]) * f);
+                                tmem_st16(O + c, t0);
                             }
                         }
-                        tmem_st16(S + 32 * c, ph);
-                        tmem_st16(S + 32 * c + 16, pl);
-                    }
-                    l += lo_of(sum) + hi_of(sum);
-                } else {
-                    uint32_t ph[64];
-                    float part;
-                    auto weights = [&]() {
-                        const float b = ref == -INFINITY ? 0.f : ref;
-                        const uint64_t nr = pair_of(-b, -b);
-                        uint64_t sum = 0;
+                        tmem_wait_st();
+                        sum = 0;
+                        const uint64_t nd = pair_of(-d, -d);
 #pragma unroll
-                        for (int c = 0; c < 4; c++) {
-                            uint64_t s[16];
-                            scores(c, s);
-#pragma unroll
-                            for (int e = 0; e < 8; e++) {
-                                const ulonglong2 v = vd[8 * c + e];
-#pragma unroll
-                                for (int k = 0; k < 2; k++) {
-                                    const uint64_t x = add2(s[2 * e + k], nr);
-                                    const uint64_t pr = pair_of(ex2(lo_of(x)), ex2(hi_of(x)));
-                                    sum = add2(sum, pr);
-                                    const uint64_t wv = mul2(pr, k ? v.y : v.x);
-                                    ph[16 * c + 2 * e + k] = half2_bits(lo_of(wv), hi_of(wv));
-                                }
-                            }
-                        }
+                        for (int e = 0; e < 8; e++) s0[e] = add2(s0[e], nd), s1[e] = add2(s1[e], nd);
+                        weights(2 * c2, s0, sum, ph[0]);
+                        weights(2 * c2 + 1, s1, sum, ph[1]);
                         part = lo_of(sum) + hi_of(sum);
-                    };
-                    weights();
-                    if (__any_sync(0xffffffffu, ref == -INFINITY || !(part * vmax <= kTcMost))) {
-                        move();
-                        weights();
                     }
                     l += part;
 #pragma unroll
-                    for (int c = 0; c < 4; c++) tmem_st16(S + 16 * c, ph + 16 * c);
+                    for (int k = 0; k < 2; k++) tmem_st_weights(S + 32 * c2 + 16 * k, ph[k]);
                 }
                 tmem_wait_st();
                 tc_fence_before();
@@ -473,7 +540,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
             const int part = 2 * blockIdx.x + (it.first == 0 ? 1 : 0);
             const int cc = row0 + row, head = it.h * p.group + cc % p.group;
             const int64_t t = it.q.q0 + cc / p.group;
-            const float f = (whole ? (l > 0.f ? 1.f / l : 0.f) : 1.f) * (1.f / kTcLift);
+            // (a row that has seen nothing has l = 0, and its output is 0)
+            const float f = (!whole ? 1.f : l == 0.f ? 0.f : 1.f / l) * (1.f / kTcLift);
 #pragma unroll 1
             for (int c = 0; c < D; c += 64) {
                 // column 8 e + k of these 64 is dimension 8 k + e
@@ -487,7 +555,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
 #pragma unroll
                         for (int e = 0; e < 8; e++) {
                             y[e] = __uint_as_float(e < 4 ? o0[8 * e + k] : o1[8 * (e - 4) + k]) * f;
-                            if (whole && !(l > 0.f)) y[e] = 0.f;
+                            if (whole && l == 0.f) y[e] = 0.f;
                         }
                         if (whole)
                             store8(static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + c + 8 * k, y);
@@ -501,10 +569,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 if (!whole)
                     p.stat[part * 2 * kRows + w * kRows + row] = make_float2(ref, l);
                 else if (p.lse)
-                    p.lse[t * p.heads + head] = l > 0.f ? (ref + log2f(l)) * kLn2 : -INFINITY;
+                    p.lse[t * p.heads + head] = l == 0.f ? -INFINITY : (ref + log2f(l)) * kLn2;
             }
             if (!whole && tid == 0) {
-                const int owner = (int)(((it.begin + 1) * ctas - 1) / total);
+                // the CTA of the item's first tile (of the item, if it is never split)
+                const int owner = (int)(((it.begin + kItemCost + 1) * ctas - 1) / total);
                 record[it.first == 0 ? 1 : 0] = make_int4(
                     it.r, it.b * p.kv_heads + it.h, it.last == it.x.tiles ? owner + 1 : 0, it.x.rows);
             }
@@ -597,29 +666,32 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                     if (lane < 2 * WN) {
                         const int wi = lane % WN, gr = lane / WN;
                         const uint8_t *src = chunk + kv4_codes_bytes(D) + gr * 8 * (D / 2) + wi * 4;
-                        uint32_t x[4][8];  // token pair, dimension
+                        uint32_t wa[4], wb[4];
+                        __half2 za[4], zb[4];
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
                             // the second half warp reads a pair's tokens in the other order (banks)
-                            const uint32_t a = *reinterpret_cast<const uint32_t *>(src + (2 * i + gr) * (D / 2));
-                            const uint32_t b = *reinterpret_cast<const uint32_t *>(src + (2 * i + 1 - gr) * (D / 2));
+                            wa[i] = *reinterpret_cast<const uint32_t *>(src + (2 * i + gr) * (D / 2));
+                            wb[i] = *reinterpret_cast<const uint32_t *>(src + (2 * i + 1 - gr) * (D / 2));
                             const int t = gr * 8 + 2 * i;
                             const __half z0 = t < live ? __high2half(pairs[16 + t]) : __ushort_as_half(0);
                             const __half z1 = t + 1 < live ? __high2half(pairs[16 + t + 1]) : __ushort_as_half(0);
                             const __half2 z = __halves2half2(z0, z1);
-                            const __half2 za = __hadd2(k1024, z), zb = __hadd2(k64, z);
-                            uint32_t lo[4], hi[4];
-                            unfold(prmt(a, b, gr ? 0x1054 : 0x5410), za, zb, lo);
-                            unfold(prmt(a, b, gr ? 0x3276 : 0x7632), za, zb, hi);
-#pragma unroll
-                            for (int e = 0; e < 4; e++) x[i][e] = lo[e], x[i][4 + e] = hi[e];
+                            za[i] = __hadd2(k1024, z), zb[i] = __hadd2(k64, z);
                         }
                         // dimension 8 wi + e is row 64 (wi / 8) + 8 e + wi % 8 of the operand
                         uint8_t *dst = V + (wi >> 3) * (8 * 2048) + (half * 8 + q * 2 + gr) * 128 + (wi & 7) * 16;
 #pragma unroll
-                        for (int e = 0; e < 8; e++)
-                            *reinterpret_cast<uint4 *>(dst + e * 2048) =
-                                make_uint4(x[0][e], x[1][e], x[2][e], x[3][e]);
+                        for (int hw = 0; hw < 2; hw++) {
+                            const uint32_t sel = hw ? (gr ? 0x3276 : 0x7632) : (gr ? 0x1054 : 0x5410);
+                            uint32_t x[4][4];  // token pair, dimension
+#pragma unroll
+                            for (int i = 0; i < 4; i++) unfold(prmt(wa[i], wb[i], sel), za[i], zb[i], x[i]);
+#pragma unroll
+                            for (int e = 0; e < 4; e++)
+                                *reinterpret_cast<uint4 *>(dst + (4 * hw + e) * 2048) =
+                                    make_uint4(x[0][e], x[1][e], x[2][e], x[3][e]);
+                        }
                     }
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.raw_empty[st]);
@@ -664,7 +736,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                         for (int s = 0; s < SPLIT; s++)
 #pragma unroll
                             for (int k = 0; k < kKeys / 16; k++)
-                                mma_f16_ts(tO[w], tS[w] + (SPLIT == 2 ? 32 * (k / 2) + 16 * s + 8 * (k % 2) : 8 * k),
+                                mma_f16_ts(tO[w], tS[w] + 16 * k + 8 * s,
                                            kmajor_desc(sb + C::oV + buf * C::kTileB + k * 256, 2048), idO,
                                            j > 0 || s + k > 0);
                         mma_commit(&bar.o_full[w]);
@@ -756,8 +828,8 @@ __global__ void __launch_bounds__(256) attn_join_rows_kernel(const AttnParams p)
         const int64_t t = q.q0 + cc / p.group;
         T *dst = static_cast<T *>(p.out) + t * p.out_stride + (int64_t)head * D + lane * 4;
 #pragma unroll
-        for (int e = 0; e < 4; e++) store_value(dst + e, l > 0.f ? x[e] / l : 0.f);
-        if (p.lse && lane == 0) p.lse[t * p.heads + head] = l > 0.f ? (m + log2f(l)) * kLn2 : -INFINITY;
+        for (int e = 0; e < 4; e++) store_value(dst + e, l == 0.f ? 0.f : x[e] / l);
+        if (p.lse && lane == 0) p.lse[t * p.heads + head] = l == 0.f ? -INFINITY : (m + log2f(l)) * kLn2;
     }
 }
 
