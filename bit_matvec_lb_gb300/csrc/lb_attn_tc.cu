@@ -446,7 +446,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 // A chunk's weights as fp16 (and what rounding took from them), 8 columns each, over
                 // its 16 scores: P of chunk c lies at columns 16 c.
                 uint64_t nb = minus_base(ref);
-#pragma unroll
+#pragma unroll 1  // (unrolled, the instruction cache becomes the limit)
                 for (int c2 = 0; c2 < 4; c2++) {
                     uint32_t ph[2][8 * SPLIT];
                     uint64_t sum = 0;
