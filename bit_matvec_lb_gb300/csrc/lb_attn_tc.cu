@@ -6,7 +6,7 @@
 namespace lb {
 
 // ------------------------------------------------------------------------------------------
-// Mathematics.  A key/value head's rows (queries x heads of the group, packed) times 128 keys at a
+// Mathematics.  A key/value head's rows (queries x heads of the group, packed) times 64 keys at a
 // time: S = Q K'^T and O += P V', K' and V' the codes less their zero, whole numbers in -15..15 and
 // exact in fp16.  The keys' scales act on the scores, x = S kd_t a_r - R_r in powers of two (a_r
 // holds the row's own power of two, scale and log2 e), the values' scales on the weights,
@@ -15,9 +15,11 @@ namespace lb {
 //
 // One CTA per SM, 14 warps: two times four for the softmax of two tiles of 128 rows (a thread per
 // row), four that turn codes into fp16 operands, one that issues the tensor-core operations and
-// one that copies cache chunks in.  S of both tiles and O of both fill tensor memory (4 x 128
-// columns); P overwrites S.  The operations are issued PV0(j) QK0(j+1) PV1(j) QK1(j+1), so each
-// tile's softmax runs under the other tile's products.
+// one that copies cache chunks in.  Tensor memory holds S twice for each row tile (4 x 64 columns)
+// and O (2 x 128); P overwrites S.  The operations are issued QK0(j+1) PV0(j) QK1(j+1) PV1(j), so a
+// row tile's next scores are there when it is done with the present ones, and its softmax, not the
+// way to the tensor core and back, sets the pace (128 keys and S once: 0.72 against 0.67 ms for a
+// bf16 prompt of 8192 tokens with 32 / 8 heads).
 //
 // One pass over the scores: the reference is the first tile's maximum and moves only when it must,
 // when the weights of 32 keys could leave fp16's range.  Then those 32 scores are read again for
@@ -25,25 +27,24 @@ namespace lb {
 // and the sum) is scaled by a power of two.  Work is split into equal runs of key tiles over the CTAs, parts of
 // an item that several CTAs share are joined by a second kernel.
 // ------------------------------------------------------------------------------------------
-constexpr int kKeys = 128;           // keys per tile
+constexpr int kKeys = 64;            // keys per tile (four chunks, one copy stage)
 constexpr int kRows = 128;           // query rows per tile, two tiles per item
-constexpr int kPiece = 64;           // keys per copy stage (four chunks)
 constexpr int kPieces = 3;           // copy stages
-constexpr int kScales = 4;           // tiles of scales kept
+constexpr int kScales = 8;           // tiles of scales kept
 constexpr int kTcThreads = 448;
-constexpr int kItemCost = 3;         // an item's queries and outputs take about as long as 3 tiles
+constexpr int kItemCost = 6;         // an item's queries and outputs take about as long as 6 tiles
 constexpr int kTcMaxCtas = 160;
-constexpr int kTcWhole = 4;          // items of at most this many tiles are never split
-constexpr int kTcMinRun = 4;
+constexpr int kTcWhole = 8;          // items of at most this many tiles are never split
+constexpr int kTcMinRun = 8;
 constexpr float kTcLift = 16.f;      // weights at the reference: 2^4
 constexpr float kTcMost = 60000.f;   // largest weight a tile may hold
 
 template <int D, int SPLIT>
 struct Prompt {
-    static constexpr int kBuf = 2 / SPLIT;             // fp16 key and value tiles
+    static constexpr int kBuf = 4 / SPLIT;             // fp16 key and value tiles
     static constexpr int kQ = kRows * D * 2;           // bytes of one part of one row tile
     static constexpr int kTileB = kKeys * D * 2;
-    static constexpr int kRaw = kPiece / 16 * kv4_chunk_bytes(D);
+    static constexpr int kRaw = kKeys / 16 * kv4_chunk_bytes(D);
     static constexpr int oQ = 0;                       // [2 tiles][SPLIT]
     static constexpr int oK = oQ + 2 * SPLIT * kQ;     // [kBuf]
     static constexpr int oV = oK + kBuf * kTileB;
@@ -54,25 +55,61 @@ struct Prompt {
 
 struct TcBars {
     uint64_t raw_full[kPieces], raw_empty[kPieces];
-    uint64_t k_full[2], k_empty[2], v_full[2], v_empty[2];
+    uint64_t k_full[4], k_empty[4], v_full[4], v_empty[4];
     uint64_t sc_full[kScales];
-    uint64_t q_full[2], s_full[2], p_full[2], o_full[2];
+    uint64_t q_full[2], s_full[2][2], p_full[2][2], o_full[2][2];  // [row tile][key tile's parity]
 };
 
-// D[tmem] (+)= A[tmem] * B[desc]^T, cta_group::1, kind::f16.
-__device__ __forceinline__ void mma_f16_ts(uint32_t tmem_d, uint32_t tmem_a, uint64_t bdesc,
-                                           uint32_t idesc, uint32_t accumulate) {
+// Shared-memory matrix descriptors (K-major, no swizzle: core matrices of 8 rows x 16 bytes, 128 B
+// apart along K, SBO bytes between groups of 8 rows) are kept as their low words; a step of 16
+// along K adds 256 >> 4.  Four steps go out as one statement: the issuing thread's own instructions
+// would otherwise set the pace.
+constexpr uint32_t desc_high(uint32_t sbo) { return ((sbo >> 4) & 0x3FFF) | 1u << 14; }
+__device__ __forceinline__ uint32_t desc_low(uint32_t saddr) {
+    return ((saddr >> 4) & 0x3FFF) | (uint32_t)(128 >> 4) << 16;
+}
+// D[tmem] (+)= A[desc] * B[desc]^T over 64 of K.
+template <uint32_t HA, uint32_t HB>
+__device__ __forceinline__ void mma4_ss(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
     asm volatile(
-        "{ .reg .pred p; setp.ne.b32 p, %4, 0; "
-        "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p; }" ::"r"(tmem_d),
-        "r"(tmem_a), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        "{ .reg .pred p; .reg .b64 a, b;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 a, {%1, %5}; mov.b64 b, {%2, %6};\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "add.s64 a, a, 16; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.s64 a, a, 16; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p;\n\t"
+        "add.s64 a, a, 16; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], a, b, %3, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(HA), "n"(HB)
         : "memory");
 }
-// Shared-memory matrix descriptor, K-major, no swizzle: core matrices of 8 rows x 16 bytes, 128 B
-// apart along K, `sbo` bytes between groups of 8 rows.
-__device__ __forceinline__ uint64_t kmajor_desc(uint32_t saddr, uint32_t sbo) {
-    return (uint64_t)((saddr >> 4) & 0x3FFF) | (uint64_t)(128 >> 4) << 16 |
-           (uint64_t)((sbo >> 4) & 0x3FFF) << 32 | (uint64_t)1 << 46;
+// D[tmem] (+)= A[tmem] * B[desc]^T over 64 of K; a step's 8 columns of A lie 16 columns apart.
+template <uint32_t HB>
+__device__ __forceinline__ void mma4_ts(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 b; .reg .b32 a;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5}; mov.b32 a, %1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "add.s32 a, a, 16; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+        "add.s32 a, a, 16; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+        "add.s32 a, a, 16; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(HB)
+        : "memory");
+}
+__device__ __forceinline__ bool elect_one() {
+    uint32_t x;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(x));
+    return x != 0;
 }
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t *r) {
     asm volatile(
@@ -206,20 +243,21 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
     using C = Prompt<D, SPLIT>;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ TcBars bar;
-    __shared__ uint32_t s_tmem, raw_valid[kPieces], sc_valid[kScales][2];
-    __shared__ float sc_max[kScales][8], row_a[2][kRows];
+    __shared__ uint32_t s_tmem, raw_valid[kPieces], sc_valid[kScales];
+    __shared__ float sc_max[kScales][4], row_a[2][kRows];
     __shared__ int64_t scan[kTcThreads / 32], s_begin;
     __shared__ int s_r, s_b, s_h;
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
 
     if (tid == 0) {
         for (int i = 0; i < kPieces; i++) mbar_init(&bar.raw_full[i], 1), mbar_init(&bar.raw_empty[i], 4);
-        for (int i = 0; i < 2; i++) {
+        for (int i = 0; i < 4; i++) {
             mbar_init(&bar.k_full[i], 4), mbar_init(&bar.k_empty[i], 1);
             mbar_init(&bar.v_full[i], 4), mbar_init(&bar.v_empty[i], 1);
-            mbar_init(&bar.q_full[i], 4), mbar_init(&bar.s_full[i], 1);
-            mbar_init(&bar.p_full[i], 4), mbar_init(&bar.o_full[i], 1);
+            mbar_init(&bar.s_full[i >> 1][i & 1], 1), mbar_init(&bar.p_full[i >> 1][i & 1], 4);
+            mbar_init(&bar.o_full[i >> 1][i & 1], 1);
         }
+        mbar_init(&bar.q_full[0], 4), mbar_init(&bar.q_full[1], 4);
         for (int i = 0; i < kScales; i++) mbar_init(&bar.sc_full[i], 4);
         fence_mbar_init();
     }
@@ -281,7 +319,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = s_tmem;
-    const uint32_t tS[2] = {tmem, tmem + 128}, tO[2] = {tmem + 256, tmem + 256 + D};
     it.r = s_r, it.b = s_b, it.h = s_h, it.begin = s_begin;
     it.set(p);
 
@@ -304,7 +341,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
         // =================== softmax: one row per thread ===================
         const int w = warp >> 2, row = tid & 127;
         const uint32_t lanes = (uint32_t)(warp & 3) << 21;  // lane quarter in the address' upper half
-        const uint32_t S = tS[w] + lanes, O = tO[w] + lanes;
+        const uint32_t S0 = tmem + 2 * kKeys * w + lanes, O = tmem + 256 + D * w + lanes;
         uint32_t cw = 0;
         while (it.next(p)) {
             const int n = it.last - it.first;
@@ -316,7 +353,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
             const int row0 = it.b * 2 * kRows + w * kRows;
             // ---- queries: a warp's 32 rows, 8 rows x 32 dimensions per step; the loads of
             // several groups of 8 rows first ----
-            constexpr int BATCH = sizeof(T) == 2 ? 4 : 2;
+            constexpr int BATCH = 2;
 #pragma unroll 1
             for (int g0 = 0; g0 < 4; g0 += BATCH) {
                 float x[BATCH][D / 32][8];
@@ -383,14 +420,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
             for (int j = 0; j < n; j++, gt++, cw++) {
                 const int slot = gt % kScales, j0 = (it.x.t0 + it.first + j) * kKeys;
                 wait(bar.sc_full[slot], gt / kScales);
-                const uint32_t ok = sc_valid[slot][0] | sc_valid[slot][1] << 4;
-                const bool inside = ok == 0xFFu && j0 >= all_lo && j0 + kKeys <= all_hi;
+                const uint32_t ok = sc_valid[slot], S = S0 + kKeys * (cw & 1);
+                const bool inside = ok == 0xFu && j0 >= all_lo && j0 + kKeys <= all_hi;
                 float vmax = 0.f;
 #pragma unroll
-                for (int e = 0; e < 8; e++) vmax = fmaxf(vmax, sc_max[slot][e]);
+                for (int e = 0; e < 4; e++) vmax = fmaxf(vmax, sc_max[slot][e]);
                 const ulonglong2 *kd = reinterpret_cast<const ulonglong2 *>(kd_s + slot * kKeys);
                 const ulonglong2 *vd = reinterpret_cast<const ulonglong2 *>(vd_s + slot * kKeys);
-                wait(bar.s_full[w], cw);
+                wait(bar.s_full[w][cw & 1], cw >> 1);
                 tc_fence_after();
 
                 // Scores of 16 keys (c), plus nb, as pairs, from the raw products in s.
@@ -432,11 +469,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 if (j == 0) {  // the first reference: this tile's maximum
                     float m = -INFINITY;
 #pragma unroll 1
-                    for (int c = 0; c < 8; c++) {
+                    for (int c = 0; c < 4; c++) {
                         tmem_ld16_wait(r0);
                         uint64_t s[8];
                         pairs_of(r0, s);
-                        tmem_ld16_start(S + 16 * ((c + 1) & 7), r0);
+                        tmem_ld16_start(S + 16 * ((c + 1) & 3), r0);
                         scores(c, s, 0);
 #pragma unroll
                         for (int e = 0; e < 8; e++) m = fmaxf(m, fmaxf(lo_of(s[e]), hi_of(s[e])));
@@ -447,7 +484,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 // its 16 scores: P of chunk c lies at columns 16 c.
                 uint64_t nb = minus_base(ref);
 #pragma unroll 1  // (unrolled, the instruction cache becomes the limit)
-                for (int c2 = 0; c2 < 4; c2++) {
+                for (int c2 = 0; c2 < kKeys / 32; c2++) {
                     uint32_t ph[2][8 * SPLIT];
                     uint64_t sum = 0;
 #pragma unroll
@@ -455,7 +492,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                         const int c = 2 * c2 + k;
                         uint32_t(&r)[16] = k ? r1 : r0;
                         tmem_ld16_wait(r);
-                        if (c < 7) tmem_ld16_start(S + 16 * (c + 1), k ? r0 : r1);
+                        if (c < kKeys / 16 - 1) tmem_ld16_start(S + 16 * (c + 1), k ? r0 : r1);
                         uint64_t s[8];
                         pairs_of(r, s);
                         scores(c, s, nb);
@@ -502,7 +539,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                             tmem_st16(S + 16 * c, t0);
                         }
                         if (j > 0) {
-                            wait(bar.o_full[w], cw - 1);
+                            wait(bar.o_full[w][(cw - 1) & 1], (cw - 1) >> 1);
                             tc_fence_after();
 #pragma unroll 1
                             for (int c = 0; c < D; c += 16) {
@@ -530,11 +567,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 tmem_wait_st();
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.p_full[w]);
+                if (lane == 0) mbar_arrive(&bar.p_full[w][cw & 1]);
             }
 
             // ---- outputs, or this CTA's part of them ----
-            wait(bar.o_full[w], cw - 1);
+            wait(bar.o_full[w][(cw - 1) & 1], (cw - 1) >> 1);
             tc_fence_after();
             const bool whole = it.first == 0 && it.last == it.x.tiles;
             const int part = 2 * blockIdx.x + (it.first == 0 ? 1 : 0);
@@ -582,7 +619,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
     } else if (warp < 12) {
         // =================== codes to fp16 operands: one chunk per warp and piece ===================
         const int q = warp - 8;
-        uint32_t piece = 0;
         const __half2 k1024 = __half2half2(__ushort_as_half(0x6400)), k64 = __half2half2(__ushort_as_half(0x5400));
         // 8 codes less their zeros: pairs (0,4) (1,5) (2,6) (3,7); z1024 = 1024 + z, z64 = 64 + z.
         auto unfold = [&](uint32_t w, __half2 z1024, __half2 z64, uint32_t (&x)[4]) {
@@ -604,29 +640,25 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 const int buf = gt % C::kBuf, slot = gt % kScales;
                 const uint32_t turn = gt / C::kBuf;
                 uint8_t *K = smem + C::oK + buf * C::kTileB, *V = smem + C::oV + buf * C::kTileB;
-                // All keys before any values: with one buffer of each, the values of the tile before
-                // are free only after the products with these keys.
                 wait(bar.k_empty[buf], turn + 1);
-#pragma unroll 1
-                for (int half = 0; half < 2; half++) {
-                    const int st = (piece + half) % kPieces;
-                    wait(bar.raw_full[st], (piece + half) / kPieces);
-                    const uint8_t *chunk = smem + C::oRaw + st * C::kRaw + q * kv4_chunk_bytes(D);
-                    const uint32_t valid = raw_valid[st];
-                    const int j0 = (it.x.t0 + it.first + j) * kKeys + half * kPiece + q * 16;
-                    const int live = valid >> q & 1 ? min(16, it.x.hi - j0) : 0;  // tokens that exist
-                    const __half2 *pairs = reinterpret_cast<const __half2 *>(chunk + 2 * kv4_codes_bytes(D));
+                const int st = gt % kPieces;
+                wait(bar.raw_full[st], gt / kPieces);
+                const uint8_t *chunk = smem + C::oRaw + st * C::kRaw + q * kv4_chunk_bytes(D);
+                const uint32_t valid = raw_valid[st];
+                const int j0 = (it.x.t0 + it.first + j) * kKeys + q * 16;
+                const int live = valid >> q & 1 ? min(16, it.x.hi - j0) : 0;  // tokens that exist
+                const __half2 *pairs = reinterpret_cast<const __half2 *>(chunk + 2 * kv4_codes_bytes(D));
                     {  // scales: lane t < 16 keys, the others values
                         const int t = lane & 15;
                         const float d = t < live ? __low2float(pairs[lane]) : 0.f;
-                        const int at = slot * kKeys + half * kPiece + q * 16 + t;
+                        const int at = slot * kKeys + q * 16 + t;
                         if (lane < 16) kd_s[at] = d;
                         else vd_s[at] = d * kTcLift;
                         float m = lane < 16 ? 0.f : d * kTcLift;
 #pragma unroll
                         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-                        if (lane == 16) sc_max[slot][half * 4 + q] = m;
-                        if (lane == 0 && q == 0) sc_valid[slot][half] = valid;
+                        if (lane == 16) sc_max[slot][q] = m;
+                        if (lane == 0 && q == 0) sc_valid[slot] = valid;
                     }
                     // ---- keys ----
                     constexpr int QN = D / 32;              // 16-byte quarters of a key row
@@ -640,7 +672,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                         const uint32_t w4[4] = {wv.x, wv.y, wv.z, wv.w};
                         const __half2 z = __half2half2(t < live ? __high2half(pairs[t]) : __ushort_as_half(0));
                         const __half2 za = __hadd2(k1024, z), zb = __hadd2(k64, z);
-                        const int tt = half * kPiece + q * 16 + t;
+                        const int tt = q * 16 + t;
                         uint8_t *dst = K + (tt >> 3) * (D * 16) + (kq * 4) * 128 + (tt & 7) * 16;
 #pragma unroll
                         for (int i = 0; i < 4; i++) {
@@ -649,18 +681,11 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                             *reinterpret_cast<uint4 *>(dst + i * 128) = make_uint4(x[0], x[1], x[2], x[3]);
                         }
                     }
-                }
                 fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&bar.k_full[buf]), mbar_arrive(&bar.sc_full[slot]);
                 wait(bar.v_empty[buf], turn + 1);
-#pragma unroll 1
-                for (int half = 0; half < 2; half++, piece++) {
-                    const int st = piece % kPieces;
-                    const uint8_t *chunk = smem + C::oRaw + st * C::kRaw + q * kv4_chunk_bytes(D);
-                    const int j0 = (it.x.t0 + it.first + j) * kKeys + half * kPiece + q * 16;
-                    const int live = raw_valid[st] >> q & 1 ? min(16, it.x.hi - j0) : 0;
-                    const __half2 *pairs = reinterpret_cast<const __half2 *>(chunk + 2 * kv4_codes_bytes(D));
+                {
                     // ---- values: 8 tokens x 8 dimensions per lane, transposed ----
                     constexpr int WN = D / 8;
                     if (lane < 2 * WN) {
@@ -680,7 +705,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                             za[i] = __hadd2(k1024, z), zb[i] = __hadd2(k64, z);
                         }
                         // dimension 8 wi + e is row 64 (wi / 8) + 8 e + wi % 8 of the operand
-                        uint8_t *dst = V + (wi >> 3) * (8 * 2048) + (half * 8 + q * 2 + gr) * 128 + (wi & 7) * 16;
+                        uint8_t *dst = V + (wi >> 3) * (8 * kKeys * 16) + (q * 2 + gr) * 128 + (wi & 7) * 16;
 #pragma unroll
                         for (int hw = 0; hw < 2; hw++) {
                             const uint32_t sel = hw ? (gr ? 0x3276 : 0x7632) : (gr ? 0x1054 : 0x5410);
@@ -689,68 +714,72 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                             for (int i = 0; i < 4; i++) unfold(prmt(wa[i], wb[i], sel), za[i], zb[i], x[i]);
 #pragma unroll
                             for (int e = 0; e < 4; e++)
-                                *reinterpret_cast<uint4 *>(dst + (4 * hw + e) * 2048) =
+                                *reinterpret_cast<uint4 *>(dst + (4 * hw + e) * (kKeys * 16)) =
                                     make_uint4(x[0][e], x[1][e], x[2][e], x[3][e]);
                         }
                     }
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.raw_empty[st]);
                 }
                 fence_proxy_async_smem();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.v_full[buf]);
+                if (lane == 0) mbar_arrive(&bar.raw_empty[st]), mbar_arrive(&bar.v_full[buf]);
             }
         }
     } else if (warp == 12) {
         // =================== tensor-core operations ===================
-        const uint32_t sb = smem_u32(smem);
+        const uint32_t sb = __shfl_sync(0xffffffffu, smem_u32(smem), 0);
+        const uint32_t tm = __shfl_sync(0xffffffffu, tmem, 0);
+        const uint32_t dQ = desc_low(sb + C::oQ), dK = desc_low(sb + C::oK), dV = desc_low(sb + C::oV);
         constexpr uint32_t idS = idesc_f16(128, kKeys), idO = idesc_f16(128, D);
-        uint32_t cw[2] = {0, 0}, nq[2] = {0, 0};
-        auto qk = [&](int w, int buf) {
-            if (lane == 0) {
+        constexpr uint32_t hQ = desc_high(D * 16), hV = desc_high(kKeys * 16);
+        uint32_t cw[2] = {0, 0}, nq[2] = {0, 0};  // key tiles and items of each row tile so far
+        auto qk = [&](int w, uint32_t tile, int buf, bool last) {
+            if (elect_one()) {
 #pragma unroll
                 for (int s = 0; s < SPLIT; s++)
 #pragma unroll
-                    for (int k = 0; k < D / 16; k++)
-                        mma_f16(tS[w], kmajor_desc(sb + C::oQ + (w * SPLIT + s) * C::kQ + k * 256, D * 16),
-                                kmajor_desc(sb + C::oK + buf * C::kTileB + k * 256, D * 16), idS, s + k > 0);
-                mma_commit(&bar.s_full[w]);
+                    for (int k = 0; k < D / 64; k++)
+                        mma4_ss<hQ, hQ>(tm + 2 * kKeys * w + kKeys * (tile & 1),
+                                        dQ + (((w * SPLIT + s) * C::kQ + k * 1024) >> 4),
+                                        dK + ((buf * C::kTileB + k * 1024) >> 4), idS, s + k > 0);
+                mma_commit(&bar.s_full[w][tile & 1]);
+                if (last) mma_commit(&bar.k_empty[buf]);
             }
             __syncwarp();
         };
         while (it.next(p)) {
-            const int n = it.last - it.first, tiles = it.x.rows > kRows ? 2 : 1;
-            for (int w = 0; w < tiles; w++) wait(bar.q_full[w], nq[w]++);
+            const int n = __shfl_sync(0xffffffffu, it.last - it.first, 0);
+            const int tiles = __shfl_sync(0xffffffffu, it.x.rows > kRows ? 2 : 1, 0);
             wait(bar.k_full[gt % C::kBuf], gt / C::kBuf);
-            tc_fence_after();
-            for (int w = 0; w < tiles; w++) qk(w, gt % C::kBuf);
-            if (lane == 0) mma_commit(&bar.k_empty[gt % C::kBuf]);
+#pragma unroll
+            for (int w = 0; w < 2; w++) {
+                if (w >= tiles) continue;
+                wait(bar.q_full[w], nq[w]++);
+                tc_fence_after();
+                qk(w, cw[w], gt % C::kBuf, w == tiles - 1);
+            }
             for (int j = 0; j < n; j++, gt++) {
                 const int buf = gt % C::kBuf, nb = (gt + 1) % C::kBuf;
-                wait(bar.v_full[buf], gt / C::kBuf);
-                for (int w = 0; w < tiles; w++) {
-                    wait(bar.p_full[w], cw[w]++);
+#pragma unroll
+                for (int w = 0; w < 2; w++) {
+                    if (w >= tiles) continue;
+                    if (j + 1 < n) {
+                        if (w == 0) wait(bar.k_full[nb], (gt + 1) / C::kBuf);
+                        tc_fence_after();
+                        qk(w, cw[w] + 1, nb, w == tiles - 1);
+                    }
+                    if (w == 0) wait(bar.v_full[buf], gt / C::kBuf);
+                    wait(bar.p_full[w][cw[w] & 1], cw[w] >> 1);
                     tc_fence_after();
-                    if (lane == 0) {
+                    if (elect_one()) {
 #pragma unroll
                         for (int s = 0; s < SPLIT; s++)
-#pragma unroll
-                            for (int k = 0; k < kKeys / 16; k++)
-                                mma_f16_ts(tO[w], tS[w] + 16 * k + 8 * s,
-                                           kmajor_desc(sb + C::oV + buf * C::kTileB + k * 256, 2048), idO,
-                                           j > 0 || s + k > 0);
-                        mma_commit(&bar.o_full[w]);
+                            mma4_ts<hV>(tm + 256 + D * w, tm + 2 * kKeys * w + kKeys * (cw[w] & 1) + 8 * s,
+                                        dV + ((buf * C::kTileB) >> 4), idO, j > 0 || s > 0);
+                        mma_commit(&bar.o_full[w][cw[w] & 1]);
                         if (w == tiles - 1) mma_commit(&bar.v_empty[buf]);
                     }
                     __syncwarp();
-                    if (j + 1 < n) {
-                        if (w == 0) {
-                            wait(bar.k_full[nb], (gt + 1) / C::kBuf);
-                            tc_fence_after();
-                        }
-                        qk(w, nb);
-                        if (w == tiles - 1 && lane == 0) mma_commit(&bar.k_empty[nb]);
-                    }
+                    cw[w]++;
                 }
             }
         }
@@ -764,12 +793,12 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
         uint32_t piece = 0;
         const int64_t page_bytes = ((int64_t)p.kv_heads << (p.shift - 4)) * kv4_chunk_bytes(D);
         while (it.next(p)) {
-            const int n = 2 * (it.last - it.first);
+            const int n = it.last - it.first;
             const uint8_t *base = p.cache + ((int64_t)it.h << (p.shift - 4)) * kv4_chunk_bytes(D);
             const int32_t *row = p.table + (int64_t)it.r * p.width;
             int page = -1;
             for (int i = 0; i < n; i++, piece++) {
-                const int tok0 = (it.x.t0 + it.first) * kKeys + i * kPiece;
+                const int tok0 = (it.x.t0 + it.first + i) * kKeys;
                 if ((i & 7) == 0) {  // the pages of the next 32 chunks, one per lane
                     const int j = tok0 + 16 * lane;
                     const int64_t c = j >> p.shift;
