@@ -135,6 +135,8 @@ def library_path() -> str:
 def load(build_if_missing: bool = True):
     """Load liblb.so (building it with nvcc if it is missing or stale)."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is None:
             path = _build.LIB
@@ -163,15 +165,15 @@ def status_string(status: int) -> str:
 def _ptr(t):
     if t is None:
         return None
-    if isinstance(t, int):
-        return t
-    if hasattr(t, "data_ptr"):
-        if not t.is_cuda:
-            raise ValueError("lb_* entry points take device tensors")
-        if not t.is_contiguous():
-            raise ValueError("lb_* entry points take contiguous tensors")
-        return t.data_ptr()
-    raise TypeError(f"cannot pass {type(t)} as a device pointer")
+    try:
+        if t.is_cuda and t.is_contiguous():
+            return t.data_ptr()
+    except AttributeError:
+        if isinstance(t, int):
+            return t
+        raise TypeError(f"cannot pass {type(t)} as a device pointer") from None
+    raise ValueError("lb_* entry points take contiguous tensors" if t.is_cuda else
+                     "lb_* entry points take device tensors")
 
 
 def _rows(t):
@@ -182,17 +184,34 @@ def _rows(t):
     if not t.is_cuda:
         raise ValueError("lb_* entry points take device tensors")
     dense = 1
-    for n, s in zip(reversed(t.shape[1:]), reversed(t.stride()[1:])):
-        if n != 1 and s != dense:
+    for n, s in zip(t.shape[:0:-1], t.stride()[:0:-1]):
+        if s != dense and n != 1:
             raise ValueError("only the first dimension may be strided")
         dense *= n
     return t.data_ptr()
 
 
+_current_stream = None
+
+
+def _find_current_stream():
+    """A function that returns the address of torch's current stream (the short way to it where this
+    torch has it: a call of these entry points costs a few microseconds, a Stream object three)."""
+    import torch
+    raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)
+    device = getattr(torch._C, "_cuda_getDevice", None)
+    if raw is None or device is None:
+        return lambda: torch.cuda.current_stream().cuda_stream
+    torch.cuda.current_stream()  # initializes CUDA
+    return lambda: raw(device())
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        return torch.cuda.current_stream().cuda_stream
+        global _current_stream
+        if _current_stream is None:
+            _current_stream = _find_current_stream()
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream

@@ -35,7 +35,7 @@ constexpr int kTcThreads = 448;
 constexpr int kItemCost = 6;         // an item's queries and outputs take about as long as 6 tiles
 constexpr int kTcMaxCtas = 160;
 constexpr int kTcWhole = 8;          // items of at most this many tiles are never split
-constexpr int kTcMinRun = 8;
+constexpr int kTcMinRun = kItemCost + 1;
 constexpr float kTcLift = 16.f;      // weights at the reference: 2^4
 constexpr float kTcMost = 60000.f;   // largest weight a tile may hold
 

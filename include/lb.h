@@ -501,7 +501,8 @@ int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8_t *cache,
  *   v not allowed by b's mask:  x = -inf, whatever it was
  *   out[b][v] = x
  * The lists are rows of one array: list b is ids[start[b] .. start[b + 1] - 1], start int32
- * [B + 1], not falling; ids int32; an id outside [0, V) is skipped.  NULL ids, values of [B] or mask
+ * [B + 1], not falling; ids int32; an id outside [0, V) is skipped.  Of a row's bias list the first
+ * LB_LOGITS_MAX_BIAS entries count; a token stands less than 2^30 times in a list.  NULL ids, values of [B] or mask
  * leave a step out (repetition without lists does nothing).  mask : uint32 words, bit
  * v % 32 of word v / 32 allows v; row mask_row_opt[b] of mask_rows rows, mask_stride words apart, or
  * row b if mask_row_opt is NULL (mask_rows >= B then); a row outside [0, mask_rows) means no mask.
@@ -510,6 +511,7 @@ int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8_t *cache,
  * 1 <= B <= 65535; 1 <= V <= LB_LOGITS_MAX_V; strides >= V; mask_stride >= ceil(V / 32).
  * Pointers aligned to their elements (16-byte rows are fastest). */
 #define LB_LOGITS_MAX_V 400000
+#define LB_LOGITS_MAX_BIAS 65535
 typedef struct lb_logit_rules {
     const int32_t *prompt_ids, *prompt_start;
     const int32_t *output_ids, *output_start;
