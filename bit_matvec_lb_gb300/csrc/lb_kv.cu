@@ -113,104 +113,151 @@ __global__ void __launch_bounds__(kPlanThreads) kv_plan_kernel(const PlanParams 
 }
 
 // ------------------------------------------------------------------------------------------
-// Append: one row (a token's key or value of one head) per D / 8 lanes, 8 values a lane, so a row
-// is read once with 16-byte loads, its extremes meet in log2(D / 8) shuffles, and a lane's eight
-// codes are one 4-byte store.
+// Append and read-back: one row (a token's key or value of one head) per D / 16 lanes, two times 8
+// values a lane (of the row's halves), so a row is read once with 16-byte loads, its extremes meet in
+// log2(D / 16) shuffles, and a lane's codes are two 4-byte stores.  The bytes allow about 7 us for the
+// append of 8191 tokens of 8 heads x 128 in bf16; what bounds it is issue, so values become whole
+// numbers and back by additions to 2^23 and 1.5 * 2^23, whose last place is 1, not by conversions (a
+// quarter of the rate), and a row's fixed work is shared by 16 values of a lane: append + read-back
+// 20.8 us; with 8 values a lane 30.4, with four rows per thread (fewer threads on an SM) 37.5.
 // ------------------------------------------------------------------------------------------
 struct KvParams {
     const void *k, *v;
     void *k_out, *v_out;
     const int64_t *slot;
     uint8_t *cache;
-    int64_t k_stride, v_stride, rows, slots;
-    int kv_heads, shift;
+    int64_t k_stride, v_stride, T, slots;
+    int kv_heads, shift, tokens;  // tokens of a CTA
+    uint32_t per_inverse;         // ceil(2^32 / (2 kv_heads)): rows of a CTA over rows of a token
 };
 
 constexpr int kKvThreads = 256;
 
-// A row's token, head and which of the two tensors; false if its slot is not in the cache.
+// Where a row lies: its token, head and tensor, and its slot (-1 for a row past the end).
 template <int D>
-__device__ __forceinline__ bool kv_row(const KvParams &p, int64_t row, int64_t &t, int &h, int &is_v,
-                                       uint8_t *&codes, uint8_t *&pair) {
-    const int per = 2 * p.kv_heads;
-    t = row / per;
-    const int i = (int)(row - t * per);
-    is_v = i >= p.kv_heads;
-    h = i - is_v * p.kv_heads;
-    const int64_t slot = p.slot[t];
-    if (slot < 0 || slot >= p.slots) return false;
-    const int in_page = (int)(slot & ((1 << p.shift) - 1));
-    uint8_t *chunk = p.cache + kv4_chunk_offset(slot >> p.shift, h, in_page, p.kv_heads, p.shift, D);
-    codes = chunk + is_v * kv4_codes_bytes(D) + (in_page & 15) * (D / 2);
-    pair = chunk + 2 * kv4_codes_bytes(D) + is_v * kKv4PairBytes + (in_page & 15) * 4;
-    return true;
-}
+struct KvRow {
+    int64_t t, slot;
+    int h, is_v;
+    bool there;
+
+    __device__ __forceinline__ KvRow(const KvParams &p, int row) {
+        // (exact while row * 2 kv_heads < 2^32)
+        const int tl = (int)__umulhi((uint32_t)row, p.per_inverse), i = row - tl * 2 * p.kv_heads;
+        t = (int64_t)blockIdx.x * p.tokens + tl;
+        there = tl < p.tokens && t < p.T;
+        is_v = i >= p.kv_heads;
+        h = i - is_v * p.kv_heads;
+        slot = there ? p.slot[t] : -1;
+    }
+    __device__ __forceinline__ bool stored(const KvParams &p) const {
+        return slot >= 0 && slot < p.slots;
+    }
+    __device__ __forceinline__ void find(const KvParams &p, uint8_t *&codes, uint8_t *&pair) const {
+        const int in_page = (int)(slot & ((1 << p.shift) - 1));
+        uint8_t *chunk = p.cache + kv4_chunk_offset(slot >> p.shift, h, in_page, p.kv_heads, p.shift, D);
+        codes = chunk + is_v * kv4_codes_bytes(D) + (in_page & 15) * (D / 2);
+        pair = chunk + 2 * kv4_codes_bytes(D) + is_v * kKv4PairBytes + (in_page & 15) * 4;
+    }
+};
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kKvThreads) kv4_append_kernel(const KvParams p) {
-    constexpr int L = D / 8;  // lanes of a row
+    constexpr int L = D / 16, STEP = kKvThreads / L;  // lanes of a row, rows of a CTA at a time
     const int sub = threadIdx.x % L;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t row = (int64_t)blockIdx.x * (kKvThreads / L) + threadIdx.x / L;
-    if (row >= p.rows) return;
-    const unsigned lanes = (L == 16 ? 0xFFFFu : 0xFFu) << (threadIdx.x % 32 / L * L);
-    int64_t t;
-    int h, is_v;
-    uint8_t *codes, *pair;
-    if (!kv_row<D>(p, row, t, h, is_v, codes, pair)) return;
-    const T *x0 = static_cast<const T *>(is_v ? p.v : p.k) + t * (is_v ? p.v_stride : p.k_stride) +
-                  (int64_t)h * D + sub * 8;
-    float x[8];
-    load8(x0, x);
-    float lo = 0.f, hi = 0.f;
+    const int rows = 2 * p.kv_heads * p.tokens;
+    for (int row0 = 0; row0 < rows; row0 += STEP) {
+        const KvRow<D> r(p, row0 + threadIdx.x / L);
+        float x[2][8] = {};
+        if (r.there) {
+            const T *src = static_cast<const T *>(r.is_v ? p.v : p.k) +
+                           r.t * (r.is_v ? p.v_stride : p.k_stride) + r.h * D + sub * 8;
+            load8(src, x[0]);
+            load8(src + D / 2, x[1]);
+        }
+        float2 m = make_float2(0.f, 0.f);  // {-lowest, highest}, 0 among them
 #pragma unroll
-    for (int i = 0; i < 8; i++) lo = fminf(lo, x[i]), hi = fmaxf(hi, x[i]);
+        for (int e = 0; e < 16; e++) m.x = fmaxf(m.x, -x[e / 8][e % 8]), m.y = fmaxf(m.y, x[e / 8][e % 8]);
+        if (sizeof(T) == 2) {  // bf16 extremes are bf16: both in one word
+            __nv_bfloat162 w = __floats2bfloat162_rn(m.x, m.y);
 #pragma unroll
-    for (int o = L / 2; o > 0; o >>= 1) {
-        lo = fminf(lo, __shfl_xor_sync(lanes, lo, o));
-        hi = fmaxf(hi, __shfl_xor_sync(lanes, hi, o));
+            for (int o = L / 2; o > 0; o >>= 1) {
+                const uint32_t other = __shfl_xor_sync(0xffffffffu, *reinterpret_cast<uint32_t *>(&w), o);
+                w = __hmax2(w, *reinterpret_cast<const __nv_bfloat162 *>(&other));
+            }
+            m = __bfloat1622float2(w);
+        } else {
+#pragma unroll
+            for (int o = L / 2; o > 0; o >>= 1) {
+                m.x = fmaxf(m.x, __shfl_xor_sync(0xffffffffu, m.x, o));
+                m.y = fmaxf(m.y, __shfl_xor_sync(0xffffffffu, m.y, o));
+            }
+        }
+        if (!r.stored(p)) continue;
+        const __half d = __float2half_rn(fminf(__fdiv_rn(__fadd_rn(m.y, m.x), 15.f), 65504.f));
+        const float df = __half2float(d);
+        const float id = df > 0.f ? __frcp_rn(df) : 0.f;
+        // round-half-even by adding 1.5 * 2^23; values are clamped at whole numbers before
+        constexpr float kRound = 12582912.f;
+        const float z = fminf(__fadd_rn(__fadd_rn(fminf(__fmul_rn(m.x, id), 64.f), kRound), -kRound), 15.f);
+        uint8_t *codes, *pair;
+        r.find(p, codes, pair);
+#pragma unroll
+        for (int half = 0; half < 2; half++) {
+            uint32_t c[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++) {
+                const float y = fminf(fmaxf(__fmul_rn(x[half][e], id), -z), 15.f - z);
+                c[e] = __float_as_uint(__fadd_rn(__fadd_rn(y, kRound), z));  // the last byte is the code
+            }
+            const uint32_t even = prmt(prmt(c[0], c[2], 0x0040), prmt(c[4], c[6], 0x0040), 0x5410);
+            const uint32_t odd = prmt(prmt(c[1], c[3], 0x0040), prmt(c[5], c[7], 0x0040), 0x5410);
+            reinterpret_cast<uint32_t *>(codes)[half * L + sub] = even | odd << 4;
+        }
+        if (sub == 0) *reinterpret_cast<__half2 *>(pair) = __halves2half2(d, __float2half_rn(z));
     }
-    const __half d = __float2half_rn(fminf(__fdiv_rn(__fsub_rn(hi, lo), 15.f), 65504.f));
-    const float df = __half2float(d);
-    const float id = df > 0.f ? __fdiv_rn(1.f, df) : 0.f;
-    const float z = fminf(fmaxf(rintf(__fmul_rn(-lo, id)), 0.f), 15.f);
-    uint32_t w = 0;
-#pragma unroll
-    for (int i = 0; i < 8; i++) {
-        const float c = fminf(fmaxf(rintf(__fmul_rn(x[i], id)) + z, 0.f), 15.f);
-        w |= (uint32_t)(int)c << (4 * i);
-    }
-    reinterpret_cast<uint32_t *>(codes)[sub] = w;
-    if (sub == 0) *reinterpret_cast<__half2 *>(pair) = __halves2half2(d, __float2half_rn(z));
 }
 
 template <int D, typename T>
 __global__ void __launch_bounds__(kKvThreads) kv4_dequant_kernel(const KvParams p) {
-    constexpr int L = D / 8;
+    constexpr int L = D / 16, STEP = kKvThreads / L;
     const int sub = threadIdx.x % L;
     pdl_wait();
     pdl_launch_dependents();
-    const int64_t row = (int64_t)blockIdx.x * (kKvThreads / L) + threadIdx.x / L;
-    if (row >= p.rows) return;
-    int64_t t;
-    int h, is_v;
-    uint8_t *codes, *pair;
-    float x[8] = {};
-    if (kv_row<D>(p, row, t, h, is_v, codes, pair)) {
-        const uint32_t w = reinterpret_cast<const uint32_t *>(codes)[sub];
-        const __half2 dz = *reinterpret_cast<const __half2 *>(pair);
-        const float d = __low2float(dz), z = __high2float(dz);
+    const int rows = 2 * p.kv_heads * p.tokens;
+    for (int row0 = threadIdx.x / L; row0 < rows; row0 += STEP) {
+        const KvRow<D> r(p, row0);
+        if (!r.there) continue;
+        uint32_t w[2] = {0, 0};
+        float d = 0.f, z = 8388608.f;
+        if (r.stored(p)) {
+            uint8_t *codes, *pair;
+            r.find(p, codes, pair);
+            w[0] = reinterpret_cast<const uint32_t *>(codes)[sub];
+            w[1] = reinterpret_cast<const uint32_t *>(codes)[L + sub];
+            const __half2 dz = *reinterpret_cast<const __half2 *>(pair);
+            d = __low2float(dz), z += __high2float(dz);
+        }
+        T *dst = static_cast<T *>(r.is_v ? p.v_out : p.k_out) + (r.t * p.kv_heads + r.h) * D + sub * 8;
 #pragma unroll
-        for (int i = 0; i < 8; i++) x[i] = __fmul_rn(d, (float)((w >> (4 * i)) & 15) - z);
+        for (int half = 0; half < 2; half++) {
+            float x[8];
+#pragma unroll
+            for (int e = 0; e < 8; e++)  // 2^23 + c, less 2^23 + z
+                x[e] = __fmul_rn(d, __uint_as_float(0x4B000000u | ((w[half] >> (4 * e)) & 15)) - z);
+            store8(dst + half * (D / 2), x);
+        }
     }
-    store8(static_cast<T *>(is_v ? p.v_out : p.k_out) + (t * p.kv_heads + h) * D + sub * 8, x);
 }
 
 template <int D, typename T>
-static int launch_kv(bool append, const KvParams &p, cudaStream_t st) {
-    constexpr int rows = kKvThreads / (D / 8);
-    const dim3 grid((unsigned)((p.rows + rows - 1) / rows));
+static int launch_kv(bool append, KvParams p, cudaStream_t st) {
+    // Tokens of a CTA: as many as give each thread one row.
+    p.tokens = kKvThreads / (D / 16) / (2 * p.kv_heads);
+    if (p.tokens < 1) p.tokens = 1;
+    p.per_inverse = (uint32_t)(((uint64_t(1) << 32) + 2 * p.kv_heads - 1) / (2 * p.kv_heads));
+    const dim3 grid((unsigned)((p.T + p.tokens - 1) / p.tokens));
     return append ? launch_pdl(kv4_append_kernel<D, T>, grid, dim3(kKvThreads), 0, st, p)
                   : launch_pdl(kv4_dequant_kernel<D, T>, grid, dim3(kKvThreads), 0, st, p);
 }
@@ -218,7 +265,7 @@ static int launch_kv(bool append, const KvParams &p, cudaStream_t st) {
 static int dispatch_kv(bool append, int D, int type, const KvParams &p, cudaStream_t st) {
     DeviceInfo di;
     if (int e = current_device_info(&di)) return e;
-    if (p.rows == 0) return LB_OK;
+    if (p.T == 0) return LB_OK;
     if (type == LB_OUT_F32)
         return D == 64 ? launch_kv<64, float>(append, p, st) : launch_kv<128, float>(append, p, st);
     return D == 64 ? launch_kv<64, __nv_bfloat16>(append, p, st)
@@ -269,7 +316,7 @@ LB_EXPORT int lb_kv4_append(const void *k, const void *v, int type, int64_t k_st
     if (!k || !v || !slot || !cache) return LB_ERR_NULL;
     if (!kv4_shape_ok(pages, page_size, kv_heads, head_dim) || T < 0 || T >= (int64_t(1) << 31) ||
         (type != LB_OUT_F32 && type != LB_OUT_BF16) || k_stride < (int64_t)kv_heads * head_dim ||
-        v_stride < (int64_t)kv_heads * head_dim || 2 * T * kv_heads >= (int64_t(1) << 34))
+        v_stride < (int64_t)kv_heads * head_dim)
         return LB_ERR_SHAPE;
     const int64_t per16 = type == LB_OUT_F32 ? 4 : 8;
     if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned_to(slot, 8) ||
@@ -277,7 +324,7 @@ LB_EXPORT int lb_kv4_append(const void *k, const void *v, int type, int64_t k_st
         return LB_ERR_ALIGN;
     KvParams p{};
     p.k = k, p.v = v, p.slot = slot, p.cache = cache, p.k_stride = k_stride, p.v_stride = v_stride;
-    p.rows = 2 * T * kv_heads, p.slots = pages * page_size, p.kv_heads = kv_heads;
+    p.T = T, p.slots = pages * page_size, p.kv_heads = kv_heads;
     p.shift = page_shift_of(page_size);
     return dispatch_kv(true, head_dim, type, p, as_stream(stream));
 }
@@ -288,14 +335,13 @@ LB_EXPORT int lb_dequantize_kv4(const uint8_t *cache, int64_t pages, int page_si
     using namespace lb;
     if (!k || !v || !slot || !cache) return LB_ERR_NULL;
     if (!kv4_shape_ok(pages, page_size, kv_heads, head_dim) || T < 0 || T >= (int64_t(1) << 31) ||
-        (out_format != LB_OUT_F32 && out_format != LB_OUT_BF16) ||
-        2 * T * kv_heads >= (int64_t(1) << 34))
+        (out_format != LB_OUT_F32 && out_format != LB_OUT_BF16))
         return LB_ERR_SHAPE;
     if (!aligned16(k) || !aligned16(v) || !aligned16(cache) || !aligned_to(slot, 8))
         return LB_ERR_ALIGN;
     KvParams p{};
     p.k_out = k, p.v_out = v, p.slot = slot, p.cache = const_cast<uint8_t *>(cache);
-    p.rows = 2 * T * kv_heads, p.slots = pages * page_size, p.kv_heads = kv_heads;
+    p.T = T, p.slots = pages * page_size, p.kv_heads = kv_heads;
     p.shift = page_shift_of(page_size);
     return dispatch_kv(false, head_dim, out_format, p, as_stream(stream));
 }

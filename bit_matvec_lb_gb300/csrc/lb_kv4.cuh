@@ -28,7 +28,7 @@ inline int page_shift_of(int page_size) {
 
 inline bool kv4_shape_ok(int64_t pages, int page_size, int kv_heads, int head_dim) {
     return pages >= 1 && pages < (int64_t(1) << 31) && page_shift_of(page_size) > 0 &&
-           kv_heads >= 1 && kv_heads <= 65535 && (head_dim == 64 || head_dim == 128);
+           kv_heads >= 1 && kv_heads <= 16384 && (head_dim == 64 || head_dim == 128);
 }
 
 inline bool aligned_to(const void *p, uintptr_t n) {

@@ -394,7 +394,7 @@ int lb_gemm_q2_0_g64_noalloc(const uint8_t *codes, const uint16_t *scales, const
  *   lb_logits_adjust  penalties, biases and grammar masks on the head's logits
  *
  * Cache: one byte buffer [pages][kv_heads][page_size / 16][16 * (head_dim + 8)], page_size in
- * {16, 32, 64, 128, 256}, head_dim in {64, 128}.  The innermost piece, a chunk, holds 16
+ * {16, 32, 64, 128, 256}, head_dim in {64, 128}, kv_heads up to 16384.  The innermost piece, a chunk, holds 16
  * consecutive tokens of one head:
  *   16 key rows of head_dim/2 bytes, 16 value rows of head_dim/2 bytes (the code of dimension 2j
  *   in the low half of byte j, of 2j + 1 in the high half),
