@@ -183,6 +183,8 @@ def _rows(t):
         return _ptr(t)
     if not t.is_cuda:
         raise ValueError("lb_* entry points take device tensors")
+    if t.is_contiguous():
+        return t.data_ptr()
     dense = 1
     for n, s in zip(t.shape[:0:-1], t.stride()[:0:-1]):
         if s != dense and n != 1:

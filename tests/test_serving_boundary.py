@@ -153,6 +153,9 @@ def test_binding_takes_row_strided_tensors_only():
         def stride(self):
             return self._s
 
+        def is_contiguous(self):
+            return False
+
         def data_ptr(self):
             return A
 
