@@ -11,16 +11,16 @@ namespace lb {
 // the columns of two products with the code matrices: with k_t = kd_t (kc_t - kz_t),
 //   s_t = scale * kd_t * (sum_i q_i kc_ti - kz_t sum_i q_i),
 //   out = sum_t p_t vd_t (vc_t - vz_t) / sum_t p_t,   p_t = 2^(s_t log2 e - R),
-// so codes enter the tensor cores as they are, whole numbers 0..15, exact in fp16, and the scales
-// act on the scores and weights.  R runs over max_t(s_t + log2 vd_t), which bounds the
+// so codes enter the tensor cores as whole numbers, exact in fp16, and the scales act on the scores
+// and weights.  R runs over max_t(s_t + log2 vd_t), which bounds the
 // weights w_t = p_t vd_t themselves (not the p_t): they enter the second product as fp16 in
 // [0, 2^15], whatever the sizes of the scales.
 //
-// Bound: reading the cache (D + 8 bytes per token and head).  A code costs 5/8 (keys) or 3/4
-// (values) of an integer operation to become fp16: masked in place, 4-bit fields at bits 0 and 16
-// of a word are the fp16 pair c * 2^-24 (subnormal, exact), at bits 4 and 20 it is 16 c * 2^-24; q
-// and the outputs carry the 16 and 2^24.  Two neighbouring tokens' words are interleaved by 16 bits
-// to pair tokens for the second product.  mma.sync serves here: rows are 8 to 16 wide, the products
+// Bound: reading the cache (D + 8 bytes per token and head), and close to it the integer pipe.  A code
+// costs 5/8 (keys) or 3/4 (values) of an integer operation to become fp16: masked in place, 4-bit
+// fields at bits 0 and 16 of a word are the mantissas' last bits of an fp16 pair, at bits 4 and 20
+// the next four.  Two neighbouring tokens' words are interleaved by 16 bits to pair tokens for the
+// second product.  mma.sync serves here: rows are 8 to 16 wide, the products
 // are a third of the issue slots at full bandwidth, and tcgen05 would need the fp16 codes written
 // to shared memory, four times the cache's bytes.
 // ------------------------------------------------------------------------------------------
@@ -49,15 +49,35 @@ __device__ __forceinline__ uint32_t transpose8x8(uint32_t a) {
     return d;
 }
 
-// Four fp16 pairs of a word of eight codes: {0,4} * 1, {1,5} * 16, {2,6} * 1, {3,7} * 16 (* 2^-24).
+// Four fp16 pairs of a word of eight codes, by pairs of places {0,4}, {1,5}, {2,6}, {3,7}: as
+// subnormals, c * 2^-24 and, the odd pairs, 16 c * 2^-24, or (NORMAL) c - 8 as normal numbers, by
+// the mantissas of 1024 and 64.  The tensor cores align a product by its factors' exponent fields and
+// cut, downwards, what lies below the last place of a sum's largest term; subnormal factors lose ten
+// of its 24 bits that way.  Values are always normal: sums over thousands of tokens nearly cancel
+// (131k tokens with subnormals: 3e-5 of an output, with normal numbers 7e-7).  Keys are with fp32
+// tensors; with bf16 ones the cut is alike for all tokens and far below the outputs' rounding, and
+// the subtraction would cost a tenth.
+template <bool NORMAL>
 __device__ __forceinline__ void spread_codes(uint32_t w, uint32_t (&x)[4]) {
-    x[0] = and_imm<0x000F000Fu>(w);
-    x[1] = and_imm<0x00F000F0u>(w);
     const uint32_t h = w >> 8;
-    x[2] = and_imm<0x000F000Fu>(h);
-    x[3] = and_imm<0x00F000F0u>(h);
+    if (NORMAL) {
+        asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(x[0]) : "r"(w));
+        asm("lop3.b32 %0, %1, 0x00F000F0, 0x54005400, 0xEA;" : "=r"(x[1]) : "r"(w));
+        asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(x[2]) : "r"(h));
+        asm("lop3.b32 %0, %1, 0x00F000F0, 0x54005400, 0xEA;" : "=r"(x[3]) : "r"(h));
+#pragma unroll
+        for (int e = 0; e < 4; e++) {
+            const __half2 less = __half2half2(__ushort_as_half(e & 1 ? 0x5480 : 0x6408));  // 72, 1032
+            const __half2 v = __hsub2(*reinterpret_cast<const __half2 *>(&x[e]), less);
+            x[e] = *reinterpret_cast<const uint32_t *>(&v);
+        }
+    } else {
+        x[0] = and_imm<0x000F000Fu>(w);
+        x[1] = and_imm<0x00F000F0u>(w);
+        x[2] = and_imm<0x000F000Fu>(h);
+        x[3] = and_imm<0x00F000F0u>(h);
+    }
 }
-
 template <int D, int SPLIT, int NT>
 struct Decode {
     static constexpr int kCols = 8 * NT / SPLIT;   // query rows of one item
@@ -91,6 +111,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
     constexpr int COLS = C::kCols;
     constexpr int W = D / 32;             // words of eight codes per thread and key row
     constexpr int VW = D / 64;            // words of eight codes per thread and value row
+    constexpr bool NORMAL = sizeof(T) == 4;  // key codes; what they are of themselves in the products
+    constexpr float UNIT = NORMAL ? 1.f : 1.f / 16777216.f, ODD = NORMAL ? 1.f : 16.f, LESS = NORMAL ? 8.f : 0.f;
     extern __shared__ __align__(128) uint8_t smem[];
     __shared__ uint64_t full[kWarps][kStages];
     __shared__ int64_t scan[kWarps];
@@ -257,11 +279,11 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
             for (int i = 0; i < W; i++)
 #pragma unroll
                 for (int e = 0; e < 4; e++) {
-                    const float s = e & 1 ? 0.0625f : 1.f;
+                    const float s = e & 1 ? 1.f / ODD : 1.f;
                     qb[nt][2 * i + e / 2][e & 1] = half2_bits(x[8 * i + e] * s, x[8 * i + e + 4] * s);
                 }
-            const float a = p.scale * kLog2e * down * 16777216.f;
-            sum *= 1.f / 16777216.f;
+            const float a = p.scale * kLog2e * down * (1.f / UNIT);
+            sum *= UNIT;
             int hi = un.hi, lo = 0;
             if (p.causal) hi = min(hi, rq.base + qi + 1);
             if (p.window) lo = rq.base + qi - p.window + 1;
@@ -337,8 +359,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
 #pragma unroll
                 for (int k = 0; k < W; k++) {
                     uint32_t xa[4], xb[4];
-                    spread_codes(wa[k], xa);
-                    spread_codes(wb[k], xb);
+                    spread_codes<NORMAL>(wa[k], xa);
+                    spread_codes<NORMAL>(wb[k], xb);
 #pragma unroll
                     for (int nt = 0; nt < NT; nt++) {
                         mma16816(acc[nt], xa[0], xb[0], xa[1], xb[1], qb[nt][2 * k][0], qb[nt][2 * k][1]);
@@ -374,7 +396,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
                     float top = -INFINITY;
 #pragma unroll
                     for (int x = 0; x < 4; x++) {
-                        float y = (kd[x].x * col_a[nt][e]) * fmaf(-kd[x].y, col_sum[nt][e], s[nt][e][x]);
+                        float y = (kd[x].x * col_a[nt][e]) * fmaf(LESS - kd[x].y, col_sum[nt][e], s[nt][e][x]);
                         if (!inside && (tj[x] >= col_hi[nt][e] || tj[x] < col_lo[nt][e])) y = -INFINITY;
                         s[nt][e][x] = y;
                         top = fmaxf(top, y + vl[x]);
@@ -421,14 +443,14 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
                     if (SPLIT == 2) {  // two parts: the second holds what rounding took from the first
                         const __half hi = __float2half_rn(w[0]);
                         q2 = __halves2half2(hi, __float2half_rn(w[0] - __half2float(hi)));
-                        zero[nt][0] = fmaf(w[0], vd[x].y, zero[nt][0]);
+                        zero[nt][0] = fmaf(w[0], vd[x].y - 8.f, zero[nt][0]);
                     } else {
                         // The zero's share uses the weights as rounded, so that an error of a
                         // weight acts on d (c - z), not on d c and d z apart.
                         q2 = __floats2half2_rn(w[0], w[1]);
                         const float2 f = __half22float2(q2);
-                        zero[nt][0] = fmaf(f.x, vd[x].y, zero[nt][0]);
-                        zero[nt][E - 1] = fmaf(f.y, vd[x].y, zero[nt][E - 1]);
+                        zero[nt][0] = fmaf(f.x, vd[x].y - 8.f, zero[nt][0]);
+                        zero[nt][E - 1] = fmaf(f.y, vd[x].y - 8.f, zero[nt][E - 1]);
                     }
                     pb[nt][x] = transpose8x8(*reinterpret_cast<const uint32_t *>(&q2));
                 }
@@ -458,8 +480,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
 #pragma unroll
                     for (int hw = 0; hw < 2; hw++) {
                         uint32_t x[4], y[4];
-                        spread_codes(prmt(v0[k], v1[k], hw ? 0x7632 : 0x5410), x);
-                        spread_codes(prmt(v2[k], v3[k], hw ? 0x7632 : 0x5410), y);
+                        spread_codes<true>(prmt(v0[k], v1[k], hw ? 0x7632 : 0x5410), x);
+                        spread_codes<true>(prmt(v2[k], v3[k], hw ? 0x7632 : 0x5410), y);
 #pragma unroll
                         for (int nt = 0; nt < NT; nt++) {
                             mma16816(o[k * 4 + hw * 2][nt], x[0], x[1], y[0], y[1], pb[nt][2 * half],
@@ -502,8 +524,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
                 for (int m = 0; m < D / 16; m++) {
                     const float a = SPLIT == 2 ? o[m][nt][0] + o[m][nt][1] : o[m][nt][e];
                     const float b = SPLIT == 2 ? o[m][nt][2] + o[m][nt][3] : o[m][nt][2 + e];
-                    // m-tile m: dimensions 2 m (times 1) and 2 m + 1 (times 16) of this thread's D / 8
-                    *reinterpret_cast<float2 *>(dst + 2 * m) = make_float2(a * 16777216.f, b * 1048576.f);
+                    // m-tile m: dimensions 2 m and 2 m + 1 of this thread's D / 8
+                    *reinterpret_cast<float2 *>(dst + 2 * m) = make_float2(a, b);
                 }
             }
         }
