@@ -18,6 +18,7 @@ struct AttnParams {
     int *error;
     float *part;     // partial sums: [slot][row][D], slot = 2 * CTA + (0: continued, 1: begun)
     float2 *stat;    // [slot][row] {reference exponent, sum of weights}
+    float4 *sums;    // sums over parts of an item's keys (prompts in fp32): [CTA][row tile][D / 4][row]
     int4 *record;    // [slot] {request, item of the request, 1 + the CTA that began the item if
                      // this is its last part else 0, rows}; x < 0: none
 };

@@ -340,3 +340,21 @@ def test_cache_beyond_32_bits():
                        dev(np.array(starts(fresh), np.int32)), dev(np.array([400, 170], np.int32)), 2,
                        T, max(fresh), 128 ** -0.5, True, 0, out, 1024, None, ws)
         assert np.array_equal(host(out), want)
+
+
+@DIMS
+@pytest.mark.parametrize("past,fresh,heads,H", [(4000, 1, 8, 2), (70000, 1, 4, 1), (4000, 3, 8, 2),
+                                                (4000, 40, 8, 2), (9000, 16, 32, 1)])
+def test_flat_sums_in_norm(past, fresh, heads, H, D):
+    """Small scores: every key has about the same weight and the sums nearly cancel, so what each
+    step of a sum loses adds up.  fp32 outputs are right to 2^-17 of their norm, 2^7 times fp32's own
+    rounding (what a sum of 10^4 terms may lose if every rounding is to the same side)."""
+    rng = np.random.default_rng(past + fresh + D)
+    n = past + fresh
+    cache = Cache(rng, [n], H, D, 64, spread=0.1)
+    q = (0.05 * rng.standard_normal((fresh, heads, D))).astype(np.float32)
+    qv, out, _ = attend(cache, q, [0, fresh], [n], heads, F32, fresh)
+    k, v, _, _, has = cache.rows(0, n)
+    want = np.stack([ref.attention(qv[t], k, v, has & (np.arange(n) <= past + t), D ** -0.5)[0]
+                     for t in range(fresh)])
+    assert np.linalg.norm(out - want) <= 2.0 ** -17 * np.linalg.norm(want)
