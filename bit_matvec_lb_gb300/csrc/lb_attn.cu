@@ -23,16 +23,33 @@ namespace lb {
 // second product.  mma.sync serves here: rows are 8 to 16 wide, the products
 // are a third of the issue slots at full bandwidth, and tcgen05 would need the fp16 codes written
 // to shared memory, four times the cache's bytes.
+//
+// Items (request, head, 4 to 16 rows) are cut into equal runs of tiles over the CTAs, three per SM by
+// registers; each warp keeps kStages tiles in flight and its own sums, which the CTA merges.  About
+// 12 us of a call are fixed (launches, requests and pages, first tiles, merge, join); beyond 131k
+// tokens more ones are read at 5.6 TB/s.  Measured (32 / 8 heads of 128): one request of 131k
+// tokens in bf16 38 us (3.8 TB/s), 64 requests of 4096 tokens 67 us in bf16 (4.3 TB/s) and 73 in fp32.
 // ------------------------------------------------------------------------------------------
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
 constexpr int kTile = 32;            // tokens of one warp step (two chunks)
 constexpr int kStages = 4;           // tiles in flight per warp
-constexpr int kWhole = 16;           // items of at most this many tiles are never split
-constexpr int kMinRun = 8;           // tiles per CTA below which no more CTAs are used
+// Items of at most kWhole tiles are never split (64 / 256 requests of 300 tokens: 14 / 37 us, split
+// 20 / 52), nor are those of half a CTA's run or less, up to kWholeMost (256 requests of 700 tokens: 58
+// against 67 us; one of 1000 tokens, whose run is 4 tiles: split 8.2, whole 12.1; 33 requests of up to
+// 1000 tokens and 20 rows, whose run is 31: split 28, those below it whole 30).
+constexpr int kWhole = 16, kWholeMost = 28;
+// Tiles per CTA below which no more CTAs are used (one request of 127 / 2047 / 4095 tokens with 4:
+// 5.1 / 8.5 / 9.9 us, 8: 7.4 / 9.0 / 9.6, 2: 5.2 / 9.5 / 11.3).
+constexpr int kMinRun = 4;
 constexpr int kMaxCtas = 608;
-constexpr int kFewRows = 32;         // query rows per head up to which this file's kernel is used
-constexpr int kFewRequests = 8;      // batches this small run as one launch
+// Query rows per head up to which this file's kernel is used (32 requests of 1000 tokens: 24 rows 39
+// against 58 us on the other, 32 rows 45 against 58, 48 rows 59 against 59; fp32 52 against 74,
+// 65 against 74, 89 against 75).
+constexpr int kFewRows = 32;
+// Batches this small run as one launch (7 decode requests of 300 tokens beside a prompt: 20 us, two
+// launches 29; of 4000 tokens: 59 against 52; 11 of 4000: 77 against 58).
+constexpr int kFewRequests = 8;
 constexpr float kLift = 256.f;       // weights are lifted by 2^8 ...
 constexpr float kSlack = 7.f;        // ... and may pass the reference by 2^7 before it moves
 
@@ -151,6 +168,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
     int4 *record = p.record + 2 * blockIdx.x;
     if (tid < 2) record[tid] = make_int4(-1, 0, 0, 0);
     if (blockIdx.x >= ctas) return;
+    const int unsplit = (int)max((int64_t)kWhole, min((int64_t)kWholeMost, total / (2 * ctas)));
     const int64_t u0 = total * blockIdx.x / ctas, u1 = total * (blockIdx.x + 1) / ctas;
     if (before <= u0 && u0 < before + mine) {
         int64_t at = before;
@@ -182,7 +200,7 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
         const int first = (int)((u - r_begin) - (int64_t)item * un.tiles);  // tile within the item
         int last = (int)min((int64_t)un.tiles, first + (u1 - u));
         u += last - first;
-        if (un.tiles <= kWhole) {  // never split: the CTA in whose run it begins takes it
+        if (un.tiles <= unsplit) {  // never split: the CTA in whose run it begins takes it
             if (first > 0) continue;
             last = un.tiles;
         }
@@ -660,8 +678,8 @@ static int dispatch_decode(const AttnParams &p, int type, int64_t max_q, uint8_t
                            int sms, cudaStream_t st) {
     const int64_t rows = max_q * p.group;
     // Row groups of one product's eight columns: two together take about as long as one after the
-    // other, so three go one by one (bf16, 20 rows of 1000 tokens, 32 requests: 37 against 41 us;
-    // two or four together: 27 against 29 and 44 against 46).
+    // other, so three go one by one (bf16, 20 rows of 1000 tokens, 32 requests: 38 against 42 us;
+    // two or four together: 28 against 30 and 45 against 48).
     const int64_t groups = (rows + (type == LB_OUT_F32 ? 3 : 7)) / (type == LB_OUT_F32 ? 4 : 8);
     const bool one = groups == 1 || groups == 3;
     if (type == LB_OUT_F32)

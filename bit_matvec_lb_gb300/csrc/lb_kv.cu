@@ -8,7 +8,7 @@ namespace lb {
 // Page plan: two prefix sums over the requests (new tokens, new pages), then one independent
 // lookup per token.  Every CTA computes both sums over all requests itself (8 B per request from
 // L2, at most 64 KB) instead of a second launch that would have to wait for them: the step is one
-// launch, bound by its latency.
+// launch, bound by its latency (8 requests 2.3 us, 512 with prompts among them 5.7 us).
 // ------------------------------------------------------------------------------------------
 struct PlanParams {
     const int32_t *past, *fresh, *free_pages, *free_from;
