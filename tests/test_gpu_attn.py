@@ -358,3 +358,26 @@ def test_flat_sums_in_norm(past, fresh, heads, H, D):
     want = np.stack([ref.attention(qv[t], k, v, has & (np.arange(n) <= past + t), D ** -0.5)[0]
                      for t in range(fresh)])
     assert np.linalg.norm(out - want) <= 2.0 ** -17 * np.linalg.norm(want)
+
+
+@TYPES
+@pytest.mark.parametrize("past", [500, 511, 600, 890, 895, 896, 900, 1030])
+def test_many_items_around_the_split(fmt, past):
+    """Many requests of one length (and some shorter): items of 16 to 33 tiles, whole and split."""
+    rng = np.random.default_rng(past)
+    R, H, heads = 128, 2, 4
+    kv_len = [past + 1 - 3 * (r % 5) for r in range(R)]
+    cache = Cache(rng, kv_len, H, 64, 32)
+    q = rng.standard_normal((R, heads, 64)).astype(np.float32)
+    check(cache, q, starts([1] * R), kv_len, heads, fmt, 1, rows=range(0, R, 3))
+
+
+@TYPES
+def test_enough_items_for_whole_ones(fmt):
+    """900 requests of 8 heads, 18 to 28 tiles each: a CTA's run is more than twice an item."""
+    rng = np.random.default_rng(5)
+    R, H, heads = 900, 8, 8
+    kv_len = [545 + (r * 37) % 352 for r in range(R)]
+    cache = Cache(rng, kv_len, H, 64, 64)
+    q = rng.standard_normal((R, heads, 64)).astype(np.float32)
+    check(cache, q, starts([1] * R), kv_len, heads, fmt, 1, rows=range(0, R, 41))
