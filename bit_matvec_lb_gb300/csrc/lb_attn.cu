@@ -26,9 +26,9 @@ namespace lb {
 //
 // Items (request, head, 4 to 16 rows) are cut into equal runs of tiles over the CTAs, three per SM by
 // registers; each warp keeps kStages tiles in flight and its own sums, which the CTA merges.  About
-// 12 us of a call are fixed (launches, requests and pages, first tiles, merge, join); beyond 131k
+// 11 us of a call are fixed (launches, requests and pages, first tiles, merge, join); beyond 131k
 // tokens more ones are read at 5.6 TB/s.  Measured (32 / 8 heads of 128): one request of 131k
-// tokens in bf16 38 us (3.8 TB/s), 64 requests of 4096 tokens 67 us in bf16 (4.3 TB/s) and 73 in fp32.
+// tokens in bf16 36 us (3.9 TB/s), 64 requests of 4096 tokens 67 us in bf16 (4.3 TB/s) and 72 in fp32.
 // ------------------------------------------------------------------------------------------
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -592,55 +592,65 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
 
 // Joins the parts of items that several CTAs shared.  The record of the CTA that took an item's
 // last part names the CTA that began it; the parts in between are the CTAs' between them.  One
-// block per CTA record and row: the parts' weights first, one part per thread, then their sum with
-// D / 4 threads per part.
+// block per CTA record and row, D / 4 threads per part.  Bound by the way from the record to the
+// parts and out again: references, parts and the request are loaded together (64 requests of up to
+// 4096 tokens: 55 us for both kernels; references, sums and parts one after another 63).
 constexpr int kJoin = 128;
 template <int D, typename T, int COLS>
 __global__ void __launch_bounds__(kJoin) attn_join_kernel(const AttnParams p) {
-    constexpr int L = D / 4, GROUPS = kJoin / L;
-    __shared__ float weight[kMaxCtas];
-    __shared__ float red[kJoin / 32], acc[GROUPS][D];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    constexpr int L = D / 4, GROUPS = kJoin / L, AHEAD = 4;
+    __shared__ float acc[GROUPS][D];
+    const int tid = threadIdx.x, lane = tid & 31;
     pdl_wait();
     pdl_launch_dependents();
     const int b = blockIdx.x, c = blockIdx.y;
     const int4 rec = p.record[2 * b];
     if (rec.x < 0 || rec.z == 0 || c >= rec.w) return;
     const int first = rec.z - 1, n = b - first + 1;
-    auto slot_of = [&](int i) { return i == 0 ? 2 * first + 1 : 2 * (first + i); };
+    auto stat_of = [&](int i) { return p.stat[(i == 0 ? 2 * first + 1 : 2 * (first + i)) * COLS + c]; };
+    auto part_of = [&](int i) {
+        const int64_t slot = i == 0 ? 2 * first + 1 : 2 * (first + i);
+        return *reinterpret_cast<const float4 *>(p.part + (slot * COLS + c) * D + tid % L * 4);
+    };
+    auto share = [](float ref, float m) { return ref == -INFINITY ? 0.f : ex2(ref - m); };
+    // All that does not depend on each other is asked for first; every warp reduces the references
+    // and sums for itself.
+    float2 s[AHEAD];
+    float ref[AHEAD];
+    float4 v[AHEAD];
+#pragma unroll
+    for (int k = 0; k < AHEAD; k++) {
+        const int i = k * 32 + lane, j = k * GROUPS + tid / L;
+        s[k] = i < n ? stat_of(i) : make_float2(-INFINITY, 0.f);
+        ref[k] = j < n ? stat_of(j).x : -INFINITY;
+        v[k] = j < n ? part_of(j) : make_float4(0.f, 0.f, 0.f, 0.f);
+    }
+    const Request q = load_request(p, rec.x);
     float m = -INFINITY, l = 0.f;
-    for (int i = tid; i < n; i += kJoin) m = fmaxf(m, p.stat[slot_of(i) * COLS + c].x);
+#pragma unroll
+    for (int k = 0; k < AHEAD; k++) m = fmaxf(m, s[k].x);
+    for (int i = AHEAD * 32 + lane; i < n; i += 32) m = fmaxf(m, stat_of(i).x);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if (lane == 0) red[warp] = m;
-    __syncthreads();
 #pragma unroll
-    for (int w = 0; w < kJoin / 32; w++) m = fmaxf(m, red[w]);
-    for (int i = tid; i < n; i += kJoin) {
-        const float2 s = p.stat[slot_of(i) * COLS + c];
-        const float f = s.x == -INFINITY ? 0.f : ex2(s.x - m);
-        weight[i] = f;
-        l = fmaf(f, s.y, l);
+    for (int k = 0; k < AHEAD; k++) l = fmaf(share(s[k].x, m), s[k].y, l);
+    for (int i = AHEAD * 32 + lane; i < n; i += 32) {
+        const float2 t = stat_of(i);
+        l = fmaf(share(t.x, m), t.y, l);
     }
-    __syncthreads();
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) l += __shfl_xor_sync(0xffffffffu, l, o);
-    if (lane == 0) red[warp] = l;
     float x[4] = {};
+    auto add = [&](float f, const float4 &y) {
+        x[0] = fmaf(f, y.x, x[0]), x[1] = fmaf(f, y.y, x[1]);
+        x[2] = fmaf(f, y.z, x[2]), x[3] = fmaf(f, y.w, x[3]);
+    };
+#pragma unroll
+    for (int k = 0; k < AHEAD; k++) add(share(ref[k], m), v[k]);
 #pragma unroll 4
-    for (int i = tid / L; i < n; i += GROUPS) {
-        const float4 v = *reinterpret_cast<const float4 *>(
-            p.part + ((int64_t)slot_of(i) * COLS + c) * D + tid % L * 4);
-        const float f = weight[i];
-        x[0] = fmaf(f, v.x, x[0]), x[1] = fmaf(f, v.y, x[1]);
-        x[2] = fmaf(f, v.z, x[2]), x[3] = fmaf(f, v.w, x[3]);
-    }
+    for (int i = AHEAD * GROUPS + tid / L; i < n; i += GROUPS) add(share(stat_of(i).x, m), part_of(i));
     *reinterpret_cast<float4 *>(&acc[tid / L][tid % L * 4]) = make_float4(x[0], x[1], x[2], x[3]);
     __syncthreads();
-    l = 0.f;
-#pragma unroll
-    for (int w = 0; w < kJoin / 32; w++) l += red[w];
-    const Request q = load_request(p, rec.x);
     const int groups = (q.n * p.group + COLS - 1) / COLS;
     const int cc = rec.y % groups * COLS + c, head = rec.y / groups * p.group + cc % p.group;
     const int64_t t = q.q0 + cc / p.group;
