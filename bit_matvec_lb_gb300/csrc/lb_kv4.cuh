@@ -35,8 +35,6 @@ inline bool aligned_to(const void *p, uintptr_t n) {
     return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
-__device__ __forceinline__ float bf16_bits_to_float(uint32_t h) { return __uint_as_float(h << 16); }
-
 // Eight consecutive values of a row as fp32.
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
     const float4 a = *reinterpret_cast<const float4 *>(p);
