@@ -434,6 +434,10 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
 
             for (int j = 0; j < n; j++, gt++, cw++) {
                 const int slot = gt % kScales, j0 = (it.x.t0 + it.first + j) * kKeys;
+                // The scores first: a warp that had no rows in the items before counted their tiles
+                // without waiting, and could take the slot's phase before last for this one.
+                wait(bar.s_full[w][cw & 1], cw >> 1);
+                tc_fence_after();
                 wait(bar.sc_full[slot], gt / kScales);
                 const uint32_t ok = sc_valid[slot], S = S0 + kKeys * (cw & 1);
                 const bool inside = ok == 0xFu && j0 >= all_lo && j0 + kKeys <= all_hi;
@@ -442,8 +446,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 for (int e = 0; e < 4; e++) vmax = fmaxf(vmax, sc_max[slot][e]);
                 const ulonglong2 *kd = reinterpret_cast<const ulonglong2 *>(kd_s + slot * kKeys);
                 const ulonglong2 *vd = reinterpret_cast<const ulonglong2 *>(vd_s + slot * kKeys);
-                wait(bar.s_full[w][cw & 1], cw >> 1);
-                tc_fence_after();
 
                 // Scores of 16 keys (c), plus nb, as pairs, from the raw products in s.
                 auto scores = [&](int c, uint64_t (&s)[8], uint64_t nb) {

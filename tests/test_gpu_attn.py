@@ -381,3 +381,19 @@ def test_enough_items_for_whole_ones(fmt):
     cache = Cache(rng, kv_len, H, 64, 64)
     q = rng.standard_normal((R, heads, 64)).astype(np.float32)
     check(cache, q, starts([1] * R), kv_len, heads, fmt, 1, rows=range(0, R, 41))
+
+
+@TYPES
+@DIMS
+@pytest.mark.parametrize("past,fresh,heads,H", [(41, 646, 20, 5), (0, 1340, 10, 5), (26, 300, 16, 8)])
+def test_whole_row_tiles_after_half_items(fmt, D, past, fresh, heads, H):
+    """Requests whose last rows fill one row tile of two, before others: a CTA goes from half items
+    to whole ones.  All requests' second row tiles and last rows."""
+    rng = np.random.default_rng(fresh)
+    kv_len = [past + fresh] * 3
+    cache = Cache(rng, kv_len, H, D, 64)
+    q = rng.standard_normal((3 * fresh, heads, D)).astype(np.float32)
+    G = heads // H
+    rows = [r * fresh + t for r in range(3) for t in
+            [*range(0, 256 // G, 7), *range(256 // G, fresh, 61), fresh - 1]]
+    check(cache, q, starts([fresh] * 3), kv_len, heads, fmt, fresh, rows=set(rows))
