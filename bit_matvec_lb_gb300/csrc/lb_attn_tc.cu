@@ -18,7 +18,7 @@ namespace lb {
 // one that copies cache chunks in.  Tensor memory holds S twice for each row tile (4 x 64 columns)
 // and O (2 x 128); P overwrites S.  The operations are issued QK0(j+1) PV0(j) QK1(j+1) PV1(j), so a
 // row tile's next scores are there when it is done with the present ones (128 keys and S once: 0.72
-// against 0.67 ms for a bf16 prompt of 8192 tokens with 32 / 8 heads, 825 TFLOP/s).  What bounds it are the
+// against 0.66 ms for a bf16 prompt of 8192 tokens with 32 / 8 heads, 840 TFLOP/s).  What bounds it are the
 // products and their hand-overs: 0.57 ms are left without softmax and expansion of the codes.
 // Score products read both operands from shared memory, 72 cycles for 128 x 64 x 16 where the
 // multiplications take 32 and one with its first operand in tensor memory 42.
