@@ -544,6 +544,9 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                         nb = minus_base(ref);
                         l *= f;
                         const __half2 fh = __float2half2_rn(f);
+                        // Loads are not ordered behind this thread's own stores without a wait: the
+                        // earlier weights must have arrived before they are read back.
+                        tmem_wait_st();
 #pragma unroll 1
                         for (int c = 0; c < 2 * c2; c++) {
                             tmem_ld16_start(S + 16 * c, t0);

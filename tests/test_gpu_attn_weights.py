@@ -1,0 +1,32 @@
+"""Attention where the weights' sizes matter: errors in norm against the formula in 64 bits, with the
+tolerance that attn_norms.py derives."""
+import numpy as np
+import pytest
+
+import bit_matvec_lb_gb300 as lb
+from attn_norms import Crafted, check_norms, queries
+
+pytestmark = pytest.mark.gpu
+
+F32, BF16 = lb.OUT_F32, lb.OUT_BF16
+SHARE = {F32: 2.0 ** -10, BF16: 2.0 ** -5}  # the tolerance's share of an output's norm at most
+
+TYPES = pytest.mark.parametrize("fmt", [F32, BF16])
+DIMS = pytest.mark.parametrize("D", [64, 128])
+
+
+@TYPES
+@DIMS
+@pytest.mark.parametrize("risen", [(1,), (1, 2, 7), (6, 8, 12)])
+def test_scores_rise_within_a_tile(fmt, D, risen):
+    """The second 32 keys of some 64 score 6 above all before them, so that weights of the first 32,
+    written under the old reference, must be scaled."""
+    rng = np.random.default_rng(D + sum(risen))
+    score = np.zeros(900)
+    for i, tile in enumerate(risen):
+        score[64 * tile + 32:] = 6 * i
+        score[64 * tile + 32:64 * tile + 64] = 6 * (i + 1)
+    score += 0.05 * rng.standard_normal(900)
+    cache = Crafted(rng, score, np.full(900, 0.25), 1, D, 64)
+    q = queries(rng, 66, 4, D)
+    check_norms(cache, q, [0, 66], [900], 4, fmt, 66, SHARE[fmt], rows={0, 1, 31, 32, 63, 64, 65})
