@@ -23,10 +23,12 @@ namespace lb {
 // Score products read both operands from shared memory, 72 cycles for 128 x 64 x 16 where the
 // multiplications take 32 and one with its first operand in tensor memory 42.
 //
-// One pass over the scores: the reference is the first tile's maximum and moves only when it must,
-// when the weights of 32 keys could leave fp16's range.  Then those 32 scores are read again for
-// their maximum, and what is already there under the old reference (the tile's earlier weights, O
-// and the sum) is scaled by a power of two.
+// One pass over the scores: the reference is the first tile's largest weight, value scale and all
+// (the largest score and the largest scale taken apart may be different keys', and weights pushed down
+// by a scale that has no part in the row lose bits), and moves only when it must, when the weights of
+// 32 keys could leave fp16's range by their sum and the tile's largest scale.  Then those 32 scores
+// are read again for their largest weight, and if that is above the reference, what is already there
+// under the old one (the tile's earlier weights, O and the sum) is scaled by a power of two.
 //
 // The tensor cores cut, downwards, what lies below an accumulator's last place, once for every 16
 // keys and part: over a long item that is far more than fp32 rounding.  With fp32 tensors O
@@ -63,8 +65,8 @@ struct Prompt {
     static constexpr int oK = oQ + 2 * SPLIT * kQ;     // [kBuf]
     static constexpr int oV = oK + kBuf * kTileB;
     static constexpr int oRaw = oV + kBuf * kTileB;    // [kPieces]
-    static constexpr int oScale = oRaw + kPieces * kRaw;  // [kScales][2][kKeys] floats
-    static constexpr int kSmem = oScale + kScales * 2 * kKeys * 4;
+    static constexpr int oScale = oRaw + kPieces * kRaw;  // [3][kScales][kKeys] floats
+    static constexpr int kSmem = oScale + kScales * 3 * kKeys * 4;
 };
 
 struct TcBars {
@@ -348,7 +350,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
         __syncwarp();
     };
     float *kd_s = reinterpret_cast<float *>(smem + C::oScale);   // [kScales][kKeys]
-    float *vd_s = kd_s + kScales * kKeys;
+    float *vd_s = kd_s + kScales * kKeys, *vl_s = vd_s + kScales * kKeys;  // vl_s: powers of two
     uint32_t gt = 0;  // tiles so far, over all items
 
     if (warp < 8) {
@@ -446,14 +448,16 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                 for (int e = 0; e < 4; e++) vmax = fmaxf(vmax, sc_max[slot][e]);
                 const ulonglong2 *kd = reinterpret_cast<const ulonglong2 *>(kd_s + slot * kKeys);
                 const ulonglong2 *vd = reinterpret_cast<const ulonglong2 *>(vd_s + slot * kKeys);
+                const ulonglong2 *vl = vd + kScales * kKeys / 4;
 
-                // Scores of 16 keys (c), plus nb, as pairs, from the raw products in s.
-                auto scores = [&](int c, uint64_t (&s)[8], uint64_t nb) {
+                // Scores of 16 keys (c), plus more(e) for each four of them, as pairs, from the raw
+                // products in s.
+                auto scores = [&](int c, uint64_t (&s)[8], auto more) {
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
-                        const ulonglong2 k = kd[4 * c + e];
-                        s[2 * e] = fma2(mul2(s[2 * e], k.x), a2, nb);
-                        s[2 * e + 1] = fma2(mul2(s[2 * e + 1], k.y), a2, nb);
+                        const ulonglong2 k = kd[4 * c + e], m = more(4 * c + e);
+                        s[2 * e] = fma2(mul2(s[2 * e], k.x), a2, m.x);
+                        s[2 * e + 1] = fma2(mul2(s[2 * e + 1], k.y), a2, m.y);
                     }
                     if (!inside) {
                         const bool there = ok >> c & 1;
@@ -480,10 +484,23 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                                 half2_bits(lo_of(wv) - __low2float(h2), hi_of(wv) - __high2float(h2));
                     }
                 };
-                const float vlog = scale_log2(vmax * (1.f / kTcLift));
+                // What is added to the scores: -ref, the value scales as powers of two (weights'
+                // sizes), or both.
+                uint64_t nb = 0;
+                auto less = [&](int) { return make_ulonglong2(nb, nb); };
+                auto sizes = [&](int e) { return vl[e]; };
+                auto sizes_less = [&](int e) {
+                    const ulonglong2 v = vl[e];
+                    return make_ulonglong2(add2(v.x, nb), add2(v.y, nb));
+                };
+                auto largest = [&](const uint64_t(&s)[8], float m) {
+#pragma unroll
+                    for (int e = 0; e < 8; e++) m = fmaxf(m, fmaxf(lo_of(s[e]), hi_of(s[e])));
+                    return m;
+                };
                 uint32_t r0[16], r1[16];
                 tmem_ld16_start(S, r0);
-                if (j == 0) {  // the first reference: this tile's maximum
+                if (j == 0) {  // the first reference: this tile's largest weight
                     float m = -INFINITY;
 #pragma unroll 1
                     for (int c = 0; c < 4; c++) {
@@ -491,15 +508,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                         uint64_t s[8];
                         pairs_of(r0, s);
                         tmem_ld16_start(S + 16 * ((c + 1) & 3), r0);
-                        scores(c, s, 0);
-#pragma unroll
-                        for (int e = 0; e < 8; e++) m = fmaxf(m, fmaxf(lo_of(s[e]), hi_of(s[e])));
+                        scores(c, s, sizes);
+                        m = largest(s, m);
                     }
-                    ref = m == -INFINITY ? m : m + vlog;  // the last load, of chunk 0, is in flight
+                    ref = m;  // the last load, of chunk 0, is in flight
                 }
                 // A chunk's weights as fp16 (and what rounding took from them), 8 columns each, over
                 // its 16 scores: P of chunk c lies at columns 16 c.
-                uint64_t nb = minus_base(ref);
+                nb = minus_base(ref);
 #pragma unroll 1  // (unrolled, the instruction cache becomes the limit)
                 for (int c2 = 0; c2 < kKeys / 32; c2++) {
                     uint32_t ph[2][8 * SPLIT];
@@ -512,84 +528,90 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                         if (c < kKeys / 16 - 1) tmem_ld16_start(S + 16 * (c + 1), k ? r0 : r1);
                         uint64_t s[8];
                         pairs_of(r, s);
-                        scores(c, s, nb);
+                        scores(c, s, less);
                         weights(c, s, sum, ph[k]);
                     }
                     float part = lo_of(sum) + hi_of(sum);
+                    bool keep = true;  // the weights just computed
                     if (__any_sync(0xffffffffu, ref == -INFINITY || !(part * vmax <= kTcMost))) {
                         // (r0 holds the next chunk's scores, or is in flight: it stays.)
+                        uint32_t t0[16];
+                        uint64_t s[8];
                         float m = -INFINITY;
-                        uint32_t t0[16], t1[16];
-                        tmem_ld16_start(S + 32 * c2, t0);
-                        tmem_ld16_start(S + 32 * c2 + 16, t1);
-                        tmem_ld16_wait(t0);
-                        tmem_ld16_wait(t1);
-                        uint64_t s0[8], s1[8];
-                        pairs_of(t0, s0);
-                        pairs_of(t1, s1);
-                        scores(2 * c2, s0, nb);
-                        scores(2 * c2 + 1, s1, nb);
-#pragma unroll
-                        for (int e = 0; e < 8; e++) {
-                            m = fmaxf(m, fmaxf(lo_of(s0[e]), hi_of(s0[e])));
-                            m = fmaxf(m, fmaxf(lo_of(s1[e]), hi_of(s1[e])));
+#pragma unroll 1
+                        for (int c = 2 * c2; c < 2 * c2 + 2; c++) {
+                            tmem_ld16_start(S + 16 * c, t0);
+                            tmem_ld16_wait(t0);
+                            pairs_of(t0, s);
+                            scores(c, s, sizes_less);
+                            m = largest(s, m);
                         }
                         float f = 1.f, d = 0.f;  // 2^-d, d a whole number
                         if (ref == -INFINITY) {
-                            if (m > -INFINITY) d = m + vlog, ref = d;  // nothing is there to scale
-                        } else if (m + vlog > 0.f) {
-                            d = ceilf(m + vlog), ref += d;
+                            if (m > -INFINITY) d = ref = m;  // nothing is there to scale
+                        } else if (m > 0.f) {
+                            d = ceilf(m), ref += d;
                             f = ex2(-d);
                         }
-                        nb = minus_base(ref);
-                        l *= f;
-                        const __half2 fh = __float2half2_rn(f);
-                        // Loads are not ordered behind this thread's own stores without a wait: the
-                        // earlier weights must have arrived before they are read back.
-                        tmem_wait_st();
+                        // (Else the bound was too wide: a large value scale beside a small weight.)
+                        if (__any_sync(0xffffffffu, d != 0.f)) {
+                            nb = minus_base(ref);
+                            l *= f;
+                            const __half2 fh = __float2half2_rn(f);
+                            // Loads are not ordered behind this thread's own stores without a wait: the
+                            // earlier weights must have arrived before they are read back.
+                            tmem_wait_st();
 #pragma unroll 1
-                        for (int c = 0; c < 2 * c2; c++) {
-                            tmem_ld16_start(S + 16 * c, t0);
-                            tmem_ld16_wait(t0);
-#pragma unroll
-                            for (int e = 0; e < 8 * SPLIT; e++) {
-                                const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&t0[e]), fh);
-                                t0[e] = *reinterpret_cast<const uint32_t *>(&v);
-                            }
-                            tmem_st16(S + 16 * c, t0);
-                        }
-                        if (j > 0) {
-                            wait(bar.o_full[w][(cw - 1) & 1], (cw - 1) >> 1);
-                            tc_fence_after();
-#pragma unroll 1
-                            for (int c = 0; c < D; c += 16) {
-                                tmem_ld16_start(O + c, t0);
+                            for (int c = 0; c < 2 * c2; c++) {
+                                tmem_ld16_start(S + 16 * c, t0);
                                 tmem_ld16_wait(t0);
 #pragma unroll
-                                for (int e = 0; e < 16; e++)
-                                    t0[e] = __float_as_uint(__uint_as_float(t0[e]) * f);
-                                tmem_st16(O + c, t0);
+                                for (int e = 0; e < 8 * SPLIT; e++) {
+                                    const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&t0[e]), fh);
+                                    t0[e] = *reinterpret_cast<const uint32_t *>(&v);
+                                }
+                                tmem_st16(S + 16 * c, t0);
                             }
-                            if (SPLIT == 2 && j > kFlush) {
+                            if (j > 0) {
+                                wait(bar.o_full[w][(cw - 1) & 1], (cw - 1) >> 1);
+                                tc_fence_after();
 #pragma unroll 1
-                                for (int c = 0; c < D / 4; c++) {
-                                    const float4 v = __ldcg(sums + c * kRows);
-                                    __stcg(sums + c * kRows, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+                                for (int c = 0; c < D; c += 16) {
+                                    tmem_ld16_start(O + c, t0);
+                                    tmem_ld16_wait(t0);
+#pragma unroll
+                                    for (int e = 0; e < 16; e++)
+                                        t0[e] = __float_as_uint(__uint_as_float(t0[e]) * f);
+                                    tmem_st16(O + c, t0);
+                                }
+                                if (SPLIT == 2 && j > kFlush) {
+#pragma unroll 1
+                                    for (int c = 0; c < D / 4; c++) {
+                                        const float4 v = __ldcg(sums + c * kRows);
+                                        __stcg(sums + c * kRows, make_float4(v.x * f, v.y * f, v.z * f, v.w * f));
+                                    }
                                 }
                             }
+                            tmem_wait_st();
+                            sum = 0;
+#pragma unroll 1
+                            for (int c = 2 * c2; c < 2 * c2 + 2; c++) {
+                                uint32_t pw[8 * SPLIT];
+                                tmem_ld16_start(S + 16 * c, t0);
+                                tmem_ld16_wait(t0);
+                                pairs_of(t0, s);
+                                scores(c, s, less);
+                                weights(c, s, sum, pw);
+                                tmem_st_weights(S + 16 * c, pw);
+                            }
+                            part = lo_of(sum) + hi_of(sum);
+                            keep = false;
                         }
-                        tmem_wait_st();
-                        sum = 0;
-                        const uint64_t nd = pair_of(-d, -d);
-#pragma unroll
-                        for (int e = 0; e < 8; e++) s0[e] = add2(s0[e], nd), s1[e] = add2(s1[e], nd);
-                        weights(2 * c2, s0, sum, ph[0]);
-                        weights(2 * c2 + 1, s1, sum, ph[1]);
-                        part = lo_of(sum) + hi_of(sum);
                     }
                     l += part;
 #pragma unroll
-                    for (int k = 0; k < 2; k++) tmem_st_weights(S + 32 * c2 + 16 * k, ph[k]);
+                    for (int k = 0; k < 2; k++)
+                        if (keep) tmem_st_weights(S + 32 * c2 + 16 * k, ph[k]);
                 }
                 if (SPLIT == 2 && j > 0 && j % kFlush == 0) {
                     wait(bar.o_full[w][(cw - 1) & 1], (cw - 1) >> 1);
@@ -708,7 +730,7 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                         const float d = t < live ? __low2float(pairs[lane]) : 0.f;
                         const int at = slot * kKeys + q * 16 + t;
                         if (lane < 16) kd_s[at] = d;
-                        else vd_s[at] = d * kTcLift;
+                        else vd_s[at] = d * kTcLift, vl_s[at] = scale_log2(d);
                         float m = lane < 16 ? 0.f : d * kTcLift;
 #pragma unroll
                         for (int o = 8; o > 0; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));

@@ -30,3 +30,37 @@ def test_scores_rise_within_a_tile(fmt, D, risen):
     cache = Crafted(rng, score, np.full(900, 0.25), 1, D, 64)
     q = queries(rng, 66, 4, D)
     check_norms(cache, q, [0, 66], [900], 4, fmt, 66, SHARE[fmt], rows={0, 1, 31, 32, 63, 64, 65})
+
+
+@TYPES
+@DIMS
+@pytest.mark.parametrize("fresh", [1, 40])
+@pytest.mark.parametrize("ratio", [7, 10, 14, 18, 22])
+def test_large_values_without_weight(fmt, D, fresh, ratio):
+    """One key whose values are 2^ratio times the others' and whose score is 25 below theirs: it has
+    no part in the outputs, and must not cost the others bits."""
+    rng = np.random.default_rng(D + ratio)
+    score = 0.3 * rng.standard_normal(63 + fresh)
+    score[5] = -25
+    vd = np.full(63 + fresh, 2.0 ** (11 - ratio))
+    vd[5] = 2.0 ** 11
+    cache = Crafted(rng, score, vd, 1, D, 64)
+    q = queries(rng, fresh, 4, D)
+    check_norms(cache, q, [0, fresh], [63 + fresh], 4, fmt, fresh, SHARE[fmt])
+
+
+@TYPES
+@DIMS
+@pytest.mark.parametrize("fresh", [1, 40])
+def test_one_key_holds_the_weight(fmt, D, fresh):
+    """One key with nearly all of the weight and values 2^20 times smaller than the others' (whose
+    sum is as large as its value): their weights must not lose their bits beside it."""
+    rng = np.random.default_rng(D)
+    n = 2000 + fresh
+    score = 0.3 * rng.standard_normal(n)
+    score[0] = 17
+    vd = np.full(n, 2.0 ** 6)
+    vd[0] = 2.0 ** -14
+    cache = Crafted(rng, score, vd, 1, D, 128)
+    q = queries(rng, fresh, 4, D)
+    check_norms(cache, q, [0, fresh], [n], 4, fmt, fresh, SHARE[fmt] * (16 if fmt == BF16 else 1))
