@@ -557,7 +557,6 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                         if (__any_sync(0xffffffffu, d != 0.f)) {
                             nb = minus_base(ref);
                             l *= f;
-                            const __half2 fh = __float2half2_rn(f);
                             // Loads are not ordered behind this thread's own stores without a wait: the
                             // earlier weights must have arrived before they are read back.
                             tmem_wait_st();
@@ -567,8 +566,8 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
                                 tmem_ld16_wait(t0);
 #pragma unroll
                                 for (int e = 0; e < 8 * SPLIT; e++) {
-                                    const __half2 v = __hmul2(*reinterpret_cast<__half2 *>(&t0[e]), fh);
-                                    t0[e] = *reinterpret_cast<const uint32_t *>(&v);
+                                    const float2 v = __half22float2(*reinterpret_cast<__half2 *>(&t0[e]));
+                                    t0[e] = half2_bits(v.x * f, v.y * f);  // (f may be below fp16)
                                 }
                                 tmem_st16(S + 16 * c, t0);
                             }

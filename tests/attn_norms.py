@@ -48,9 +48,9 @@ def signs(D):
     return np.where(np.arange(D) * 7 % 5 < 2, -1, 1)
 
 
-def queries(rng, T, heads, D):
-    """Queries near signs(D): scores differ by a few hundredths of themselves from row to row."""
-    return (signs(D) * (1 + 0.1 * rng.standard_normal((T, heads, D)))).astype(np.float32)
+def queries(rng, T, heads, D, noise=0.1):
+    """Queries near signs(D): scores differ by about noise / sqrt(D) of themselves from row to row."""
+    return (signs(D) * (1 + noise * rng.standard_normal((T, heads, D)))).astype(np.float32)
 
 
 def check_norms(cache, q, q_start, kv_len, heads, fmt, max_q, share, causal=True, window=0, rows=None):

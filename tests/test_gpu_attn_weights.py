@@ -64,3 +64,15 @@ def test_one_key_holds_the_weight(fmt, D, fresh):
     cache = Crafted(rng, score, vd, 1, D, 128)
     q = queries(rng, fresh, 4, D)
     check_norms(cache, q, [0, fresh], [n], 4, fmt, fresh, SHARE[fmt] * (16 if fmt == BF16 else 1))
+
+
+@DIMS
+def test_weights_scaled_by_less_than_fp16_holds(D):
+    """A weight 2^11.5 above the reference, then one 2^24.6 above it in the same 64 keys: the first is
+    scaled by 2^-25, below fp16's numbers, and is still 2^-13 of the second."""
+    rng = np.random.default_rng(D)
+    score = np.zeros(192)
+    score[70], score[100] = 11.5 * np.log(2), 24.6 * np.log(2)
+    cache = Crafted(rng, score, np.full(192, 0.25), 1, D, 64)
+    q = queries(rng, 40, 4, D, 0.005)
+    check_norms(cache, q, [0, 40], [192], 4, F32, 40, SHARE[F32])
