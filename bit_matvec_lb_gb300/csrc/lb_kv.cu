@@ -296,6 +296,17 @@ LB_EXPORT int lb_kv_plan(const int32_t *past, const int32_t *fresh, int64_t R,
         return LB_ERR_SHAPE;
     DeviceInfo di;
     if (int e = current_device_info(&di)) return e;
+    // The lengths and the free list are read by every CTA, at any time: none of them may be an output.
+    struct {
+        const void *p;
+        size_t bytes;
+    } const in[] = {{past, (size_t)R * 4}, {fresh, (size_t)R * 4}, {free_pages, (size_t)n_free * 4},
+                    {free_from_opt, 4}},
+      written[] = {{block_table, (size_t)R * table_width * 4}, {q_start, (size_t)(R + 1) * 4},
+                   {kv_len, (size_t)R * 4}, {position, (size_t)T * 4}, {slot, (size_t)T * 8}, {counts, 8}};
+    for (const auto &a : in)
+        for (const auto &b : written)
+            if (overlap(a.p, a.bytes, b.p, b.bytes)) return LB_ERR_SHAPE;
     const PlanParams p{past,    fresh,  free_pages, free_from_opt, block_table, q_start, kv_len,
                        position, counts, slot,       table_width,   T,           n_free, (int)R,
                        shift};

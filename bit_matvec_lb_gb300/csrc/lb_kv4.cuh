@@ -35,6 +35,11 @@ inline bool aligned_to(const void *p, uintptr_t n) {
     return (reinterpret_cast<uintptr_t>(p) & (n - 1)) == 0;
 }
 
+inline bool overlap(const void *a, size_t a_bytes, const void *b, size_t b_bytes) {
+    const uintptr_t x = reinterpret_cast<uintptr_t>(a), y = reinterpret_cast<uintptr_t>(b);
+    return a && b && a_bytes && b_bytes && x < y + b_bytes && y < x + a_bytes;
+}
+
 // Eight consecutive values of a row as fp32.
 __device__ __forceinline__ void load8(const float *p, float (&x)[8]) {
     const float4 a = *reinterpret_cast<const float4 *>(p);

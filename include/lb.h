@@ -422,7 +422,9 @@ int lb_gemm_q2_0_g64_noalloc(const uint8_t *codes, const uint16_t *scales, const
  *   past, fresh : [R] int32.   free_pages : [n_free] int32.   block_table : [R][table_width]
  *   int32, read and written.   q_start : [R + 1] int32.   kv_len : [R] int32.
  *   position : [T] int32, slot : [T] int64; entries past q_start[R] are set to -1.
- *   counts : [2] int32, not the memory that free_from_opt points to.
+ *   counts : [2] int32.
+ * No output may overlap past, fresh, free_pages or free_from_opt (LB_ERR_SHAPE): lengths that
+ * advance in place need a second buffer, as counts does.
  * Where free_pages runs out or a row of the table is full, the entries without a page are -1
  * and the slots of their tokens are -1 (lb_kv4_append skips them and lb_attn_kv4 does not see
  * them); counts[1] > n_free tells of the first case, counts[0] > T that tokens were left out.
