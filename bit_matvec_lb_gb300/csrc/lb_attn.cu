@@ -316,9 +316,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
                 }
             const float a = p.scale * kLog2e * down * (1.f / UNIT);
             sum *= UNIT;
-            int hi = un.hi, lo = 0;
+            int hi = un.hi;
             if (p.causal) hi = min(hi, rq.base + qi + 1);
-            if (p.window) lo = rq.base + qi - p.window + 1;
+            const int lo = window_start(p, rq, qi);
 #pragma unroll
             for (int e = 0; e < 2; e++) {
                 const int from = (2 * tg + e) * 4;
@@ -329,9 +329,9 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
             }
         }
         // Tokens that every column sees: no mask in a tile inside them.
-        int all_hi = un.hi, all_lo = 0;
+        int all_hi = un.hi;
         if (p.causal) all_hi = min(all_hi, rq.base + col0 / p.group + 1);
-        if (p.window) all_lo = rq.base + (col0 + ncol - 1) / p.group - p.window + 1;
+        const int all_lo = window_start(p, rq, (col0 + ncol - 1) / p.group);
 
         float o[D / 16][NT][4];
         float ref[NT][2], base[NT][2], sum[NT][2], zero[NT][2];

@@ -42,17 +42,23 @@ __device__ __forceinline__ Request load_request(const AttnParams &p, int r) {
     q.n = max(min(p.q_start[r + 1], T) - q.q0, 0);
     const int len = p.kv_len[r];
     q.len = (int)min((int64_t)max(len, 0), p.width << p.shift);
-    q.base = len - q.n;
+    q.base = max(len, 0) - q.n;
     const int64_t rows = (int64_t)q.n * p.group;
     if (rows <= p.rows_lo || rows > p.rows_hi) q.n = 0;
     return q;
+}
+
+// First token that the window shows to query i, 0 without one.  (In 64 bits: a request may have more
+// queries than tokens, and the window may be as long as "no limit" is written.)
+__device__ __forceinline__ int window_start(const AttnParams &p, const Request &q, int i) {
+    return p.window ? (int)max((int64_t)q.base + i - p.window + 1, (int64_t)0) : 0;
 }
 
 // Tokens [lo, hi) that the queries i0 .. i1 - 1 of a request can see among them.
 __device__ __forceinline__ void visible_range(const AttnParams &p, const Request &q, int i0, int i1,
                                               int &lo, int &hi) {
     hi = p.causal ? max(0, min(q.len, q.base + i1)) : q.len;
-    lo = p.window ? min(max(0, q.base + i0 - p.window + 1), hi) : 0;
+    lo = min(window_start(p, q, i0), hi);
 }
 
 // Orders this thread's ordinary shared-memory accesses before later bulk copies into the same bytes.

@@ -423,15 +423,13 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
             const uint64_t a2 = pair_of(a, a);
             // Keys this row sees, and those all rows of the tile see.
             const int qi = (row0 + min(row, ncol - 1)) / p.group;
-            int hi = it.x.hi, lo = 0, all_hi = hi, all_lo = 0;
+            int hi = it.x.hi, all_hi = hi;
             if (p.causal) {
                 hi = min(hi, it.q.base + qi + 1);
                 all_hi = min(all_hi, it.q.base + row0 / p.group + 1);
             }
-            if (p.window) {
-                lo = it.q.base + qi - p.window + 1;
-                all_lo = it.q.base + (row0 + ncol - 1) / p.group - p.window + 1;
-            }
+            const int lo = window_start(p, it.q, qi);
+            const int all_lo = window_start(p, it.q, (row0 + ncol - 1) / p.group);
             float ref = -INFINITY, l = 0.f;
 
             for (int j = 0; j < n; j++, gt++, cw++) {
