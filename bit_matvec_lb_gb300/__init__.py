@@ -539,7 +539,7 @@ def lb_logits_adjust(logits, type: int, stride: int, out, out_stride: int, B: in
     """Penalties, biases and grammar masks on logits [B][V] (OUT_F32 or OUT_BF16, rows strided);
     out may be logits.  What is None is left out; mask_rows defaults to mask's rows."""
     if mask is not None and mask_rows is None:
-        mask_rows = mask.numel() // int(mask_stride)
+        mask_rows = mask.numel() // int(mask_stride) if mask_stride > 0 else 0
     rules = lb_logit_rules(
         _ptr(prompt_ids), _ptr(prompt_start), _ptr(output_ids), _ptr(output_start),
         _ptr(repetition), _ptr(presence), _ptr(frequency), _ptr(bias_ids), _ptr(bias_values),
