@@ -5,6 +5,7 @@ import pytest
 
 import bit_matvec_lb_gb300 as lb
 from attn_norms import Crafted, check_norms, queries
+from test_gpu_attn import Cache, attend, starts
 
 pytestmark = pytest.mark.gpu
 
@@ -76,3 +77,44 @@ def test_weights_scaled_by_less_than_fp16_holds(D):
     cache = Crafted(rng, score, np.full(192, 0.25), 1, D, 64)
     q = queries(rng, 40, 4, D, 0.005)
     check_norms(cache, q, [0, 40], [192], 4, F32, 40, SHARE[F32])
+
+
+@TYPES
+@DIMS
+@pytest.mark.parametrize("fresh", [1, 2, 8, 40])
+@pytest.mark.parametrize("n", [60, 200])
+def test_ordinary_rows(fmt, D, fresh, n):
+    """Value scales that differ by e^1 from key to key and scores of about 1: with fp32 tensors the
+    tolerance is below what queries or weights of one fp16 part would be off by (test_attn_norms.py)."""
+    rng = np.random.default_rng(n + fresh + D)
+    score = rng.standard_normal(n)
+    cache = Crafted(rng, score, 0.25 * np.exp(rng.standard_normal(n)), 2, D, 32)
+    q = queries(rng, fresh, 8, D)
+    rows = {0, fresh // 2, fresh - 1}
+    check_norms(cache, q, [0, fresh], [n], 8, fmt, fresh, 2.0 ** -13 if fmt == F32 else 2.0 ** -6, rows=rows)
+
+
+@TYPES
+@DIMS
+@pytest.mark.parametrize("heads,H,fresh", [
+    (8, 2, [1, 120, 1, 8, 9, 0, 1, 2, 300, 1, 1, 70, 1]),   # 8 queries are 32 rows, 9 are 36
+    (8, 2, [1, 2, 1, 8, 1, 0, 1, 2, 3, 1, 1, 7, 1]),        # no request of many rows
+    (8, 2, [40, 50, 9, 10, 33, 200, 64, 65, 32, 31, 30]),   # no request of few
+    (40, 1, [1, 1, 1, 2, 1, 1, 1, 5, 1, 1])])               # one query is 40 rows
+def test_mixed_batch_in_two_launches(fmt, D, heads, H, fresh):
+    """More than eight requests and a bound of many rows: requests of few rows go to one kernel, the
+    others to the other, with one workspace.  Contexts long enough that both split their items; one
+    request with no token at all, one with fewer tokens than queries."""
+    rng = np.random.default_rng(len(fresh) + heads + D)
+    past = ([700, 0, 2000, 33, 500, 90, 0, 1500, 64, 5, 1023, 300, 8] * 2)[:len(fresh)]
+    kv_len = [a + b for a, b in zip(past, fresh)]
+    kv_len[6] = 0
+    kv_len[8] = max(fresh[8] // 2, 1)
+    cache = Cache(rng, kv_len, H, D, 64, spread=0.1)
+    q = (0.5 * rng.standard_normal((sum(fresh), heads, D))).astype(np.float32)
+    at = starts(fresh)
+    rows = set(at[:-1]) | {a - 1 for a in at[1:]} | set(range(0, at[-1], 29))
+    check_norms(cache, q, at, kv_len, heads, fmt, 300, SHARE[fmt], rows=rows)
+    _, a, la = attend(cache, q, at, kv_len, heads, fmt, 300)
+    _, b, lb_ = attend(cache, q, at, kv_len, heads, fmt, 300)
+    assert np.array_equal(a, b) and np.array_equal(la, lb_)
