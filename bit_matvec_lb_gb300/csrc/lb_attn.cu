@@ -2,6 +2,7 @@
 // (decode, verification of drafted tokens), and the entry point.
 #include "lb_attn.cuh"
 
+#include <float.h>
 #include <math.h>
 
 namespace lb {
@@ -314,7 +315,8 @@ __global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2) attn_decode_kernel(
                     const float s = e & 1 ? 1.f / ODD : 1.f;
                     qb[nt][2 * i + e / 2][e & 1] = half2_bits(x[8 * i + e] * s, x[8 * i + e + 4] * s);
                 }
-            const float a = p.scale * kLog2e * down * (1.f / UNIT);
+            // (finite for the largest queries too: keys whose scale is 0 score 0)
+            const float a = fminf(p.scale * kLog2e * down * (1.f / UNIT), FLT_MAX);
             sum *= UNIT;
             int hi = un.hi;
             if (p.causal) hi = min(hi, rq.base + qi + 1);

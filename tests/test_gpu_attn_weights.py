@@ -118,3 +118,15 @@ def test_mixed_batch_in_two_launches(fmt, D, heads, H, fresh):
     _, a, la = attend(cache, q, at, kv_len, heads, fmt, 300)
     _, b, lb_ = attend(cache, q, at, kv_len, heads, fmt, 300)
     assert np.array_equal(a, b) and np.array_equal(la, lb_)
+
+
+@TYPES
+@DIMS
+@pytest.mark.parametrize("fresh", [1, 3, 40])
+@pytest.mark.parametrize("size", [1e-38, 1e30, 2e38])
+def test_queries_near_the_ends_of_the_types(fmt, D, fresh, size):
+    """Keys of zero scale score 0 whatever the query is: every visible token has the same weight."""
+    rng = np.random.default_rng(fresh + D)
+    cache = Crafted(rng, np.zeros(150), 0.25 * np.exp(rng.standard_normal(150)), 2, D, 16)
+    q = (size * queries(rng, fresh, 8, D)).astype(np.float32)
+    check_norms(cache, q, [0, fresh], [150], 8, fmt, fresh, 2.0 ** -13 if fmt == F32 else 2.0 ** -6)
