@@ -26,10 +26,11 @@ namespace lb {
 // to shared memory, four times the cache's bytes.
 //
 // Items (request, head, 4 to 16 rows) are cut into equal runs of tiles over the CTAs, three per SM by
-// registers; each warp keeps kStages tiles in flight and its own sums, which the CTA merges.  About
-// 11 us of a call are fixed (launches, requests and pages, first tiles, merge, join); beyond 131k
+// registers; each warp keeps kStages tiles in flight and its own sums, which the CTA merges.  Of a
+// call that splits its items over all CTAs about 11 us are fixed (launches, requests and pages, first
+// tiles, merge, join; calls with less work skip some of it and take 5 us or more in all); beyond 131k
 // tokens more ones are read at 5.6 TB/s.  Measured (32 / 8 heads of 128): one request of 131k
-// tokens in bf16 36 us (3.9 TB/s), 64 requests of 4096 tokens 67 us in bf16 (4.3 TB/s) and 72 in fp32.
+// tokens in bf16 37 us (3.9 TB/s), 64 requests of 4096 tokens 68 us in bf16 (4.2 TB/s) and 73 in fp32.
 // ------------------------------------------------------------------------------------------
 constexpr int kWarps = 4;
 constexpr int kThreads = kWarps * 32;
@@ -44,12 +45,25 @@ constexpr int kWhole = 16, kWholeMost = 28;
 // 5.1 / 8.5 / 9.9 us, 8: 7.4 / 9.0 / 9.6, 2: 5.2 / 9.5 / 11.3).
 constexpr int kMinRun = 4;
 constexpr int kMaxCtas = 608;
-// Query rows per head up to which this file's kernel is used (32 requests of 1000 tokens: 24 rows 39
-// against 58 us on the other, 32 rows 45 against 58, 48 rows 59 against 59; fp32 52 against 74,
-// 65 against 74, 89 against 75).
+// Query rows per head up to which this file's kernel is used.  32 requests of 1000 tokens, us here
+// against the other:  rows         24         32         40         48
+//      128 dimensions, bf16     38 / 58    44 / 58    57 / 58    59 / 58
+//                      fp32     54 / 74    68 / 75    81 / 75    91 / 76
+//      64 dimensions,  bf16     31 / 57    35 / 58    45 / 58    46 / 58
+//                      fp32     39 / 68    48 / 68    58 / 69    65 / 69
+// and one of 30000 tokens alike (128, bf16: 32 / 41 at 32 rows, 45 / 42 at 40).  One bound for all:
+// 64 dimensions would take this kernel up to 48 rows, too (bf16: a fifth of the time).
 constexpr int kFewRows = 32;
-// Batches this small run as one launch (7 decode requests of 300 tokens beside a prompt: 20 us, two
-// launches 29; of 4000 tokens: 59 against 52; 11 of 4000: 77 against 58).
+// Batches this small run as one launch.  The host knows neither the lengths nor how many of the
+// requests have few rows, so the rule sees their number alone: it saves the second launch and its
+// join for prompts and short contexts and costs decode requests of long contexts beside a prompt
+// whole row tiles.  us in one launch against two, bf16 (fp32):
+//      three chunks of 500 queries, no decode       72 /  79  (104 / 109)
+//      beside a chunk of 256, decode contexts of
+//               300 tokens: 3 requests 18 / 27 (25 / 36),    7  18 /  29 (25 /  38),  11  24 /  29  (36 /  38)
+//              1000                    23 / 35 (31 / 42),       33 /  41 (47 /  47),      38 /  43  (55 /  49)
+//              4000                    35 / 41 (51 / 48),       49 /  47 (75 /  54),      69 /  53 (104 /  59)
+//             32000                   126 / 71 (198 / 77),     258 / 114 (408 / 117),    380 / 154 (597 / 156).
 constexpr int kFewRequests = 8;
 constexpr float kLift = 256.f;       // weights are lifted by 2^8 ...
 constexpr float kSlack = 7.f;        // ... and may pass the reference by 2^7 before it moves

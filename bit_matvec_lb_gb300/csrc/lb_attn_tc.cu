@@ -18,8 +18,9 @@ namespace lb {
 // one that copies cache chunks in.  Tensor memory holds S twice for each row tile (4 x 64 columns)
 // and O (2 x 128); P overwrites S.  The operations are issued QK0(j+1) PV0(j) QK1(j+1) PV1(j), so a
 // row tile's next scores are there when it is done with the present ones (128 keys and S once: 0.72
-// against 0.66 ms for a bf16 prompt of 8192 tokens with 32 / 8 heads, 840 TFLOP/s).  What bounds it are the
-// products and their hand-overs: 0.57 ms are left without softmax and expansion of the codes.
+// against 0.66 ms for a bf16 prompt of 8192 tokens with 32 / 8 heads; now 0.67, 825 TFLOP/s).  What
+// bounds it are the products and their hand-overs: 0.57 ms are left without softmax and expansion of
+// the codes.
 // Score products read both operands from shared memory, 72 cycles for 128 x 64 x 16 where the
 // multiplications take 32 and one with its first operand in tensor memory 42.
 //
@@ -28,14 +29,16 @@ namespace lb {
 // by a scale that has no part in the row lose bits), and moves only when it must, when the weights of
 // 32 keys could leave fp16's range by their sum and the tile's largest scale.  Then those 32 scores
 // are read again for their largest weight, and if that is above the reference, what is already there
-// under the old one (the tile's earlier weights, O and the sum) is scaled by a power of two.
+// under the old one (the tile's earlier weights, O and the sum) is scaled by a power of two.  (With
+// the two maxima taken apart: 0.660 instead of 0.667 ms, but 4e-5 and more in norm with fp32 tensors
+// where a key without weight has values 2^14 times the others'; now 3e-7.)
 //
 // The tensor cores cut, downwards, what lies below an accumulator's last place, once for every 16
 // keys and part: over a long item that is far more than fp32 rounding.  With fp32 tensors O
 // therefore holds kFlush tiles at most, is then added to a sum in memory (atomics without a return
 // value, which nobody waits for; only one thread adds to an address, so the order is fixed) and
 // begins anew.  3 x 1021 queries after 1300 to 3800 tokens, error in norm and time: never 2.6e-6
-// and 178 us, every 8 tiles 1.0e-6 and 190, 6 0.9e-6 and 194, 4 0.8e-6 and 201.
+// and 178 us, every 8 tiles 1.0e-6 and 190, 6 0.9e-6 and 194 (197 with later changes), 4 0.8e-6 and 201.
 //
 // Work is split into equal runs of key tiles over the CTAs, parts of
 // an item that several CTAs share are joined by a second kernel.
@@ -45,8 +48,10 @@ constexpr int kRows = 128;           // query rows per tile, two tiles per item
 constexpr int kPieces = 3;           // copy stages
 constexpr int kScales = 8;           // tiles of scales kept
 constexpr int kTcThreads = 448;
-constexpr int kItemCost = 6;         // an item's queries and outputs take about as long as 6 tiles
-                                     // (a prompt of 2048 tokens: 80 us; counted as 3 90, as 12 83)
+// An item's queries and outputs take about as long as 6 tiles.  A prompt of 2048 / 8192 tokens, us:
+// 128 dimensions bf16 79 / 663 (counted as 3: 90 / 837, as 12: 83 / 685), fp32 115 / 1049 (139 /
+// 1353, 120 / 1079); 64 dimensions bf16 69 / 640 (70 / 670, 73 / 663), fp32 90 / 865 (97 / 926, 95 / 898).
+constexpr int kItemCost = 6;
 constexpr int kTcMaxCtas = 160;
 constexpr int kTcWhole = 8;          // items of at most this many tiles are never split
                                      // (8 x 64 queries, 364 keys: 20 us, split 29)

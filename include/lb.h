@@ -481,8 +481,13 @@ int lb_dequantize_kv4(const uint8_t *cache, int64_t pages, int page_size, int kv
  *   max_q  : an upper bound of every request's number of queries, read on the host to choose the
  *            kernels (a request with more is computed all the same, on slower ones).
  * Sums, softmax statistics and outputs accumulate in binary32.  Weights and queries enter the
- * tensor cores as fp16: with bf16 tensors one part (weights round to 11 bits, queries are exact),
- * with fp32 tensors two (22 bits).
+ * tensor cores as fp16: with fp32 tensors in two parts (22 bits), with bf16 ones in one (weights
+ * round to 11 bits, queries are exact; up to four rows per key/value head take two).  The parts end
+ * 2^-28 below a row's largest weight times value scale: what is smaller than 2^-6 (one part:
+ * 2^-17) of that keeps fewer bits.  Scores' sums are cut by the tensor cores: a score is off by up to 2^-20 of
+ * scale * 15 * its key's d * sum_i |q_i|, with bf16 tensors and few rows also by up to 2^-13 of
+ * scale * 15 * d * max_i |q_i| (codes enter as fp16 subnormals there).  Scores are expected below
+ * 2^20 in size: beyond, binary32 no longer tells close ones apart, and a row's values are unspecified.
  * heads % kv_heads == 0, heads / kv_heads <= 64; 1 <= R <= LB_KV_MAX_REQUESTS; 0 <= T (0: nothing
  * is done), T * heads / kv_heads < 2^31; 1 <= table_width, table_width * page_size <= 2^30; max_q >= 1; 0 < scale
  * finite; window >= 0, and 0 without causal; 16-byte alignment of q, out, cache, workspace and the
