@@ -27,6 +27,8 @@ __all__ = [
     "lb_pack_base3", "lb_gemv_base3", "base3_row_bytes", "lb_test_inject_wait_timeout",
     "lb_kv_plan", "lb_kv4_append", "lb_dequantize_kv4", "lb_attn_kv4_workspace_bytes",
     "lb_attn_kv4", "lb_logits_adjust", "kv4_cache_bytes",
+    "lb_gemv_q4", "lb_gemm_q4_workspace_bytes", "lb_gemm_q4", "lb_route_workspace_bytes", "lb_route",
+    "lb_experts_q4_workspace_bytes", "lb_experts_q4", "ROUTE_SOFTMAX", "ROUTE_SIGMOID",
 ]
 
 LB_STATUS = {0: "LB_OK", -1: "LB_ERR_NULL", -2: "LB_ERR_ALIGN", -3: "LB_ERR_SHAPE",
@@ -69,6 +71,11 @@ class lb_logit_rules(ctypes.Structure):
                 ("repetition", P), ("presence", P), ("frequency", P), ("bias_ids", P),
                 ("bias_values", P), ("bias_start", P), ("mask", P), ("mask_stride", I64),
                 ("mask_rows", I64), ("mask_row_opt", P)]
+
+
+class lb_route_rules(ctypes.Structure):
+    _fields_ = [("scoring", I32), ("groups", I32), ("keep_groups", I32), ("group_best", I32),
+                ("renormalize", I32), ("scale", F32), ("bias_opt", P), ("live_opt", P)]
 
 
 GEMM_MAX_GROUP = 8
@@ -120,10 +127,22 @@ SIGNATURES = {
     "lb_attn_kv4": (I32, [P, I32, I64, P, I64, I32, I32, I32, I32, P, I64, P, P, I64, I64, I64,
                           F32, I32, I64, P, I64, P, P, ctypes.c_size_t, P]),
     "lb_logits_adjust": (I32, [P, I32, I64, P, I64, I64, I64, ctypes.POINTER(lb_logit_rules), P]),
+    "lb_gemv_q4": (I32, [P, P, P, I32, P, I32, I64, P, I64, I64, I64, I32, P]),
+    "lb_gemm_q4_workspace_bytes": (ctypes.c_size_t, [I64, I64, I64, I32]),
+    "lb_gemm_q4": (I32, [P, P, P, I32, P, I32, I64, P, I64, I64, I64, I64, P, ctypes.c_size_t, P]),
+    "lb_route_workspace_bytes": (ctypes.c_size_t, [I64, I32]),
+    "lb_route": (I32, [P, I32, I64, I64, I32, I32, ctypes.POINTER(lb_route_rules), P, P, P, P, P,
+                       ctypes.c_size_t, P]),
+    "lb_experts_q4_workspace_bytes": (ctypes.c_size_t, [I64, I32, I32, I64, I64, I32]),
+    "lb_experts_q4": (I32, [P, I32, I64, I64, I32, I32, I64, I64, I32, P, P, P, P, P, P, P, P, P, P,
+                            P, I64, P, ctypes.c_size_t, P]),
 }
 
 OUT_F32 = 0
 OUT_BF16 = 1
+
+ROUTE_SOFTMAX = 0
+ROUTE_SIGMOID = 1
 
 NOALLOC_SCRATCH_BYTES = 8 << 20
 
@@ -547,3 +566,68 @@ def lb_logits_adjust(logits, type: int, stride: int, out, out_stride: int, B: in
     _check("lb_logits_adjust", load().lb_logits_adjust(
         _rows(logits), int(type), int(stride), _rows(out), int(out_stride), int(B), int(V),
         ctypes.byref(rules), _stream(stream)))
+
+
+def _bytes_of(workspace, workspace_bytes):
+    return int(workspace.numel() * workspace.element_size() if workspace_bytes is None else workspace_bytes)
+
+
+def lb_gemv_q4(codes, scales, zeros, group: int, x, type: int, x_stride: int, y, y_stride: int, N: int,
+               K: int, B: int, stream=None):
+    """y [B][N] = x [B][K] times 4-bit weights with group scales, B in 1..8; x and y of one type
+    (OUT_F32 or OUT_BF16), rows strided; zeros: None or the groups' zero points."""
+    _check("lb_gemv_q4", load().lb_gemv_q4(
+        _ptr(codes), _ptr(scales), _ptr(zeros), int(group), _rows(x), int(type), int(x_stride), _rows(y),
+        int(y_stride), int(N), int(K), int(B), _stream(stream)))
+
+
+def lb_gemm_q4_workspace_bytes(M: int, N: int, K: int, type: int) -> int:
+    """Bytes of device scratch lb_gemm_q4 needs."""
+    return int(load().lb_gemm_q4_workspace_bytes(int(M), int(N), int(K), int(type)))
+
+
+def lb_gemm_q4(codes, scales, zeros, group: int, x, type: int, x_stride: int, y, y_stride: int, M: int,
+               N: int, K: int, workspace, workspace_bytes=None, stream=None):
+    """lb_gemv_q4 for any number of tokens; workspace: a device tensor (its size is passed) or a
+    pointer with workspace_bytes."""
+    _check("lb_gemm_q4", load().lb_gemm_q4(
+        _ptr(codes), _ptr(scales), _ptr(zeros), int(group), _rows(x), int(type), int(x_stride), _rows(y),
+        int(y_stride), int(M), int(N), int(K), _ptr(workspace), _bytes_of(workspace, workspace_bytes),
+        _stream(stream)))
+
+
+def lb_route_workspace_bytes(T: int, E: int) -> int:
+    """Bytes of device scratch lb_route needs."""
+    return int(load().lb_route_workspace_bytes(int(T), int(E)))
+
+
+def lb_route(logits, type: int, stride: int, T: int, E: int, k: int, scoring: int, ids, weights,
+             expert_start, order, workspace, *, bias=None, groups: int = 1, keep_groups: int = 1,
+             group_best: int = 1, renormalize: bool = True, scale: float = 1.0, live=None,
+             workspace_bytes=None, stream=None):
+    """Experts of T tokens from logits [T][E] (OUT_F32 or OUT_BF16, rows strided), and the pairs by
+    expert; scoring ROUTE_SOFTMAX or ROUTE_SIGMOID; live: None or a one-element tensor."""
+    rules = lb_route_rules(int(scoring), int(groups), int(keep_groups), int(group_best),
+                           int(bool(renormalize)), float(scale), _ptr(bias), _ptr(live))
+    _check("lb_route", load().lb_route(
+        _rows(logits), int(type), int(stride), int(T), int(E), int(k), ctypes.byref(rules), _ptr(ids),
+        _ptr(weights), _ptr(expert_start), _ptr(order), _ptr(workspace),
+        _bytes_of(workspace, workspace_bytes), _stream(stream)))
+
+
+def lb_experts_q4_workspace_bytes(T: int, E: int, k: int, hidden: int, ffn: int, type: int) -> int:
+    """Bytes of device scratch lb_experts_q4 needs."""
+    return int(load().lb_experts_q4_workspace_bytes(int(T), int(E), int(k), int(hidden), int(ffn),
+                                                    int(type)))
+
+
+def lb_experts_q4(x, type: int, x_stride: int, T: int, E: int, k: int, hidden: int, ffn: int, group: int,
+                  up, down, ids, weights, expert_start, order, y, y_stride: int, workspace,
+                  workspace_bytes=None, stream=None):
+    """y [T][hidden] = the weighted sum of each token's experts' gated blocks; up and down:
+    (codes, scales, zeros or None) of all experts; ids, weights, expert_start and order from lb_route."""
+    _check("lb_experts_q4", load().lb_experts_q4(
+        _rows(x), int(type), int(x_stride), int(T), int(E), int(k), int(hidden), int(ffn), int(group),
+        *(_ptr(m) for m in up), *(_ptr(m) for m in down), _ptr(ids), _ptr(weights), _ptr(expert_start),
+        _ptr(order), _rows(y), int(y_stride), _ptr(workspace), _bytes_of(workspace, workspace_bytes),
+        _stream(stream)))

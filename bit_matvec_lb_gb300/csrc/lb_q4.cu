@@ -1,0 +1,172 @@
+// lb_q4.cu -- entry points over 4-bit weights with group scales: the product for a few and for many
+// tokens, and the experts' feed-forward blocks.
+//
+// Experts: the gate and up rows are one product that ends in h = silu(gate) * up, kept in binary32 at
+// the pairs' places by expert; the down rows' product leaves an output row per pair; a last kernel adds
+// each token's up in the order of its places (no atomics, so the same inputs give the same bits).
+#include "lb_q4.cuh"
+
+#include <algorithm>
+
+namespace lb {
+
+constexpr int kCombineThreads = 256;
+
+// Four columns of a token per thread.
+template <typename T>
+__global__ void __launch_bounds__(kCombineThreads)
+    experts_combine_kernel(const float *part, const int32_t *ids, const float *weights, T *y,
+                           int64_t y_stride, int64_t tokens, int k, int columns) {
+    pdl_launch_dependents();
+    pdl_wait();
+    const int quads = columns / 4;
+    const int64_t i = blockIdx.x * (int64_t)kCombineThreads + threadIdx.x;
+    if (i >= tokens * quads) return;
+    const int64_t t = i / quads;
+    const int c = (int)(i % quads) * 4;
+    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int j = 0; j < k; j++) {
+        if (ids[t * k + j] < 0) continue;
+        const float w = weights[t * k + j];
+        const float4 a = *reinterpret_cast<const float4 *>(part + (t * k + j) * columns + c);
+        v.x = fmaf(w, a.x, v.x), v.y = fmaf(w, a.y, v.y);
+        v.z = fmaf(w, a.z, v.z), v.w = fmaf(w, a.w, v.w);
+    }
+    T *to = y + t * y_stride + c;
+    if constexpr (sizeof(T) == 4) {
+        if ((reinterpret_cast<uintptr_t>(to) & 15) == 0) *reinterpret_cast<float4 *>(to) = v;
+        else to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+    } else {
+        if ((reinterpret_cast<uintptr_t>(to) & 7) == 0) {
+            *reinterpret_cast<uint2 *>(to) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
+        } else {
+            to[0] = __float2bfloat16_rn(v.x), to[1] = __float2bfloat16_rn(v.y);
+            to[2] = __float2bfloat16_rn(v.z), to[3] = __float2bfloat16_rn(v.w);
+        }
+    }
+}
+
+// Arguments that lb_gemv_q4 and lb_gemm_q4 share.
+static int check_product(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int group,
+                         const void *x, int type, int64_t x_stride, const void *y, int64_t y_stride,
+                         int64_t M, int64_t N, int64_t K) {
+    if (!codes || !scales || !x || !y) return LB_ERR_NULL;
+    if (!q4_group_ok(group) || !q4_type_ok(type) || M < 0 || M > (1 << 20) || N < 1 || N > (1 << 23) ||
+        K < group || K > LB_Q4_MAX_K || K % group != 0 || x_stride < K || y_stride < N ||
+        x_stride > 0x7fffffff || y_stride > 0x7fffffff)
+        return LB_ERR_SHAPE;
+    const int size = type == LB_OUT_F32 ? 4 : 2;
+    if (!aligned16(codes) || !aligned16(scales) || !aligned16(zeros) || !aligned16(x) ||
+        x_stride * size % 16 != 0 || !aligned_to(y, size))
+        return LB_ERR_ALIGN;
+    return LB_OK;
+}
+
+static Q4Params product_of(const uint16_t *scales, const uint8_t *zeros, int group, const void *x,
+                           int64_t x_stride, void *y, int64_t y_stride, int64_t M, int64_t N, int64_t K) {
+    Q4Params p{};
+    p.scales = scales, p.zeros = zeros, p.group = group, p.pitch = q4_pitch(K, group);
+    p.x = x, p.x_stride = x_stride, p.y = y, p.y_stride = y_stride;
+    p.N = N, p.T = M, p.K = (int)K;
+    p.error = device_error_word();
+    return p;
+}
+
+static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+
+}  // namespace lb
+
+LB_EXPORT int lb_gemv_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros_opt, int group,
+                         const void *x, int type, int64_t x_stride, void *y, int64_t y_stride, int64_t N,
+                         int64_t K, int B, void *stream) {
+    using namespace lb;
+    if (int e = check_product(codes, scales, zeros_opt, group, x, type, x_stride, y, y_stride, 1, N, K)) return e;
+    if (B < 1 || B > 8) return LB_ERR_BATCH;
+    DeviceInfo di;
+    if (int e = current_device_info(&di)) return e;
+    const Q4Params p = product_of(scales, zeros_opt, group, x, x_stride, y, y_stride, B, N, K);
+    if (!p.error) return LB_ERR_LAUNCH;
+    return q4_gemv(p, kQ4Dense, type, codes, N, di.sms, as_stream(stream));
+}
+
+LB_EXPORT size_t lb_gemm_q4_workspace_bytes(int64_t M, int64_t N, int64_t K, int type) {
+    using namespace lb;
+    if (M < 0 || M > (1 << 20) || N < 1 || N > (1 << 23) || K < 32 || K > LB_Q4_MAX_K || !q4_type_ok(type))
+        return 0;
+    return 256;
+}
+
+LB_EXPORT int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros_opt, int group,
+                         const void *x, int type, int64_t x_stride, void *y, int64_t y_stride, int64_t M,
+                         int64_t N, int64_t K, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace lb;
+    if (!workspace) return LB_ERR_NULL;
+    if (int e = check_product(codes, scales, zeros_opt, group, x, type, x_stride, y, y_stride, M, N, K)) return e;
+    if (!aligned16(workspace)) return LB_ERR_ALIGN;
+    if (workspace_bytes < lb_gemm_q4_workspace_bytes(M, N, K, type)) return LB_ERR_SHAPE;
+    DeviceInfo di;
+    if (int e = current_device_info(&di)) return e;
+    if (M == 0) return LB_OK;
+    const Q4Params p = product_of(scales, zeros_opt, group, x, x_stride, y, y_stride, M, N, K);
+    if (!p.error) return LB_ERR_LAUNCH;
+    return q4_gemv(p, kQ4Dense, type, codes, N, di.sms, as_stream(stream));
+}
+
+LB_EXPORT size_t lb_experts_q4_workspace_bytes(int64_t T, int E, int k, int64_t hidden, int64_t ffn,
+                                               int type) {
+    using namespace lb;
+    if (T < 0 || E < 1 || E > LB_ROUTE_MAX_EXPERTS || k < 1 || k > LB_ROUTE_MAX_CHOSEN ||
+        T > (1 << 24) / k || hidden < 32 || hidden > LB_Q4_MAX_K || ffn < 32 || ffn > LB_Q4_MAX_K ||
+        !q4_type_ok(type))
+        return 0;
+    return 256 + align256((size_t)T * k * ffn * 4) + align256((size_t)T * k * hidden * 4);
+}
+
+LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T, int E, int k,
+                            int64_t hidden, int64_t ffn, int group, const uint8_t *up_codes,
+                            const uint16_t *up_scales, const uint8_t *up_zeros_opt,
+                            const uint8_t *down_codes, const uint16_t *down_scales,
+                            const uint8_t *down_zeros_opt, const int32_t *ids, const float *weights,
+                            const int32_t *expert_start, const int32_t *order, void *y, int64_t y_stride,
+                            void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace lb;
+    if (!x || !up_codes || !up_scales || !down_codes || !down_scales || !ids || !weights ||
+        !expert_start || !order || !y || !workspace)
+        return LB_ERR_NULL;
+    if (!q4_group_ok(group) || hidden % group != 0 || ffn % group != 0 || x_stride < hidden ||
+        y_stride < hidden || x_stride > 0x7fffffff || y_stride > 0x7fffffff)
+        return LB_ERR_SHAPE;
+    const size_t need = lb_experts_q4_workspace_bytes(T, E, k, hidden, ffn, type);
+    if (!need || workspace_bytes < need) return LB_ERR_SHAPE;
+    const int size = type == LB_OUT_F32 ? 4 : 2;
+    for (const void *q : {(const void *)x, (const void *)up_codes, (const void *)up_scales,
+                          (const void *)up_zeros_opt, (const void *)down_codes, (const void *)down_scales,
+                          (const void *)down_zeros_opt, (const void *)workspace})
+        if (!aligned16(q)) return LB_ERR_ALIGN;
+    for (const void *q : {(const void *)ids, (const void *)weights, (const void *)expert_start,
+                          (const void *)order})
+        if (!aligned_to(q, 4)) return LB_ERR_ALIGN;
+    if (x_stride * size % 16 != 0 || !aligned_to(y, size)) return LB_ERR_ALIGN;
+    DeviceInfo di;
+    if (int e = current_device_info(&di)) return e;
+    if (T == 0) return LB_OK;
+    const int64_t pairs = T * k;
+    cudaStream_t st = as_stream(stream);
+    float *h = static_cast<float *>(workspace);
+    float *part = h + align256((size_t)pairs * ffn * 4) / 4;
+    Q4Params up = product_of(up_scales, up_zeros_opt, group, x, x_stride, h, ffn, pairs, ffn, hidden);
+    if (!up.error) return LB_ERR_LAUNCH;
+    up.start = expert_start, up.order = order, up.E = E, up.k = k;
+    if (int e = q4_gemv(up, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
+    Q4Params down = product_of(down_scales, down_zeros_opt, group, h, ffn, part, hidden, pairs, hidden, ffn);
+    down.start = expert_start, down.order = order, down.E = E, down.k = k;
+    if (int e = q4_gemv(down, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
+    const int64_t blocks = (T * (hidden / 4) + kCombineThreads - 1) / kCombineThreads;
+    if (blocks > 0x7fffffff) return LB_ERR_SHAPE;
+    if (type == LB_OUT_F32)
+        return launch_pdl(experts_combine_kernel<float>, dim3((unsigned)blocks), dim3(kCombineThreads), 0, st,
+                          part, ids, weights, static_cast<float *>(y), y_stride, T, k, (int)hidden);
+    return launch_pdl(experts_combine_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kCombineThreads), 0,
+                      st, part, ids, weights, static_cast<__nv_bfloat16 *>(y), y_stride, T, k, (int)hidden);
+}

@@ -1,0 +1,457 @@
+// lb_route.cu -- routing of tokens to experts: scores, the chosen experts and their weights, and the
+// tokens of each expert.
+//
+// Mathematics.  A warp takes a token, lane l the experts l, l + 32, ...  Without a bias the scores
+// grow with the logits, so the order of the logits is the order of the experts and only the chosen
+// ones' scores are needed; with one the keys s + bias are compared.  Two of them may lie closer
+// together than binary32 tells apart: the keys carry a bound of their error, and a token of which two
+// neighbours in the order (or the last kept and the first dropped group) lie within it is chosen
+// again with binary64 keys (about one token in 500 of sigmoid scores of 256 experts), so the experts
+// are those of the 64-bit definition while the FP64 units (1/64 of the FP32 rate) stay out of the way.
+//
+// By expert: up to 64 tokens are one CTA's, which marks each token in its experts' 64-bit masks; a
+// pair's place is its expert's start plus the marks below its token, whatever order the marks came in.
+// More tokens take a second kernel: the first leaves each CTA's counts per expert, the second adds
+// up the counts of the CTAs before its own and places its tokens by the same masks.
+//
+// What bounds it: latency.  One token is the launch, one load and k rounds of two warp reductions;
+// many are the rounds' latency over the warps an SM holds.
+#include "lb_kv4.cuh"
+
+#include <cfloat>
+
+namespace lb {
+
+constexpr int kRouteTile = 64;         // tokens whose marks fit a mask
+constexpr int kRouteMaxCtas = 256;     // of the first kernel: bounds what the second adds up
+constexpr int kPlaceThreads = 512;
+
+struct RouteParams {
+    const void *logits;
+    int64_t stride;
+    const float *bias;
+    const int32_t *live;
+    int32_t *ids, *start, *order;
+    float *weights;
+    uint16_t *counts;  // [CTA][pitch]
+    int T, E, k, sigmoid, groups, keep, best, renormalize, tile, pitch;
+    float scale;
+};
+
+__device__ __forceinline__ float route_load(const float *p) { return *p; }
+__device__ __forceinline__ float route_load(const __nv_bfloat16 *p) { return __bfloat162float(*p); }
+
+__device__ __forceinline__ float warp_max(float v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, o));
+    return v;
+}
+template <typename R>
+__device__ __forceinline__ R warp_add(R v) {
+#pragma unroll
+    for (int o = 16; o; o >>= 1) v += __shfl_xor_sync(0xffffffffu, v, o);
+    return v;
+}
+
+// The largest of the lanes' values and, of equal ones, the lowest index; -inf everywhere leaves
+// index INT_MAX.  (No value is NaN or -0.)
+__device__ __forceinline__ void warp_best(float &v, int &i) {
+    const uint32_t b = __float_as_uint(v);
+    const uint32_t u = b & 0x80000000u ? ~b : b | 0x80000000u;
+    const uint32_t m = __reduce_max_sync(0xffffffffu, u);
+    v = __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
+    i = (int)__reduce_min_sync(0xffffffffu, u == m && v != -INFINITY ? (uint32_t)i : 0x7fffffffu);
+}
+__device__ __forceinline__ void warp_best(double &v, int &i) {
+    if (v == -INFINITY) i = 0x7fffffff;
+#pragma unroll
+    for (int o = 16; o; o >>= 1) {
+        const double w = __shfl_xor_sync(0xffffffffu, v, o);
+        const int j = __shfl_xor_sync(0xffffffffu, i, o);
+        if (w > v || (w == v && j < i)) v = w, i = j;
+    }
+}
+
+__device__ __forceinline__ float exp_of(float v) { return expf(v); }
+__device__ __forceinline__ double exp_of(double v) { return exp(v); }
+// x - m and what its rounding left out.
+__device__ __forceinline__ float exp_difference(float x, float m) {
+    const float t = x - m, back = x - t;
+    const float rest = (x - (t + back)) + (back - m);
+    const float s = expf(t);
+    return t < -100.f ? s : fmaf(s, rest, s);  // (infinite differences leave no rest)
+}
+__device__ __forceinline__ double exp_difference(double x, double m) { return exp(x - m); }
+
+struct Chosen {
+    int id;        // lane j's expert, -1 without
+    bool close;    // binary32 does not tell the order
+    float sum;     // softmax: sum of exp(x - max)
+};
+
+// The k experts of a token, one per lane.  x: the lane's logits (-inf: not to be chosen), m their
+// warp's maximum.
+template <int EL, typename R>
+__device__ __forceinline__ Chosen choose(const RouteParams &p, const float (&x)[EL], float m, R *keys,
+                                         int lane) {
+    const bool plain = !p.bias && p.best == 1;
+    constexpr bool kFloat = sizeof(R) == 4;
+    Chosen c{-1, false, 0.f};
+    R key[EL], tol = 0;
+    if (plain) {
+#pragma unroll
+        for (int i = 0; i < EL; i++) key[i] = (R)x[i] + (R)0;  // -0 and 0 are the same number
+        if (!p.sigmoid && !p.renormalize) {
+            float s = 0.f;
+#pragma unroll
+            for (int i = 0; i < EL; i++) s += x[i] > -INFINITY ? exp_difference(x[i], m) : 0.f;
+            c.sum = warp_add(s);
+        }
+    } else {
+        R bias[EL], s = 0;
+        float most = 0.f;
+#pragma unroll
+        for (int i = 0; i < EL; i++) {
+            const bool in = x[i] > -INFINITY;
+            bias[i] = in && p.bias ? (R)p.bias[lane + 32 * i] : (R)0;
+            most = fmaxf(most, fabsf((float)bias[i]));
+            key[i] = !in ? (R)0
+                     : p.sigmoid ? (R)1 / ((R)1 + exp_of(-(R)x[i]))
+                                 : exp_difference((R)x[i], (R)m);
+            s += key[i];
+        }
+        if (!p.sigmoid) {
+            s = warp_add(s);
+            c.sum = (float)s;
+        }
+        const R one = p.sigmoid ? (R)1 : s;
+#pragma unroll
+        for (int i = 0; i < EL; i++)
+            key[i] = x[i] > -INFINITY ? key[i] / one + bias[i] + (R)0 : -(R)INFINITY;
+        // exp to 2 units in the last place, a sum, a quotient and a sum: well below 2^-21 of the largest score
+        if (kFloat)
+            tol = (p.sigmoid ? 0x1p-21f : 0x1p-20f / (float)one) + 0x1p-22f * warp_max(most) + 1e-37f;
+    }
+    if (p.groups > 1) {
+        // lanes [g * part, (g + 1) * part) look through group g
+        const int per = p.E / p.groups, part = 32 >> (32 - __clz(p.groups - 1));
+        const int g = lane / part;
+#pragma unroll
+        for (int i = 0; i < EL; i++)
+            if (lane + 32 * i < p.E) keys[lane + 32 * i] = key[i];
+        __syncwarp();
+        R first = -(R)INFINITY, second = -(R)INFINITY;
+        if (g < p.groups)
+            for (int e = lane % part; e < per; e += part) {
+                const R v = keys[g * per + e];
+                if (v > first) second = first, first = v;
+                else if (v > second) second = v;
+            }
+        __syncwarp();
+        for (int o = 1; o < part; o <<= 1) {
+            const R a = __shfl_xor_sync(0xffffffffu, first, o), b = __shfl_xor_sync(0xffffffffu, second, o);
+            const R low = first < a ? first : a;
+            first = first < a ? a : first;
+            second = second < b ? b : second;
+            second = second < low ? low : second;
+        }
+        R value = p.best == 2 && second > -(R)INFINITY ? first + second + (R)0 : first;
+        uint32_t kept = 0;
+        R last = 0;
+        for (int j = 0; j <= p.keep; j++) {
+            R v = g < p.groups && !(kept >> g & 1) ? value : -(R)INFINITY;
+            int at = g;
+            warp_best(v, at);
+            if (v == -(R)INFINITY) break;
+            if (j == p.keep) {
+                if (kFloat && !plain && last - v <= 4 * tol) c.close = true;
+                break;
+            }
+            kept |= 1u << at;
+            last = v;
+        }
+#pragma unroll
+        for (int i = 0; i < EL; i++)
+            if (!(kept >> min((lane + 32 * i) / per, 31) & 1)) key[i] = -(R)INFINITY;
+    }
+    R last = 0;
+    for (int j = 0; j <= p.k; j++) {
+        R v = key[0];
+        int at = lane;
+#pragma unroll
+        for (int i = 1; i < EL; i++)
+            if (key[i] > v) v = key[i], at = lane + 32 * i;
+        if (j == p.k && (!kFloat || plain)) break;
+        warp_best(v, at);
+        if (v == -(R)INFINITY) break;
+        if (kFloat && !plain && j && last - v <= 2 * tol) c.close = true;
+        if (j == p.k) break;
+        last = v;
+        if (lane == j) c.id = at;
+#pragma unroll
+        for (int i = 0; i < EL; i++)
+            if (at == lane + 32 * i) key[i] = -(R)INFINITY;
+    }
+    return c;
+}
+template <int EL>
+__device__ __noinline__ Chosen choose_again(const RouteParams &p, const float (&x)[EL], float m,
+                                            double *keys, int lane) {
+    return choose<EL, double>(p, x, m, keys, lane);
+}
+
+// Weight of the expert whose logit is x, one per lane (in: the lane has one).
+__device__ __forceinline__ float weight_of(const RouteParams &p, float x, bool in, float m, float sum) {
+    float s;
+    if (!p.renormalize) {
+        s = p.sigmoid ? 1.f / (1.f + expf(-x)) : exp_difference(x, m) / sum;
+        return in ? s * p.scale : 0.f;
+    }
+    // the largest chosen logit's power of e goes out of all of them, so their sum is never 0
+    const float top = warp_max(in ? x : -INFINITY);
+    if (p.sigmoid) {
+        const float low = fminf(top, 0.f);
+        s = x < 0.f ? exp_difference(x, low) / (1.f + expf(x)) : 1.f / (1.f + expf(-x));
+    } else {
+        s = exp_difference(x, top);
+    }
+    s = in ? s : 0.f;
+    const float all = warp_add(s);
+    return in ? s / all * p.scale : 0.f;
+}
+
+// Exclusive sums over the experts of `count` (shared, [E]) in place; all threads.  Returns the total.
+template <int THREADS>
+__device__ __forceinline__ int scan_experts(int32_t *count, int E, int32_t *part) {
+    constexpr int kEach = LB_ROUTE_MAX_EXPERTS / THREADS > 1 ? LB_ROUTE_MAX_EXPERTS / THREADS : 1;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    int v[kEach], sum = 0;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        v[i] = tid * kEach + i < E ? count[tid * kEach + i] : 0;
+        sum += v[i];
+    }
+    int run = sum;
+#pragma unroll
+    for (int o = 1; o < 32; o <<= 1) {
+        const int w = __shfl_up_sync(0xffffffffu, run, o);
+        if (lane >= o) run += w;
+    }
+    if (lane == 31) part[warp] = run;
+    __syncthreads();
+    int before = 0, total = 0;
+#pragma unroll
+    for (int w = 0; w < THREADS / 32; w++) {
+        const int c = part[w];
+        before += w < warp ? c : 0;
+        total += c;
+    }
+    before += run - sum;
+#pragma unroll
+    for (int i = 0; i < kEach; i++) {
+        if (tid * kEach + i < E) count[tid * kEach + i] = before;
+        before += v[i];
+    }
+    __syncthreads();
+    return total;
+}
+
+template <typename T, int EL, int THREADS, bool ALONE>
+__global__ void __launch_bounds__(THREADS) route_kernel(const __grid_constant__ RouteParams p) {
+    extern __shared__ uint64_t route_smem[];  // marks or counts [E], then with groups keys [warp][E]
+    __shared__ int32_t start[ALONE ? LB_ROUTE_MAX_EXPERTS : 1], part[THREADS / 32];
+    constexpr int kWarps = THREADS / 32, kHeld = kRouteTile / kWarps;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    uint64_t *mark = route_smem;
+    int32_t *count = reinterpret_cast<int32_t *>(route_smem);
+    double *keys = reinterpret_cast<double *>(route_smem + p.E) + (p.groups > 1 ? warp * p.E : 0);
+    pdl_launch_dependents();
+    for (int e = tid; e < p.E; e += THREADS) mark[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    const int live = p.live ? min(max(*p.live, 0), p.T) : p.T;
+    const int t0 = blockIdx.x * p.tile, t1 = min(t0 + p.tile, p.T);
+    int held[ALONE ? kHeld : 1];
+    for (int n = 0; t0 + n * kWarps < t1; n++) {
+        const int t = t0 + n * kWarps + warp;
+        int id = -1;
+        if (t < t1) {
+            float w = 0.f;
+            if (t < live) {
+                const T *row = static_cast<const T *>(p.logits) + t * p.stride;
+                float x[EL], m = -INFINITY;
+#pragma unroll
+                for (int i = 0; i < EL; i++) {
+                    const int e = lane + 32 * i;
+                    x[i] = e < p.E ? fminf(route_load(row + e), FLT_MAX) : -INFINITY;
+                    if (e < p.E && isnan(route_load(row + e))) x[i] = -INFINITY;
+                    if (p.bias && e < p.E && !(p.bias[e] > -INFINITY)) x[i] = -INFINITY;
+                    m = fmaxf(m, x[i]);
+                }
+                m = warp_max(m);
+                Chosen c = choose<EL, float>(p, x, m, reinterpret_cast<float *>(keys), lane);
+                if (c.close) c.id = choose_again<EL>(p, x, m, keys, lane).id;
+                id = c.id;
+                const float xj = id >= 0 ? fminf(route_load(row + id), FLT_MAX) : 0.f;
+                w = weight_of(p, xj, id >= 0, m, c.sum);
+            }
+            if (lane < p.k) {
+                p.ids[(int64_t)t * p.k + lane] = id;
+                p.weights[(int64_t)t * p.k + lane] = w;
+            }
+            if (id >= 0) {
+                if (ALONE) atomicOr(reinterpret_cast<unsigned long long *>(mark + id), 1ull << (t - t0));
+                else atomicAdd(count + id, 1);
+            }
+        }
+        if (ALONE) {
+#pragma unroll
+            for (int i = 0; i < kHeld; i++)
+                if (i == n) held[i] = id;
+        }
+    }
+    __syncthreads();
+    if constexpr (!ALONE) {
+        for (int e = tid; e < p.pitch; e += THREADS)
+            p.counts[(int64_t)blockIdx.x * p.pitch + e] = e < p.E ? (uint16_t)count[e] : 0;
+    } else {
+        for (int e = tid; e < p.E; e += THREADS) start[e] = __popcll(mark[e]);
+        __syncthreads();
+        const int total = scan_experts<THREADS>(start, p.E, part);
+        for (int e = tid; e <= p.E; e += THREADS) p.start[e] = e < p.E ? start[e] : total;
+#pragma unroll
+        for (int n = 0; n < kHeld; n++) {
+            const int at = n * kWarps + warp;
+            if (t0 + at < t1 && held[n] >= 0)
+                p.order[start[held[n]] + __popcll(mark[held[n]] & ((1ull << at) - 1))] = at * p.k + lane;
+        }
+        for (int i = total + tid; i < p.T * p.k; i += THREADS) p.order[i] = -1;
+    }
+}
+
+// The second kernel: CTA b places the tokens of the first one's CTA b.
+__global__ void __launch_bounds__(kPlaceThreads) place_kernel(const __grid_constant__ RouteParams p) {
+    __shared__ int32_t before[LB_ROUTE_MAX_EXPERTS], start[LB_ROUTE_MAX_EXPERTS], part[kPlaceThreads / 32];
+    __shared__ uint64_t mark[LB_ROUTE_MAX_EXPERTS];
+    const int tid = threadIdx.x;
+    pdl_launch_dependents();
+    for (int e = tid; e < LB_ROUTE_MAX_EXPERTS; e += kPlaceThreads) before[e] = start[e] = 0;
+    __syncthreads();
+    pdl_wait();
+    // a thread adds up two experts' counts over every `parts`-th CTA
+    const int words = p.pitch / 2, parts = kPlaceThreads / words;
+    const uint32_t *counts = reinterpret_cast<const uint32_t *>(p.counts);
+    const int w = tid % words, q = tid / words;
+    if (q < parts) {
+        uint32_t all[2] = {0, 0}, mine[2] = {0, 0};
+#pragma unroll 8
+        for (int c = q; c < (int)gridDim.x; c += parts) {
+            const uint32_t v = counts[c * words + w];
+            all[0] += v & 0xffff, all[1] += v >> 16;
+            if (c < (int)blockIdx.x) mine[0] += v & 0xffff, mine[1] += v >> 16;
+        }
+#pragma unroll
+        for (int i = 0; i < 2; i++) {
+            atomicAdd(start + 2 * w + i, (int)all[i]);
+            atomicAdd(before + 2 * w + i, (int)mine[i]);
+        }
+    }
+    __syncthreads();
+    const int total = scan_experts<kPlaceThreads>(start, p.E, part);
+    if (blockIdx.x == 0)
+        for (int e = tid; e <= p.E; e += kPlaceThreads) p.start[e] = e < p.E ? start[e] : total;
+    for (int e = tid; e < p.E; e += kPlaceThreads) before[e] += start[e];
+    const int t0 = blockIdx.x * p.tile, t1 = min(t0 + p.tile, p.T);
+    for (int t = t0; t < t1; t += kRouteTile) {
+        __syncthreads();
+        for (int e = tid; e < p.E; e += kPlaceThreads) mark[e] = 0;
+        __syncthreads();
+        const int n = min(kRouteTile, t1 - t) * p.k;
+        const int32_t *ids = p.ids + (int64_t)t * p.k;
+        for (int i = tid; i < n; i += kPlaceThreads)
+            if (ids[i] >= 0)
+                atomicOr(reinterpret_cast<unsigned long long *>(mark + ids[i]), 1ull << (i / p.k));
+        __syncthreads();
+        for (int i = tid; i < n; i += kPlaceThreads) {
+            const int e = ids[i];
+            if (e >= 0) p.order[before[e] + __popcll(mark[e] & ((1ull << (i / p.k)) - 1))] = t * p.k + i;
+        }
+        __syncthreads();
+        for (int e = tid; e < p.E; e += kPlaceThreads) before[e] += __popcll(mark[e]);
+    }
+    const int64_t pairs = (int64_t)p.T * p.k;
+    for (int64_t i = total + blockIdx.x * (int64_t)kPlaceThreads + tid; i < pairs;
+         i += (int64_t)gridDim.x * kPlaceThreads)
+        p.order[i] = -1;
+}
+
+static int route_tile(int64_t T) {
+    return (int)((T + kRouteTile * kRouteMaxCtas - 1) / (kRouteTile * kRouteMaxCtas)) * kRouteTile;
+}
+
+template <typename T, int EL, int THREADS>
+static int launch_route(RouteParams p, cudaStream_t st) {
+    const size_t smem = (size_t)p.E * 8 * (1 + (p.groups > 1 ? THREADS / 32 : 0));
+    int per_sm;
+    if (p.T <= kRouteTile) {
+        p.tile = kRouteTile;
+        auto kernel = route_kernel<T, EL, THREADS, true>;
+        if (int e = prepare_kernel((const void *)kernel, THREADS, smem, &per_sm)) return e;
+        return launch_pdl(kernel, dim3(1), dim3(THREADS), smem, st, p);
+    }
+    p.tile = route_tile(p.T);
+    const int ctas = (p.T + p.tile - 1) / p.tile;
+    auto kernel = route_kernel<T, EL, THREADS, false>;
+    if (int e = prepare_kernel((const void *)kernel, THREADS, smem, &per_sm)) return e;
+    if (int e = launch_pdl(kernel, dim3(ctas), dim3(THREADS), smem, st, p)) return e;
+    return launch_pdl(place_kernel, dim3(ctas), dim3(kPlaceThreads), 0, st, p);
+}
+
+template <typename T>
+static int dispatch_route(const RouteParams &p, cudaStream_t st) {
+    if (p.E <= 64) return launch_route<T, 2, 1024>(p, st);
+    if (p.E <= 128) return launch_route<T, 4, 1024>(p, st);
+    if (p.E <= 256) return launch_route<T, 8, 1024>(p, st);
+    return launch_route<T, 32, 256>(p, st);
+}
+
+}  // namespace lb
+
+LB_EXPORT size_t lb_route_workspace_bytes(int64_t T, int E) {
+    using namespace lb;
+    if (T < 0 || T > (1 << 20) || E < 1 || E > LB_ROUTE_MAX_EXPERTS) return 0;
+    if (T <= kRouteTile) return 16;
+    const int64_t tile = route_tile(T);
+    return (size_t)((T + tile - 1) / tile) * ((E + 7) / 8 * 8) * 2;
+}
+
+LB_EXPORT int lb_route(const void *logits, int type, int64_t stride, int64_t T, int E, int k,
+                       const lb_route_rules *rules, int32_t *ids, float *weights, int32_t *expert_start,
+                       int32_t *order, void *workspace, size_t workspace_bytes, void *stream) {
+    using namespace lb;
+    if (!rules || !expert_start || !workspace || (T > 0 && (!logits || !ids || !weights || !order)))
+        return LB_ERR_NULL;
+    const lb_route_rules &r = *rules;
+    if ((type != LB_OUT_F32 && type != LB_OUT_BF16) || T < 0 || T > (1 << 20) || E < 1 ||
+        E > LB_ROUTE_MAX_EXPERTS || k < 1 || k > LB_ROUTE_MAX_CHOSEN || k > E || stride < E ||
+        (r.scoring != LB_ROUTE_SOFTMAX && r.scoring != LB_ROUTE_SIGMOID) || r.groups < 1 ||
+        r.groups > 32 || E % r.groups != 0 || r.keep_groups < 1 || r.keep_groups > r.groups ||
+        (r.group_best != 1 && r.group_best != 2) || !(r.scale > -INFINITY && r.scale < INFINITY) ||
+        workspace_bytes < lb_route_workspace_bytes(T, E))
+        return LB_ERR_SHAPE;
+    if (!aligned_to(logits, type == LB_OUT_F32 ? 4 : 2) || !aligned16(workspace)) return LB_ERR_ALIGN;
+    for (const void *q : {(const void *)ids, (const void *)weights, (const void *)expert_start,
+                          (const void *)order, (const void *)r.bias_opt, (const void *)r.live_opt})
+        if (!aligned_to(q, 4)) return LB_ERR_ALIGN;
+    DeviceInfo di;
+    if (int e = current_device_info(&di)) return e;
+    RouteParams p{};
+    p.logits = logits, p.stride = stride, p.bias = r.bias_opt, p.live = r.live_opt;
+    p.ids = ids, p.weights = weights, p.start = expert_start, p.order = order;
+    p.counts = static_cast<uint16_t *>(workspace);
+    p.T = (int)T, p.E = E, p.k = k, p.sigmoid = r.scoring == LB_ROUTE_SIGMOID;
+    p.groups = r.groups, p.keep = r.keep_groups, p.best = r.group_best;
+    p.renormalize = r.renormalize != 0, p.scale = r.scale, p.pitch = (E + 7) / 8 * 8;
+    cudaStream_t st = as_stream(stream);
+    return type == LB_OUT_F32 ? dispatch_route<float>(p, st) : dispatch_route<__nv_bfloat16>(p, st);
+}

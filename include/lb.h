@@ -533,6 +533,104 @@ typedef struct lb_logit_rules {
 int lb_logits_adjust(const void *logits, int type, int64_t stride, void *out, int64_t out_stride,
                      int64_t B, int64_t V, const lb_logit_rules *rules, void *stream);
 
+/* ---------------------------------------------------------------------------------------
+ * 4-bit weights with group scales, and the mixture of experts around them.  No counterpart in the
+ * source pages; conveniences of this library for models that keep some of their matrices in 4 bits:
+ *   lb_gemv_q4, lb_gemm_q4   y = W x for one to eight tokens, for any number
+ *   lb_route                 gate logits -> experts, weights, and the tokens of each expert
+ *   lb_experts_q4            the experts' gated feed-forward blocks, added up per token
+ *
+ * Weights [N][K]: codes [N][K / 2] bytes, column 2j in the low half of byte j and 2j + 1 in the high
+ * one; scales [N][LB_SCALE_STRIDE(K, group)] fp16, one for `group` columns; zeros_opt NULL or [N]
+ * [LB_SCALE_STRIDE(K, group)] bytes, one for `group` columns, 0..15.  A code c stands for
+ *   w = d * (c - z),   z = 8 without zeros.
+ * (What lies in a row's scales and zeros behind K / group is not used.)
+ * group in {32, 64, 128}; K a multiple of it.  codes, scales and zeros 16-byte aligned.
+ * Like the other products, these may read codes, scales and zeros while the previous kernel of
+ * this library in the stream is still finishing.
+ * ------------------------------------------------------------------------------------- */
+#define LB_Q4_MAX_K 32768
+
+/* y[t][n] = sum_k w[n][k] x[t][k] for B in [1, 8] tokens (LB_ERR_BATCH otherwise), M of any number.
+ *   x : [B][K], y : [B][N], both fp32 (type LB_OUT_F32) or both bf16 (LB_OUT_BF16); rows x_stride /
+ *       y_stride elements apart.  y may not overlap x.
+ *   workspace : at least lb_gemm_q4_workspace_bytes(M, N, K, type) bytes, 16-byte aligned, owned by the
+ *       caller, not used by another call that may run at the same time; it needs no initialization.
+ * Up to eight tokens every product c - z times x is exact (an fp32 x enters as three bf16 parts), a
+ * group's products are added up on the tensor cores and its scale acts on the sum in binary32.  For
+ * more tokens, with bf16 tensors, weights round to 11 bits; with fp32 ones they, and x, enter as two fp16 parts
+ * (22 bits of a row of x below its largest value, and 2^-38 of that).  Sums are held in binary32.
+ * 1 <= N <= 2^23; group <= K <= LB_Q4_MAX_K; 0 <= M <= 2^20 (0: nothing is done); x and its stride in
+ * bytes 16-byte aligned, y aligned to its elements; strides >= K and N, below 2^31. */
+int lb_gemv_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros_opt, int group,
+               const void *x, int type, int64_t x_stride, void *y, int64_t y_stride, int64_t N,
+               int64_t K, int B, void *stream);
+size_t lb_gemm_q4_workspace_bytes(int64_t M, int64_t N, int64_t K, int type);
+int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros_opt, int group,
+               const void *x, int type, int64_t x_stride, void *y, int64_t y_stride, int64_t M,
+               int64_t N, int64_t K, void *workspace, size_t workspace_bytes, void *stream);
+
+/* Routing of T tokens to k of E experts.  Token t, expert e, logit x (bf16 or fp32; +inf counts as
+ * the largest finite number):
+ *   score  s_e = exp(x_e) / sum of exp(x)  (LB_ROUTE_SOFTMAX)  or  1 / (1 + exp(-x_e))  (LB_ROUTE_SIGMOID)
+ *   key    x_e if there is no bias and group_best is 1 (the logits' own order), else the binary64
+ *          number s_e + bias_e (bias 0 without one)
+ *   An expert whose logit or bias is NaN or -inf is never chosen and adds nothing to a sum.
+ *   With groups > 1, group g holds the experts [g E / groups, (g + 1) E / groups); its value is the sum
+ *   of its group_best (1 or 2; fewer if fewer can be chosen) largest keys, and only the experts of the
+ *   keep_groups groups of largest value can be chosen.
+ *   ids[t]     = the k experts of largest key, in falling order (ties of keys and of groups: the lower
+ *                index first); -1 where there are no more
+ *   weights[t] = scale * s_e, with renormalize scale * s_e / sum of the chosen experts' s; 0 at -1
+ *   expert_start[e], e = 0..E : the number of pairs (t, j) with 0 <= ids[t][j] < e
+ *   order      = the pairs t * k + j with ids[t][j] >= 0, by expert and then by t; -1 behind them
+ * Tokens from *live_opt on (NULL: none; below 0 counts as 0) get ids -1 and weights 0, and their logits are not read.
+ *   logits : [T][E] fp32 (type LB_OUT_F32) or bf16 (LB_OUT_BF16), rows `stride` elements apart.
+ *   ids : [T][k] int32.  weights : [T][k] fp32.  expert_start : [E + 1] int32.  order : [T * k] int32.
+ *   workspace : lb_route_workspace_bytes(T, E) bytes, 16-byte aligned, as above.
+ * Scores are computed in binary32, and in binary64 where two keys lie too close together for that;
+ * exp(x - max) of experts more than 100 below the row's largest logit counts as 0 in the weights.
+ * 0 <= T <= 2^20 (at 0 only expert_start is written); 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= min(E,
+ * LB_ROUTE_MAX_CHOSEN); groups <= 32 divides E; 1 <= keep_groups <= groups; stride >= E; pointers aligned to
+ * their elements. */
+#define LB_ROUTE_SOFTMAX 0
+#define LB_ROUTE_SIGMOID 1
+#define LB_ROUTE_MAX_EXPERTS 1024
+#define LB_ROUTE_MAX_CHOSEN 32
+typedef struct lb_route_rules {
+    int32_t scoring, groups, keep_groups, group_best, renormalize;
+    float scale;
+    const float *bias_opt;   /* [E] */
+    const int32_t *live_opt; /* [1] */
+} lb_route_rules;
+size_t lb_route_workspace_bytes(int64_t T, int E);
+int lb_route(const void *logits, int type, int64_t stride, int64_t T, int E, int k,
+             const lb_route_rules *rules, int32_t *ids, float *weights, int32_t *expert_start,
+             int32_t *order, void *workspace, size_t workspace_bytes, void *stream);
+
+/* The experts' blocks.  Expert e has gate and up rows in one matrix up_e [2 ffn][hidden] (rows 0..ffn-1
+ * the gate's) and down_e [hidden][ffn]; both are arrays of E matrices, one behind the other.
+ *   h = silu(gate_e x[t]) * (up_e x[t]),   silu(v) = v / (1 + exp(-v))
+ *   y[t] = sum over j with ids[t][j] >= 0 of weights[t][j] * (down_e h),  e = ids[t][j]
+ * A token without experts gets zeros.
+ *   x, y : [T][hidden], both fp32 or both bf16 (type), rows x_stride / y_stride elements apart; y may not
+ *          overlap x.
+ *   ids, weights, expert_start, order : as lb_route leaves them.  ids at -1 are left out; the experts'
+ *          pairs are those of order and expert_start (not falling, at most T * k; entries of order outside
+ *          [0, T * k) are passed over).  The sum over j runs from 0 on.
+ *   workspace : lb_experts_q4_workspace_bytes(T, E, k, hidden, ffn, type) bytes, 16-byte aligned, as above.
+ * Precision as in lb_gemv_q4 / lb_gemm_q4; h and the experts' outputs are kept to at least two bf16 parts (16
+ * bits) with bf16 tensors, in binary32 with fp32 ones.
+ * 0 <= T (0: nothing is done), T * k <= 2^24; 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= LB_ROUTE_MAX_CHOSEN; hidden and
+ * ffn multiples of group, at most LB_Q4_MAX_K; alignment as in lb_gemv_q4, 4-byte for the routing's. */
+size_t lb_experts_q4_workspace_bytes(int64_t T, int E, int k, int64_t hidden, int64_t ffn, int type);
+int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T, int E, int k, int64_t hidden,
+                  int64_t ffn, int group, const uint8_t *up_codes, const uint16_t *up_scales,
+                  const uint8_t *up_zeros_opt, const uint8_t *down_codes, const uint16_t *down_scales,
+                  const uint8_t *down_zeros_opt, const int32_t *ids, const float *weights,
+                  const int32_t *expert_start, const int32_t *order, void *y, int64_t y_stride,
+                  void *workspace, size_t workspace_bytes, void *stream);
+
 #ifdef __cplusplus
 }
 #endif
