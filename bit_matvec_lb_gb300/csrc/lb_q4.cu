@@ -74,6 +74,42 @@ static Q4Params product_of(const uint16_t *scales, const uint8_t *zeros, int gro
 }
 
 static size_t align256(size_t n) { return (n + 255) / 256 * 256; }
+static int parts_of(int type) { return type == LB_OUT_F32 ? 2 : 1; }
+
+// A piece of a workspace: rows of x as the tensor cores take them.
+struct RowsAt {
+    uint16_t *to;
+    float *scale;
+    int64_t plane;
+};
+static size_t rows_bytes(int64_t n, int64_t K, int type) {
+    return align256((size_t)n * K * 2) * parts_of(type) + align256((size_t)n * 4);
+}
+static RowsAt rows_at(uint8_t *at, int64_t n, int64_t K, int type) {
+    RowsAt r;
+    const size_t one = align256((size_t)n * K * 2);
+    r.to = reinterpret_cast<uint16_t *>(at), r.plane = (int64_t)(one / 2);
+    r.scale = reinterpret_cast<float *>(at + one * parts_of(type));
+    return r;
+}
+
+// Pairs per expert from which the experts' products run on tcgen05: below, most of its tiles would be empty
+// columns.
+constexpr int kManyPairs = 6;
+
+struct ExpertsAt {
+    size_t x, h, h_rows, part, bytes;
+};
+static ExpertsAt experts_at(int64_t T, int k, int64_t hidden, int64_t ffn, int type) {
+    ExpertsAt a;
+    const size_t pairs = (size_t)T * k;
+    a.x = 0;
+    a.h = a.x + rows_bytes(T, hidden, type);
+    a.h_rows = a.h + align256(pairs * ffn * 4);
+    a.part = a.h_rows + rows_bytes(pairs, ffn, type);
+    a.bytes = a.part + align256(pairs * hidden * 4) + 256;
+    return a;
+}
 
 }  // namespace lb
 
@@ -94,7 +130,7 @@ LB_EXPORT size_t lb_gemm_q4_workspace_bytes(int64_t M, int64_t N, int64_t K, int
     using namespace lb;
     if (M < 0 || M > (1 << 20) || N < 1 || N > (1 << 23) || K < 32 || K > LB_Q4_MAX_K || !q4_type_ok(type))
         return 0;
-    return 256;
+    return M <= 8 ? 256 : 256 + rows_bytes(M, K, type);
 }
 
 LB_EXPORT int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros_opt, int group,
@@ -108,9 +144,16 @@ LB_EXPORT int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uin
     DeviceInfo di;
     if (int e = current_device_info(&di)) return e;
     if (M == 0) return LB_OK;
-    const Q4Params p = product_of(scales, zeros_opt, group, x, x_stride, y, y_stride, M, N, K);
+    Q4Params p = product_of(scales, zeros_opt, group, x, x_stride, y, y_stride, M, N, K);
     if (!p.error) return LB_ERR_LAUNCH;
-    return q4_gemv(p, kQ4Dense, type, codes, N, di.sms, as_stream(stream));
+    cudaStream_t st = as_stream(stream);
+    if (M <= 8) return q4_gemv(p, kQ4Dense, type, codes, N, di.sms, st);
+    const RowsAt r = rows_at(static_cast<uint8_t *>(workspace), M, K, type);
+    if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, M, (int)K, nullptr, parts_of(type), r.to, r.plane, r.scale,
+                        st))
+        return e;
+    p.x = r.to, p.x_stride = K;
+    return q4_gemm(p, {r.scale, r.plane}, kQ4Dense, type, codes, N, di.sms, st);
 }
 
 LB_EXPORT size_t lb_experts_q4_workspace_bytes(int64_t T, int E, int k, int64_t hidden, int64_t ffn,
@@ -120,7 +163,7 @@ LB_EXPORT size_t lb_experts_q4_workspace_bytes(int64_t T, int E, int k, int64_t 
         T > (1 << 24) / k || hidden < 32 || hidden > LB_Q4_MAX_K || ffn < 32 || ffn > LB_Q4_MAX_K ||
         !q4_type_ok(type))
         return 0;
-    return 256 + align256((size_t)T * k * ffn * 4) + align256((size_t)T * k * hidden * 4);
+    return experts_at(T, k, hidden, ffn, type).bytes;
 }
 
 LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T, int E, int k,
@@ -153,15 +196,30 @@ LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T
     if (T == 0) return LB_OK;
     const int64_t pairs = T * k;
     cudaStream_t st = as_stream(stream);
-    float *h = static_cast<float *>(workspace);
-    float *part = h + align256((size_t)pairs * ffn * 4) / 4;
+    uint8_t *ws = static_cast<uint8_t *>(workspace);
+    const ExpertsAt at = experts_at(T, k, hidden, ffn, type);
+    float *h = reinterpret_cast<float *>(ws + at.h), *part = reinterpret_cast<float *>(ws + at.part);
     Q4Params up = product_of(up_scales, up_zeros_opt, group, x, x_stride, h, ffn, pairs, ffn, hidden);
     if (!up.error) return LB_ERR_LAUNCH;
     up.start = expert_start, up.order = order, up.E = E, up.k = k;
-    if (int e = q4_gemv(up, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
     Q4Params down = product_of(down_scales, down_zeros_opt, group, h, ffn, part, hidden, pairs, hidden, ffn);
     down.start = expert_start, down.order = order, down.E = E, down.k = k;
-    if (int e = q4_gemv(down, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
+    if (pairs < (int64_t)kManyPairs * E) {
+        if (int e = q4_gemv(up, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
+        if (int e = q4_gemv(down, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
+    } else {
+        const RowsAt xr = rows_at(ws + at.x, T, hidden, type), hr = rows_at(ws + at.h_rows, pairs, ffn, type);
+        const int parts = parts_of(type);
+        if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, T, (int)hidden, nullptr, parts, xr.to, xr.plane,
+                            xr.scale, st))
+            return e;
+        up.x = xr.to, up.x_stride = hidden;
+        if (int e = q4_gemm(up, {xr.scale, xr.plane}, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
+        if (int e = q4_rows(h, true, ffn, pairs, (int)ffn, expert_start + E, parts, hr.to, hr.plane, hr.scale, st))
+            return e;
+        down.x = hr.to;
+        if (int e = q4_gemm(down, {hr.scale, hr.plane}, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
+    }
     const int64_t blocks = (T * (hidden / 4) + kCombineThreads - 1) / kCombineThreads;
     if (blocks > 0x7fffffff) return LB_ERR_SHAPE;
     if (type == LB_OUT_F32)

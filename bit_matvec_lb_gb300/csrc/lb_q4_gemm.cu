@@ -1,0 +1,745 @@
+// lb_q4_gemm.cu -- products of 4-bit weights with group scales for many tokens, on the 5th-generation
+// tensor cores.
+//
+// Mathematics.  D[n][t] = sum_k w[n][k] x[t][k], 128 weight rows (the accumulator's lanes) times up to
+// 256 tokens.  The weights are expanded once per item by eight warps, a thread per row, from 16-byte loads
+// of codes straight into tensor memory, from where the tensor cores read them as their first operand; x
+// comes through shared memory.  Two forms:
+//   bf16 tensors: the operand is d (c - z), rounded to fp16's 11 bits (an eighth of a bf16
+//     output's own rounding); the accumulator runs over all of K.
+//   fp32 tensors: the operand is c - z, exact; x enters as two fp16 parts, one product each; the sums of
+//     a group leave the accumulator, of which there are two in turn, and are added to binary32 sums in
+//     registers with the group's scale.  (The tensor cores cut what lies below an accumulator's last
+//     place downwards at every step of 16: over a long row that is far more than binary32 rounding.)
+// Rows of x are scaled by powers of two into fp16's range beforehand (q4_rows), and stored in the order
+// in which the codes of a word unfold, pairs (0, 4), (1, 5), (2, 6), (3, 7).
+//
+// One CTA per SM, 20 warps: eight that take the sums out (a quarter of the lanes times half of
+// the columns each), eight that expand weights, three that copy x in (16-byte asynchronous copies by rows,
+// so an expert's tokens need not lie together), one that issues the tensor-core operations.  Calls with
+// few tiles are split along K over a cluster; the parts are added up through distributed shared memory.
+#include "lb_q4.cuh"
+#include "lb_tc.cuh"
+
+#include <algorithm>
+
+namespace lb {
+
+constexpr int kGmRows = 128;
+constexpr int kGmStep = 64;              // columns of K of a stage
+constexpr int kGmOutWarps = 8, kGmExpandWarps = 8, kGmCopyWarps = 3;
+constexpr int kGmWarps = kGmOutWarps + kGmExpandWarps + kGmCopyWarps + 1;
+constexpr int kGmThreads = 32 * kGmWarps;
+constexpr int kGmOutThreads = 32 * kGmOutWarps;
+constexpr int kGmB = 32768;              // bytes of a stage of x
+constexpr int kGmBStages = 6;
+constexpr int kGmAStages = 8;            // of expanded weights, 32 columns of tensor memory each
+constexpr int kGmABase = 256;            // they lie behind the accumulators
+constexpr int kGmLag = 3;                // copies of x in flight before a stage is handed on
+constexpr int kGmAhead = 4;              // steps of codes in registers
+constexpr int kGmMaxSplit = 8;
+constexpr int kGmSmem = kGmBStages * kGmB;
+
+struct GmLaunch {
+    int steps;        // of K, of a CTA
+    int split;        // CTAs along K
+    int tiles;        // of weight rows
+};
+
+struct GmBars {
+    uint64_t a_full[kGmAStages], a_empty[kGmAStages];
+    uint64_t b_full[kGmBStages], b_empty[kGmBStages];
+    uint64_t d_full[2], d_empty[2], done;
+};
+
+constexpr uint32_t gm_desc_high() { return ((1024 >> 4) & 0x3FFF) | 1u << 14; }
+__device__ __forceinline__ uint32_t gm_desc_low(uint32_t saddr) {
+    return ((saddr >> 4) & 0x3FFF) | (uint32_t)(128 >> 4) << 16;
+}
+// D[tmem] (+)= A[tmem] * B[desc]^T over 64 of K.
+__device__ __forceinline__ void gm_mma4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 b; .reg .b32 a;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5}; mov.b32 a, %1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "add.s32 a, a, 8; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+        "add.s32 a, a, 8; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+        "add.s32 a, a, 8; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(gm_desc_high())
+        : "memory");
+}
+// The same over 32 of K.
+__device__ __forceinline__ void gm_mma2(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
+                                        uint32_t accumulate) {
+    asm volatile(
+        "{ .reg .pred p; .reg .b64 b; .reg .b32 a;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "mov.b64 b, {%2, %5}; mov.b32 a, %1;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
+        "setp.eq.b32 p, 0, 0;\n\t"
+        "add.s32 a, a, 8; add.s64 b, b, 16;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p; }" ::"r"(d),
+        "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(gm_desc_high())
+        : "memory");
+}
+__device__ __forceinline__ bool gm_elect() {
+    uint32_t x;
+    asm volatile("{ .reg .pred p; elect.sync _|p, 0xffffffff; selp.u32 %0, 1, 0, p; }" : "=r"(x));
+    return x != 0;
+}
+__device__ __forceinline__ void gm_tmem_st16(uint32_t taddr, const uint32_t *r) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]),
+        "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
+
+// Eight codes of a word less the zero, times the scale: pairs (0, 4), (1, 5), (2, 6), (3, 7) of fp16.  The codes
+// go under the exponent of 1024, at the last place or (times 16) four above it.
+// low: 1024 + z twice, high: -(64 + z) twice.
+template <bool SCALED>
+__device__ __forceinline__ void expand_f16(uint32_t w, __half2 low, __half2 high, __half2 d, uint32_t *r) {
+    const __half2 sixteenth = half2_of(0x2C002C00u);
+    const uint32_t s = w >> 8;
+    uint32_t v[4];
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(v[0]) : "r"(w));
+    asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(v[1]) : "r"(w));
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(v[2]) : "r"(s));
+    asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(v[3]) : "r"(s));
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        __half2 h = i & 1 ? __hfma2(half2_of(v[i]), sixteenth, high) : __hsub2(half2_of(v[i]), low);
+        if (SCALED) h = __hmul2(h, d);
+        r[i] = bits_of(h);
+    }
+}
+
+__device__ __forceinline__ void gm_store(float *p, float v) { *p = v; }
+__device__ __forceinline__ void gm_store(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
+
+__device__ __forceinline__ float gm_cluster_load(const float *p, uint32_t rank) {
+    uint32_t a;
+    float v;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
+    return v;
+}
+__device__ __forceinline__ void gm_cluster_sync() {
+    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+}
+
+// An item: up to kTokens tokens (of one expert) times one tile of weight rows.
+struct GmItem {
+    int expert, t0, tokens, tile;
+};
+
+// T: the tensors' type.  F32: their two-part form.
+template <Q4Use USE, typename T, int GROUP, bool ZEROS>
+__global__ void __launch_bounds__(kGmThreads, 1)
+    q4_gemm_kernel(const __grid_constant__ Q4Params p, const __grid_constant__ Q4Rows r,
+                   const __grid_constant__ GmLaunch l, const uint8_t *codes) {
+    constexpr bool F32 = sizeof(T) == 4;
+    constexpr int kTokens = F32 ? 128 : 256;
+    constexpr int kParts = F32 ? 2 : 1;
+    constexpr int kCols = kTokens / 2;           // of an output warp
+    extern __shared__ __align__(1024) uint8_t smem[];
+    __shared__ GmBars bar;
+    __shared__ uint32_t s_tmem;
+    __shared__ int s_first[USE == kQ4Dense ? 1 : LB_ROUTE_MAX_EXPERTS + 1];  // pieces before an expert's
+    __shared__ int s_part[32];
+    __shared__ float col_scale[kTokens];
+    __shared__ int col_row[kTokens];
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int rank = blockIdx.x % l.split;
+
+    if (tid == 0) {
+        for (int i = 0; i < kGmAStages; i++) mbar_init(&bar.a_full[i], 4), mbar_init(&bar.a_empty[i], 1);
+        for (int i = 0; i < kGmBStages; i++) mbar_init(&bar.b_full[i], kGmCopyWarps), mbar_init(&bar.b_empty[i], 1);
+        for (int i = 0; i < 2; i++) mbar_init(&bar.d_full[i], 1), mbar_init(&bar.d_empty[i], kGmOutWarps);
+        mbar_init(&bar.done, 1);
+        fence_mbar_init();
+    }
+    pdl_wait();
+    // Pieces of at most kTokens tokens: their number, and where an expert's begin.
+    int pieces;
+    if constexpr (USE == kQ4Dense) {
+        pieces = (int)((p.T + kTokens - 1) / kTokens);
+    } else {
+        constexpr int kEach = (LB_ROUTE_MAX_EXPERTS + kGmThreads - 1) / kGmThreads;
+        int n[kEach], sum = 0;
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            const int e = tid * kEach + i;
+            n[i] = 0;
+            if (e < p.E) {
+                const int first = min(max(p.start[e], 0), (int)p.T);
+                n[i] = (max(min(p.start[e + 1], (int)p.T) - first, 0) + kTokens - 1) / kTokens;
+            }
+            sum += n[i];
+        }
+        int run = sum;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += w;
+        }
+        if (lane == 31) s_part[warp] = run;
+        __syncthreads();
+        int before = run - sum, total = 0;
+        for (int w = 0; w < kGmWarps; w++) {
+            before += w < warp ? s_part[w] : 0;
+            total += s_part[w];
+        }
+#pragma unroll
+        for (int i = 0; i < kEach; i++) {
+            if (tid * kEach + i < p.E) s_first[tid * kEach + i] = before;
+            before += n[i];
+        }
+        if (tid == 0) s_first[p.E] = total;
+        pieces = total;
+    }
+    // Tensor memory is taken when the kernels before this one have ended, and the next one may start only after
+    // it: neither waits for the other's columns.
+    if (warp == kGmWarps - 1) tmem_alloc(&s_tmem, 512);
+    tc_fence_before();
+    __syncthreads();
+    tc_fence_after();
+    pdl_launch_dependents();
+    const uint32_t tmem = s_tmem;
+    const int64_t items = (int64_t)pieces * l.tiles;
+    const int64_t each = gridDim.x / l.split;
+    auto item_of = [&](int64_t i) {
+        GmItem it;
+        const int piece = (int)(i / l.tiles);
+        it.tile = (int)(i % l.tiles);
+        if constexpr (USE == kQ4Dense) {
+            it.expert = 0;
+            it.t0 = piece * kTokens;
+            it.tokens = (int)min((int64_t)kTokens, p.T - it.t0);
+        } else {
+            int lo = 0, hi = p.E;   // the last expert whose pieces begin at or before this one
+            while (hi - lo > 1) {
+                const int m = (lo + hi) / 2;
+                if (s_first[m] <= piece) lo = m;
+                else hi = m;
+            }
+            it.expert = lo;
+            const int first = min(max(p.start[lo], 0), (int)p.T), end = min(p.start[lo + 1], (int)p.T);
+            it.t0 = first + (piece - s_first[lo]) * kTokens;
+            it.tokens = min(kTokens, end - it.t0);
+        }
+        return it;
+    };
+    // Row of the weights (among all matrices' rows) that a lane of the accumulator holds, and whether it is one.
+    const int64_t matrix_rows = USE == kQ4Up ? 2 * p.N : p.N;
+    auto row_of = [&](const GmItem &it, int at, bool &in) -> int64_t {
+        if (USE == kQ4Up) {   // 16 gate rows, then the same 16 up rows
+            const int64_t n = it.tile * (int64_t)(kGmRows / 2) + (at >> 5) * 16 + (at & 15);
+            in = n < p.N;
+            return it.expert * matrix_rows + (at & 16 ? p.N : 0) + n;
+        }
+        const int64_t n = it.tile * (int64_t)kGmRows + at;
+        in = n < p.N;
+        return it.expert * matrix_rows + n;
+    };
+    const int k0 = rank * l.steps * kGmStep;                             // this CTA's slice of K
+    const int columns = min(p.K - k0, l.steps * kGmStep);
+    const int steps = (columns + kGmStep - 1) / kGmStep;
+
+    // Bounded: about 2 s (2000 tries of up to a millisecond), after the first that ran out a few tries.
+    int tries = 2000;
+    auto wait = [&](uint64_t &b, uint32_t parity) {
+        int i = 0;
+        while (!mbar_try_wait_hint(&b, parity & 1, 1000000u) && i < tries) i++;
+        if (i >= tries) {
+            *p.error = 1;
+            tries = 4;
+        }
+        __syncwarp();
+    };
+
+    if (warp < kGmOutWarps) {
+        // =================== sums out: a lane per weight row ===================
+        const int quarter = warp & 3, c0 = (warp >> 2) * kCols;
+        const uint32_t at_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        uint32_t turn = 0;   // accumulators taken so far
+        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+            const GmItem it = item_of(i);
+            named_sync(1, kGmOutThreads);   // the last item's columns are done with
+            for (int c = tid; c < it.tokens; c += kGmOutThreads) {
+                int from = it.t0 + c, to = from;
+                if (USE != kQ4Dense) {
+                    const int pair = p.order[it.t0 + c];
+                    const bool in = pair >= 0 && pair < p.T;
+                    if (USE == kQ4Up) from = in ? pair / p.k : -1;
+                    else to = in ? pair : -1;
+                }
+                col_scale[c] = from >= 0 ? r.row_scale[from] : 0.f;
+                col_row[c] = to;
+            }
+            named_sync(1, kGmOutThreads);
+            bool in;
+            const int64_t row = row_of(it, quarter * 32 + lane, in);
+            const int mine = min(max(it.tokens - c0, 0), kCols);   // columns of this warp
+            // where a finished sum goes
+            auto put = [&](int c, float v) {
+                const int to = col_row[c0 + c];
+                if (USE == kQ4Dense)
+                    gm_store(static_cast<T *>(p.y) + to * p.y_stride + row, v);
+                else if (to >= 0)
+                    static_cast<float *>(p.y)[to * p.y_stride + (row - it.expert * matrix_rows)] = v;
+            };
+            // gate and up rows of a column pair meet: lanes 0..15 make h of column c, 16..31 of c + 1
+            auto put_up = [&](int c, float a, float b) {
+                a *= col_scale[c0 + c];
+                b *= col_scale[c0 + min(c + 1, mine - 1)];
+                const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? b : a, 16);
+                const float gate = lane < 16 ? a : other, up = lane < 16 ? other : b;
+                const int col = c + (lane >> 4);
+                const int64_t n = it.tile * (int64_t)(kGmRows / 2) + quarter * 16 + (lane & 15);
+                if (col < mine && n < p.N)
+                    static_cast<float *>(p.y)[(int64_t)col_row[c0 + col] * p.y_stride + n] =
+                        gate / (1.f + expf(-gate)) * up;
+            };
+            float *park = reinterpret_cast<float *>(smem) + quarter * 32 + lane;   // [column][128]
+            if constexpr (F32) {
+                uint64_t total[kCols / 2];   // pairs of columns
+#pragma unroll
+                for (int c = 0; c < kCols / 2; c++) total[c] = 0;
+                auto sum_of = [&](int c) { return __uint_as_float((uint32_t)(total[c / 2] >> (32 * (c & 1)))); };
+                const uint16_t *ds = p.scales + (in ? row : 0) * p.pitch + k0 / GROUP;
+                const int groups = columns / GROUP;
+                float d = f16_bits_to_float(ds[0]);
+                for (int g = 0; g < groups; g++, turn++) {
+                    const float next = f16_bits_to_float(ds[min(g + 1, groups - 1)]);
+                    wait(bar.d_full[turn & 1], turn >> 1);
+                    tc_fence_after();
+                    const uint64_t d2 = (uint64_t)__float_as_uint(d) << 32 | __float_as_uint(d);
+#pragma unroll
+                    for (int q = 0; q < kCols / 16; q++) {
+                        if (16 * q >= mine) break;
+                        uint64_t v[8];
+                        tmem_ld16_pairs(at_lane + (turn & 1) * kTokens + c0 + 16 * q, v);
+#pragma unroll
+                        for (int c = 0; c < 8; c++) ffma2p(total[8 * q + c], v[c], d2);
+                    }
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.d_empty[turn & 1]);
+                    d = next;
+                }
+                if (l.split > 1) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c++)
+                        if (c < mine) park[(c0 + c) * kGmRows] = sum_of(c);
+                } else if (USE == kQ4Up) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c += 2)
+                        if (c < mine) put_up(c, sum_of(c), sum_of(c + 1));
+                } else if (in) {
+#pragma unroll
+                    for (int c = 0; c < kCols; c++)
+                        if (c < mine) put(c, sum_of(c) * col_scale[c0 + c]);
+                }
+            } else {
+                wait(bar.d_full[0], turn);
+                tc_fence_after();
+#pragma unroll 1
+                for (int q = 0; q < kCols / 32; q++) {
+                    if (32 * q >= mine) break;
+                    uint32_t v[32];
+                    __syncwarp();
+                    tmem_ld32(at_lane + c0 + 32 * q, v);
+                    if (l.split > 1) {
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (32 * q + c < mine) park[(c0 + 32 * q + c) * kGmRows] = __uint_as_float(v[c]);
+                    } else if (USE == kQ4Up) {
+#pragma unroll
+                        for (int c = 0; c < 32; c += 2)
+                            if (32 * q + c < mine)
+                                put_up(32 * q + c, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
+                    } else if (in) {
+#pragma unroll
+                        for (int c = 0; c < 32; c++)
+                            if (32 * q + c < mine)
+                                put(32 * q + c, __uint_as_float(v[c]) * col_scale[c0 + 32 * q + c]);
+                    }
+                }
+                turn++;
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.d_empty[0]);
+            }
+        }
+    } else if (warp < kGmOutWarps + kGmExpandWarps) {
+        // =================== weights: a thread per row, every other step ===================
+        const int quarter = warp & 3, half = (warp - kGmOutWarps) >> 2;
+        const uint32_t to = tmem + kGmABase + ((uint32_t)(quarter * 32) << 16);
+        constexpr int kPer = GROUP == 32 ? 2 : 1;   // groups of a step
+        uint32_t turn = 0;   // this CTA's steps so far
+        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+            const GmItem it = item_of(i);
+            bool in;
+            const int64_t row = row_of(it, quarter * 32 + lane, in);
+            const uint8_t *src = codes + (in ? row : 0) * (p.K / 2) + k0 / 2;
+            const uint16_t *ds = p.scales + (in ? row : 0) * p.pitch + k0 / GROUP;
+            const uint8_t *zs = ZEROS ? p.zeros + (in ? row : 0) * p.pitch + k0 / GROUP : nullptr;
+            uint4 w[kGmAhead][2];
+            uint32_t d[kGmAhead], z[kGmAhead];
+            // the step's own half of the steps: turn + s, with the same parity as `half`
+            const int s0 = (half ^ turn) & 1;
+            auto load = [&](int j, int s) {
+                if (s >= steps) return;
+                w[j][0] = ldg_stream(src + s * (kGmStep / 2));
+                w[j][1] = s * kGmStep + 32 < columns ? ldg_stream(src + s * (kGmStep / 2) + 16) : make_uint4(0, 0, 0, 0);
+                const int g = s * kGmStep / GROUP;
+                if (!F32) d[j] = kPer == 2 ? *reinterpret_cast<const uint32_t *>(ds + g) : ds[g];
+                if (ZEROS) z[j] = kPer == 2 ? *reinterpret_cast<const uint16_t *>(zs + g) : zs[g];
+            };
+#pragma unroll
+            for (int j = 0; j < kGmAhead; j++) load(j, s0 + 2 * j);
+            for (int sb = s0; sb < steps; sb += 2 * kGmAhead) {
+#pragma unroll
+                for (int j = 0; j < kGmAhead; j++) {
+                    const int s = sb + 2 * j;
+                    if (s >= steps) break;
+                    const uint32_t stage = (turn + s) % kGmAStages, round = (turn + s) / kGmAStages;
+                    wait(bar.a_empty[stage], round ^ 1);
+                    tc_fence_after();
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const uint32_t zh = ZEROS ? (kPer == 2 ? z[j] >> (8 * h) & 0xff : z[j]) : 8u;
+                        const __half2 low = half2_of(0x64006400u + zh * 0x10001u);   // 1024 + z
+                        // 64 + z has its last place at 2^-4
+                        const __half2 high = half2_of(0xD400D400u + zh * 0x00100010u);
+                        const uint32_t dh = F32 ? 0 : (kPer == 2 ? (h ? d[j] >> 16 : d[j] & 0xffff) : d[j]) * 0x10001u;
+                        uint32_t v[16];
+                        const uint4 c = w[j][h];
+                        if (s * kGmStep + 32 * h < columns) {
+                            expand_f16<!F32>(c.x, low, high, half2_of(dh), v);
+                            expand_f16<!F32>(c.y, low, high, half2_of(dh), v + 4);
+                            expand_f16<!F32>(c.z, low, high, half2_of(dh), v + 8);
+                            expand_f16<!F32>(c.w, low, high, half2_of(dh), v + 12);
+                        } else {
+#pragma unroll
+                            for (int e = 0; e < 16; e++) v[e] = 0;
+                        }
+                        gm_tmem_st16(to + stage * 32 + 16 * h, v);
+                    }
+                    load(j, s + 2 * kGmAhead);
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.a_full[stage]);
+                }
+            }
+            turn += steps;
+        }
+    } else if (warp < kGmOutWarps + kGmExpandWarps + kGmCopyWarps) {
+        // =================== x: 8 rows x 4 chunks of 16 bytes an instruction ===================
+        const int cw = warp - kGmOutWarps - kGmExpandWarps;
+        constexpr int kRowGroups = (kTokens / 8 + kGmCopyWarps - 1) / kGmCopyWarps;   // of a warp
+        const uint16_t *x = static_cast<const uint16_t *>(p.x);
+        uint32_t turn = 0;
+        auto hand_on = [&](uint32_t s) {
+            fence_proxy_async_smem();
+            __syncwarp();
+            if (lane == 0) mbar_arrive(&bar.b_full[s % kGmBStages]);
+        };
+        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+            const GmItem it = item_of(i);
+            int from[kRowGroups];
+#pragma unroll
+            for (int q = 0; q < kRowGroups; q++) {
+                const int c = (q * kGmCopyWarps + cw) * 8 + (lane & 7);
+                from[q] = -1;
+                if (c < it.tokens) {
+                    from[q] = it.t0 + c;
+                    if (USE == kQ4Up) {
+                        const int pair = p.order[it.t0 + c];
+                        from[q] = pair >= 0 && pair < p.T ? pair / p.k : -1;
+                    }
+                }
+            }
+            const int used = (it.tokens + 15) / 16 * 2;   // groups of 8 rows that the products read
+            for (int s = 0; s < steps; s++, turn++) {
+                const uint32_t stage = turn % kGmBStages;
+                wait(bar.b_empty[stage], (turn / kGmBStages) ^ 1);
+                const uint32_t dst = smem_u32(smem) + stage * kGmB + (lane & 7) * 16;
+#pragma unroll
+                for (int q = 0; q < kRowGroups; q++) {
+                    const int rg = q * kGmCopyWarps + cw;
+                    if (rg >= used) break;
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        const int chunk = 4 * h + (lane >> 3), k = s * kGmStep + chunk * 8;
+                        const bool there = from[q] >= 0 && k < columns;
+                        const uint16_t *src = x + (there ? from[q] * p.x_stride + k0 + k : 0);
+                        const uint32_t at = dst + rg * 1024 + chunk * 128;
+                        const int bytes = there ? 16 : 0;   // (the rest is zeros)
+#pragma unroll
+                        for (int part = 0; part < kParts; part++)
+                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                                             at + part * (kGmB / 2)),
+                                         "l"(src + part * r.plane), "r"(bytes)
+                                         : "memory");
+                    }
+                }
+                asm volatile("cp.async.commit_group;" ::: "memory");
+                if (turn >= kGmLag) {
+                    asm volatile("cp.async.wait_group %0;" ::"n"(kGmLag) : "memory");
+                    hand_on(turn - kGmLag);
+                }
+            }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (uint32_t s = turn > kGmLag ? turn - kGmLag : 0; s < turn; s++) hand_on(s);
+    } else {
+        // =================== tensor-core operations ===================
+        uint32_t turn = 0, taken = 0;   // steps, accumulators
+        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+            const GmItem it = item_of(i);
+            const uint32_t idesc = idesc_f16(kGmRows, (it.tokens + 15) / 16 * 16);
+            if (!F32) wait(bar.d_empty[0], taken ^ 1);
+            for (int s = 0; s < steps; s++, turn++) {
+                const uint32_t sa = turn % kGmAStages, sb = turn % kGmBStages;
+                wait(bar.a_full[sa], turn / kGmAStages);
+                wait(bar.b_full[sb], turn / kGmBStages);
+                tc_fence_after();
+                const uint32_t a = tmem + kGmABase + sa * 32, b = gm_desc_low(smem_u32(smem) + sb * kGmB);
+                if constexpr (!F32) {
+                    if (gm_elect()) gm_mma4(tmem, a, b, idesc, s > 0);
+                } else {
+                    constexpr int kTurns = GROUP == 32 ? 2 : 1;   // accumulators of a step
+#pragma unroll
+                    for (int h = 0; h < kTurns; h++) {
+                        if (s * kGmStep + 32 * h >= columns) break;
+                        const bool begin = GROUP < 128 || s % 2 == 0;
+                        const uint32_t buf = taken & 1, d = tmem + buf * kTokens;
+                        if (begin) {
+                            wait(bar.d_empty[buf], (taken >> 1) ^ 1);
+                            tc_fence_after();
+                        }
+                        if (gm_elect()) {
+                            if (GROUP == 32) {
+                                gm_mma2(d, a + 16 * h, b + 32 * h, idesc, 0);
+                                gm_mma2(d, a + 16 * h, b + 32 * h + (kGmB / 2 >> 4), idesc, 1);
+                            } else {
+                                gm_mma4(d, a, b, idesc, !begin);
+                                gm_mma4(d, a, b + (kGmB / 2 >> 4), idesc, 1);
+                            }
+                        }
+                        __syncwarp();
+                        if (GROUP < 128 || s % 2 == 1) {
+                            if (gm_elect()) mma_commit(&bar.d_full[buf]);
+                            taken++;
+                        }
+                    }
+                }
+                __syncwarp();
+                if (gm_elect()) {
+                    mma_commit(&bar.a_empty[sa]);
+                    mma_commit(&bar.b_empty[sb]);
+                }
+                __syncwarp();
+            }
+            if (!F32) {
+                if (gm_elect()) mma_commit(&bar.d_full[0]);
+                __syncwarp();
+                taken++;
+            }
+        }
+        if (gm_elect()) mma_commit(&bar.done);
+        __syncwarp();
+        wait(bar.done, 0);
+        tc_fence_before();
+    }
+    __syncthreads();
+    tc_fence_after();
+    if (l.split > 1) {
+        // one item per cluster: its parts' sums, a share of the columns per CTA, a warp per column
+        gm_cluster_sync();
+        const int64_t i = blockIdx.x / l.split;
+        if (i < items) {
+            const GmItem it = item_of(i);
+            const float *park = reinterpret_cast<const float *>(smem);
+            for (int c = rank + l.split * warp; c < it.tokens; c += l.split * kGmWarps) {
+                const float scale = col_scale[c];
+                const int to = col_row[c];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const int at = j * 32 + lane;
+                    float v = 0.f;
+                    for (int q = 0; q < l.split; q++) v += gm_cluster_load(park + c * kGmRows + at, q);
+                    v *= scale;
+                    bool in;
+                    const int64_t row = row_of(it, at, in);
+                    if (USE == kQ4Up) {
+                        const float up = __shfl_xor_sync(0xffffffffu, v, 16);
+                        if (lane < 16 && in)
+                            static_cast<float *>(p.y)[to * p.y_stride + (row - it.expert * matrix_rows)] =
+                                v / (1.f + expf(-v)) * up;
+                    } else if (in) {
+                        if (USE == kQ4Dense) gm_store(static_cast<T *>(p.y) + to * p.y_stride + row, v);
+                        else if (to >= 0)
+                            static_cast<float *>(p.y)[to * p.y_stride + (row - it.expert * matrix_rows)] = v;
+                    }
+                }
+            }
+        }
+        gm_cluster_sync();
+    }
+    if (warp == kGmWarps - 1) tmem_dealloc(tmem, 512);
+}
+
+// ------------------------------------------------------------------------------------------
+// Rows of x for the tensor cores: scaled so that the largest lies in [2^14, 2^15), in fp16 (one part, or two
+// that hold 22 bits), each eight columns in the order 0 4 1 5 2 6 3 7.
+// ------------------------------------------------------------------------------------------
+constexpr int kRowThreads = 128;
+constexpr int kRowHold = 4;   // groups of eight columns that a thread keeps between its two passes
+
+template <typename X, int PARTS>
+__global__ void __launch_bounds__(kRowThreads)
+    q4_rows_kernel(const X *x, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, uint16_t *to,
+                   int64_t plane, float *row_scale) {
+    __shared__ float most[kRowThreads / 32];
+    const int tid = threadIdx.x;
+    pdl_launch_dependents();
+    pdl_wait();
+    const int64_t row = blockIdx.x;
+    if (n_opt && row >= min(max(*n_opt, 0), (int)n)) return;
+    const X *src = x + row * x_stride;
+    const int units = K / 8;
+    float held[kRowHold][8], m = 0.f;
+#pragma unroll
+    for (int h = 0; h < kRowHold; h++) {
+        const int u = tid + h * kRowThreads;
+        if (u >= units) break;
+        load8(src + 8 * u, held[h]);
+#pragma unroll
+        for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(held[h][j]));
+    }
+    for (int u = tid + kRowHold * kRowThreads; u < units; u += kRowThreads) {
+        float v[8];
+        load8(src + 8 * u, v);
+#pragma unroll
+        for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
+    }
+#pragma unroll
+    for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
+    if ((tid & 31) == 0) most[tid >> 5] = m;
+    __syncthreads();
+    m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    // 2^(14 - e) for m in [2^e, 2^(e + 1)), kept to powers whose inverse is normal too
+    const int e = min(max(268 - (int)(__float_as_uint(m) >> 23), 1), 253);
+    const float up = __uint_as_float((uint32_t)e << 23);
+    if (tid == 0) row_scale[row] = __uint_as_float((uint32_t)(254 - e) << 23);
+    auto put = [&](int u, const float (&v)[8]) {
+        uint32_t hi[4], lo[4];
+#pragma unroll
+        for (int j = 0; j < 4; j++) {
+            const float a = v[j] * up, b = v[j + 4] * up;
+            const __half2 h = __floats2half2_rn(a, b);
+            hi[j] = bits_of(h);
+            if (PARTS == 2) lo[j] = bits_of(__floats2half2_rn(a - __low2float(h), b - __high2float(h)));
+        }
+        uint16_t *dst = to + row * K + 8 * u;
+        *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
+        if (PARTS == 2) *reinterpret_cast<uint4 *>(dst + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+    };
+#pragma unroll
+    for (int h = 0; h < kRowHold; h++) {
+        const int u = tid + h * kRowThreads;
+        if (u >= units) break;
+        put(u, held[h]);
+    }
+    for (int u = tid + kRowHold * kRowThreads; u < units; u += kRowThreads) {
+        float v[8];
+        load8(src + 8 * u, v);
+        put(u, v);
+    }
+}
+
+int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, int parts,
+            uint16_t *to, int64_t plane, float *row_scale, cudaStream_t st) {
+    const dim3 grid((unsigned)n), block(kRowThreads);
+    if (f32) {
+        auto kernel = parts == 2 ? q4_rows_kernel<float, 2> : q4_rows_kernel<float, 1>;
+        return launch_pdl(kernel, grid, block, 0, st, static_cast<const float *>(x), x_stride, n, K, n_opt, to,
+                          plane, row_scale);
+    }
+    return launch_pdl(q4_rows_kernel<__nv_bfloat16, 1>, grid, block, 0, st,
+                      static_cast<const __nv_bfloat16 *>(x), x_stride, n, K, n_opt, to, plane, row_scale);
+}
+
+template <Q4Use USE, typename T, int GROUP>
+static int launch_gemm(const Q4Params &p, const Q4Rows &r, const GmLaunch &l, unsigned grid, const uint8_t *codes,
+                       cudaStream_t st) {
+    auto kernel = p.zeros ? q4_gemm_kernel<USE, T, GROUP, true> : q4_gemm_kernel<USE, T, GROUP, false>;
+    int per_sm;
+    if (int e = prepare_kernel((const void *)kernel, kGmThreads, kGmSmem, &per_sm)) return e;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(grid), cfg.blockDim = dim3(kGmThreads), cfg.dynamicSmemBytes = kGmSmem, cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = (unsigned)l.split, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr, cfg.numAttrs = l.split > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, r, l, codes);
+    if (e == cudaSuccess) return LB_OK;
+    record_cuda_error(e);
+    return LB_ERR_LAUNCH;
+}
+
+template <Q4Use USE, typename T>
+static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *codes, int sms, cudaStream_t st) {
+    const int tokens = sizeof(T) == 4 ? 128 : 256, rows = USE == kQ4Up ? kGmRows / 2 : kGmRows;
+    GmLaunch l;
+    const int64_t tiles = (p.N + rows - 1) / rows, pieces = (p.T + tokens - 1) / tokens;
+    l.tiles = (int)tiles;
+    const int steps = (p.K + kGmStep - 1) / kGmStep;
+    l.split = 1, l.steps = steps;
+    int64_t items = tiles * pieces;
+    if (USE != kQ4Dense) items = tiles * std::min(p.T, std::min((int64_t)p.E, p.T) + p.T / tokens);
+    if (USE == kQ4Dense && items * 2 <= sms) {
+        // slices of an even number of steps (whole groups), at least four
+        l.split = (int)std::min<int64_t>({(int64_t)sms / items, (int64_t)kGmMaxSplit, (int64_t)std::max(steps / 4, 1)});
+        l.steps = (steps + l.split - 1) / l.split;
+        l.steps = (l.steps + 1) / 2 * 2;
+        l.split = (steps + l.steps - 1) / l.steps;
+    }
+    const unsigned grid = (unsigned)(std::min<int64_t>(items * l.split, l.split > 1 ? items * l.split : sms));
+    switch (p.group) {
+        case 32: return launch_gemm<USE, T, 32>(p, r, l, grid, codes, st);
+        case 64: return launch_gemm<USE, T, 64>(p, r, l, grid, codes, st);
+        default: return launch_gemm<USE, T, 128>(p, r, l, grid, codes, st);
+    }
+}
+
+int q4_gemm(const Q4Params &p, const Q4Rows &r, Q4Use use, int type, const uint8_t *codes, int64_t rows,
+            int sms, cudaStream_t st) {
+    const bool f32 = type == LB_OUT_F32;
+    if (use == kQ4Dense)
+        return f32 ? dispatch_gemm<kQ4Dense, float>(p, r, codes, sms, st)
+                   : dispatch_gemm<kQ4Dense, __nv_bfloat16>(p, r, codes, sms, st);
+    if (use == kQ4Up)
+        return f32 ? dispatch_gemm<kQ4Up, float>(p, r, codes, sms, st)
+                   : dispatch_gemm<kQ4Up, __nv_bfloat16>(p, r, codes, sms, st);
+    return f32 ? dispatch_gemm<kQ4Down, float>(p, r, codes, sms, st)
+               : dispatch_gemm<kQ4Down, __nv_bfloat16>(p, r, codes, sms, st);
+}
+
+}  // namespace lb

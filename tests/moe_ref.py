@@ -36,12 +36,14 @@ def product(x, w, dtype, tokens=None):
     is left is binary32 addition, cut on the tensor cores: per group 8 steps (24 with three parts) that
     lose below 2^-22 of its magnitudes each, then at most 1024 groups in up to eight chains, 2^-24 each
     of all of it: below 1e-5 of the sum of magnitudes.  More bf16 tokens: weights rounded to 11 bits,
-    2^-11 of the magnitudes; fp32: both factors to 22 bits, sums cut as above."""
+    2^-11 of the magnitudes; fp32: x to 22 bits, sums cut as above.  A row of more tokens is scaled so that its
+    largest value lies below 2^15, and fp16's last place is 2^-24 (half of it is lost): 2^-39 of that value."""
     xd = x.double()
     y, mag = xd @ w.t(), xd.abs() @ w.abs().t()
     many = (x.shape[0] if tokens is None else tokens) > 8
     rel = 2.0 ** -11 if dtype == torch.bfloat16 and many else 1e-5
-    return y, rel * mag + half_step(dtype) * y.abs() + 1e-30
+    lost = 2.0 ** -39 * xd.abs().amax(1, keepdim=True) * w.abs().sum(1)
+    return y, rel * mag + lost + half_step(dtype) * y.abs() + 1e-30
 
 
 def experts(x, up, down, group, ids, wts, dtype):
@@ -59,11 +61,13 @@ def experts(x, up, down, group, ids, wts, dtype):
         wu = weights(*(None if m is None else m[e] for m in up), H, group)
         wd = weights(*(None if m is None else m[e] for m in down), F, group)
         xe = x[t].double()
-        both, mag = xe @ wu.t(), xe.abs() @ wu.abs().t()
+        both = xe @ wu.t()
+        mag = xe.abs() @ wu.abs().t() + 2.0 ** -39 / rel * xe.abs().amax(1, keepdim=True) * wu.abs().sum(1)
         g, u, dg, du = both[:, :F], both[:, F:], rel * mag[:, :F], rel * mag[:, F:]
         s = g * torch.sigmoid(g)
         h = s * u
-        dh = 1.1 * dg * (u.abs() + du) + s.abs() * du + 2.0 ** -(15 if dtype == torch.bfloat16 else 22) * h.abs()
+        dh = 1.1 * dg * (u.abs() + du) + s.abs() * du + 2.0 ** -(11 if dtype == torch.bfloat16 else 22) * h.abs()
+        dh = dh + 2.0 ** -39 * h.abs().amax(1, keepdim=True)
         w = wts[t, j].double()[:, None]
         y.index_add_(0, t, w * (h @ wd.t()))
         off.index_add_(0, t, w.abs() * (dh @ wd.abs().t() + rel * (h.abs() + dh) @ wd.abs().t()))
