@@ -146,7 +146,8 @@ int encode_rows_map(CUtensorMap *map, const void *base, uint64_t row_bytes, uint
     const cuuint32_t estr[2] = {1, 1};
     const CUresult r = g_encode_tiled(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<void *>(base),
                                       dims, strides, box, estr, CU_TENSOR_MAP_INTERLEAVE_NONE,
-                                      swizzle_bytes == 64   ? CU_TENSOR_MAP_SWIZZLE_64B
+                                      swizzle_bytes == 128  ? CU_TENSOR_MAP_SWIZZLE_128B
+                                      : swizzle_bytes == 64 ? CU_TENSOR_MAP_SWIZZLE_64B
                                       : swizzle_bytes == 32 ? CU_TENSOR_MAP_SWIZZLE_32B
                                                             : CU_TENSOR_MAP_SWIZZLE_NONE,
                                       CU_TENSOR_MAP_L2_PROMOTION_L2_128B,

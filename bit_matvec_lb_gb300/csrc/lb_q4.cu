@@ -80,17 +80,13 @@ static int parts_of(int type) { return type == LB_OUT_F32 ? 2 : 1; }
 struct RowsAt {
     uint16_t *to;
     float *scale;
-    int64_t plane;
 };
 static size_t rows_bytes(int64_t n, int64_t K, int type) {
-    return align256((size_t)n * K * 2) * parts_of(type) + align256((size_t)n * 4);
+    return align256((size_t)n * K * 2 * parts_of(type)) + align256((size_t)n * 4);
 }
 static RowsAt rows_at(uint8_t *at, int64_t n, int64_t K, int type) {
-    RowsAt r;
-    const size_t one = align256((size_t)n * K * 2);
-    r.to = reinterpret_cast<uint16_t *>(at), r.plane = (int64_t)(one / 2);
-    r.scale = reinterpret_cast<float *>(at + one * parts_of(type));
-    return r;
+    return {reinterpret_cast<uint16_t *>(at),
+            reinterpret_cast<float *>(at + align256((size_t)n * K * 2 * parts_of(type)))};
 }
 
 // Pairs per expert from which the experts' products run on tcgen05: below, most of its tiles would be empty
@@ -144,16 +140,14 @@ LB_EXPORT int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uin
     DeviceInfo di;
     if (int e = current_device_info(&di)) return e;
     if (M == 0) return LB_OK;
-    Q4Params p = product_of(scales, zeros_opt, group, x, x_stride, y, y_stride, M, N, K);
+    const Q4Params p = product_of(scales, zeros_opt, group, x, x_stride, y, y_stride, M, N, K);
     if (!p.error) return LB_ERR_LAUNCH;
     cudaStream_t st = as_stream(stream);
     if (M <= 8) return q4_gemv(p, kQ4Dense, type, codes, N, di.sms, st);
     const RowsAt r = rows_at(static_cast<uint8_t *>(workspace), M, K, type);
-    if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, M, (int)K, nullptr, parts_of(type), r.to, r.plane, r.scale,
-                        st))
+    if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, M, (int)K, nullptr, parts_of(type), r.to, r.scale, st))
         return e;
-    p.x = r.to, p.x_stride = K;
-    return q4_gemm(p, {r.scale, r.plane}, kQ4Dense, type, codes, N, di.sms, st);
+    return q4_gemm(p, {r.to, r.scale, M}, kQ4Dense, type, codes, N, di.sms, st);
 }
 
 LB_EXPORT size_t lb_experts_q4_workspace_bytes(int64_t T, int E, int k, int64_t hidden, int64_t ffn,
@@ -210,15 +204,12 @@ LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T
     } else {
         const RowsAt xr = rows_at(ws + at.x, T, hidden, type), hr = rows_at(ws + at.h_rows, pairs, ffn, type);
         const int parts = parts_of(type);
-        if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, T, (int)hidden, nullptr, parts, xr.to, xr.plane,
-                            xr.scale, st))
+        if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, T, (int)hidden, nullptr, parts, xr.to, xr.scale, st))
             return e;
-        up.x = xr.to, up.x_stride = hidden;
-        if (int e = q4_gemm(up, {xr.scale, xr.plane}, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
-        if (int e = q4_rows(h, true, ffn, pairs, (int)ffn, expert_start + E, parts, hr.to, hr.plane, hr.scale, st))
+        if (int e = q4_gemm(up, {xr.to, xr.scale, T}, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
+        if (int e = q4_rows(h, true, ffn, pairs, (int)ffn, expert_start + E, parts, hr.to, hr.scale, st))
             return e;
-        down.x = hr.to;
-        if (int e = q4_gemm(down, {hr.scale, hr.plane}, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
+        if (int e = q4_gemm(down, {hr.to, hr.scale, pairs}, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
     }
     const int64_t blocks = (T * (hidden / 4) + kCombineThreads - 1) / kCombineThreads;
     if (blocks > 0x7fffffff) return LB_ERR_SHAPE;

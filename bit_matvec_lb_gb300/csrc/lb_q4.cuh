@@ -32,18 +32,19 @@ inline bool q4_type_ok(int type) { return type == LB_OUT_F32 || type == LB_OUT_B
 int q4_gemv(const Q4Params &p, Q4Use use, int type, const uint8_t *codes, int64_t rows, int sms,
             cudaStream_t st);
 
-// More tokens, on tcgen05: lb_q4_gemm.cu.  p.x is what q4_rows left: rows of K fp16 numbers (and with
-// fp32 tensors, `plane` elements behind, their second parts), each scaled by a power of two that
-// row_scale takes back.
+// More tokens, on tcgen05: lb_q4_gemm.cu.  r is what q4_rows left: rows of K fp16 numbers (and with
+// fp32 tensors, behind all of them, their second parts), each scaled by a power of two that row_scale
+// takes back.
 struct Q4Rows {
+    const uint16_t *x;
     const float *row_scale;
-    int64_t plane;
+    int64_t rows;        // of a part
 };
 int q4_gemm(const Q4Params &p, const Q4Rows &r, Q4Use use, int type, const uint8_t *codes, int64_t rows,
             int sms, cudaStream_t st);
 // rows [n][K] of x (fp32 if f32 else bf16), x_stride apart -> fp16 parts and row_scale.  n_opt: NULL, or where
 // the number of rows that are there lies.
 int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, int parts,
-            uint16_t *to, int64_t plane, float *row_scale, cudaStream_t st);
+            uint16_t *to, float *row_scale, cudaStream_t st);
 
 }  // namespace lb

@@ -14,10 +14,11 @@
 // Rows of x are scaled by powers of two into fp16's range beforehand (q4_rows), and stored in the order
 // in which the codes of a word unfold, pairs (0, 4), (1, 5), (2, 6), (3, 7).
 //
-// One CTA per SM, 20 warps: eight that take the sums out (a quarter of the lanes times half of
-// the columns each), eight that expand weights, three that copy x in (16-byte asynchronous copies by rows,
-// so an expert's tokens need not lie together), one that issues the tensor-core operations.  Calls with
-// few tiles are split along K over a cluster; the parts are added up through distributed shared memory.
+// One CTA per SM, 19 warps: eight that take the sums out (a quarter of the lanes times half of
+// the columns each), eight that expand weights, one that has codes copied in (tensor copies, 128 rows x 128
+// columns), one that has x copied in (tensor copies of 32 rows x 64 columns, or of four rows from anywhere for
+// an expert's tokens), one that issues the tensor-core operations.  Calls with few tiles are
+// split along K over a cluster; the parts are added up through distributed shared memory.
 #include "lb_q4.cuh"
 #include "lb_tc.cuh"
 
@@ -27,18 +28,21 @@ namespace lb {
 
 constexpr int kGmRows = 128;
 constexpr int kGmStep = 64;              // columns of K of a stage
-constexpr int kGmOutWarps = 8, kGmExpandWarps = 8, kGmCopyWarps = 3;
-constexpr int kGmWarps = kGmOutWarps + kGmExpandWarps + kGmCopyWarps + 1;
+constexpr int kGmOutWarps = 8, kGmExpandWarps = 8;
+constexpr int kGmCodeWarp = kGmOutWarps + kGmExpandWarps, kGmCopyWarp = kGmCodeWarp + 1;
+constexpr int kGmMmaWarp = kGmCopyWarp + 1;
+constexpr int kGmWarps = kGmMmaWarp + 1;
 constexpr int kGmThreads = 32 * kGmWarps;
 constexpr int kGmOutThreads = 32 * kGmOutWarps;
 constexpr int kGmB = 32768;              // bytes of a stage of x
-constexpr int kGmBStages = 6;
+constexpr int kGmBStages = 5;
+constexpr int kGmC = kGmRows * 64;       // bytes of a stage of codes: two steps
+constexpr int kGmCStages = 6;
 constexpr int kGmAStages = 8;            // of expanded weights, 32 columns of tensor memory each
 constexpr int kGmABase = 256;            // they lie behind the accumulators
-constexpr int kGmLag = 3;                // copies of x in flight before a stage is handed on
-constexpr int kGmAhead = 4;              // steps of codes in registers
+constexpr int kGmBox = 32;               // tokens of a copy
 constexpr int kGmMaxSplit = 8;
-constexpr int kGmSmem = kGmBStages * kGmB;
+constexpr int kGmSmem = kGmBStages * kGmB + kGmCStages * kGmC;
 
 struct GmLaunch {
     int steps;        // of K, of a CTA
@@ -49,13 +53,14 @@ struct GmLaunch {
 struct GmBars {
     uint64_t a_full[kGmAStages], a_empty[kGmAStages];
     uint64_t b_full[kGmBStages], b_empty[kGmBStages];
+    uint64_t c_full[kGmCStages], c_empty[kGmCStages];
     uint64_t d_full[2], d_empty[2], done;
 };
 
-constexpr uint32_t gm_desc_high() { return ((1024 >> 4) & 0x3FFF) | 1u << 14; }
-__device__ __forceinline__ uint32_t gm_desc_low(uint32_t saddr) {
-    return ((saddr >> 4) & 0x3FFF) | (uint32_t)(128 >> 4) << 16;
-}
+// Shared-memory matrix descriptor, K-major rows of 128 bytes under the 128-byte swizzle: eight rows are 1024
+// bytes, a step of 16 along K is 32 bytes further.
+constexpr uint32_t gm_desc_high() { return (1024 >> 4) | 1u << 14 | 2u << 29; }
+__device__ __forceinline__ uint32_t gm_desc_low(uint32_t saddr) { return ((saddr >> 4) & 0x3FFF) | 1u << 16; }
 // D[tmem] (+)= A[tmem] * B[desc]^T over 64 of K.
 __device__ __forceinline__ void gm_mma4(uint32_t d, uint32_t a, uint32_t b, uint32_t idesc,
                                         uint32_t accumulate) {
@@ -65,11 +70,11 @@ __device__ __forceinline__ void gm_mma4(uint32_t d, uint32_t a, uint32_t b, uint
         "mov.b64 b, {%2, %5}; mov.b32 a, %1;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
         "setp.eq.b32 p, 0, 0;\n\t"
-        "add.s32 a, a, 8; add.s64 b, b, 16;\n\t"
+        "add.s32 a, a, 8; add.s64 b, b, 2;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
-        "add.s32 a, a, 8; add.s64 b, b, 16;\n\t"
+        "add.s32 a, a, 8; add.s64 b, b, 2;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
-        "add.s32 a, a, 8; add.s64 b, b, 16;\n\t"
+        "add.s32 a, a, 8; add.s64 b, b, 2;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p; }" ::"r"(d),
         "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(gm_desc_high())
         : "memory");
@@ -83,7 +88,7 @@ __device__ __forceinline__ void gm_mma2(uint32_t d, uint32_t a, uint32_t b, uint
         "mov.b64 b, {%2, %5}; mov.b32 a, %1;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p;\n\t"
         "setp.eq.b32 p, 0, 0;\n\t"
-        "add.s32 a, a, 8; add.s64 b, b, 16;\n\t"
+        "add.s32 a, a, 8; add.s64 b, b, 2;\n\t"
         "tcgen05.mma.cta_group::1.kind::f16 [%0], [a], b, %3, p; }" ::"r"(d),
         "r"(a), "r"(b), "r"(idesc), "r"(accumulate), "n"(gm_desc_high())
         : "memory");
@@ -138,6 +143,17 @@ __device__ __forceinline__ void gm_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
+// Four rows of a matrix, 128 bytes from byte x on, to dst (a row index past the end reads zeros).
+__device__ __forceinline__ void gm_gather4(uint32_t dst, const CUtensorMap *map, int x, const int (&row)[4],
+                                           uint64_t *b) {
+    asm volatile(
+        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, "
+        "{%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
+        "r"(smem_u32(b))
+        : "memory");
+}
+
 // An item: up to kTokens tokens (of one expert) times one tile of weight rows.
 struct GmItem {
     int expert, t0, tokens, tile;
@@ -146,8 +162,9 @@ struct GmItem {
 // T: the tensors' type.  F32: their two-part form.
 template <Q4Use USE, typename T, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kGmThreads, 1)
-    q4_gemm_kernel(const __grid_constant__ Q4Params p, const __grid_constant__ Q4Rows r,
-                   const __grid_constant__ GmLaunch l, const uint8_t *codes) {
+    q4_gemm_kernel(const __grid_constant__ CUtensorMap code_map, const __grid_constant__ CUtensorMap x_map,
+                   const __grid_constant__ Q4Params p, const __grid_constant__ Q4Rows r,
+                   const __grid_constant__ GmLaunch l) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int kTokens = F32 ? 128 : 256;
     constexpr int kParts = F32 ? 2 : 1;
@@ -164,7 +181,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kGmAStages; i++) mbar_init(&bar.a_full[i], 4), mbar_init(&bar.a_empty[i], 1);
-        for (int i = 0; i < kGmBStages; i++) mbar_init(&bar.b_full[i], kGmCopyWarps), mbar_init(&bar.b_empty[i], 1);
+        for (int i = 0; i < kGmBStages; i++) mbar_init(&bar.b_full[i], 1), mbar_init(&bar.b_empty[i], 1);
+        for (int i = 0; i < kGmCStages; i++) mbar_init(&bar.c_full[i], 1), mbar_init(&bar.c_empty[i], kGmExpandWarps);
         for (int i = 0; i < 2; i++) mbar_init(&bar.d_full[i], 1), mbar_init(&bar.d_empty[i], kGmOutWarps);
         mbar_init(&bar.done, 1);
         fence_mbar_init();
@@ -210,7 +228,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     }
     // Tensor memory is taken when the kernels before this one have ended, and the next one may start only after
     // it: neither waits for the other's columns.
-    if (warp == kGmWarps - 1) tmem_alloc(&s_tmem, 512);
+    if (warp == kGmMmaWarp) tmem_alloc(&s_tmem, 512);
     tc_fence_before();
     __syncthreads();
     tc_fence_after();
@@ -317,11 +335,15 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 #pragma unroll
                 for (int c = 0; c < kCols / 2; c++) total[c] = 0;
                 auto sum_of = [&](int c) { return __uint_as_float((uint32_t)(total[c / 2] >> (32 * (c & 1)))); };
-                const uint16_t *ds = p.scales + (in ? row : 0) * p.pitch + k0 / GROUP;
+                const uint4 *ds = reinterpret_cast<const uint4 *>(p.scales + (in ? row : 0) * p.pitch) + k0 / GROUP / 8;
                 const int groups = columns / GROUP;
-                float d = f16_bits_to_float(ds[0]);
+                uint4 held = ds[0];   // eight groups' scales
+                int part = k0 / GROUP % 8;
+#pragma unroll 1
                 for (int g = 0; g < groups; g++, turn++) {
-                    const float next = f16_bits_to_float(ds[min(g + 1, groups - 1)]);
+                    const uint32_t two = part & 4 ? (part & 2 ? held.w : held.z) : (part & 2 ? held.y : held.x);
+                    const float d = f16_bits_to_float((uint16_t)(part & 1 ? two >> 16 : two));
+                    if (++part == 8 && g + 1 < groups) part = 0, held = *++ds;
                     wait(bar.d_full[turn & 1], turn >> 1);
                     tc_fence_after();
                     const uint64_t d2 = (uint64_t)__float_as_uint(d) << 32 | __float_as_uint(d);
@@ -336,7 +358,6 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                     tc_fence_before();
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.d_empty[turn & 1]);
-                    d = next;
                 }
                 if (l.split > 1) {
 #pragma unroll
@@ -386,125 +407,171 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         // =================== weights: a thread per row, every other step ===================
         const int quarter = warp & 3, half = (warp - kGmOutWarps) >> 2;
         const uint32_t to = tmem + kGmABase + ((uint32_t)(quarter * 32) << 16);
-        constexpr int kPer = GROUP == 32 ? 2 : 1;   // groups of a step
-        uint32_t turn = 0;   // this CTA's steps so far
+        constexpr int kBlock = 8 * GROUP / kGmStep;   // steps of eight groups, whose scales are held
+        // the lane's row of a stage of codes, under the 64-byte swizzle
+        const int at = USE == kQ4Up ? (lane & 16) * 4 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
+        const uint32_t from = smem_u32(smem) + kGmBStages * kGmB + at * 64, swizzle = (at >> 1) & 3;
+        uint32_t turn = 0, taken = 0;   // this CTA's steps, stages of codes so far
         for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
             const GmItem it = item_of(i);
             bool in;
             const int64_t row = row_of(it, quarter * 32 + lane, in);
-            const uint8_t *src = codes + (in ? row : 0) * (p.K / 2) + k0 / 2;
-            const uint16_t *ds = p.scales + (in ? row : 0) * p.pitch + k0 / GROUP;
-            const uint8_t *zs = ZEROS ? p.zeros + (in ? row : 0) * p.pitch + k0 / GROUP : nullptr;
-            uint4 w[kGmAhead][2];
-            uint32_t d[kGmAhead], z[kGmAhead];
-            // the step's own half of the steps: turn + s, with the same parity as `half`
-            const int s0 = (half ^ turn) & 1;
-            auto load = [&](int j, int s) {
-                if (s >= steps) return;
-                w[j][0] = ldg_stream(src + s * (kGmStep / 2));
-                w[j][1] = s * kGmStep + 32 < columns ? ldg_stream(src + s * (kGmStep / 2) + 16) : make_uint4(0, 0, 0, 0);
-                const int g = s * kGmStep / GROUP;
-                if (!F32) d[j] = kPer == 2 ? *reinterpret_cast<const uint32_t *>(ds + g) : ds[g];
-                if (ZEROS) z[j] = kPer == 2 ? *reinterpret_cast<const uint16_t *>(zs + g) : zs[g];
+            const uint4 *ds = reinterpret_cast<const uint4 *>(p.scales + (in ? row : 0) * p.pitch);
+            const uint2 *zs = ZEROS ? reinterpret_cast<const uint2 *>(p.zeros + (in ? row : 0) * p.pitch) : nullptr;
+            const int parity = (half ^ turn) & 1;   // of the steps that are this warp's
+            const int s_begin = k0 / kGmStep;       // steps are counted from the row's start here
+            int next = s_begin / kBlock;
+            uint4 d8 = make_uint4(0, 0, 0, 0), d_next = d8;
+            uint2 z8 = make_uint2(0, 0), z_next = z8;
+            auto ask = [&]() {
+                if (next * kBlock * kGmStep >= p.K) return;
+                if (!F32) d_next = ds[next];
+                if (ZEROS) z_next = zs[next];
+                next++;
             };
+            ask();
+            for (int sb = s_begin / kBlock * kBlock; sb < s_begin + steps; sb += kBlock) {
+                d8 = d_next, z8 = z_next;
+                ask();
+                const uint32_t dw[4] = {d8.x, d8.y, d8.z, d8.w};
+                const uint32_t zw[2] = {z8.x, z8.y};
 #pragma unroll
-            for (int j = 0; j < kGmAhead; j++) load(j, s0 + 2 * j);
-            for (int sb = s0; sb < steps; sb += 2 * kGmAhead) {
+                for (int j = 0; j < kBlock / 2; j++) {
+                    const int sj = 2 * j + ((parity ^ s_begin) & 1), s = sb + sj - s_begin;
+                    if (s < 0 || s >= steps) continue;
+                    // the scales (and zeros) of its two halves
+                    uint32_t d[2], z[2] = {8, 8};
+                    if (GROUP == 32) {
+                        const uint32_t w = sj & 1 ? dw[(2 * j + 1) & 3] : dw[(2 * j) & 3];
+                        d[0] = w & 0xffff, d[1] = w >> 16;
+                        if (ZEROS) {
+                            const uint32_t v = zw[j & 1] >> (sj & 1 ? 16 : 0);
+                            z[0] = v & 0xff, z[1] = v >> 8 & 0xff;
+                        }
+                    } else if (GROUP == 64) {
+                        d[0] = d[1] = sj & 1 ? dw[j & 3] >> 16 : dw[j & 3] & 0xffff;
+                        if (ZEROS) z[0] = z[1] = zw[j >> 1 & 1] >> (16 * (j & 1) + (sj & 1 ? 8 : 0)) & 0xff;
+                    } else {
+                        d[0] = d[1] = dw[j >> 1 & 3] >> (16 * (j & 1)) & 0xffff;
+                        if (ZEROS) z[0] = z[1] = zw[j >> 2 & 1] >> (8 * (j & 3)) & 0xff;
+                    }
+                    const uint32_t cs = (taken + s / 2) % kGmCStages, cr = (taken + s / 2) / kGmCStages;
+                    wait(bar.c_full[cs], cr);
+                    uint4 c[2];
 #pragma unroll
-                for (int j = 0; j < kGmAhead; j++) {
-                    const int s = sb + 2 * j;
-                    if (s >= steps) break;
+                    for (int h = 0; h < 2; h++)
+                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                     : "=r"(c[h].x), "=r"(c[h].y), "=r"(c[h].z), "=r"(c[h].w)
+                                     : "r"(from + cs * kGmC + ((2 * (s & 1) + h) ^ swizzle) * 16)
+                                     : "memory");
                     const uint32_t stage = (turn + s) % kGmAStages, round = (turn + s) / kGmAStages;
                     wait(bar.a_empty[stage], round ^ 1);
                     tc_fence_after();
 #pragma unroll
                     for (int h = 0; h < 2; h++) {
-                        const uint32_t zh = ZEROS ? (kPer == 2 ? z[j] >> (8 * h) & 0xff : z[j]) : 8u;
-                        const __half2 low = half2_of(0x64006400u + zh * 0x10001u);   // 1024 + z
-                        // 64 + z has its last place at 2^-4
-                        const __half2 high = half2_of(0xD400D400u + zh * 0x00100010u);
-                        const uint32_t dh = F32 ? 0 : (kPer == 2 ? (h ? d[j] >> 16 : d[j] & 0xffff) : d[j]) * 0x10001u;
+                        const __half2 low = half2_of(0x64006400u + z[h] * 0x10001u);   // 1024 + z
+                        // -(64 + z), whose last place is 2^-4
+                        const __half2 high = half2_of(0xD400D400u + z[h] * 0x00100010u);
+                        const __half2 scale = half2_of(d[h] * 0x10001u);
                         uint32_t v[16];
-                        const uint4 c = w[j][h];
                         if (s * kGmStep + 32 * h < columns) {
-                            expand_f16<!F32>(c.x, low, high, half2_of(dh), v);
-                            expand_f16<!F32>(c.y, low, high, half2_of(dh), v + 4);
-                            expand_f16<!F32>(c.z, low, high, half2_of(dh), v + 8);
-                            expand_f16<!F32>(c.w, low, high, half2_of(dh), v + 12);
+                            expand_f16<!F32>(c[h].x, low, high, scale, v);
+                            expand_f16<!F32>(c[h].y, low, high, scale, v + 4);
+                            expand_f16<!F32>(c[h].z, low, high, scale, v + 8);
+                            expand_f16<!F32>(c[h].w, low, high, scale, v + 12);
                         } else {
 #pragma unroll
                             for (int e = 0; e < 16; e++) v[e] = 0;
                         }
                         gm_tmem_st16(to + stage * 32 + 16 * h, v);
                     }
-                    load(j, s + 2 * kGmAhead);
                     asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                     tc_fence_before();
                     __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.a_full[stage]);
+                    if (lane == 0) mbar_arrive(&bar.a_full[stage]), mbar_arrive(&bar.c_empty[cs]);
                 }
+            }
+            // (an odd number of steps leaves half a stage of codes that one half of the warps has nothing of)
+            if ((steps & 1) && parity) {
+                const uint32_t cs = (taken + steps / 2) % kGmCStages;
+                wait(bar.c_full[cs], (taken + steps / 2) / kGmCStages);
+                if (lane == 0) mbar_arrive(&bar.c_empty[cs]);
             }
             turn += steps;
+            taken += (steps + 1) / 2;
         }
-    } else if (warp < kGmOutWarps + kGmExpandWarps + kGmCopyWarps) {
-        // =================== x: 8 rows x 4 chunks of 16 bytes an instruction ===================
-        const int cw = warp - kGmOutWarps - kGmExpandWarps;
-        constexpr int kRowGroups = (kTokens / 8 + kGmCopyWarps - 1) / kGmCopyWarps;   // of a warp
-        const uint16_t *x = static_cast<const uint16_t *>(p.x);
+    } else if (warp == kGmCodeWarp) {
+        // =================== codes: two copies of 64 rows x 128 columns a stage ===================
         uint32_t turn = 0;
-        auto hand_on = [&](uint32_t s) {
-            fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) mbar_arrive(&bar.b_full[s % kGmBStages]);
-        };
         for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
             const GmItem it = item_of(i);
-            int from[kRowGroups];
-#pragma unroll
-            for (int q = 0; q < kRowGroups; q++) {
-                const int c = (q * kGmCopyWarps + cw) * 8 + (lane & 7);
-                from[q] = -1;
-                if (c < it.tokens) {
-                    from[q] = it.t0 + c;
-                    if (USE == kQ4Up) {
-                        const int pair = p.order[it.t0 + c];
-                        from[q] = pair >= 0 && pair < p.T ? pair / p.k : -1;
-                    }
+            const int64_t first = it.expert * matrix_rows + it.tile * (int64_t)(USE == kQ4Up ? kGmRows / 2 : kGmRows);
+            const int64_t second = USE == kQ4Up ? first + p.N : first + kGmRows / 2;
+            for (int s = 0; s < steps; s += 2, turn++) {
+                const uint32_t stage = turn % kGmCStages;
+                wait(bar.c_empty[stage], (turn / kGmCStages) ^ 1);
+                if (lane == 0) {
+                    uint8_t *dst = smem + kGmBStages * kGmB + stage * kGmC;
+                    mbar_arrive_expect_tx(&bar.c_full[stage], kGmC);
+                    tma_load_2d(dst, &code_map, (k0 + s * kGmStep) / 2, (int)first, &bar.c_full[stage]);
+                    tma_load_2d(dst + kGmC / 2, &code_map, (k0 + s * kGmStep) / 2, (int)second, &bar.c_full[stage]);
                 }
+                __syncwarp();
             }
-            const int used = (it.tokens + 15) / 16 * 2;   // groups of 8 rows that the products read
+        }
+        // no copy may still be landing when the CTA exits
+        for (uint32_t t = turn > kGmCStages ? turn - kGmCStages : 0; t < turn; t++)
+            wait(bar.c_full[t % kGmCStages], t / kGmCStages);
+    } else if (warp == kGmCopyWarp) {
+        // =================== x ===================
+        uint32_t turn = 0;
+        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+            const GmItem it = item_of(i);
+            constexpr int kFours = kTokens / 4 / 32;   // groups of four rows of a lane
+            int four[kFours][4];
+            const int boxes = (it.tokens + kGmBox - 1) / kGmBox;
+            const int fours = (it.tokens + 15) / 16 * 4;
+            if (USE == kQ4Up) {
+#pragma unroll
+                for (int q = 0; q < kFours; q++)
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int c = (q * 32 + lane) * 4 + e;
+                        const int pair = c < it.tokens ? p.order[it.t0 + c] : -1;
+                        four[q][e] = pair >= 0 && pair < p.T ? pair / p.k : kParts * (int)r.rows;   // (zeros)
+                    }
+            }
             for (int s = 0; s < steps; s++, turn++) {
                 const uint32_t stage = turn % kGmBStages;
                 wait(bar.b_empty[stage], (turn / kGmBStages) ^ 1);
-                const uint32_t dst = smem_u32(smem) + stage * kGmB + (lane & 7) * 16;
+                const uint32_t dst = smem_u32(smem) + stage * kGmB;
+                const int byte = (k0 + s * kGmStep) * 2;
+                uint64_t *b = &bar.b_full[stage];
+                if (lane == 0)
+                    mbar_arrive_expect_tx(b, kParts * (USE == kQ4Up ? fours * 512 : boxes * kGmBox * 128));
+                __syncwarp();
+                if (USE == kQ4Up) {
 #pragma unroll
-                for (int q = 0; q < kRowGroups; q++) {
-                    const int rg = q * kGmCopyWarps + cw;
-                    if (rg >= used) break;
+                    for (int q = 0; q < kFours; q++) {
+                        if (q * 32 + lane >= fours) break;
+                        gm_gather4(dst + (q * 32 + lane) * 512, &x_map, byte, four[q], b);
+                        if (kParts == 2) {
+                            int second[4];
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const int chunk = 4 * h + (lane >> 3), k = s * kGmStep + chunk * 8;
-                        const bool there = from[q] >= 0 && k < columns;
-                        const uint16_t *src = x + (there ? from[q] * p.x_stride + k0 + k : 0);
-                        const uint32_t at = dst + rg * 1024 + chunk * 128;
-                        const int bytes = there ? 16 : 0;   // (the rest is zeros)
-#pragma unroll
-                        for (int part = 0; part < kParts; part++)
-                            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
-                                             at + part * (kGmB / 2)),
-                                         "l"(src + part * r.plane), "r"(bytes)
-                                         : "memory");
+                            for (int e = 0; e < 4; e++) second[e] = four[q][e] + (int)r.rows;
+                            gm_gather4(dst + kGmB / 2 + (q * 32 + lane) * 512, &x_map, byte, second, b);
+                        }
                     }
+                } else if (lane < boxes) {
+                    uint8_t *to = smem + stage * kGmB + lane * kGmBox * 128;
+                    tma_load_2d(to, &x_map, byte, it.t0 + lane * kGmBox, b);
+                    if (kParts == 2) tma_load_2d(to + kGmB / 2, &x_map, byte, (int)r.rows + it.t0 + lane * kGmBox, b);
                 }
-                asm volatile("cp.async.commit_group;" ::: "memory");
-                if (turn >= kGmLag) {
-                    asm volatile("cp.async.wait_group %0;" ::"n"(kGmLag) : "memory");
-                    hand_on(turn - kGmLag);
-                }
+                __syncwarp();
             }
         }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-        for (uint32_t s = turn > kGmLag ? turn - kGmLag : 0; s < turn; s++) hand_on(s);
+        for (uint32_t t = turn > kGmBStages ? turn - kGmBStages : 0; t < turn; t++)
+            wait(bar.b_full[t % kGmBStages], t / kGmBStages);
     } else {
         // =================== tensor-core operations ===================
         uint32_t turn = 0, taken = 0;   // steps, accumulators
@@ -533,8 +600,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                         }
                         if (gm_elect()) {
                             if (GROUP == 32) {
-                                gm_mma2(d, a + 16 * h, b + 32 * h, idesc, 0);
-                                gm_mma2(d, a + 16 * h, b + 32 * h + (kGmB / 2 >> 4), idesc, 1);
+                                gm_mma2(d, a + 16 * h, b + 4 * h, idesc, 0);
+                                gm_mma2(d, a + 16 * h, b + 4 * h + (kGmB / 2 >> 4), idesc, 1);
                             } else {
                                 gm_mma4(d, a, b, idesc, !begin);
                                 gm_mma4(d, a, b + (kGmB / 2 >> 4), idesc, 1);
@@ -600,7 +667,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         }
         gm_cluster_sync();
     }
-    if (warp == kGmWarps - 1) tmem_dealloc(tmem, 512);
+    if (warp == kGmMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------------------------------
@@ -613,7 +680,7 @@ constexpr int kRowHold = 4;   // groups of eight columns that a thread keeps bet
 template <typename X, int PARTS>
 __global__ void __launch_bounds__(kRowThreads)
     q4_rows_kernel(const X *x, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, uint16_t *to,
-                   int64_t plane, float *row_scale) {
+                   float *row_scale) {
     __shared__ float most[kRowThreads / 32];
     const int tid = threadIdx.x;
     pdl_launch_dependents();
@@ -657,7 +724,7 @@ __global__ void __launch_bounds__(kRowThreads)
         }
         uint16_t *dst = to + row * K + 8 * u;
         *reinterpret_cast<uint4 *>(dst) = make_uint4(hi[0], hi[1], hi[2], hi[3]);
-        if (PARTS == 2) *reinterpret_cast<uint4 *>(dst + plane) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
+        if (PARTS == 2) *reinterpret_cast<uint4 *>(dst + n * K) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     };
 #pragma unroll
     for (int h = 0; h < kRowHold; h++) {
@@ -673,20 +740,20 @@ __global__ void __launch_bounds__(kRowThreads)
 }
 
 int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, int parts,
-            uint16_t *to, int64_t plane, float *row_scale, cudaStream_t st) {
+            uint16_t *to, float *row_scale, cudaStream_t st) {
     const dim3 grid((unsigned)n), block(kRowThreads);
     if (f32) {
         auto kernel = parts == 2 ? q4_rows_kernel<float, 2> : q4_rows_kernel<float, 1>;
         return launch_pdl(kernel, grid, block, 0, st, static_cast<const float *>(x), x_stride, n, K, n_opt, to,
-                          plane, row_scale);
+                          row_scale);
     }
     return launch_pdl(q4_rows_kernel<__nv_bfloat16, 1>, grid, block, 0, st,
-                      static_cast<const __nv_bfloat16 *>(x), x_stride, n, K, n_opt, to, plane, row_scale);
+                      static_cast<const __nv_bfloat16 *>(x), x_stride, n, K, n_opt, to, row_scale);
 }
 
 template <Q4Use USE, typename T, int GROUP>
-static int launch_gemm(const Q4Params &p, const Q4Rows &r, const GmLaunch &l, unsigned grid, const uint8_t *codes,
-                       cudaStream_t st) {
+static int launch_gemm(const CUtensorMap &code_map, const CUtensorMap &x_map, const Q4Params &p, const Q4Rows &r,
+                       const GmLaunch &l, unsigned grid, cudaStream_t st) {
     auto kernel = p.zeros ? q4_gemm_kernel<USE, T, GROUP, true> : q4_gemm_kernel<USE, T, GROUP, false>;
     int per_sm;
     if (int e = prepare_kernel((const void *)kernel, kGmThreads, kGmSmem, &per_sm)) return e;
@@ -698,14 +765,15 @@ static int launch_gemm(const Q4Params &p, const Q4Rows &r, const GmLaunch &l, un
     attr[1].id = cudaLaunchAttributeClusterDimension;
     attr[1].val.clusterDim.x = (unsigned)l.split, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr, cfg.numAttrs = l.split > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, p, r, l, codes);
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, code_map, x_map, p, r, l);
     if (e == cudaSuccess) return LB_OK;
     record_cuda_error(e);
     return LB_ERR_LAUNCH;
 }
 
 template <Q4Use USE, typename T>
-static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *codes, int sms, cudaStream_t st) {
+static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *codes, int64_t code_rows, int sms,
+                         cudaStream_t st) {
     const int tokens = sizeof(T) == 4 ? 128 : 256, rows = USE == kQ4Up ? kGmRows / 2 : kGmRows;
     GmLaunch l;
     const int64_t tiles = (p.N + rows - 1) / rows, pieces = (p.T + tokens - 1) / tokens;
@@ -722,10 +790,15 @@ static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *code
         l.split = (steps + l.steps - 1) / l.steps;
     }
     const unsigned grid = (unsigned)(std::min<int64_t>(items * l.split, l.split > 1 ? items * l.split : sms));
+    CUtensorMap codes_map, x_map;
+    if (int e = encode_rows_map(&codes_map, codes, (uint64_t)p.K / 2, (uint64_t)code_rows, 64, kGmRows / 2, 64)) return e;
+    if (int e = encode_rows_map(&x_map, r.x, (uint64_t)p.K * 2, (uint64_t)r.rows * (sizeof(T) == 4 ? 2 : 1), 128,
+                                USE == kQ4Up ? 1 : kGmBox, 128))
+        return e;
     switch (p.group) {
-        case 32: return launch_gemm<USE, T, 32>(p, r, l, grid, codes, st);
-        case 64: return launch_gemm<USE, T, 64>(p, r, l, grid, codes, st);
-        default: return launch_gemm<USE, T, 128>(p, r, l, grid, codes, st);
+        case 32: return launch_gemm<USE, T, 32>(codes_map, x_map, p, r, l, grid, st);
+        case 64: return launch_gemm<USE, T, 64>(codes_map, x_map, p, r, l, grid, st);
+        default: return launch_gemm<USE, T, 128>(codes_map, x_map, p, r, l, grid, st);
     }
 }
 
@@ -733,13 +806,13 @@ int q4_gemm(const Q4Params &p, const Q4Rows &r, Q4Use use, int type, const uint8
             int sms, cudaStream_t st) {
     const bool f32 = type == LB_OUT_F32;
     if (use == kQ4Dense)
-        return f32 ? dispatch_gemm<kQ4Dense, float>(p, r, codes, sms, st)
-                   : dispatch_gemm<kQ4Dense, __nv_bfloat16>(p, r, codes, sms, st);
+        return f32 ? dispatch_gemm<kQ4Dense, float>(p, r, codes, rows, sms, st)
+                   : dispatch_gemm<kQ4Dense, __nv_bfloat16>(p, r, codes, rows, sms, st);
     if (use == kQ4Up)
-        return f32 ? dispatch_gemm<kQ4Up, float>(p, r, codes, sms, st)
-                   : dispatch_gemm<kQ4Up, __nv_bfloat16>(p, r, codes, sms, st);
-    return f32 ? dispatch_gemm<kQ4Down, float>(p, r, codes, sms, st)
-               : dispatch_gemm<kQ4Down, __nv_bfloat16>(p, r, codes, sms, st);
+        return f32 ? dispatch_gemm<kQ4Up, float>(p, r, codes, rows, sms, st)
+                   : dispatch_gemm<kQ4Up, __nv_bfloat16>(p, r, codes, rows, sms, st);
+    return f32 ? dispatch_gemm<kQ4Down, float>(p, r, codes, rows, sms, st)
+               : dispatch_gemm<kQ4Down, __nv_bfloat16>(p, r, codes, rows, sms, st);
 }
 
 }  // namespace lb
