@@ -100,7 +100,7 @@ static ExpertsAt experts_at(int64_t T, int k, int64_t hidden, int64_t ffn, int t
     ExpertsAt a;
     const size_t pairs = (size_t)T * k;
     a.x = 0;
-    a.h = a.x + rows_bytes(T, hidden, type);
+    a.h = a.x + rows_bytes(pairs, hidden, type);
     a.h_rows = a.h + align256(pairs * ffn * 4);
     a.part = a.h_rows + rows_bytes(pairs, ffn, type);
     a.bytes = a.part + align256(pairs * hidden * 4) + 256;
@@ -145,7 +145,7 @@ LB_EXPORT int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uin
     cudaStream_t st = as_stream(stream);
     if (M <= 8) return q4_gemv(p, kQ4Dense, type, codes, N, di.sms, st);
     const RowsAt r = rows_at(static_cast<uint8_t *>(workspace), M, K, type);
-    if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, M, (int)K, nullptr, parts_of(type), r.to, r.scale, st))
+    if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, M, (int)K, nullptr, nullptr, 1, parts_of(type), r.to, r.scale, st))
         return e;
     return q4_gemm(p, {r.to, r.scale, M}, kQ4Dense, type, codes, N, di.sms, st);
 }
@@ -202,12 +202,13 @@ LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T
         if (int e = q4_gemv(up, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
         if (int e = q4_gemv(down, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
     } else {
-        const RowsAt xr = rows_at(ws + at.x, T, hidden, type), hr = rows_at(ws + at.h_rows, pairs, ffn, type);
+        const RowsAt xr = rows_at(ws + at.x, pairs, hidden, type), hr = rows_at(ws + at.h_rows, pairs, ffn, type);
         const int parts = parts_of(type);
-        if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, T, (int)hidden, nullptr, parts, xr.to, xr.scale, st))
+        if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, pairs, (int)hidden, expert_start + E, order, k, parts, xr.to,
+                            xr.scale, st))
             return e;
-        if (int e = q4_gemm(up, {xr.to, xr.scale, T}, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
-        if (int e = q4_rows(h, true, ffn, pairs, (int)ffn, expert_start + E, parts, hr.to, hr.scale, st))
+        if (int e = q4_gemm(up, {xr.to, xr.scale, pairs}, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
+        if (int e = q4_rows(h, true, ffn, pairs, (int)ffn, expert_start + E, nullptr, 1, parts, hr.to, hr.scale, st))
             return e;
         if (int e = q4_gemm(down, {hr.to, hr.scale, pairs}, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
     }

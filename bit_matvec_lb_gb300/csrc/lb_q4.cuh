@@ -43,8 +43,8 @@ struct Q4Rows {
 int q4_gemm(const Q4Params &p, const Q4Rows &r, Q4Use use, int type, const uint8_t *codes, int64_t rows,
             int sms, cudaStream_t st);
 // rows [n][K] of x (fp32 if f32 else bf16), x_stride apart -> fp16 parts and row_scale.  n_opt: NULL, or where
-// the number of rows that are there lies.
-int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, int parts,
-            uint16_t *to, float *row_scale, cudaStream_t st);
+// the number of rows that are there lies.  order: NULL, or the n pairs, whose rows of x are pair / k.
+int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt,
+            const int32_t *order, int k, int parts, uint16_t *to, float *row_scale, cudaStream_t st);
 
 }  // namespace lb

@@ -14,11 +14,12 @@
 // Rows of x are scaled by powers of two into fp16's range beforehand (q4_rows), and stored in the order
 // in which the codes of a word unfold, pairs (0, 4), (1, 5), (2, 6), (3, 7).
 //
-// One CTA per SM, 19 warps: eight that take the sums out (a quarter of the lanes times half of
+// One CTA per SM, 20 warps: eight that take the sums out (a quarter of the lanes times half of
 // the columns each), eight that expand weights, one that has codes copied in (tensor copies, 128 rows x 128
-// columns), one that has x copied in (tensor copies of 32 rows x 64 columns, or of four rows from anywhere for
-// an expert's tokens), one that issues the tensor-core operations.  Calls with few tiles are
-// split along K over a cluster; the parts are added up through distributed shared memory.
+// columns), one that has x copied in (tensor copies of 64 rows x 64 columns), one that issues the tensor-core operations.  Calls with few tiles are
+// split along K over a cluster; the parts are added up through distributed shared memory.  In others two CTAs
+// with neighbouring tiles of the same tokens form a cluster and copy half of x each, to both: every SM on its
+// own would ask the L2 for 64 bytes a cycle.
 #include "lb_q4.cuh"
 #include "lb_tc.cuh"
 
@@ -31,7 +32,7 @@ constexpr int kGmStep = 64;              // columns of K of a stage
 constexpr int kGmOutWarps = 8, kGmExpandWarps = 8;
 constexpr int kGmCodeWarp = kGmOutWarps + kGmExpandWarps, kGmCopyWarp = kGmCodeWarp + 1;
 constexpr int kGmMmaWarp = kGmCopyWarp + 1;
-constexpr int kGmWarps = kGmMmaWarp + 1;
+constexpr int kGmWarps = kGmMmaWarp + 2;   // (whole groups of four)
 constexpr int kGmThreads = 32 * kGmWarps;
 constexpr int kGmOutThreads = 32 * kGmOutWarps;
 constexpr int kGmB = 32768;              // bytes of a stage of x
@@ -40,14 +41,18 @@ constexpr int kGmC = kGmRows * 64;       // bytes of a stage of codes: two steps
 constexpr int kGmCStages = 6;
 constexpr int kGmAStages = 8;            // of expanded weights, 32 columns of tensor memory each
 constexpr int kGmABase = 256;            // they lie behind the accumulators
-constexpr int kGmBox = 32;               // tokens of a copy
+constexpr int kGmBox = 128;              // tokens of a copy, at most
 constexpr int kGmMaxSplit = 8;
+constexpr int kGmShare = 2;
 constexpr int kGmSmem = kGmBStages * kGmB + kGmCStages * kGmC;
 
 struct GmLaunch {
     int steps;        // of K, of a CTA
-    int split;        // CTAs along K
-    int tiles;        // of weight rows
+    int split;        // CTAs along K, a cluster
+    int share;        // CTAs that take the same tokens times tiles side by side, a cluster (split 1 then)
+    int box;          // tokens of a copy
+    int pairs;        // two rows of a bf16 y may be stored as one word
+    int tiles;        // of weight rows, a multiple of share (the last ones may lie behind the matrix)
 };
 
 struct GmBars {
@@ -109,6 +114,37 @@ __device__ __forceinline__ void gm_tmem_st16(uint32_t taddr, const uint32_t *r) 
 __device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 
+// A group of four warps' registers per thread.  640 threads start with 96 (61440); then 256 have 144, 256 have
+// 80 and 128 have 32 (61440), and in the end all 96 again.  The others take theirs back only after the 256 have given
+// theirs up: a CTA without work would otherwise have nothing left for warps that still wait for their 144.
+template <int N>
+__device__ __forceinline__ void gm_more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void gm_fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
+// 32 columns asked for; they are there after gm_ld32_wait.
+__device__ __forceinline__ void gm_ld32_start(uint32_t taddr, uint32_t *r) {
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
+        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
+          "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
+          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
+          "=r"(r[31])
+        : "r"(taddr)
+        : "memory");
+}
+__device__ __forceinline__ void gm_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
+// (no use of r is moved before this)
+__device__ __forceinline__ void gm_hold8(uint32_t *r) {
+    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+}
+
 // Eight codes of a word less the zero, times the scale: pairs (0, 4), (1, 5), (2, 6), (3, 7) of fp16.  The codes
 // go under the exponent of 1024, at the last place or (times 16) four above it.
 // low: 1024 + z twice, high: -(64 + z) twice.
@@ -143,14 +179,22 @@ __device__ __forceinline__ void gm_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// Four rows of a matrix, 128 bytes from byte x on, to dst (a row index past the end reads zeros).
-__device__ __forceinline__ void gm_gather4(uint32_t dst, const CUtensorMap *map, int x, const int (&row)[4],
-                                           uint64_t *b) {
+// 2-D tensor copy into the same place of every CTA of the cluster that mask names, counted on each one's own
+// barrier at b's place.
+__device__ __forceinline__ void gm_load_multicast(void *dst, const CUtensorMap *map, int x, int y, uint64_t *b,
+                                                  uint16_t mask) {
     asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.tile::gather4.mbarrier::complete_tx::bytes [%0], [%1, "
-        "{%2, %3, %4, %5, %6}], [%7];" ::"r"(dst),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(row[0]), "r"(row[1]), "r"(row[2]), "r"(row[3]),
-        "r"(smem_u32(b))
+        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
+        "{%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
+        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(b)), "h"(mask)
+        : "memory");
+}
+// Arrive once on `b` of every CTA that mask names when the products issued so far have completed.
+__device__ __forceinline__ void gm_commit_multicast(uint64_t *b, uint16_t mask) {
+    asm volatile(
+        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
+            smem_u32(b)),
+        "h"(mask)
         : "memory");
 }
 
@@ -177,11 +221,12 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     __shared__ float col_scale[kTokens];
     __shared__ int col_row[kTokens];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int rank = blockIdx.x % l.split;
+    const int rank = blockIdx.x % l.split;            // along K
+    const int cluster = l.split * l.share;
 
     if (tid == 0) {
         for (int i = 0; i < kGmAStages; i++) mbar_init(&bar.a_full[i], 4), mbar_init(&bar.a_empty[i], 1);
-        for (int i = 0; i < kGmBStages; i++) mbar_init(&bar.b_full[i], 1), mbar_init(&bar.b_empty[i], 1);
+        for (int i = 0; i < kGmBStages; i++) mbar_init(&bar.b_full[i], 1), mbar_init(&bar.b_empty[i], l.share);
         for (int i = 0; i < kGmCStages; i++) mbar_init(&bar.c_full[i], 1), mbar_init(&bar.c_empty[i], kGmExpandWarps);
         for (int i = 0; i < 2; i++) mbar_init(&bar.d_full[i], 1), mbar_init(&bar.d_empty[i], kGmOutWarps);
         mbar_init(&bar.done, 1);
@@ -230,16 +275,17 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     // it: neither waits for the other's columns.
     if (warp == kGmMmaWarp) tmem_alloc(&s_tmem, 512);
     tc_fence_before();
-    __syncthreads();
+    if (l.share > 1) gm_cluster_sync();   // (everybody's barriers are there)
+    else __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = s_tmem;
-    const int64_t items = (int64_t)pieces * l.tiles;
-    const int64_t each = gridDim.x / l.split;
+    const int64_t items = (int64_t)pieces * (l.tiles / l.share);   // of a cluster
+    const int64_t each = gridDim.x / cluster;
     auto item_of = [&](int64_t i) {
         GmItem it;
-        const int piece = (int)(i / l.tiles);
-        it.tile = (int)(i % l.tiles);
+        const int side = l.tiles / l.share, piece = (int)(i / side);
+        it.tile = (int)(i % side) * l.share + blockIdx.x % l.share;
         if constexpr (USE == kQ4Dense) {
             it.expert = 0;
             it.t0 = piece * kTokens;
@@ -291,18 +337,18 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         const int quarter = warp & 3, c0 = (warp >> 2) * kCols;
         const uint32_t at_lane = tmem + ((uint32_t)(quarter * 32) << 16);
         uint32_t turn = 0;   // accumulators taken so far
-        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+        gm_more_registers<144>();
+        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
+            __syncwarp();
             named_sync(1, kGmOutThreads);   // the last item's columns are done with
             for (int c = tid; c < it.tokens; c += kGmOutThreads) {
-                int from = it.t0 + c, to = from;
-                if (USE != kQ4Dense) {
+                int to = it.t0 + c;
+                if (USE == kQ4Down) {
                     const int pair = p.order[it.t0 + c];
-                    const bool in = pair >= 0 && pair < p.T;
-                    if (USE == kQ4Up) from = in ? pair / p.k : -1;
-                    else to = in ? pair : -1;
+                    to = pair >= 0 && pair < p.T ? pair : -1;
                 }
-                col_scale[c] = from >= 0 ? r.row_scale[from] : 0.f;
+                col_scale[c] = r.row_scale[it.t0 + c];
                 col_row[c] = to;
             }
             named_sync(1, kGmOutThreads);
@@ -318,16 +364,16 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                     static_cast<float *>(p.y)[to * p.y_stride + (row - it.expert * matrix_rows)] = v;
             };
             // gate and up rows of a column pair meet: lanes 0..15 make h of column c, 16..31 of c + 1
-            auto put_up = [&](int c, float a, float b) {
-                a *= col_scale[c0 + c];
-                b *= col_scale[c0 + min(c + 1, mine - 1)];
+            auto meet_up = [&](float a, float b) {
                 const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? b : a, 16);
                 const float gate = lane < 16 ? a : other, up = lane < 16 ? other : b;
+                return gate / (1.f + expf(-gate)) * up;
+            };
+            auto put_up = [&](int c, float h) {
                 const int col = c + (lane >> 4);
                 const int64_t n = it.tile * (int64_t)(kGmRows / 2) + quarter * 16 + (lane & 15);
                 if (col < mine && n < p.N)
-                    static_cast<float *>(p.y)[(int64_t)col_row[c0 + col] * p.y_stride + n] =
-                        gate / (1.f + expf(-gate)) * up;
+                    static_cast<float *>(p.y)[(int64_t)(it.t0 + c0 + col) * p.y_stride + n] = h;
             };
             float *park = reinterpret_cast<float *>(smem) + quarter * 32 + lane;   // [column][128]
             if constexpr (F32) {
@@ -366,45 +412,90 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 } else if (USE == kQ4Up) {
 #pragma unroll
                     for (int c = 0; c < kCols; c += 2)
-                        if (c < mine) put_up(c, sum_of(c), sum_of(c + 1));
+                        if (c < mine)
+                            put_up(c, meet_up(sum_of(c) * col_scale[c0 + c],
+                                              sum_of(c + 1) * col_scale[c0 + min(c + 1, mine - 1)]));
                 } else if (in) {
 #pragma unroll
                     for (int c = 0; c < kCols; c++)
                         if (c < mine) put(c, sum_of(c) * col_scale[c0 + c]);
                 }
             } else {
+                // The accumulator is free for the next item when its second half is in registers; the first one's
+                // results wait there, too (a down product's, of which there are as many as sums, are stored at once).
+                constexpr int kHalf = kCols / 2;
+                uint32_t v[kHalf], done[kHalf / 2];
+                // what this lane stores for columns c and c + 1
+                auto meet = [&](int c, uint32_t va, uint32_t vb) -> uint32_t {
+                    const float a = __uint_as_float(va) * col_scale[c0 + c];
+                    const float b = __uint_as_float(vb) * col_scale[c0 + min(c + 1, mine - 1)];
+                    if (USE == kQ4Up) return __float_as_uint(meet_up(a, b));
+                    if (!l.pairs) return bf16_pair(a, b);
+                    // rows 2i and 2i + 1 meet: even lanes store both of column c, odd ones of c + 1
+                    const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
+                    return lane & 1 ? bf16_pair(other, b) : bf16_pair(a, other);
+                };
+                auto keep = [&](int c, uint32_t w) {
+                    if (USE == kQ4Up) {
+                        put_up(c, __uint_as_float(w));
+                    } else {
+                        uint16_t *y = static_cast<uint16_t *>(p.y) + (it.t0 + c0 + c) * p.y_stride + row;
+                        if (l.pairs) {
+                            if (lane & 1) y += p.y_stride - 1;
+                            if (in && c + (lane & 1) < mine) *reinterpret_cast<uint32_t *>(y) = w;
+                        } else if (in) {
+                            y[0] = (uint16_t)w;
+                            if (c + 1 < mine) y[p.y_stride] = (uint16_t)(w >> 16);
+                        }
+                    }
+                };
                 wait(bar.d_full[0], turn);
+                turn++;
                 tc_fence_after();
-#pragma unroll 1
-                for (int q = 0; q < kCols / 32; q++) {
-                    if (32 * q >= mine) break;
-                    uint32_t v[32];
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
                     __syncwarp();
-                    tmem_ld32(at_lane + c0 + 32 * q, v);
+#pragma unroll
+                    for (int q = 0; q < kHalf / 32; q++)
+                        gm_ld32_start(at_lane + c0 + h * kHalf + 32 * q, v + 32 * q);
+                    gm_ld_wait();
+#pragma unroll
+                    for (int c = 0; c < kHalf; c += 8) gm_hold8(v + c);
+                    if (h == 1) {
+                        tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) mbar_arrive(&bar.d_empty[0]);
+                    }
                     if (l.split > 1) {
 #pragma unroll
-                        for (int c = 0; c < 32; c++)
-                            if (32 * q + c < mine) park[(c0 + 32 * q + c) * kGmRows] = __uint_as_float(v[c]);
-                    } else if (USE == kQ4Up) {
+                        for (int c = 0; c < kHalf; c++)
+                            if (h * kHalf + c < mine) park[(c0 + h * kHalf + c) * kGmRows] = __uint_as_float(v[c]);
+                    } else if (USE == kQ4Down) {
 #pragma unroll
-                        for (int c = 0; c < 32; c += 2)
-                            if (32 * q + c < mine)
-                                put_up(32 * q + c, __uint_as_float(v[c]), __uint_as_float(v[c + 1]));
-                    } else if (in) {
+                        for (int c = 0; c < kHalf; c++)
+                            if (h * kHalf + c < mine && in)
+                                put(h * kHalf + c, __uint_as_float(v[c]) * col_scale[c0 + h * kHalf + c]);
+                    } else if (h == 0) {
 #pragma unroll
-                        for (int c = 0; c < 32; c++)
-                            if (32 * q + c < mine)
-                                put(32 * q + c, __uint_as_float(v[c]) * col_scale[c0 + 32 * q + c]);
+                        for (int c = 0; c < kHalf; c += 2)
+                            if (c < mine) done[c / 2] = meet(c, v[c], v[c + 1]);
+                    } else {
+#pragma unroll
+                        for (int c = 0; c < kHalf; c += 2)
+                            if (c < mine) keep(c, done[c / 2]);
+#pragma unroll
+                        for (int c = 0; c < kHalf; c += 2)
+                            if (kHalf + c < mine) keep(kHalf + c, meet(kHalf + c, v[c], v[c + 1]));
                     }
                 }
-                turn++;
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.d_empty[0]);
             }
         }
+        __syncwarp();
+        gm_fewer_registers<96>();
+        named_sync(2, kGmThreads);
     } else if (warp < kGmOutWarps + kGmExpandWarps) {
         // =================== weights: a thread per row, every other step ===================
+        gm_fewer_registers<80>();
         const int quarter = warp & 3, half = (warp - kGmOutWarps) >> 2;
         const uint32_t to = tmem + kGmABase + ((uint32_t)(quarter * 32) << 16);
         constexpr int kBlock = 8 * GROUP / kGmStep;   // steps of eight groups, whose scales are held
@@ -412,7 +503,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         const int at = USE == kQ4Up ? (lane & 16) * 4 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
         const uint32_t from = smem_u32(smem) + kGmBStages * kGmB + at * 64, swizzle = (at >> 1) & 3;
         uint32_t turn = 0, taken = 0;   // this CTA's steps, stages of codes so far
-        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
             bool in;
             const int64_t row = row_of(it, quarter * 32 + lane, in);
@@ -500,17 +591,22 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             turn += steps;
             taken += (steps + 1) / 2;
         }
-    } else if (warp == kGmCodeWarp) {
+        __syncwarp();
+        named_sync(2, kGmThreads);
+        gm_more_registers<96>();
+    } else {
+      gm_fewer_registers<32>();
+      if (warp == kGmCodeWarp) {
         // =================== codes: two copies of 64 rows x 128 columns a stage ===================
         uint32_t turn = 0;
-        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
             const int64_t first = it.expert * matrix_rows + it.tile * (int64_t)(USE == kQ4Up ? kGmRows / 2 : kGmRows);
             const int64_t second = USE == kQ4Up ? first + p.N : first + kGmRows / 2;
             for (int s = 0; s < steps; s += 2, turn++) {
                 const uint32_t stage = turn % kGmCStages;
                 wait(bar.c_empty[stage], (turn / kGmCStages) ^ 1);
-                if (lane == 0) {
+                if (gm_elect()) {
                     uint8_t *dst = smem + kGmBStages * kGmB + stage * kGmC;
                     mbar_arrive_expect_tx(&bar.c_full[stage], kGmC);
                     tma_load_2d(dst, &code_map, (k0 + s * kGmStep) / 2, (int)first, &bar.c_full[stage]);
@@ -525,57 +621,42 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     } else if (warp == kGmCopyWarp) {
         // =================== x ===================
         uint32_t turn = 0;
-        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
-            constexpr int kFours = kTokens / 4 / 32;   // groups of four rows of a lane
-            int four[kFours][4];
-            const int boxes = (it.tokens + kGmBox - 1) / kGmBox;
-            const int fours = (it.tokens + 15) / 16 * 4;
-            if (USE == kQ4Up) {
-#pragma unroll
-                for (int q = 0; q < kFours; q++)
-#pragma unroll
-                    for (int e = 0; e < 4; e++) {
-                        const int c = (q * 32 + lane) * 4 + e;
-                        const int pair = c < it.tokens ? p.order[it.t0 + c] : -1;
-                        four[q][e] = pair >= 0 && pair < p.T ? pair / p.k : kParts * (int)r.rows;   // (zeros)
-                    }
-            }
+            const int boxes = (it.tokens + l.box - 1) / l.box;
+            const uint32_t bytes = (uint32_t)(kParts * boxes * l.box * 128);
+            const int side = l.share > 1 ? blockIdx.x % l.share : 0;
             for (int s = 0; s < steps; s++, turn++) {
                 const uint32_t stage = turn % kGmBStages;
                 wait(bar.b_empty[stage], (turn / kGmBStages) ^ 1);
-                const uint32_t dst = smem_u32(smem) + stage * kGmB;
-                const int byte = (k0 + s * kGmStep) * 2;
-                uint64_t *b = &bar.b_full[stage];
-                if (lane == 0)
-                    mbar_arrive_expect_tx(b, kParts * (USE == kQ4Up ? fours * 512 : boxes * kGmBox * 128));
-                __syncwarp();
-                if (USE == kQ4Up) {
+                // (one thread issues everything: copies of several lanes go out one after the other, slower)
+                if (gm_elect()) {
+                    uint64_t *b = &bar.b_full[stage];
+                    mbar_arrive_expect_tx(b, bytes);
+                    const int byte = (k0 + s * kGmStep) * 2;
+                    // the CTAs that share the tokens copy every share-th box to all of them
+                    for (int box = side; box < boxes; box += l.share) {
 #pragma unroll
-                    for (int q = 0; q < kFours; q++) {
-                        if (q * 32 + lane >= fours) break;
-                        gm_gather4(dst + (q * 32 + lane) * 512, &x_map, byte, four[q], b);
-                        if (kParts == 2) {
-                            int second[4];
-#pragma unroll
-                            for (int e = 0; e < 4; e++) second[e] = four[q][e] + (int)r.rows;
-                            gm_gather4(dst + kGmB / 2 + (q * 32 + lane) * 512, &x_map, byte, second, b);
+                        for (int part = 0; part < kParts; part++) {
+                            uint8_t *to = smem + stage * kGmB + part * (kGmB / 2) + box * l.box * 128;
+                            const int row = part * (int)r.rows + it.t0 + box * l.box;
+                            if (l.share > 1) gm_load_multicast(to, &x_map, byte, row, b, (uint16_t)((1 << l.share) - 1));
+                            else tma_load_2d(to, &x_map, byte, row, b);
                         }
                     }
-                } else if (lane < boxes) {
-                    uint8_t *to = smem + stage * kGmB + lane * kGmBox * 128;
-                    tma_load_2d(to, &x_map, byte, it.t0 + lane * kGmBox, b);
-                    if (kParts == 2) tma_load_2d(to + kGmB / 2, &x_map, byte, (int)r.rows + it.t0 + lane * kGmBox, b);
                 }
                 __syncwarp();
             }
         }
-        for (uint32_t t = turn > kGmBStages ? turn - kGmBStages : 0; t < turn; t++)
+        // (the other CTA's arrivals have to have come, too, before this one may exit)
+        for (uint32_t t = turn > kGmBStages ? turn - kGmBStages : 0; t < turn; t++) {
             wait(bar.b_full[t % kGmBStages], t / kGmBStages);
-    } else {
+            wait(bar.b_empty[t % kGmBStages], t / kGmBStages);
+        }
+    } else if (warp == kGmMmaWarp) {
         // =================== tensor-core operations ===================
         uint32_t turn = 0, taken = 0;   // steps, accumulators
-        for (int64_t i = blockIdx.x / l.split; i < items; i += each) {
+        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
             const uint32_t idesc = idesc_f16(kGmRows, (it.tokens + 15) / 16 * 16);
             if (!F32) wait(bar.d_empty[0], taken ^ 1);
@@ -617,7 +698,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 __syncwarp();
                 if (gm_elect()) {
                     mma_commit(&bar.a_empty[sa]);
-                    mma_commit(&bar.b_empty[sb]);
+                    if (l.share > 1) gm_commit_multicast(&bar.b_empty[sb], (uint16_t)((1 << l.share) - 1));
+                    else mma_commit(&bar.b_empty[sb]);
                 }
                 __syncwarp();
             }
@@ -631,13 +713,17 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         __syncwarp();
         wait(bar.done, 0);
         tc_fence_before();
+      }
+      __syncwarp();
+      named_sync(2, kGmThreads);
+      gm_more_registers<96>();
     }
     __syncthreads();
     tc_fence_after();
     if (l.split > 1) {
         // one item per cluster: its parts' sums, a share of the columns per CTA, a warp per column
         gm_cluster_sync();
-        const int64_t i = blockIdx.x / l.split;
+        const int64_t i = blockIdx.x / cluster;
         if (i < items) {
             const GmItem it = item_of(i);
             const float *park = reinterpret_cast<const float *>(smem);
@@ -667,11 +753,13 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         }
         gm_cluster_sync();
     }
+    if (l.share > 1) gm_cluster_sync();   // nobody's copies or arrivals come after a CTA has gone
     if (warp == kGmMmaWarp) tmem_dealloc(tmem, 512);
 }
 
 // ------------------------------------------------------------------------------------------
-// Rows of x for the tensor cores: scaled so that the largest lies in [2^14, 2^15), in fp16 (one part, or two
+// Rows of x for the tensor cores (with an order, row i is that of pair order[i], zeros where there is none;
+// four-row gathering copies of the tensors' own rows take four times as long as the products): scaled so that the largest lies in [2^14, 2^15), in fp16 (one part, or two
 // that hold 22 bits), each eight columns in the order 0 4 1 5 2 6 3 7.
 // ------------------------------------------------------------------------------------------
 constexpr int kRowThreads = 128;
@@ -679,15 +767,20 @@ constexpr int kRowHold = 4;   // groups of eight columns that a thread keeps bet
 
 template <typename X, int PARTS>
 __global__ void __launch_bounds__(kRowThreads)
-    q4_rows_kernel(const X *x, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, uint16_t *to,
-                   float *row_scale) {
+    q4_rows_kernel(const X *x, int64_t x_stride, int64_t n, int K, const int32_t *n_opt,
+                   const int32_t *order, int k, uint16_t *to, float *row_scale) {
     __shared__ float most[kRowThreads / 32];
     const int tid = threadIdx.x;
     pdl_launch_dependents();
     pdl_wait();
     const int64_t row = blockIdx.x;
     if (n_opt && row >= min(max(*n_opt, 0), (int)n)) return;
-    const X *src = x + row * x_stride;
+    int64_t from = row;
+    if (order) {
+        const int pair = order[row];
+        from = pair >= 0 && pair < n ? pair / k : -1;
+    }
+    const X *src = x + max(from, (int64_t)0) * x_stride;
     const int units = K / 8;
     float held[kRowHold][8], m = 0.f;
 #pragma unroll
@@ -717,7 +810,7 @@ __global__ void __launch_bounds__(kRowThreads)
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) {
-            const float a = v[j] * up, b = v[j + 4] * up;
+            const float a = from < 0 ? 0.f : v[j] * up, b = from < 0 ? 0.f : v[j + 4] * up;
             const __half2 h = __floats2half2_rn(a, b);
             hi[j] = bits_of(h);
             if (PARTS == 2) lo[j] = bits_of(__floats2half2_rn(a - __low2float(h), b - __high2float(h)));
@@ -739,16 +832,17 @@ __global__ void __launch_bounds__(kRowThreads)
     }
 }
 
-int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, int parts,
-            uint16_t *to, float *row_scale, cudaStream_t st) {
+int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt,
+            const int32_t *order, int k, int parts, uint16_t *to, float *row_scale, cudaStream_t st) {
     const dim3 grid((unsigned)n), block(kRowThreads);
     if (f32) {
         auto kernel = parts == 2 ? q4_rows_kernel<float, 2> : q4_rows_kernel<float, 1>;
-        return launch_pdl(kernel, grid, block, 0, st, static_cast<const float *>(x), x_stride, n, K, n_opt, to,
-                          row_scale);
+        return launch_pdl(kernel, grid, block, 0, st, static_cast<const float *>(x), x_stride, n, K, n_opt, order,
+                          k, to, row_scale);
     }
     return launch_pdl(q4_rows_kernel<__nv_bfloat16, 1>, grid, block, 0, st,
-                      static_cast<const __nv_bfloat16 *>(x), x_stride, n, K, n_opt, to, row_scale);
+                      static_cast<const __nv_bfloat16 *>(x), x_stride, n, K, n_opt, order, k, to,
+                      row_scale);
 }
 
 template <Q4Use USE, typename T, int GROUP>
@@ -763,8 +857,8 @@ static int launch_gemm(const CUtensorMap &code_map, const CUtensorMap &x_map, co
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)l.split, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr, cfg.numAttrs = l.split > 1 ? 2 : 1;
+    attr[1].val.clusterDim.x = (unsigned)(l.split * l.share), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr, cfg.numAttrs = l.split * l.share > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, code_map, x_map, p, r, l);
     if (e == cudaSuccess) return LB_OK;
     record_cuda_error(e);
@@ -779,7 +873,9 @@ static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *code
     const int64_t tiles = (p.N + rows - 1) / rows, pieces = (p.T + tokens - 1) / tokens;
     l.tiles = (int)tiles;
     const int steps = (p.K + kGmStep - 1) / kGmStep;
-    l.split = 1, l.steps = steps;
+    l.split = 1, l.steps = steps, l.share = 1;
+    l.pairs = p.N % 2 == 0 && p.y_stride % 2 == 0 && aligned_to(p.y, 4);
+    l.box = p.T <= 16 ? 16 : p.T <= 32 ? 32 : p.T <= 64 ? 64 : kGmBox;
     int64_t items = tiles * pieces;
     if (USE != kQ4Dense) items = tiles * std::min(p.T, std::min((int64_t)p.E, p.T) + p.T / tokens);
     if (USE == kQ4Dense && items * 2 <= sms) {
@@ -789,11 +885,17 @@ static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *code
         l.steps = (l.steps + 1) / 2 * 2;
         l.split = (steps + l.steps - 1) / l.steps;
     }
-    const unsigned grid = (unsigned)(std::min<int64_t>(items * l.split, l.split > 1 ? items * l.split : sms));
+    if (l.split == 1 && tiles > 1) {
+        l.share = kGmShare;
+        l.tiles = (int)((tiles + l.share - 1) / l.share * l.share);
+        items = items / tiles * (l.tiles / l.share);   // a cluster's
+    }
+    const int64_t most = l.split > 1 ? items : sms / l.share;
+    const unsigned grid = (unsigned)(std::min(items, most) * l.split * l.share);
     CUtensorMap codes_map, x_map;
     if (int e = encode_rows_map(&codes_map, codes, (uint64_t)p.K / 2, (uint64_t)code_rows, 64, kGmRows / 2, 64)) return e;
     if (int e = encode_rows_map(&x_map, r.x, (uint64_t)p.K * 2, (uint64_t)r.rows * (sizeof(T) == 4 ? 2 : 1), 128,
-                                USE == kQ4Up ? 1 : kGmBox, 128))
+                                (uint32_t)l.box, 128))
         return e;
     switch (p.group) {
         case 32: return launch_gemm<USE, T, 32>(codes_map, x_map, p, r, l, grid, st);
