@@ -35,16 +35,15 @@ constexpr int kGmMmaWarp = kGmCopyWarp + 1;
 constexpr int kGmWarps = kGmMmaWarp + 2;   // (whole groups of four)
 constexpr int kGmThreads = 32 * kGmWarps;
 constexpr int kGmOutThreads = 32 * kGmOutWarps;
+constexpr int kGmStages = 5;             // of x and of expanded weights
 constexpr int kGmB = 32768;              // bytes of a stage of x
-constexpr int kGmBStages = 5;
 constexpr int kGmC = kGmRows * 64;       // bytes of a stage of codes: two steps
 constexpr int kGmCStages = 6;
-constexpr int kGmAStages = 8;            // of expanded weights, 32 columns of tensor memory each
-constexpr int kGmABase = 256;            // they lie behind the accumulators
+constexpr int kGmABase = 256;            // expanded weights, 32 columns of tensor memory a stage, lie behind the accumulators
 constexpr int kGmBox = 128;              // tokens of a copy, at most
 constexpr int kGmMaxSplit = 8;
 constexpr int kGmShare = 2;
-constexpr int kGmSmem = kGmBStages * kGmB + kGmCStages * kGmC;
+constexpr int kGmSmem = kGmStages * kGmB + kGmCStages * kGmC;
 
 struct GmLaunch {
     int steps;        // of K, of a CTA
@@ -56,8 +55,7 @@ struct GmLaunch {
 };
 
 struct GmBars {
-    uint64_t a_full[kGmAStages], a_empty[kGmAStages];
-    uint64_t b_full[kGmBStages], b_empty[kGmBStages];
+    uint64_t full[kGmStages], empty[kGmStages];
     uint64_t c_full[kGmCStages], c_empty[kGmCStages];
     uint64_t d_full[2], d_empty[2], done;
 };
@@ -198,6 +196,37 @@ __device__ __forceinline__ void gm_commit_multicast(uint64_t *b, uint16_t mask) 
         : "memory");
 }
 
+// On to the next scales and zeros of a warp that takes every other step of 64 columns.
+template <int GROUP>
+__device__ __forceinline__ void q4_rotate(uint4 &d, uint2 &z) {
+    if (GROUP == 32) {
+        d.x = d.z, d.y = d.w;
+        z.x = z.y;
+    } else if (GROUP == 64) {
+        d.x = d.y, d.y = d.z, d.z = d.w;
+        z.x = __funnelshift_r(z.x, z.y, 16), z.y >>= 16;
+    } else {
+        d.x = __funnelshift_r(d.x, d.y, 16), d.y = __funnelshift_r(d.y, d.z, 16);
+        d.z = __funnelshift_r(d.z, d.w, 16), d.w >>= 16;
+        z.x = __funnelshift_r(z.x, z.y, 8), z.y >>= 8;
+    }
+}
+
+// A place in a ring of N stages, and the parity of its present phase.
+template <int N>
+struct GmRing {
+    uint32_t i = 0, phase = 0;
+    __device__ __forceinline__ void next(uint32_t n = 1) {   // n <= N
+        i += n;
+        if (i >= N) i -= N, phase ^= 1;
+    }
+    __device__ __forceinline__ void skip(uint32_t n) {
+        i += n;
+        phase ^= (i / N) & 1;
+        i %= N;
+    }
+};
+
 // An item: up to kTokens tokens (of one expert) times one tile of weight rows.
 struct GmItem {
     int expert, t0, tokens, tile;
@@ -225,8 +254,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     const int cluster = l.split * l.share;
 
     if (tid == 0) {
-        for (int i = 0; i < kGmAStages; i++) mbar_init(&bar.a_full[i], 4), mbar_init(&bar.a_empty[i], 1);
-        for (int i = 0; i < kGmBStages; i++) mbar_init(&bar.b_full[i], 1), mbar_init(&bar.b_empty[i], l.share);
+        // a stage is full when its four warps of weights and the copies of x are there
+        for (int i = 0; i < kGmStages; i++) mbar_init(&bar.full[i], 5), mbar_init(&bar.empty[i], l.share);
         for (int i = 0; i < kGmCStages; i++) mbar_init(&bar.c_full[i], 1), mbar_init(&bar.c_empty[i], kGmExpandWarps);
         for (int i = 0; i < 2; i++) mbar_init(&bar.d_full[i], 1), mbar_init(&bar.d_empty[i], kGmOutWarps);
         mbar_init(&bar.done, 1);
@@ -323,11 +352,13 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     // Bounded: about 2 s (2000 tries of up to a millisecond), after the first that ran out a few tries.
     int tries = 2000;
     auto wait = [&](uint64_t &b, uint32_t parity) {
-        int i = 0;
-        while (!mbar_try_wait_hint(&b, parity & 1, 1000000u) && i < tries) i++;
-        if (i >= tries) {
-            *p.error = 1;
-            tries = 4;
+        if (!mbar_try_wait(&b, parity & 1)) {
+            int i = 0;
+            while (!mbar_try_wait_hint(&b, parity & 1, 1000000u) && i < tries) i++;
+            if (i >= tries) {
+                *p.error = 1;
+                tries = 4;
+            }
         }
         __syncwarp();
     };
@@ -367,7 +398,8 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             auto meet_up = [&](float a, float b) {
                 const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? b : a, 16);
                 const float gate = lane < 16 ? a : other, up = lane < 16 ? other : b;
-                return gate / (1.f + expf(-gate)) * up;
+                // (exp and quotient to a few units of 2^-22: nothing beside a bf16 output's rounding)
+                return (F32 ? gate / (1.f + expf(-gate)) : __fdividef(gate, 1.f + __expf(-gate))) * up;
             };
             auto put_up = [&](int c, float h) {
                 const int col = c + (lane >> 4);
@@ -501,8 +533,10 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         constexpr int kBlock = 8 * GROUP / kGmStep;   // steps of eight groups, whose scales are held
         // the lane's row of a stage of codes, under the 64-byte swizzle
         const int at = USE == kQ4Up ? (lane & 16) * 4 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
-        const uint32_t from = smem_u32(smem) + kGmBStages * kGmB + at * 64, swizzle = (at >> 1) & 3;
-        uint32_t turn = 0, taken = 0;   // this CTA's steps, stages of codes so far
+        const uint32_t from = smem_u32(smem) + kGmStages * kGmB + at * 64, swizzle = (at >> 1) & 3;
+        GmRing<kGmStages> ring;
+        GmRing<kGmCStages> code;
+        uint32_t turn = 0;   // this CTA's steps so far
         for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
             bool in;
@@ -510,10 +544,10 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             const uint4 *ds = reinterpret_cast<const uint4 *>(p.scales + (in ? row : 0) * p.pitch);
             const uint2 *zs = ZEROS ? reinterpret_cast<const uint2 *>(p.zeros + (in ? row : 0) * p.pitch) : nullptr;
             const int parity = (half ^ turn) & 1;   // of the steps that are this warp's
-            const int s_begin = k0 / kGmStep;       // steps are counted from the row's start here
+            const int s_begin = k0 / kGmStep;       // (even)
             int next = s_begin / kBlock;
-            uint4 d8 = make_uint4(0, 0, 0, 0), d_next = d8;
-            uint2 z8 = make_uint2(0, 0), z_next = z8;
+            uint4 d_next = make_uint4(0, 0, 0, 0);
+            uint2 z_next = make_uint2(0, 0);
             auto ask = [&]() {
                 if (next * kBlock * kGmStep >= p.K) return;
                 if (!F32) d_next = ds[next];
@@ -521,75 +555,79 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 next++;
             };
             ask();
-            for (int sb = s_begin / kBlock * kBlock; sb < s_begin + steps; sb += kBlock) {
-                d8 = d_next, z8 = z_next;
-                ask();
-                const uint32_t dw[4] = {d8.x, d8.y, d8.z, d8.w};
-                const uint32_t zw[2] = {z8.x, z8.y};
-#pragma unroll
-                for (int j = 0; j < kBlock / 2; j++) {
-                    const int sj = 2 * j + ((parity ^ s_begin) & 1), s = sb + sj - s_begin;
-                    if (s < 0 || s >= steps) continue;
-                    // the scales (and zeros) of its two halves
-                    uint32_t d[2], z[2] = {8, 8};
-                    if (GROUP == 32) {
-                        const uint32_t w = sj & 1 ? dw[(2 * j + 1) & 3] : dw[(2 * j) & 3];
-                        d[0] = w & 0xffff, d[1] = w >> 16;
-                        if (ZEROS) {
-                            const uint32_t v = zw[j & 1] >> (sj & 1 ? 16 : 0);
-                            z[0] = v & 0xff, z[1] = v >> 8 & 0xff;
-                        }
-                    } else if (GROUP == 64) {
-                        d[0] = d[1] = sj & 1 ? dw[j & 3] >> 16 : dw[j & 3] & 0xffff;
-                        if (ZEROS) z[0] = z[1] = zw[j >> 1 & 1] >> (16 * (j & 1) + (sj & 1 ? 8 : 0)) & 0xff;
-                    } else {
-                        d[0] = d[1] = dw[j >> 1 & 3] >> (16 * (j & 1)) & 0xffff;
-                        if (ZEROS) z[0] = z[1] = zw[j >> 2 & 1] >> (8 * (j & 3)) & 0xff;
-                    }
-                    const uint32_t cs = (taken + s / 2) % kGmCStages, cr = (taken + s / 2) / kGmCStages;
-                    wait(bar.c_full[cs], cr);
-                    uint4 c[2];
-#pragma unroll
-                    for (int h = 0; h < 2; h++)
-                        asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                     : "=r"(c[h].x), "=r"(c[h].y), "=r"(c[h].z), "=r"(c[h].w)
-                                     : "r"(from + cs * kGmC + ((2 * (s & 1) + h) ^ swizzle) * 16)
-                                     : "memory");
-                    const uint32_t stage = (turn + s) % kGmAStages, round = (turn + s) / kGmAStages;
-                    wait(bar.a_empty[stage], round ^ 1);
-                    tc_fence_after();
-#pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        const __half2 low = half2_of(0x64006400u + z[h] * 0x10001u);   // 1024 + z
-                        // -(64 + z), whose last place is 2^-4
-                        const __half2 high = half2_of(0xD400D400u + z[h] * 0x00100010u);
-                        const __half2 scale = half2_of(d[h] * 0x10001u);
-                        uint32_t v[16];
-                        if (s * kGmStep + 32 * h < columns) {
-                            expand_f16<!F32>(c[h].x, low, high, scale, v);
-                            expand_f16<!F32>(c[h].y, low, high, scale, v + 4);
-                            expand_f16<!F32>(c[h].z, low, high, scale, v + 8);
-                            expand_f16<!F32>(c[h].w, low, high, scale, v + 12);
-                        } else {
-#pragma unroll
-                            for (int e = 0; e < 16; e++) v[e] = 0;
-                        }
-                        gm_tmem_st16(to + stage * 32 + 16 * h, v);
-                    }
-                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                    tc_fence_before();
-                    __syncwarp();
-                    if (lane == 0) mbar_arrive(&bar.a_full[stage]), mbar_arrive(&bar.c_empty[cs]);
+            GmRing<kGmStages> at_step = ring;
+            at_step.next(parity);
+            // the block of eight groups that is held: step `sj` of it is next
+            uint4 d8 = make_uint4(0, 0, 0, 0);
+            uint2 z8 = make_uint2(0, 0);
+            int sj = kBlock;
+#pragma unroll 1
+            for (int s = parity; s < steps; s += 2) {
+                if (sj >= kBlock) {
+                    d8 = d_next, z8 = z_next;
+                    sj = (s_begin + s) % kBlock;
+                    ask();
+                    // (a slice of K may begin inside a block)
+                    for (int skip = sj / 2; skip > 0; skip--) q4_rotate<GROUP>(d8, z8);
                 }
+                // the scales (and zeros) of the step's two halves
+                uint32_t d[2], z[2] = {8, 8};
+                if (GROUP == 32) {
+                    const uint32_t w = parity ? d8.y : d8.x, v = parity ? z8.x >> 16 : z8.x;
+                    d[0] = w & 0xffff, d[1] = w >> 16;
+                    if (ZEROS) z[0] = v & 0xff, z[1] = v >> 8 & 0xff;
+                } else if (GROUP == 64) {
+                    d[0] = d[1] = parity ? d8.x >> 16 : d8.x & 0xffff;
+                    if (ZEROS) z[0] = z[1] = (parity ? z8.x >> 8 : z8.x) & 0xff;
+                } else {
+                    d[0] = d[1] = d8.x & 0xffff;
+                    if (ZEROS) z[0] = z[1] = z8.x & 0xff;
+                }
+                q4_rotate<GROUP>(d8, z8);
+                sj += 2;
+                wait(bar.c_full[code.i], code.phase);
+                uint4 c[2];
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(c[h].x), "=r"(c[h].y), "=r"(c[h].z), "=r"(c[h].w)
+                                 : "r"(from + code.i * kGmC + ((2 * parity + h) ^ swizzle) * 16)
+                                 : "memory");
+                wait(bar.empty[at_step.i], at_step.phase ^ 1);
+                tc_fence_after();
+#pragma unroll
+                for (int h = 0; h < 2; h++) {
+                    const __half2 low = half2_of(0x64006400u + z[h] * 0x10001u);   // 1024 + z
+                    // -(64 + z), whose last place is 2^-4
+                    const __half2 high = half2_of(0xD400D400u + z[h] * 0x00100010u);
+                    const __half2 scale = half2_of(d[h] * 0x10001u);
+                    uint32_t v[16];
+                    if (s * kGmStep + 32 * h < columns) {
+                        expand_f16<!F32>(c[h].x, low, high, scale, v);
+                        expand_f16<!F32>(c[h].y, low, high, scale, v + 4);
+                        expand_f16<!F32>(c[h].z, low, high, scale, v + 8);
+                        expand_f16<!F32>(c[h].w, low, high, scale, v + 12);
+                    } else {
+#pragma unroll
+                        for (int e = 0; e < 16; e++) v[e] = 0;
+                    }
+                    gm_tmem_st16(to + at_step.i * 32 + 16 * h, v);
+                }
+                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                tc_fence_before();
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.full[at_step.i]), mbar_arrive(&bar.c_empty[code.i]);
+                at_step.next(2);
+                code.next();
             }
             // (an odd number of steps leaves half a stage of codes that one half of the warps has nothing of)
             if ((steps & 1) && parity) {
-                const uint32_t cs = (taken + steps / 2) % kGmCStages;
-                wait(bar.c_full[cs], (taken + steps / 2) / kGmCStages);
-                if (lane == 0) mbar_arrive(&bar.c_empty[cs]);
+                wait(bar.c_full[code.i], code.phase);
+                if (lane == 0) mbar_arrive(&bar.c_empty[code.i]);
+                code.next();
             }
             turn += steps;
-            taken += (steps + 1) / 2;
+            ring.skip(steps);
         }
         __syncwarp();
         named_sync(2, kGmThreads);
@@ -598,47 +636,55 @@ __global__ void __launch_bounds__(kGmThreads, 1)
       gm_fewer_registers<32>();
       if (warp == kGmCodeWarp) {
         // =================== codes: two copies of 64 rows x 128 columns a stage ===================
-        uint32_t turn = 0;
+        GmRing<kGmCStages> code;
+        int used = 0;
         for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
             const int64_t first = it.expert * matrix_rows + it.tile * (int64_t)(USE == kQ4Up ? kGmRows / 2 : kGmRows);
             const int64_t second = USE == kQ4Up ? first + p.N : first + kGmRows / 2;
-            for (int s = 0; s < steps; s += 2, turn++) {
-                const uint32_t stage = turn % kGmCStages;
-                wait(bar.c_empty[stage], (turn / kGmCStages) ^ 1);
+#pragma unroll 1
+            for (int s = 0; s < steps; s += 2) {
+                wait(bar.c_empty[code.i], code.phase ^ 1);
                 if (gm_elect()) {
-                    uint8_t *dst = smem + kGmBStages * kGmB + stage * kGmC;
-                    mbar_arrive_expect_tx(&bar.c_full[stage], kGmC);
-                    tma_load_2d(dst, &code_map, (k0 + s * kGmStep) / 2, (int)first, &bar.c_full[stage]);
-                    tma_load_2d(dst + kGmC / 2, &code_map, (k0 + s * kGmStep) / 2, (int)second, &bar.c_full[stage]);
+                    uint8_t *dst = smem + kGmStages * kGmB + code.i * kGmC;
+                    uint64_t *b = &bar.c_full[code.i];
+                    mbar_arrive_expect_tx(b, kGmC);
+                    tma_load_2d(dst, &code_map, (k0 + s * kGmStep) / 2, (int)first, b);
+                    tma_load_2d(dst + kGmC / 2, &code_map, (k0 + s * kGmStep) / 2, (int)second, b);
                 }
                 __syncwarp();
+                code.next();
+                used = min(used + 1, kGmCStages);
             }
         }
         // no copy may still be landing when the CTA exits
-        for (uint32_t t = turn > kGmCStages ? turn - kGmCStages : 0; t < turn; t++)
-            wait(bar.c_full[t % kGmCStages], t / kGmCStages);
+        for (int n = 0; n < used; n++) {
+            if (code.i == 0) code.i = kGmCStages, code.phase ^= 1;
+            code.i--;
+            wait(bar.c_full[code.i], code.phase);
+        }
     } else if (warp == kGmCopyWarp) {
         // =================== x ===================
-        uint32_t turn = 0;
+        GmRing<kGmStages> ring;
+        int used = 0;
         for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
             const int boxes = (it.tokens + l.box - 1) / l.box;
             const uint32_t bytes = (uint32_t)(kParts * boxes * l.box * 128);
             const int side = l.share > 1 ? blockIdx.x % l.share : 0;
-            for (int s = 0; s < steps; s++, turn++) {
-                const uint32_t stage = turn % kGmBStages;
-                wait(bar.b_empty[stage], (turn / kGmBStages) ^ 1);
+#pragma unroll 1
+            for (int s = 0; s < steps; s++) {
+                wait(bar.empty[ring.i], ring.phase ^ 1);
                 // (one thread issues everything: copies of several lanes go out one after the other, slower)
                 if (gm_elect()) {
-                    uint64_t *b = &bar.b_full[stage];
+                    uint64_t *b = &bar.full[ring.i];
                     mbar_arrive_expect_tx(b, bytes);
                     const int byte = (k0 + s * kGmStep) * 2;
                     // the CTAs that share the tokens copy every share-th box to all of them
                     for (int box = side; box < boxes; box += l.share) {
 #pragma unroll
                         for (int part = 0; part < kParts; part++) {
-                            uint8_t *to = smem + stage * kGmB + part * (kGmB / 2) + box * l.box * 128;
+                            uint8_t *to = smem + ring.i * kGmB + part * (kGmB / 2) + box * l.box * 128;
                             const int row = part * (int)r.rows + it.t0 + box * l.box;
                             if (l.share > 1) gm_load_multicast(to, &x_map, byte, row, b, (uint16_t)((1 << l.share) - 1));
                             else tma_load_2d(to, &x_map, byte, row, b);
@@ -646,28 +692,36 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                     }
                 }
                 __syncwarp();
+                ring.next();
+                used = min(used + 1, kGmStages);
             }
         }
         // (the other CTA's arrivals have to have come, too, before this one may exit)
-        for (uint32_t t = turn > kGmBStages ? turn - kGmBStages : 0; t < turn; t++) {
-            wait(bar.b_full[t % kGmBStages], t / kGmBStages);
-            wait(bar.b_empty[t % kGmBStages], t / kGmBStages);
+        for (int n = 0; n < used; n++) {
+            if (ring.i == 0) ring.i = kGmStages, ring.phase ^= 1;
+            ring.i--;
+            wait(bar.full[ring.i], ring.phase);
+            wait(bar.empty[ring.i], ring.phase);
         }
     } else if (warp == kGmMmaWarp) {
         // =================== tensor-core operations ===================
-        uint32_t turn = 0, taken = 0;   // steps, accumulators
+        GmRing<kGmStages> ring;
+        uint32_t taken = 0;   // accumulators
         for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
             const GmItem it = item_of(i);
             const uint32_t idesc = idesc_f16(kGmRows, (it.tokens + 15) / 16 * 16);
             if (!F32) wait(bar.d_empty[0], taken ^ 1);
-            for (int s = 0; s < steps; s++, turn++) {
-                const uint32_t sa = turn % kGmAStages, sb = turn % kGmBStages;
-                wait(bar.a_full[sa], turn / kGmAStages);
-                wait(bar.b_full[sb], turn / kGmBStages);
+#pragma unroll 1
+            for (int s = 0; s < steps; s++) {
+                wait(bar.full[ring.i], ring.phase);
                 tc_fence_after();
-                const uint32_t a = tmem + kGmABase + sa * 32, b = gm_desc_low(smem_u32(smem) + sb * kGmB);
+                const uint32_t a = tmem + kGmABase + ring.i * 32, b = gm_desc_low(smem_u32(smem) + ring.i * kGmB);
                 if constexpr (!F32) {
-                    if (gm_elect()) gm_mma4(tmem, a, b, idesc, s > 0);
+                    if (gm_elect()) {
+                        gm_mma4(tmem, a, b, idesc, s > 0);
+                        if (l.share > 1) gm_commit_multicast(&bar.empty[ring.i], (uint16_t)((1 << l.share) - 1));
+                        else mma_commit(&bar.empty[ring.i]);
+                    }
                 } else {
                     constexpr int kTurns = GROUP == 32 ? 2 : 1;   // accumulators of a step
 #pragma unroll
@@ -687,21 +741,18 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                                 gm_mma4(d, a, b, idesc, !begin);
                                 gm_mma4(d, a, b + (kGmB / 2 >> 4), idesc, 1);
                             }
+                            if (GROUP < 128 || s % 2 == 1) mma_commit(&bar.d_full[buf]);
                         }
+                        if (GROUP < 128 || s % 2 == 1) taken++;
                         __syncwarp();
-                        if (GROUP < 128 || s % 2 == 1) {
-                            if (gm_elect()) mma_commit(&bar.d_full[buf]);
-                            taken++;
-                        }
+                    }
+                    if (gm_elect()) {
+                        if (l.share > 1) gm_commit_multicast(&bar.empty[ring.i], (uint16_t)((1 << l.share) - 1));
+                        else mma_commit(&bar.empty[ring.i]);
                     }
                 }
                 __syncwarp();
-                if (gm_elect()) {
-                    mma_commit(&bar.a_empty[sa]);
-                    if (l.share > 1) gm_commit_multicast(&bar.b_empty[sb], (uint16_t)((1 << l.share) - 1));
-                    else mma_commit(&bar.b_empty[sb]);
-                }
-                __syncwarp();
+                ring.next();
             }
             if (!F32) {
                 if (gm_elect()) mma_commit(&bar.d_full[0]);
