@@ -14,7 +14,7 @@
 // Rows of x are scaled by powers of two into fp16's range beforehand (q4_rows), and stored in the order
 // in which the codes of a word unfold, pairs (0, 4), (1, 5), (2, 6), (3, 7).
 //
-// One CTA per SM, 20 warps: eight that take the sums out (a quarter of the lanes times half of
+// One CTA per SM, 19 warps: eight that take the sums out (a quarter of the lanes times half of
 // the columns each), eight that expand weights, one that has codes copied in (tensor copies, 128 rows x 128
 // columns), one that has x copied in (tensor copies of 64 rows x 64 columns), one that issues the tensor-core operations.  Calls with few tiles are
 // split along K over a cluster; the parts are added up through distributed shared memory.  In others two CTAs
@@ -32,7 +32,7 @@ constexpr int kGmStep = 64;              // columns of K of a stage
 constexpr int kGmOutWarps = 8, kGmExpandWarps = 8;
 constexpr int kGmCodeWarp = kGmOutWarps + kGmExpandWarps, kGmCopyWarp = kGmCodeWarp + 1;
 constexpr int kGmMmaWarp = kGmCopyWarp + 1;
-constexpr int kGmWarps = kGmMmaWarp + 2;   // (whole groups of four)
+constexpr int kGmWarps = kGmMmaWarp + 1;
 constexpr int kGmThreads = 32 * kGmWarps;
 constexpr int kGmOutThreads = 32 * kGmOutWarps;
 constexpr int kGmStages = 5;             // of x and of expanded weights
@@ -112,35 +112,23 @@ __device__ __forceinline__ void gm_tmem_st16(uint32_t taddr, const uint32_t *r) 
 __device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 
-// A group of four warps' registers per thread.  640 threads start with 96 (61440); then 256 have 144, 256 have
-// 80 and 128 have 32 (61440), and in the end all 96 again.  The others take theirs back only after the 256 have given
-// theirs up: a CTA without work would otherwise have nothing left for warps that still wait for their 144.
-template <int N>
-__device__ __forceinline__ void gm_more_registers() {
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
-}
-template <int N>
-__device__ __forceinline__ void gm_fewer_registers() {
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
-}
-// 32 columns asked for; they are there after gm_ld32_wait.
-__device__ __forceinline__ void gm_ld32_start(uint32_t taddr, uint32_t *r) {
+// 16 columns asked for; they are there after gm_ld_wait.
+__device__ __forceinline__ void gm_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
-        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,"
-        "%14,%15,%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        "tcgen05.ld.sync.aligned.32x32b.x16.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, [%16];"
         : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]),
           "=r"(r[7]), "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]),
-          "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]), "=r"(r[18]),
-          "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
-          "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]),
-          "=r"(r[31])
+          "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
         : "r"(taddr)
         : "memory");
 }
-__device__ __forceinline__ void gm_ld_wait() { asm volatile("tcgen05.wait::ld.sync.aligned;" ::: "memory"); }
-// (no use of r is moved before this)
-__device__ __forceinline__ void gm_hold8(uint32_t *r) {
-    asm volatile("" : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7])::"memory");
+__device__ __forceinline__ void gm_ld_wait(uint32_t (&r)[16]) {
+    asm volatile("tcgen05.wait::ld.sync.aligned;"
+                 : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]),
+                   "+r"(r[6]), "+r"(r[7]), "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]),
+                   "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
+                 :
+                 : "memory");
 }
 
 // Eight codes of a word less the zero, times the scale: pairs (0, 4), (1, 5), (2, 6), (3, 7) of fp16.  The codes
@@ -245,10 +233,11 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ GmBars bar;
     __shared__ uint32_t s_tmem;
-    __shared__ int s_first[USE == kQ4Dense ? 1 : LB_ROUTE_MAX_EXPERTS + 1];  // pieces before an expert's
+    constexpr int kExperts = USE == kQ4Dense ? 1 : LB_ROUTE_MAX_EXPERTS;
+    __shared__ int s_first[kExperts], s_row[kExperts], s_count[kExperts];  // pieces and pairs before an expert's, pairs
     __shared__ int s_part[32];
-    __shared__ float col_scale[kTokens];
-    __shared__ int col_row[kTokens];
+    __shared__ __align__(16) float col_scale[2][kTokens];   // of an item and the next one
+    __shared__ __align__(16) int col_row[2][kTokens];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int rank = blockIdx.x % l.split;            // along K
     const int cluster = l.split * l.share;
@@ -275,7 +264,9 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             n[i] = 0;
             if (e < p.E) {
                 const int first = min(max(p.start[e], 0), (int)p.T);
-                n[i] = (max(min(p.start[e + 1], (int)p.T) - first, 0) + kTokens - 1) / kTokens;
+                const int count = max(min(p.start[e + 1], (int)p.T) - first, 0);
+                s_row[e] = first, s_count[e] = count;
+                n[i] = (count + kTokens - 1) / kTokens;
             }
             sum += n[i];
         }
@@ -297,7 +288,6 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             if (tid * kEach + i < p.E) s_first[tid * kEach + i] = before;
             before += n[i];
         }
-        if (tid == 0) s_first[p.E] = total;
         pieces = total;
     }
     // Tensor memory is taken when the kernels before this one have ended, and the next one may start only after
@@ -309,12 +299,13 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = s_tmem;
-    const int64_t items = (int64_t)pieces * (l.tiles / l.share);   // of a cluster
-    const int64_t each = gridDim.x / cluster;
-    auto item_of = [&](int64_t i) {
+    const int side = l.tiles / l.share;
+    const int items = pieces * side;   // of a cluster
+    const int each = gridDim.x / cluster, begin = blockIdx.x / cluster;
+    auto item_of = [&](int i) {
         GmItem it;
-        const int side = l.tiles / l.share, piece = (int)(i / side);
-        it.tile = (int)(i % side) * l.share + blockIdx.x % l.share;
+        const int piece = i / side;
+        it.tile = (i - piece * side) * l.share + blockIdx.x % l.share;
         if constexpr (USE == kQ4Dense) {
             it.expert = 0;
             it.t0 = piece * kTokens;
@@ -327,9 +318,9 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 else hi = m;
             }
             it.expert = lo;
-            const int first = min(max(p.start[lo], 0), (int)p.T), end = min(p.start[lo + 1], (int)p.T);
-            it.t0 = first + (piece - s_first[lo]) * kTokens;
-            it.tokens = min(kTokens, end - it.t0);
+            const int at = (piece - s_first[lo]) * kTokens;
+            it.t0 = s_row[lo] + at;
+            it.tokens = min(kTokens, s_count[lo] - at);
         }
         return it;
     };
@@ -366,53 +357,100 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     if (warp < kGmOutWarps) {
         // =================== sums out: a lane per weight row ===================
         const int quarter = warp & 3, c0 = (warp >> 2) * kCols;
-        const uint32_t at_lane = tmem + ((uint32_t)(quarter * 32) << 16);
+        const uint32_t at_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
         uint32_t turn = 0;   // accumulators taken so far
-        gm_more_registers<144>();
-        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
+        // scale and output row of an item's column tid
+        float scale = 0.f;
+        int to = 0;
+        auto ask = [&](int i) {
+            if (i >= items) return;
             const GmItem it = item_of(i);
-            __syncwarp();
-            named_sync(1, kGmOutThreads);   // the last item's columns are done with
-            for (int c = tid; c < it.tokens; c += kGmOutThreads) {
-                int to = it.t0 + c;
-                if (USE == kQ4Down) {
-                    const int pair = p.order[it.t0 + c];
-                    to = pair >= 0 && pair < p.T ? pair : -1;
-                }
-                col_scale[c] = r.row_scale[it.t0 + c];
-                col_row[c] = to;
+            if (tid >= it.tokens) return;
+            scale = r.row_scale[it.t0 + tid];
+            to = it.t0 + tid;
+            if (USE == kQ4Down) {
+                const int pair = p.order[it.t0 + tid];
+                to = pair >= 0 && pair < p.T ? pair : -1;
             }
+        };
+        int buf = 0;
+        auto tell = [&]() {
+            if (tid < kTokens) col_scale[buf][tid] = scale, col_row[buf][tid] = to;
+            __syncwarp();
             named_sync(1, kGmOutThreads);
+        };
+        ask(begin);
+        tell();
+#pragma unroll 1
+        for (int i = begin; i < items; i += each) {
+            const GmItem it = item_of(i);
+            ask(i + each);
             bool in;
             const int64_t row = row_of(it, quarter * 32 + lane, in);
             const int mine = min(max(it.tokens - c0, 0), kCols);   // columns of this warp
-            // where a finished sum goes
-            auto put = [&](int c, float v) {
-                const int to = col_row[c0 + c];
-                if (USE == kQ4Dense)
-                    gm_store(static_cast<T *>(p.y) + to * p.y_stride + row, v);
-                else if (to >= 0)
-                    static_cast<float *>(p.y)[to * p.y_stride + (row - it.expert * matrix_rows)] = v;
+            float *park = reinterpret_cast<float *>(smem) + c0 * kGmRows + quarter * 32 + lane;   // [column][128]
+            // 16 columns from c (of this warp's) on
+            auto emit = [&](int c, const float (&v)[16]) {
+                if (l.split > 1) {
+#pragma unroll
+                    for (int j = 0; j < 16; j++)
+                        if (c + j < mine) park[(c + j) * kGmRows] = v[j];
+                    return;
+                }
+                float x[16];
+#pragma unroll
+                for (int j = 0; j < 4; j++) {
+                    const float4 f = *reinterpret_cast<const float4 *>(&col_scale[buf][c0 + c + 4 * j]);
+                    x[4 * j] = v[4 * j] * f.x, x[4 * j + 1] = v[4 * j + 1] * f.y;
+                    x[4 * j + 2] = v[4 * j + 2] * f.z, x[4 * j + 3] = v[4 * j + 3] * f.w;
+                }
+                const int left = mine - c;
+                if constexpr (USE == kQ4Up) {
+                    // gate and up rows of a column pair meet: lanes 0..15 make h of the first column, 16..31 of the second
+                    const int64_t n = it.tile * (int64_t)(kGmRows / 2) + quarter * 16 + (lane & 15);
+                    float *h = static_cast<float *>(p.y) + (int64_t)(it.t0 + c0 + c + (lane >> 4)) * p.y_stride + n;
+                    const int mine_left = n < p.N ? left - (lane >> 4) : 0;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2, h += 2 * p.y_stride) {
+                        const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? x[j + 1] : x[j], 16);
+                        const float gate = lane < 16 ? x[j] : other, up = lane < 16 ? other : x[j + 1];
+                        // (bf16: exp and quotient to a few units of 2^-22, nothing beside an output's rounding)
+                        const float silu = F32 ? gate / (1.f + expf(-gate)) : __fdividef(gate, 1.f + __expf(-gate));
+                        if (j < mine_left) *h = silu * up;
+                    }
+                } else if constexpr (USE == kQ4Down) {
+#pragma unroll
+                    for (int j = 0; j < 16; j++) {
+                        const int at = col_row[buf][c0 + c + j];
+                        if (j < left && in && at >= 0)
+                            static_cast<float *>(p.y)[at * p.y_stride + (row - it.expert * matrix_rows)] = x[j];
+                    }
+                } else if constexpr (F32) {
+                    float *y = static_cast<float *>(p.y) + (it.t0 + c0 + c) * p.y_stride + row;
+#pragma unroll
+                    for (int j = 0; j < 16; j++, y += p.y_stride)
+                        if (j < left && in) *y = x[j];
+                } else if (l.pairs) {
+                    // rows 2i and 2i + 1 meet: even lanes store both of a pair's first column, odd ones of the second
+                    uint16_t *y = static_cast<uint16_t *>(p.y) + (it.t0 + c0 + c + (lane & 1)) * p.y_stride + (row & ~1);
+                    const int mine_left = in ? left - (lane & 1) : 0;
+#pragma unroll
+                    for (int j = 0; j < 16; j += 2, y += 2 * p.y_stride) {
+                        const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? x[j] : x[j + 1], 1);
+                        const uint32_t two = lane & 1 ? bf16_pair(other, x[j + 1]) : bf16_pair(x[j], other);
+                        if (j < mine_left) *reinterpret_cast<uint32_t *>(y) = two;
+                    }
+                } else {
+                    __nv_bfloat16 *y = static_cast<__nv_bfloat16 *>(p.y) + (it.t0 + c0 + c) * p.y_stride + row;
+#pragma unroll
+                    for (int j = 0; j < 16; j++, y += p.y_stride)
+                        if (j < left && in) *y = __float2bfloat16_rn(x[j]);
+                }
             };
-            // gate and up rows of a column pair meet: lanes 0..15 make h of column c, 16..31 of c + 1
-            auto meet_up = [&](float a, float b) {
-                const float other = __shfl_xor_sync(0xffffffffu, lane < 16 ? b : a, 16);
-                const float gate = lane < 16 ? a : other, up = lane < 16 ? other : b;
-                // (exp and quotient to a few units of 2^-22: nothing beside a bf16 output's rounding)
-                return (F32 ? gate / (1.f + expf(-gate)) : __fdividef(gate, 1.f + __expf(-gate))) * up;
-            };
-            auto put_up = [&](int c, float h) {
-                const int col = c + (lane >> 4);
-                const int64_t n = it.tile * (int64_t)(kGmRows / 2) + quarter * 16 + (lane & 15);
-                if (col < mine && n < p.N)
-                    static_cast<float *>(p.y)[(int64_t)(it.t0 + c0 + col) * p.y_stride + n] = h;
-            };
-            float *park = reinterpret_cast<float *>(smem) + quarter * 32 + lane;   // [column][128]
             if constexpr (F32) {
                 uint64_t total[kCols / 2];   // pairs of columns
 #pragma unroll
                 for (int c = 0; c < kCols / 2; c++) total[c] = 0;
-                auto sum_of = [&](int c) { return __uint_as_float((uint32_t)(total[c / 2] >> (32 * (c & 1)))); };
                 const uint4 *ds = reinterpret_cast<const uint4 *>(p.scales + (in ? row : 0) * p.pitch) + k0 / GROUP / 8;
                 const int groups = columns / GROUP;
                 uint4 held = ds[0];   // eight groups' scales
@@ -429,7 +467,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                     for (int q = 0; q < kCols / 16; q++) {
                         if (16 * q >= mine) break;
                         uint64_t v[8];
-                        tmem_ld16_pairs(at_lane + (turn & 1) * kTokens + c0 + 16 * q, v);
+                        tmem_ld16_pairs(at_lane + (turn & 1) * kTokens + 16 * q, v);
 #pragma unroll
                         for (int c = 0; c < 8; c++) ffma2p(total[8 * q + c], v[c], d2);
                     }
@@ -437,97 +475,51 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                     __syncwarp();
                     if (lane == 0) mbar_arrive(&bar.d_empty[turn & 1]);
                 }
-                if (l.split > 1) {
 #pragma unroll
-                    for (int c = 0; c < kCols; c++)
-                        if (c < mine) park[(c0 + c) * kGmRows] = sum_of(c);
-                } else if (USE == kQ4Up) {
+                for (int q = 0; q < kCols / 16; q++) {
+                    if (16 * q >= mine) break;
+                    float v[16];
 #pragma unroll
-                    for (int c = 0; c < kCols; c += 2)
-                        if (c < mine)
-                            put_up(c, meet_up(sum_of(c) * col_scale[c0 + c],
-                                              sum_of(c + 1) * col_scale[c0 + min(c + 1, mine - 1)]));
-                } else if (in) {
-#pragma unroll
-                    for (int c = 0; c < kCols; c++)
-                        if (c < mine) put(c, sum_of(c) * col_scale[c0 + c]);
+                    for (int c = 0; c < 16; c++)
+                        v[c] = __uint_as_float((uint32_t)(total[8 * q + c / 2] >> (32 * (c & 1))));
+                    emit(16 * q, v);
                 }
             } else {
-                // The accumulator is free for the next item when its second half is in registers; the first one's
-                // results wait there, too (a down product's, of which there are as many as sums, are stored at once).
-                constexpr int kHalf = kCols / 2;
-                uint32_t v[kHalf], done[kHalf / 2];
-                // what this lane stores for columns c and c + 1
-                auto meet = [&](int c, uint32_t va, uint32_t vb) -> uint32_t {
-                    const float a = __uint_as_float(va) * col_scale[c0 + c];
-                    const float b = __uint_as_float(vb) * col_scale[c0 + min(c + 1, mine - 1)];
-                    if (USE == kQ4Up) return __float_as_uint(meet_up(a, b));
-                    if (!l.pairs) return bf16_pair(a, b);
-                    // rows 2i and 2i + 1 meet: even lanes store both of column c, odd ones of c + 1
-                    const float other = __shfl_xor_sync(0xffffffffu, lane & 1 ? a : b, 1);
-                    return lane & 1 ? bf16_pair(other, b) : bf16_pair(a, other);
-                };
-                auto keep = [&](int c, uint32_t w) {
-                    if (USE == kQ4Up) {
-                        put_up(c, __uint_as_float(w));
-                    } else {
-                        uint16_t *y = static_cast<uint16_t *>(p.y) + (it.t0 + c0 + c) * p.y_stride + row;
-                        if (l.pairs) {
-                            if (lane & 1) y += p.y_stride - 1;
-                            if (in && c + (lane & 1) < mine) *reinterpret_cast<uint32_t *>(y) = w;
-                        } else if (in) {
-                            y[0] = (uint16_t)w;
-                            if (c + 1 < mine) y[p.y_stride] = (uint16_t)(w >> 16);
-                        }
-                    }
-                };
+                // 16 columns are asked for while the 16 before them go out (a small loop: results kept in
+                // registers, to free the accumulator sooner, took code that pushed the other warps' out of the
+                // instruction cache)
                 wait(bar.d_full[0], turn);
                 turn++;
                 tc_fence_after();
-#pragma unroll
-                for (int h = 0; h < 2; h++) {
+                auto leave = [&]() {   // the next item may have the accumulator
+                    tc_fence_before();
                     __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.d_empty[0]);
+                };
+                uint32_t a[16], b[16];
+                auto out = [&](int c, uint32_t (&now)[16], uint32_t (&then)[16]) {
+                    gm_ld_wait(now);
+                    if (c + 16 < mine) gm_ld16_start(at_lane + c + 16, then);
+                    else leave();
+                    float v[16];
 #pragma unroll
-                    for (int q = 0; q < kHalf / 32; q++)
-                        gm_ld32_start(at_lane + c0 + h * kHalf + 32 * q, v + 32 * q);
-                    gm_ld_wait();
-#pragma unroll
-                    for (int c = 0; c < kHalf; c += 8) gm_hold8(v + c);
-                    if (h == 1) {
-                        tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) mbar_arrive(&bar.d_empty[0]);
-                    }
-                    if (l.split > 1) {
-#pragma unroll
-                        for (int c = 0; c < kHalf; c++)
-                            if (h * kHalf + c < mine) park[(c0 + h * kHalf + c) * kGmRows] = __uint_as_float(v[c]);
-                    } else if (USE == kQ4Down) {
-#pragma unroll
-                        for (int c = 0; c < kHalf; c++)
-                            if (h * kHalf + c < mine && in)
-                                put(h * kHalf + c, __uint_as_float(v[c]) * col_scale[c0 + h * kHalf + c]);
-                    } else if (h == 0) {
-#pragma unroll
-                        for (int c = 0; c < kHalf; c += 2)
-                            if (c < mine) done[c / 2] = meet(c, v[c], v[c + 1]);
-                    } else {
-#pragma unroll
-                        for (int c = 0; c < kHalf; c += 2)
-                            if (c < mine) keep(c, done[c / 2]);
-#pragma unroll
-                        for (int c = 0; c < kHalf; c += 2)
-                            if (kHalf + c < mine) keep(kHalf + c, meet(kHalf + c, v[c], v[c + 1]));
-                    }
+                    for (int j = 0; j < 16; j++) v[j] = __uint_as_float(now[j]);
+                    emit(c, v);
+                    __syncwarp();
+                };
+                if (mine > 0) gm_ld16_start(at_lane, a);
+                else leave();
+#pragma unroll 1
+                for (int c = 0; c < mine; c += 32) {
+                    out(c, a, b);
+                    if (c + 16 < mine) out(c + 16, b, a);
                 }
             }
+            buf ^= 1;
+            tell();
         }
-        __syncwarp();
-        gm_fewer_registers<96>();
-        named_sync(2, kGmThreads);
     } else if (warp < kGmOutWarps + kGmExpandWarps) {
         // =================== weights: a thread per row, every other step ===================
-        gm_fewer_registers<80>();
         const int quarter = warp & 3, half = (warp - kGmOutWarps) >> 2;
         const uint32_t to = tmem + kGmABase + ((uint32_t)(quarter * 32) << 16);
         constexpr int kBlock = 8 * GROUP / kGmStep;   // steps of eight groups, whose scales are held
@@ -537,36 +529,53 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         GmRing<kGmStages> ring;
         GmRing<kGmCStages> code;
         uint32_t turn = 0;   // this CTA's steps so far
-        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
-            const GmItem it = item_of(i);
-            bool in;
-            const int64_t row = row_of(it, quarter * 32 + lane, in);
-            const uint4 *ds = reinterpret_cast<const uint4 *>(p.scales + (in ? row : 0) * p.pitch);
-            const uint2 *zs = ZEROS ? reinterpret_cast<const uint2 *>(p.zeros + (in ? row : 0) * p.pitch) : nullptr;
+        // Scales and zeros of eight groups are asked for before the eight before them are used, an item's first ones
+        // during the item before it.
+        const int s_begin = k0 / kGmStep, first_block = s_begin / kBlock;       // (s_begin is even)
+        const int end_block = (s_begin + steps + kBlock - 1) / kBlock;
+        uint4 d_next = make_uint4(0, 0, 0, 0);
+        uint2 z_next = make_uint2(0, 0);
+        int held = -1, next = 0, asked = -1;   // the item of d_next, the next block, the item that `at` is for
+        int64_t at_row = 0;
+        auto ask = [&](int i, int block) {
+            if (i >= items) return;
+            if (asked != i) {
+                bool in;
+                const int64_t row = row_of(item_of(i), quarter * 32 + lane, in);
+                at_row = (in ? row : 0) * p.pitch;
+                asked = i;
+            }
+            if (!F32) d_next = reinterpret_cast<const uint4 *>(p.scales + at_row)[block];
+            if (ZEROS) z_next = reinterpret_cast<const uint2 *>(p.zeros + at_row)[block];
+            held = i;
+        };
+        for (int i = begin; i < items; i += each) {
             const int parity = (half ^ turn) & 1;   // of the steps that are this warp's
-            const int s_begin = k0 / kGmStep;       // (even)
-            int next = s_begin / kBlock;
-            uint4 d_next = make_uint4(0, 0, 0, 0);
-            uint2 z_next = make_uint2(0, 0);
-            auto ask = [&]() {
-                if (next * kBlock * kGmStep >= p.K) return;
-                if (!F32) d_next = ds[next];
-                if (ZEROS) z_next = zs[next];
-                next++;
-            };
-            ask();
+            if (held != i) ask(i, first_block);
+            next = first_block + 1;
             GmRing<kGmStages> at_step = ring;
             at_step.next(parity);
             // the block of eight groups that is held: step `sj` of it is next
             uint4 d8 = make_uint4(0, 0, 0, 0);
             uint2 z8 = make_uint2(0, 0);
             int sj = kBlock;
+            uint4 c[2];
+            bool there = false;
+            auto load = [&]() {
+#pragma unroll
+                for (int h = 0; h < 2; h++)
+                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
+                                 : "=r"(c[h].x), "=r"(c[h].y), "=r"(c[h].z), "=r"(c[h].w)
+                                 : "r"(from + code.i * kGmC + ((2 * parity + h) ^ swizzle) * 16)
+                                 : "memory");
+            };
 #pragma unroll 1
             for (int s = parity; s < steps; s += 2) {
                 if (sj >= kBlock) {
                     d8 = d_next, z8 = z_next;
                     sj = (s_begin + s) % kBlock;
-                    ask();
+                    if (next < end_block) ask(i, next++);
+                    else ask(i + each, first_block);
                     // (a slice of K may begin inside a block)
                     for (int skip = sj / 2; skip > 0; skip--) q4_rotate<GROUP>(d8, z8);
                 }
@@ -585,14 +594,10 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 }
                 q4_rotate<GROUP>(d8, z8);
                 sj += 2;
-                wait(bar.c_full[code.i], code.phase);
-                uint4 c[2];
-#pragma unroll
-                for (int h = 0; h < 2; h++)
-                    asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
-                                 : "=r"(c[h].x), "=r"(c[h].y), "=r"(c[h].z), "=r"(c[h].w)
-                                 : "r"(from + code.i * kGmC + ((2 * parity + h) ^ swizzle) * 16)
-                                 : "memory");
+                if (!there) {
+                    wait(bar.c_full[code.i], code.phase);
+                    load();
+                }
                 wait(bar.empty[at_step.i], at_step.phase ^ 1);
                 tc_fence_after();
 #pragma unroll
@@ -613,12 +618,17 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                     }
                     gm_tmem_st16(to + at_step.i * 32 + 16 * h, v);
                 }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&bar.c_empty[code.i]);
+                code.next();
+                // the next step's codes, if they have come, while the weights are on their way
+                there = s + 2 < steps && __all_sync(0xffffffffu, mbar_try_wait(&bar.c_full[code.i], code.phase));
+                if (there) load();
                 asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
                 tc_fence_before();
                 __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.full[at_step.i]), mbar_arrive(&bar.c_empty[code.i]);
+                if (lane == 0) mbar_arrive(&bar.full[at_step.i]);
                 at_step.next(2);
-                code.next();
             }
             // (an odd number of steps leaves half a stage of codes that one half of the warps has nothing of)
             if ((steps & 1) && parity) {
@@ -629,16 +639,11 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             turn += steps;
             ring.skip(steps);
         }
-        __syncwarp();
-        named_sync(2, kGmThreads);
-        gm_more_registers<96>();
-    } else {
-      gm_fewer_registers<32>();
-      if (warp == kGmCodeWarp) {
+    } else if (warp == kGmCodeWarp) {
         // =================== codes: two copies of 64 rows x 128 columns a stage ===================
         GmRing<kGmCStages> code;
         int used = 0;
-        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
+        for (int i = begin; i < items; i += each) {
             const GmItem it = item_of(i);
             const int64_t first = it.expert * matrix_rows + it.tile * (int64_t)(USE == kQ4Up ? kGmRows / 2 : kGmRows);
             const int64_t second = USE == kQ4Up ? first + p.N : first + kGmRows / 2;
@@ -667,7 +672,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         // =================== x ===================
         GmRing<kGmStages> ring;
         int used = 0;
-        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
+        for (int i = begin; i < items; i += each) {
             const GmItem it = item_of(i);
             const int boxes = (it.tokens + l.box - 1) / l.box;
             const uint32_t bytes = (uint32_t)(kParts * boxes * l.box * 128);
@@ -707,7 +712,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         // =================== tensor-core operations ===================
         GmRing<kGmStages> ring;
         uint32_t taken = 0;   // accumulators
-        for (int64_t i = blockIdx.x / cluster; i < items; i += each) {
+        for (int i = begin; i < items; i += each) {
             const GmItem it = item_of(i);
             const uint32_t idesc = idesc_f16(kGmRows, (it.tokens + 15) / 16 * 16);
             if (!F32) wait(bar.d_empty[0], taken ^ 1);
@@ -764,23 +769,18 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         __syncwarp();
         wait(bar.done, 0);
         tc_fence_before();
-      }
-      __syncwarp();
-      named_sync(2, kGmThreads);
-      gm_more_registers<96>();
     }
     __syncthreads();
     tc_fence_after();
     if (l.split > 1) {
         // one item per cluster: its parts' sums, a share of the columns per CTA, a warp per column
         gm_cluster_sync();
-        const int64_t i = blockIdx.x / cluster;
-        if (i < items) {
-            const GmItem it = item_of(i);
+        if (begin < items) {
+            const GmItem it = item_of(begin);
             const float *park = reinterpret_cast<const float *>(smem);
             for (int c = rank + l.split * warp; c < it.tokens; c += l.split * kGmWarps) {
-                const float scale = col_scale[c];
-                const int to = col_row[c];
+                const float scale = col_scale[0][c];
+                const int to = col_row[0][c];
 #pragma unroll
                 for (int j = 0; j < 4; j++) {
                     const int at = j * 32 + lane;
