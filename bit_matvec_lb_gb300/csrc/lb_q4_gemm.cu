@@ -14,7 +14,7 @@
 // Rows of x are scaled by powers of two into fp16's range beforehand (q4_rows), and stored in the order
 // in which the codes of a word unfold, pairs (0, 4), (1, 5), (2, 6), (3, 7).
 //
-// One CTA per SM, 19 warps: eight that take the sums out (a quarter of the lanes times half of
+// One CTA per SM, 20 warps (one has nothing to do): eight that take the sums out (a quarter of the lanes times half of
 // the columns each), eight that expand weights, one that has codes copied in (tensor copies, 128 rows x 128
 // columns), one that has x copied in (tensor copies of 64 rows x 64 columns), one that issues the tensor-core operations.  Calls with few tiles are
 // split along K over a cluster; the parts are added up through distributed shared memory.  In others two CTAs
@@ -32,7 +32,7 @@ constexpr int kGmStep = 64;              // columns of K of a stage
 constexpr int kGmOutWarps = 8, kGmExpandWarps = 8;
 constexpr int kGmCodeWarp = kGmOutWarps + kGmExpandWarps, kGmCopyWarp = kGmCodeWarp + 1;
 constexpr int kGmMmaWarp = kGmCopyWarp + 1;
-constexpr int kGmWarps = kGmMmaWarp + 1;
+constexpr int kGmWarps = kGmMmaWarp + 2;   // (whole groups of four)
 constexpr int kGmThreads = 32 * kGmWarps;
 constexpr int kGmOutThreads = 32 * kGmOutWarps;
 constexpr int kGmStages = 5;             // of x and of expanded weights
@@ -112,6 +112,18 @@ __device__ __forceinline__ void gm_tmem_st16(uint32_t taddr, const uint32_t *r) 
 __device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
 __device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
 
+// A group of four warps' registers per thread.  640 threads start with 96 (61440); with fp32 tensors 256 have 144 then,
+// 256 have 80 and 128 have 32 (61440), and in the end all 96 again.  The others take theirs back only after the
+// 256 have given theirs up: a CTA without work would otherwise have nothing left for warps that still wait
+// for their 144.
+template <int N>
+__device__ __forceinline__ void gm_more_registers() {
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N));
+}
+template <int N>
+__device__ __forceinline__ void gm_fewer_registers() {
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N));
+}
 // 16 columns asked for; they are there after gm_ld_wait.
 __device__ __forceinline__ void gm_ld16_start(uint32_t taddr, uint32_t (&r)[16]) {
     asm volatile(
@@ -356,6 +368,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
 
     if (warp < kGmOutWarps) {
         // =================== sums out: a lane per weight row ===================
+        if constexpr (F32) gm_more_registers<144>();
         const int quarter = warp & 3, c0 = (warp >> 2) * kCols;
         const uint32_t at_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
         uint32_t turn = 0;   // accumulators taken so far
@@ -518,8 +531,13 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             buf ^= 1;
             tell();
         }
+        if constexpr (F32) {
+            gm_fewer_registers<96>();
+            named_sync(2, kGmThreads);
+        }
     } else if (warp < kGmOutWarps + kGmExpandWarps) {
         // =================== weights: a thread per row, every other step ===================
+        if constexpr (F32) gm_fewer_registers<80>();
         const int quarter = warp & 3, half = (warp - kGmOutWarps) >> 2;
         const uint32_t to = tmem + kGmABase + ((uint32_t)(quarter * 32) << 16);
         constexpr int kBlock = 8 * GROUP / kGmStep;   // steps of eight groups, whose scales are held
@@ -639,7 +657,14 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             turn += steps;
             ring.skip(steps);
         }
-    } else if (warp == kGmCodeWarp) {
+        __syncwarp();
+        if constexpr (F32) {
+            named_sync(2, kGmThreads);
+            gm_more_registers<96>();
+        }
+    } else {
+      if constexpr (F32) gm_fewer_registers<32>();
+      if (warp == kGmCodeWarp) {
         // =================== codes: two copies of 64 rows x 128 columns a stage ===================
         GmRing<kGmCStages> code;
         int used = 0;
@@ -769,6 +794,12 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         __syncwarp();
         wait(bar.done, 0);
         tc_fence_before();
+      }
+      __syncwarp();
+      if constexpr (F32) {
+          named_sync(2, kGmThreads);
+          gm_more_registers<96>();
+      }
     }
     __syncthreads();
     tc_fence_after();
