@@ -91,7 +91,7 @@ static RowsAt rows_at(uint8_t *at, int64_t n, int64_t K, int type) {
 
 // Pairs per expert from which the experts' products run on tcgen05: below, most of its tiles would be empty
 // columns.
-constexpr int kManyPairs = 6;
+constexpr int kManyPairs = 8;
 
 struct ExpertsAt {
     size_t x, h, h_rows, part, bytes;

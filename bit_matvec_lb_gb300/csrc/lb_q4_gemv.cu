@@ -6,20 +6,25 @@
 // three bf16 parts, which together are all its 24 bits, so the products are exact.  The scale acts
 // on a group's sum in binary32: a fused multiply-add per group, row and token.
 //
-// A CTA takes 128 rows and a slice of K; up to eight CTAs along K form a cluster and add their sums
-// up through distributed shared memory in a fixed order.  One warp copies blocks of 128 rows x
-// 512 columns (32 KB) with tensor copies into a ring; they start before the previous kernel in the
-// stream has ended.  Eight warps take 16 rows each: ldmatrix hands a lane whole words of eight
+// Work: units of 128 rows (of a token piece), each split along K over a cluster of up to eight CTAs; a cluster
+// takes an equal run of units, so x is laid out once (experts: once per piece) and weights keep coming across the units' borders.
+// One warp copies blocks of 128 rows x 512 columns (32 KB, tensor copies, with their scales and zeros) into a
+// ring; the first ones start before the previous kernel in the stream has ended.  Eight warps take 16 rows
+// each (experts' up products: 8 gate and the same 8 up rows): ldmatrix hands a lane whole words of eight
 // consecutive columns of its row, which are four operand registers after a shift, a logic
 // operation that puts the codes under the exponent of 128, and a subtraction of 128 + z.  The eight
 // columns of a word enter as pairs (0, 4), (1, 5), (2, 6), (3, 7); x is laid out in shared memory in that
-// order, so a 16-byte read is the other operand of two steps.
+// order, so a 16-byte read is the other operand of two steps.  A warp sends its sums to the CTA of the
+// cluster that is to finish its rows, and that CTA adds them up, in the order of the ranks, after its next unit.
 //
 // What bounds it: HBM.  Per 512 weights a warp issues about 30 instructions, 0.6 of what the SM has at
 // the rate the weights come in.
 #include "lb_q4.cuh"
 
 #include <algorithm>
+#include <map>
+#include <mutex>
+#include <tuple>
 #include <type_traits>
 
 namespace lb {
@@ -33,13 +38,14 @@ constexpr int kMvThreads = 32 * (kMvWarps + 1);
 constexpr int kMvTokens = 8;
 constexpr int kMvMaxSplit = 8;
 constexpr int kMvMaxStages = 3;
+constexpr size_t kMvShared = 226 * 1024;         // shared memory of an SM's CTAs, static and dynamic
 
 struct MvLaunch {
     int blocks;    // blocks of K of a CTA
     int stages;
-    int tokens;    // most tokens of a CTA
-    int split;     // CTAs along K
-    int packed;    // the parts of all tokens lie in one operand's eight columns
+    int tokens;    // most tokens of a piece
+    int split;     // CTAs along K, a cluster
+    int tiles;     // of 128 rows
 };
 
 __device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
@@ -80,62 +86,37 @@ __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int by
     else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
     else asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(dst), "l"(src) : "memory");
 }
-__device__ __forceinline__ void cluster_arrive_wait() {
+// The address of this CTA's shared memory's p in another CTA of the cluster.
+__device__ __forceinline__ uint32_t address_in(const void *p, uint32_t rank) {
+    uint32_t a;
+    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
+    return a;
+}
+__device__ __forceinline__ void store_in(uint32_t a, float x, float y) {
+    asm volatile("st.shared::cluster.v2.f32 [%0], {%1, %2};" ::"r"(a), "f"(x), "f"(y) : "memory");
+}
+__device__ __forceinline__ void arrive_in(uint32_t a) {
+    asm volatile("mbarrier.arrive.release.cluster.shared::cluster.b64 _, [%0];" ::"r"(a) : "memory");
+}
+__device__ __forceinline__ bool mv_try_wait_cluster(uint64_t *bar, uint32_t parity) {
+    uint32_t ok;
+    asm volatile(
+        "{ .reg .pred p; mbarrier.try_wait.parity.acquire.cluster.shared::cta.b64 p, [%1], %2, %3; "
+        "selp.u32 %0, 1, 0, p; }"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000u)
+        : "memory");
+    return ok != 0;
+}
+__device__ __forceinline__ void mv_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
-__device__ __forceinline__ float load_cluster(const float *p, uint32_t rank) {
-    uint32_t a;
-    float v;
-    asm volatile("mapa.shared::cluster.u32 %0, %1, %2;" : "=r"(a) : "r"(smem_u32(p)), "r"(rank));
-    asm volatile("ld.shared::cluster.f32 %0, [%1];" : "=f"(v) : "r"(a) : "memory");
-    return v;
+// cp.async's of this thread so far arrive once on bar when they have landed (counted in the barrier's number).
+__device__ __forceinline__ void copies_arrive(uint64_t *bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
 }
 __device__ __forceinline__ void store_y(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_y(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
-
-// The item'th piece of at most `tokens` pairs of one expert: its expert, first pair and pairs (0: none).
-__device__ __forceinline__ void find_piece(const Q4Params &p, int item, int tokens, int *found) {
-    const int tid = threadIdx.x, lane = tid & 31;
-    __shared__ int sums[kMvThreads / 32];
-    constexpr int kEach = (LB_ROUTE_MAX_EXPERTS + kMvThreads - 1) / kMvThreads;
-    int first[kEach], count[kEach], pieces = 0;
-    if (tid == 0) found[2] = 0;
-#pragma unroll
-    for (int i = 0; i < kEach; i++) {
-        const int e = tid * kEach + i;
-        first[i] = count[i] = 0;
-        if (e < p.E) {
-            first[i] = min(max(p.start[e], 0), (int)p.T);
-            count[i] = max(min(p.start[e + 1], (int)p.T) - first[i], 0);
-        }
-        pieces += (count[i] + tokens - 1) / tokens;
-    }
-    int run = pieces;
-#pragma unroll
-    for (int o = 1; o < 32; o <<= 1) {
-        const int w = __shfl_up_sync(0xffffffffu, run, o);
-        if (lane >= o) run += w;
-    }
-    if (lane == 31) sums[tid >> 5] = run;
-    __syncthreads();
-    int before = run - pieces;
-#pragma unroll
-    for (int w = 0; w < kMvThreads / 32; w++) before += w < (tid >> 5) ? sums[w] : 0;
-    if (item >= before && item < before + pieces) {
-#pragma unroll
-        for (int i = 0; i < kEach; i++) {
-            const int n = (count[i] + tokens - 1) / tokens;
-            if (item >= before && item < before + n) {
-                const int at = (item - before) * tokens;
-                found[0] = tid * kEach + i;
-                found[1] = first[i] + at;
-                found[2] = min(tokens, count[i] - at);
-            }
-            before += n;
-        }
-    }
-    __syncthreads();
-}
 
 // T: the type of x (dense, up; h is fp32) and of a dense y; PARTS: bf16 parts of an x.
 template <Q4Use USE, typename T, int PARTS, int GROUP, bool ZEROS>
@@ -143,256 +124,424 @@ __global__ void __launch_bounds__(kMvThreads, 2)
     q4_gemv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Q4Params p,
                    const __grid_constant__ MvLaunch l) {
     using X = typename std::conditional<USE == kQ4Down, float, T>::type;
+    constexpr int kPer = kMvBlock / GROUP;                       // groups of a block
+    constexpr int kExperts = USE == kQ4Dense ? 1 : LB_ROUTE_MAX_EXPERTS;
     extern __shared__ __align__(1024) uint8_t smem[];
-    __shared__ uint64_t full[kMvMaxStages], empty[kMvMaxStages];
-    __shared__ int found[3], row_of[kMvTokens];
+    __shared__ uint64_t full[kMvMaxStages], empty[kMvMaxStages], sums_full[2];
+    __shared__ __align__(16) uint16_t ds[kMvMaxStages][kMvRows][kPer];
+    __shared__ __align__(16) uint8_t zs[ZEROS ? kMvMaxStages : 1][kMvRows][kPer];
+    __shared__ __align__(16) float sums[2][8][16][kMvTokens];    // [rank, own warp][row][column]
+    __shared__ int row_of[kMvTokens];
+    __shared__ uint16_t s_first[kExperts];                       // pieces before an expert's
+    __shared__ int s_part[kMvThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = l.blocks * kMvBlock, rank = blockIdx.x % l.split;
-    const int64_t tile = blockIdx.x / l.split;
-    const int k0 = rank * slice, columns = min(p.K - k0, slice);   // (columns <= 0: nothing to add)
-    const int blocks = max((columns + kMvBlock - 1) / kMvBlock, 0);
-    const int groups = l.blocks * (kMvBlock / GROUP);              // of the slice
+    const int k0 = rank * slice, columns = min(p.K - k0, slice);
+    const int blocks = max((columns + kMvBlock - 1) / kMvBlock, 0);   // (the last CTAs along K may have none)
     const int x_pitch = 2 * slice + 64;
-    uint8_t *ring = smem;
-    uint8_t *xs = ring + l.stages * kMvStage;
-    uint16_t *ds = reinterpret_cast<uint16_t *>(xs + (l.packed ? kMvTokens : PARTS * l.tokens) * x_pitch);
-    uint8_t *zs = reinterpret_cast<uint8_t *>(ds + kMvRows * groups);
+    uint8_t *ring = smem, *xs = smem + l.stages * kMvStage;
 
     pdl_launch_dependents();
     if (tid == 0) {
-        for (int i = 0; i < kMvMaxStages; i++) mbar_init(&full[i], 1), mbar_init(&empty[i], kMvWarps);
+        // a stage is full when the copies of codes and the 32 lanes' copies of scales have landed
+        for (int i = 0; i < kMvMaxStages; i++) mbar_init(&full[i], 33), mbar_init(&empty[i], kMvWarps);
+        // sums of 16 groups of 8 rows come to a CTA, whatever the split
+        mbar_init(&sums_full[0], 16), mbar_init(&sums_full[1], 16);
         fence_mbar_init();
     }
-    // experts: which one, and which of its pairs
-    int64_t matrix = 0;   // first row of the matrix among all rows
-    int t0, tokens;
-    if (USE == kQ4Dense) {
-        t0 = blockIdx.y * l.tokens;
-        tokens = (int)min((int64_t)l.tokens, p.T - t0);
-        __syncthreads();
+    // Pieces of at most l.tokens tokens (of one expert).
+    int pieces;
+    if constexpr (USE == kQ4Dense) {
+        pieces = (int)((p.T + l.tokens - 1) / l.tokens);
     } else {
         pdl_wait();
-        find_piece(p, blockIdx.y, l.tokens, found);
-        t0 = found[1], tokens = found[2];
-        if (!tokens) return;  // the whole cluster's
-        matrix = (int64_t)found[0] * (USE == kQ4Up ? 2 * p.N : p.N);
-    }
-    // The CTA's 128 rows: an up product's are 64 of the gate and the same 64 of the up rows.
-    const int64_t n0 = tile * (USE == kQ4Up ? kMvRows / 2 : kMvRows);
-    const int64_t upper = USE == kQ4Up ? p.N + n0 : n0 + kMvRows / 2;   // row of the CTA's row 64
-    auto issue = [&](int b) {
-        uint64_t *bar = &full[b % l.stages];
-        mbar_arrive_expect_tx(bar, kMvStage);
-        uint8_t *dst = ring + (b % l.stages) * kMvStage;
+        constexpr int kEach = (LB_ROUTE_MAX_EXPERTS + kMvThreads - 1) / kMvThreads;
+        int n[kEach], mine = 0;
 #pragma unroll
-        for (int j = 0; j < kMvBlock / 128; j++) {
-            const int at = (k0 + b * kMvBlock) / 2 + 64 * j;
-            tma_load_2d(dst + j * kMvBox, &map, at, (int)(matrix + n0), bar);
-            tma_load_2d(dst + j * kMvBox + kMvBox / 2, &map, at, (int)(matrix + upper), bar);
-        }
-    };
-    if (tid == 32 * kMvWarps)
-        for (int b = 0; b < min(l.stages, blocks); b++) issue(b);
-    // scales and zeros of the slice (they are weights too)
-    {
-        constexpr int per = kMvBlock / GROUP;      // a block's, of one row
-        const int64_t last = USE == kQ4Up ? matrix + 2 * p.N : matrix + p.N;
-        for (int i = tid; i < kMvRows * blocks; i += kMvThreads) {
-            const int r = i / blocks, b = i % blocks;
-            const int64_t row = matrix + (r < kMvRows / 2 ? n0 + r : upper + r - kMvRows / 2);
-            if (row >= last) continue;   // the products of rows behind the matrix go nowhere
-            const int64_t from = row * p.pitch + k0 / GROUP + b * per;
-            const int to = r * groups + b * per;
-            // (a row's entries reach to a multiple of eight, a block's may be four)
-            if (per == 4) copy_async(smem_u32(ds + to), p.scales + from, 8);
-            else
-                for (int j = 0; j < per; j += 8)
-                    if (k0 / GROUP + b * per + j < p.pitch)
-                        copy_async(smem_u32(ds + to + j), p.scales + from + j, 16);
-            if (ZEROS) {
-                if (per == 4) copy_async(smem_u32(zs + to), p.zeros + from, 4);
-                else
-                    for (int j = 0; j < per; j += 8)
-                        if (k0 / GROUP + b * per + j < p.pitch)
-                            copy_async(smem_u32(zs + to + j), p.zeros + from + j, 8);
+        for (int i = 0; i < kEach; i++) {
+            const int e = tid * kEach + i;
+            n[i] = 0;
+            if (e < p.E) {
+                const int first = min(max(p.start[e], 0), (int)p.T);
+                n[i] = (max(min(p.start[e + 1], (int)p.T) - first, 0) + l.tokens - 1) / l.tokens;
             }
+            mine += n[i];
         }
-    }
-    if (USE == kQ4Dense) pdl_wait();
-    if (USE != kQ4Dense) {
-        if (tid < tokens) row_of[tid] = p.order[t0 + tid];
+        int run = mine;
+#pragma unroll
+        for (int o = 1; o < 32; o <<= 1) {
+            const int w = __shfl_up_sync(0xffffffffu, run, o);
+            if (lane >= o) run += w;
+        }
+        if (lane == 31) s_part[warp] = run;
         __syncthreads();
-    }
-    // x of the slice: operand row (packed ? token * PARTS + part : part * tokens + token), columns in
-    // the order of the codes' pairs, zeros behind K
-    const int units = blocks * (kMvBlock / 8);
-    for (int i = tid; i < tokens * units; i += kMvThreads) {
-        const int t = i / units, u = i % units;
-        float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-        int64_t from = t0 + t;
-        bool in = 8 * u < columns;
-        if (USE != kQ4Dense) {
-            const int pair = row_of[t];
-            in = in && pair >= 0 && pair < p.T;
-            if (USE == kQ4Up) from = pair / p.k;
+        int before = run - mine;
+        pieces = 0;
+#pragma unroll
+        for (int w = 0; w < kMvThreads / 32; w++) {
+            before += w < warp ? s_part[w] : 0;
+            pieces += s_part[w];
         }
-        if (in) load8(static_cast<const X *>(p.x) + from * p.x_stride + k0 + 8 * u, v);
+        pieces = min(pieces, 65535);
 #pragma unroll
-        for (int part = 0; part < PARTS; part++) {
-            const int row = l.packed ? t * PARTS + part : part * tokens + t;
-            *reinterpret_cast<uint4 *>(xs + row * x_pitch + 16 * u) =
-                make_uint4(high_halves(v[0], v[4]), high_halves(v[1], v[5]), high_halves(v[2], v[6]),
-                           high_halves(v[3], v[7]));
-#pragma unroll
-            for (int j = 0; j < 8; j++) v[j] = rest_of(v[j]);
+        for (int i = 0; i < kEach; i++) {
+            if (tid * kEach + i < p.E) s_first[tid * kEach + i] = (uint16_t)min(before, 65535);
+            before += n[i];
         }
     }
-    asm volatile("cp.async.wait_all;" ::: "memory");
-    __syncthreads();
+    if (l.split > 1) mv_cluster_sync();   // (everybody's barriers are there)
+    else __syncthreads();
+    struct Piece {
+        int expert, t0, tokens;
+    };
+    auto piece_of = [&](int i) {
+        Piece q;
+        if constexpr (USE == kQ4Dense) {
+            q.expert = 0, q.t0 = i * l.tokens;
+            q.tokens = (int)min((int64_t)l.tokens, p.T - q.t0);
+        } else {
+            int lo = 0, hi = p.E;   // the last expert whose pieces begin at or before this one
+            while (hi - lo > 1) {
+                const int m = (lo + hi) / 2;
+                if (s_first[m] <= i) lo = m;
+                else hi = m;
+            }
+            const int first = min(max(p.start[lo], 0), (int)p.T), end = min(p.start[lo + 1], (int)p.T);
+            q.expert = lo, q.t0 = first + (i - s_first[lo]) * l.tokens;
+            q.tokens = min(l.tokens, end - q.t0);
+        }
+        return q;
+    };
+    // This cluster's units.
+    const int64_t units = (int64_t)pieces * l.tiles, clusters = gridDim.x / l.split, c = blockIdx.x / l.split;
+    const int64_t u_begin = units * c / clusters, u_end = units * (c + 1) / clusters;
+    constexpr int kTileRows = USE == kQ4Up ? kMvRows / 2 : kMvRows;
 
-    float total[4] = {0.f, 0.f, 0.f, 0.f};
-    const int cols = l.packed ? tokens * PARTS : tokens;
     if (warp == kMvWarps) {
-        if (lane == 0) {
-            int b = min(l.stages, blocks);
-            for (; b < blocks; b++) {
-                if (!mbar_wait(&empty[b % l.stages], (uint32_t)(b / l.stages - 1) & 1u)) {
-                    atomicOr(p.error, 1);
+        // =================== copies ===================
+        int stage = 0, used = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        int at_piece = -1;
+        Piece q{0, 0, 0};
+        for (int64_t u = u_begin; u < u_end && ok; u++) {
+            const int piece = (int)(u / l.tiles);
+            const int64_t n0 = (u - (int64_t)piece * l.tiles) * kTileRows;
+            if (piece != at_piece) q = piece_of(piece), at_piece = piece;
+            const int64_t matrix = (int64_t)q.expert * (USE == kQ4Up ? 2 * p.N : p.N);
+            const int64_t last = matrix + (USE == kQ4Up ? 2 * p.N : p.N);
+            const int64_t upper = matrix + (USE == kQ4Up ? p.N + n0 : n0 + kMvRows / 2);   // the tile's row 64
+            for (int b = 0; b < blocks; b++) {
+                ok = __all_sync(0xffffffffu, mbar_wait(&empty[stage], phase ^ 1));
+                if (!ok) {
+                    if (lane == 0) atomicOr(p.error, 1);
                     break;
                 }
-                issue(b);
-            }
-            // no copy may still be landing when the ring is written to or the CTA exits
-            for (int i = max(0, b - l.stages); i < b; i++)
-                mbar_wait(&full[i % l.stages], (uint32_t)(i / l.stages) & 1u);
-        }
-    } else {
-        const int g = lane >> 2, t = lane & 3;
-        const int row = warp * 16 + (lane & 15);      // the row this lane points ldmatrix at
-        const uint32_t at_row = smem_u32(ring) + row * 64, turn = (row >> 1) & 3;
-        const int scale_row = (warp * 16 + g) * groups;
-        const int planes = l.packed ? 1 : PARTS;
-        const uint8_t *xrow = xs + g * x_pitch + 16 * t;
-        const int plane = tokens * x_pitch;
-        const bool have = g < cols;
-        float sum[4] = {0.f, 0.f, 0.f, 0.f};
-        for (int b = 0; b < blocks; b++) {
-            const int s = b % l.stages;
-            if (!__all_sync(0xffffffffu, mbar_wait(&full[s], (uint32_t)(b / l.stages) & 1u))) {
-                if (lane == 0) atomicOr(p.error, 1);
-                break;
-            }
-            const int chunks = min(kMvBlock, columns - b * kMvBlock) / 32;   // of 32 columns
+                uint64_t *bar = &full[stage];
+                if (lane == 0) {
+                    mbar_arrive_expect_tx(bar, kMvStage);
+                    uint8_t *dst = ring + stage * kMvStage;
 #pragma unroll
-            for (int j = 0; j < kMvBlock / 128; j++) {
-                if (4 * j >= chunks) break;
+                    for (int j = 0; j < kMvBlock / 128; j++) {
+                        const int at = (k0 + b * kMvBlock) / 2 + 64 * j;
+                        tma_load_2d(dst + j * kMvBox, &map, at, (int)(matrix + n0), bar);
+                        tma_load_2d(dst + j * kMvBox + kMvBox / 2, &map, at, (int)upper, bar);
+                    }
+                }
+                __syncwarp();
+                // (a row's entries reach to a multiple of eight, a block's may be four)
+                const int first = k0 / GROUP + b * kPer;
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    if (4 * j + 2 * h >= chunks) break;
-                    uint32_t w[4];   // rows g and g + 8 of chunk 2h, then of chunk 2h + 1
-                    ldmatrix4(w, at_row + s * kMvStage + j * kMvBox +
-                                     (((uint32_t)(2 * h) + (lane >> 4)) ^ turn) * 16);
+                for (int j = 0; j < kMvRows / 32; j++) {
+                    const int r = j * 32 + lane;
+                    const int64_t row = r < kMvRows / 2 ? matrix + n0 + r : upper + r - kMvRows / 2;
+                    if (row >= last) continue;   // the products of rows behind the matrix go nowhere
+                    const int64_t from = row * p.pitch + first;
+                    if constexpr (kPer == 4) {
+                        copy_async(smem_u32(&ds[stage][r][0]), p.scales + from, 8);
+                        if (ZEROS) copy_async(smem_u32(&zs[ZEROS ? stage : 0][r][0]), p.zeros + from, 4);
+                    } else {
 #pragma unroll
-                    for (int c = 0; c < 2; c++) {
-                        const int chunk = 4 * j + 2 * h + c;
-                        if (chunk >= chunks) break;   // (K is a multiple of 32)
-                        const int gi = b * (kMvBlock / GROUP) + chunk / (GROUP / 32);
-                        uint32_t bias[2] = {0x43084308u, 0x43084308u};
-                        if (ZEROS) {
-                            bias[0] = 0x43004300u | zs[scale_row + gi] * 0x10001u;
-                            bias[1] = 0x43004300u | zs[scale_row + 8 * groups + gi] * 0x10001u;
-                        }
-                        uint32_t a[2][4];
-                        expand_bf16(w[2 * c], bias[0], a[0]);
-                        expand_bf16(w[2 * c + 1], bias[1], a[1]);
-                        const uint8_t *xc = xrow + (b * (kMvBlock / 32) + chunk) * 64;
-#pragma unroll
-                        for (int q = 0; q < PARTS; q++) {
-                            if (q >= planes) break;
-                            uint4 x = make_uint4(0, 0, 0, 0);
-                            if (have) x = *reinterpret_cast<const uint4 *>(xc + q * plane);
-                            mma_bf16(sum, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                            mma_bf16(sum, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
-                        }
-                        if ((chunk + 1) % (GROUP / 32) == 0) {
-                            const float d0 = f16_bits_to_float(ds[scale_row + gi]);
-                            const float d1 = f16_bits_to_float(ds[scale_row + 8 * groups + gi]);
-                            total[0] = fmaf(d0, sum[0], total[0]);
-                            total[1] = fmaf(d0, sum[1], total[1]);
-                            total[2] = fmaf(d1, sum[2], total[2]);
-                            total[3] = fmaf(d1, sum[3], total[3]);
-                            sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+                        for (int e = 0; e < kPer; e += 8) {
+                            if (first + e >= p.pitch) break;
+                            copy_async(smem_u32(&ds[stage][r][e]), p.scales + from + e, 16);
+                            if (ZEROS) copy_async(smem_u32(&zs[ZEROS ? stage : 0][r][e]), p.zeros + from + e, 8);
                         }
                     }
                 }
-            }
-            if (b + l.stages < blocks) {
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&empty[s]);
+                copies_arrive(bar);
+                if (++stage == l.stages) stage = 0, phase ^= 1;
+                used = min(used + 1, l.stages);
             }
         }
-    }
-    // The sums, [operand column][row], where the weights were.
-    __syncthreads();
-    float *out = reinterpret_cast<float *>(ring);
-    constexpr int out_pitch = kMvRows + 4;
-    if (warp < kMvWarps) {
-        const int r = warp * 16 + (lane >> 2), c = 2 * (lane & 3);
+        // no copy may still be landing when the CTA exits
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        for (int i = 0; i < used; i++) {
+            if (stage == 0) stage = l.stages, phase ^= 1;
+            stage--;
+            mbar_wait(&full[stage], phase);
+        }
+        if (USE == kQ4Dense) pdl_wait();
+    } else {
+        // =================== products ===================
+        if (USE == kQ4Dense) pdl_wait();
+        const int g = lane >> 2, t = lane & 3;
+        // the row this lane points ldmatrix at, and the two rows of its sums, in the tile
+        const int row = USE == kQ4Up ? warp * 8 + (lane & 7) + (lane & 8) * 8 : warp * 16 + (lane & 15);
+        const int row0 = USE == kQ4Up ? warp * 8 + g : warp * 16 + g, row1 = USE == kQ4Up ? row0 + 64 : row0 + 8;
+        const uint32_t at_row = smem_u32(ring) + row * 64, turn = (row >> 1) & 3;
+        const int own = kMvWarps / l.split;              // warps whose rows a CTA finishes
+        const uint32_t owner = warp / own;
+        const uint32_t send_to = address_in(&sums[0][rank * own + warp % own][g][2 * t], owner);
+        const uint32_t tell[2] = {address_in(&sums_full[0], owner), address_in(&sums_full[1], owner)};
+        int stage = 0;
+        uint32_t phase = 0;
+        bool ok = true;
+        int at_piece = -1, cols = 0, planes = 1;
+        Piece q{0, 0, 0};
+        // The parts of few tokens lie in one operand's eight columns, of more in an operand each.
+        auto packed = [](const Piece &a) { return a.tokens * PARTS <= kMvTokens; };
+        // What a finished unit leaves to be done after the next one's products.
+        Piece q_done{0, 0, 0};
+        int64_t n_done = 0;
+        // the sums of unit number n (of this cluster's), added up over the ranks and stored
+        auto finish = [&](int n) {
+            if (ok) {
+                const uint64_t t_0 = global_ns();
+                bool there = mv_try_wait_cluster(&sums_full[n & 1], (uint32_t)(n >> 1) & 1u);
+                for (uint32_t i = 1; !there; i++) {
+                    there = mv_try_wait_cluster(&sums_full[n & 1], (uint32_t)(n >> 1) & 1u);
+                    if ((i & 15u) == 0 && global_ns() - t_0 > 2000000000ull) break;
+                }
+                if (!__all_sync(0xffffffffu, there)) {
+                    if (lane == 0) atomicOr(p.error, 1);
+                    ok = false;
+                }
+            }
+            const int parts = packed(q_done) ? PARTS : 1;
+            const int per_warp = USE == kQ4Up ? 8 : 16, rows = own * per_warp;
+            for (int i = tid; i < rows * q_done.tokens; i += 32 * kMvWarps) {
+                const int tk = i / rows, r = i % rows, w = r / per_warp, rr = r % per_warp;
+                const int64_t row_n = n_done + (rank * own + w) * per_warp + rr;
+                float v[2] = {0.f, 0.f};
 #pragma unroll
-        for (int i = 0; i < 4; i++) {
-            const int col = c + (i & 1);
-            if (col < cols) out[col * out_pitch + r + 8 * (i >> 1)] = total[i];
+                for (int h = 0; h < (USE == kQ4Up ? 2 : 1); h++)
+                    for (int k = 0; k < parts; k++)
+                        for (int s = 0; s < l.split; s++)
+                            v[h] += sums[n & 1][s * own + w][rr + 8 * h][tk * parts + k];
+                if (row_n >= p.N) continue;
+                if (USE == kQ4Dense) {
+                    store_y(static_cast<T *>(p.y) + (q_done.t0 + tk) * p.y_stride + row_n, v[0]);
+                } else if (USE == kQ4Up) {
+                    static_cast<float *>(p.y)[(int64_t)(q_done.t0 + tk) * p.y_stride + row_n] =
+                        v[0] / (1.f + expf(-v[0])) * v[1];
+                } else {
+                    const int pair = p.order[q_done.t0 + tk];
+                    if (pair >= 0 && pair < p.T)
+                        static_cast<float *>(p.y)[(int64_t)pair * p.y_stride + row_n] = v[0];
+                }
+            }
+        };
+        int n = 0;
+        for (int64_t u = u_begin; u < u_end; u++, n++) {
+            const int piece = (int)(u / l.tiles);
+            if (piece != at_piece) {
+                // x of the slice: operand row (packed: token * PARTS + part, else part * tokens + token), columns in
+                // the order of the codes' pairs, zeros behind K
+                q = piece_of(piece), at_piece = piece;
+                named_sync(1, 32 * kMvWarps);   // the last piece's x is done with
+                if (USE != kQ4Dense) {
+                    if (tid < q.tokens) row_of[tid] = p.order[q.t0 + tid];
+                    named_sync(1, 32 * kMvWarps);
+                }
+                const bool pack = packed(q);
+                cols = pack ? q.tokens * PARTS : q.tokens, planes = pack ? 1 : PARTS;
+                const int each = blocks * (kMvBlock / 8);
+                for (int i = tid; i < q.tokens * each; i += 32 * kMvWarps) {
+                    const int tk = i / each, at = i % each;
+                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
+                    int64_t from = q.t0 + tk;
+                    bool in = 8 * at < columns;
+                    if (USE != kQ4Dense) {
+                        const int pair = row_of[tk];
+                        in = in && pair >= 0 && pair < p.T;
+                        if (USE == kQ4Up) from = pair / p.k;
+                    }
+                    if (in) load8(static_cast<const X *>(p.x) + from * p.x_stride + k0 + 8 * at, v);
+#pragma unroll
+                    for (int part = 0; part < PARTS; part++) {
+                        const int to = pack ? tk * PARTS + part : part * q.tokens + tk;
+                        *reinterpret_cast<uint4 *>(xs + to * x_pitch + 16 * at) =
+                            make_uint4(high_halves(v[0], v[4]), high_halves(v[1], v[5]), high_halves(v[2], v[6]),
+                                       high_halves(v[3], v[7]));
+#pragma unroll
+                        for (int j = 0; j < 8; j++) v[j] = rest_of(v[j]);
+                    }
+                }
+                named_sync(1, 32 * kMvWarps);
+            }
+            const uint8_t *xrow = xs + g * x_pitch + 16 * t;
+            const int plane = q.tokens * x_pitch;
+            const bool have = g < cols;
+            float total[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+            for (int b = 0; b < blocks && ok; b++) {
+                if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
+                    if (lane == 0) atomicOr(p.error, 1);
+                    ok = false;
+                    break;
+                }
+                const int chunks = min(kMvBlock, columns - b * kMvBlock) / 32;   // of 32 columns
+#pragma unroll
+                for (int j = 0; j < kMvBlock / 128; j++) {
+                    if (4 * j >= chunks) break;
+#pragma unroll
+                    for (int h = 0; h < 2; h++) {
+                        if (4 * j + 2 * h >= chunks) break;
+                        uint32_t w[4];   // the lane's two rows of chunk 2h, then of chunk 2h + 1
+                        ldmatrix4(w, at_row + stage * kMvStage + j * kMvBox +
+                                         (((uint32_t)(2 * h) + (lane >> 4)) ^ turn) * 16);
+#pragma unroll
+                        for (int e = 0; e < 2; e++) {
+                            const int chunk = 4 * j + 2 * h + e;
+                            if (chunk >= chunks) break;   // (K is a multiple of 32)
+                            constexpr int kEach = GROUP / 32;
+                            uint32_t bias[2] = {0x43084308u, 0x43084308u};
+                            if (ZEROS) {
+                                bias[0] = 0x43004300u | zs[ZEROS ? stage : 0][row0][chunk / kEach] * 0x10001u;
+                                bias[1] = 0x43004300u | zs[ZEROS ? stage : 0][row1][chunk / kEach] * 0x10001u;
+                            }
+                            uint32_t a[2][4];
+                            expand_bf16(w[2 * e], bias[0], a[0]);
+                            expand_bf16(w[2 * e + 1], bias[1], a[1]);
+                            const uint8_t *xc = xrow + (b * (kMvBlock / 32) + chunk) * 64;
+#pragma unroll
+                            for (int k = 0; k < PARTS; k++) {
+                                if (k >= planes) break;
+                                uint4 x = make_uint4(0, 0, 0, 0);
+                                if (have) x = *reinterpret_cast<const uint4 *>(xc + k * plane);
+                                mma_bf16(sum, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                                mma_bf16(sum, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                            }
+                            if ((chunk + 1) % kEach == 0) {
+                                const float d0 = f16_bits_to_float(ds[stage][row0][chunk / kEach]);
+                                const float d1 = f16_bits_to_float(ds[stage][row1][chunk / kEach]);
+                                total[0] = fmaf(d0, sum[0], total[0]);
+                                total[1] = fmaf(d0, sum[1], total[1]);
+                                total[2] = fmaf(d1, sum[2], total[2]);
+                                total[3] = fmaf(d1, sum[3], total[3]);
+                                sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
+                            }
+                        }
+                    }
+                }
+                __syncwarp();
+                if (lane == 0) mbar_arrive(&empty[stage]);
+                if (++stage == l.stages) stage = 0, phase ^= 1;
+            }
+            if (n > 0) finish(n - 1);
+            // (a CTA that has sent has done with the unit before the last one: its sums' place may be written to)
+            named_sync(1, 32 * kMvWarps);
+            // rows g and g + 8, columns 2t and 2t + 1, to the CTA that finishes them
+            const uint32_t to = send_to + (n & 1) * (uint32_t)(sizeof(sums) / 2);
+            store_in(to, total[0], total[1]);
+            store_in(to + 8 * kMvTokens * 4, total[2], total[3]);
+            __syncwarp();
+            if (lane < 2) arrive_in(tell[n & 1]);
+            q_done = q;
+            n_done = (u - (int64_t)piece * l.tiles) * kTileRows;
         }
+        if (n > 0) finish(n - 1);
     }
-    if (l.split > 1) cluster_arrive_wait();
-    else __syncthreads();
-    auto sum_of = [&](int t, int r) {
-        const int parts = l.packed ? PARTS : 1;
-        float v = 0.f;
-        for (int q = 0; q < parts; q++) {
-            const float *at = out + (t * parts + q) * out_pitch + r;
-            if (l.split > 1)
-                for (int c = 0; c < l.split; c++) v += load_cluster(at, c);
-            else
-                v += *at;
+    __syncwarp();
+    if (l.split > 1) mv_cluster_sync();   // nobody's sums come after a CTA has gone
+}
+
+// How a call of given sizes is cut up.
+struct MvPlan {
+    MvLaunch l;
+    int64_t clusters = 0;
+    size_t smem = 0;
+};
+
+// The split whose longest run of blocks is the shortest; of equal ones the smallest.  `fixed`: static shared memory.
+static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces, int K, int parts, size_t fixed, int sms) {
+    const int blocks = (K + kMvBlock - 1) / kMvBlock;
+    MvPlan best;
+    int64_t best_time = 0;
+    for (int split = 1; split <= kMvMaxSplit; split *= 2) {
+        MvLaunch l{};
+        l.blocks = (blocks + split - 1) / split;
+        l.split = split, l.tiles = tiles;
+        // Tokens: eight, or as many as their parts' slices fit beside two stages.
+        const size_t pitch = 2 * (size_t)l.blocks * kMvBlock + 64;
+        l.tokens = (int)std::min<int64_t>(T, kMvTokens);
+        const size_t most = kMvShared - fixed - 2 * kMvStage;
+        if (parts * l.tokens * pitch > most && split < kMvMaxSplit) continue;
+        while (parts * l.tokens * pitch > most && l.tokens > 1) l.tokens--;
+        // Three stages, or two where two CTAs fit an SM then (or three do not fit at all).
+        l.stages = 3;
+        size_t smem = l.stages * kMvStage + parts * l.tokens * pitch;
+        if (smem + fixed > kMvShared || (smem + fixed > kMvShared / 2 && smem + fixed - kMvStage <= kMvShared / 2))
+            l.stages = 2, smem -= kMvStage;
+        int per_sm;
+        if (prepare_kernel(kernel, kMvThreads, smem, &per_sm)) continue;
+        int held = sms * per_sm;
+        if (split > 1) {
+            cudaLaunchConfig_t cfg = {};
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = (unsigned)split, attr[0].val.clusterDim.y = attr[0].val.clusterDim.z = 1;
+            cfg.gridDim = dim3((unsigned)split), cfg.blockDim = dim3(kMvThreads), cfg.dynamicSmemBytes = smem;
+            cfg.attrs = attr, cfg.numAttrs = 1;
+            if (cudaOccupancyMaxActiveClusters(&held, kernel, &cfg) != cudaSuccess) {
+                cudaGetLastError();
+                continue;
+            }
         }
-        return v;
-    };
-    const int rows = USE == kQ4Up ? kMvRows / 2 : kMvRows;
-    const int share = (rows + l.split - 1) / l.split;
-    for (int i = tid; i < tokens * share; i += kMvThreads) {
-        const int t = i / share, r = rank * share + i % share;
-        if (r >= rows || n0 + r >= p.N) continue;
-        if (USE == kQ4Dense) {
-            store_y(static_cast<T *>(p.y) + (t0 + t) * p.y_stride + n0 + r, sum_of(t, r));
-        } else if (USE == kQ4Up) {
-            const float gate = sum_of(t, r), up = sum_of(t, r + kMvRows / 2);
-            static_cast<float *>(p.y)[(int64_t)(t0 + t) * p.y_stride + n0 + r] =
-                gate / (1.f + expf(-gate)) * up;
-        } else {
-            const int pair = row_of[t];
-            if (pair >= 0 && pair < p.T)
-                static_cast<float *>(p.y)[(int64_t)pair * p.y_stride + n0 + r] = sum_of(t, r);
-        }
+        if (held < 1) continue;
+        const int64_t units = (pieces ? pieces : (T + l.tokens - 1) / l.tokens) * tiles;
+        const int64_t clusters = std::min<int64_t>(units, held);
+        const int64_t time = (units + clusters - 1) / clusters * l.blocks;
+        if (!best.clusters || time < best_time) best.l = l, best.clusters = clusters, best.smem = smem, best_time = time;
     }
-    if (l.split > 1) cluster_arrive_wait();   // nobody's sums go before all have read them
+    return best;
 }
 
 template <Q4Use USE, typename T, int PARTS, int GROUP>
-static int launch_gemv(const Q4Params &p, const CUtensorMap &map, const MvLaunch &l, dim3 grid, size_t smem,
-                       cudaStream_t st) {
+static int launch_gemv(const Q4Params &p, const CUtensorMap &map, int64_t pieces, int sms, cudaStream_t st) {
     auto kernel = p.zeros ? q4_gemv_kernel<USE, T, PARTS, GROUP, true> : q4_gemv_kernel<USE, T, PARTS, GROUP, false>;
-    int per_sm;
-    if (int e = prepare_kernel((const void *)kernel, kMvThreads, smem, &per_sm)) return e;
+    // (asking the driver for each split takes longer than the launch: remembered by sizes)
+    static std::mutex mutex;
+    static std::map<std::tuple<int, bool, int64_t, int64_t, int64_t, int>, MvPlan> known;
+    int dev = 0;
+    cudaGetDevice(&dev);
+    MvPlan plan;
+    {
+        std::lock_guard<std::mutex> lock(mutex);
+        MvPlan &at = known[std::make_tuple(dev, p.zeros != nullptr, p.T, pieces, p.N, p.K)];
+        if (!at.clusters) {
+            constexpr int kTileRows = USE == kQ4Up ? kMvRows / 2 : kMvRows;
+            cudaFuncAttributes fa{};
+            const cudaError_t e = cudaFuncGetAttributes(&fa, (const void *)kernel);
+            if (e != cudaSuccess) {
+                record_cuda_error(e);
+                return LB_ERR_LAUNCH;
+            }
+            at = plan_gemv((const void *)kernel, p.T, (int)((p.N + kTileRows - 1) / kTileRows), pieces, p.K, PARTS,
+                           fa.sharedSizeBytes + 1024, sms);
+        }
+        plan = at;
+    }
+    if (!plan.clusters) return LB_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
-    cfg.gridDim = grid, cfg.blockDim = dim3(kMvThreads), cfg.dynamicSmemBytes = smem, cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)l.split, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr, cfg.numAttrs = l.split > 1 ? 2 : 1;
-    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, map, p, l);
+    attr[1].val.clusterDim.x = (unsigned)plan.l.split, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.gridDim = dim3((unsigned)(plan.clusters * plan.l.split)), cfg.blockDim = dim3(kMvThreads);
+    cfg.dynamicSmemBytes = plan.smem, cfg.stream = st, cfg.attrs = attr, cfg.numAttrs = plan.l.split > 1 ? 2 : 1;
+    const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, map, p, plan.l);
     if (e == cudaSuccess) return LB_OK;
     record_cuda_error(e);
     return LB_ERR_LAUNCH;
@@ -400,37 +549,14 @@ static int launch_gemv(const Q4Params &p, const CUtensorMap &map, const MvLaunch
 
 template <Q4Use USE, typename T, int PARTS>
 static int dispatch_gemv(const Q4Params &p, const uint8_t *codes, int64_t rows, int sms, cudaStream_t st) {
-    const int64_t tiles = (p.N + (USE == kQ4Up ? kMvRows / 2 : kMvRows) - 1) / (USE == kQ4Up ? kMvRows / 2 : kMvRows);
-    const int blocks = (p.K + kMvBlock - 1) / kMvBlock;
-    MvLaunch l;
-    // Slices of K: one block each where that gives at most eight.
-    l.blocks = (blocks + kMvMaxSplit - 1) / kMvMaxSplit;
-    l.split = (blocks + l.blocks - 1) / l.blocks;
-    l.stages = std::min(l.blocks, kMvMaxStages);
-    // Tokens: eight, or as many as their parts' slices fit beside the rest.
-    const size_t pitch = 2 * (size_t)l.blocks * kMvBlock + 64;
-    const size_t fixed = (size_t)l.stages * kMvStage +
-                         (size_t)kMvRows * l.blocks * (kMvBlock / p.group) * (p.zeros ? 3 : 2);
-    constexpr size_t kMost = 220 * 1024;
-    const int64_t most = USE == kQ4Dense ? p.T : kMvTokens;
-    l.tokens = (int)std::min(most, (int64_t)kMvTokens);
-    l.packed = l.tokens * PARTS <= kMvTokens;
-    while (!l.packed && fixed + (size_t)PARTS * l.tokens * pitch > kMost) {
-        l.tokens--;
-        l.packed = l.tokens * PARTS <= kMvTokens;
-    }
-    const size_t smem = fixed + (size_t)(l.packed ? kMvTokens : PARTS * l.tokens) * pitch;
-    const int64_t items = USE == kQ4Dense ? (p.T + l.tokens - 1) / l.tokens
-                                          : std::min(p.T, std::min((int64_t)p.E, p.T) + p.T / l.tokens);
     CUtensorMap map;
     if (int e = encode_rows_map(&map, codes, (uint64_t)p.K / 2, (uint64_t)rows, 64, kMvRows / 2, 64)) return e;
-    // (grid y holds 65535 pieces at most)
-    if (items > 65535 || tiles * l.split > 0x7fffffff) return LB_ERR_SHAPE;
-    const dim3 grid((unsigned)(tiles * l.split), (unsigned)items);
+    // (experts: as many pieces as experts, if there are that many pairs)
+    const int64_t pieces = USE == kQ4Dense ? 0 : std::min<int64_t>(p.T, p.E);
     switch (p.group) {
-        case 32: return launch_gemv<USE, T, PARTS, 32>(p, map, l, grid, smem, st);
-        case 64: return launch_gemv<USE, T, PARTS, 64>(p, map, l, grid, smem, st);
-        default: return launch_gemv<USE, T, PARTS, 128>(p, map, l, grid, smem, st);
+        case 32: return launch_gemv<USE, T, PARTS, 32>(p, map, pieces, sms, st);
+        case 64: return launch_gemv<USE, T, PARTS, 64>(p, map, pieces, sms, st);
+        default: return launch_gemv<USE, T, PARTS, 128>(p, map, pieces, sms, st);
     }
 }
 
