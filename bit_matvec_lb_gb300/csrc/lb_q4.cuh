@@ -27,6 +27,33 @@ inline int q4_pitch(int64_t K, int group) { return (int)((K / group + 7) / 8 * 8
 inline bool q4_group_ok(int group) { return group == 32 || group == 64 || group == 128; }
 inline bool q4_type_ok(int type) { return type == LB_OUT_F32 || type == LB_OUT_BF16; }
 
+__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
+__device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
+
+// Eight codes of a word less the zero, times the scale: pairs (0, 4), (1, 5), (2, 6), (3, 7) of fp16.  The codes
+// go under the exponent of 1024, at the last place or (times 16) four above it.
+// low: 1024 + z twice, high: -(64 + z) twice.
+template <bool SCALED>
+__device__ __forceinline__ void expand_f16(uint32_t w, __half2 low, __half2 high, __half2 d, uint32_t *r) {
+    const __half2 sixteenth = half2_of(0x2C002C00u);
+    const uint32_t s = w >> 8;
+    uint32_t v[4];
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(v[0]) : "r"(w));
+    asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(v[1]) : "r"(w));
+    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(v[2]) : "r"(s));
+    asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(v[3]) : "r"(s));
+#pragma unroll
+    for (int i = 0; i < 4; i++) {
+        __half2 h = i & 1 ? __hfma2(half2_of(v[i]), sixteenth, high) : __hsub2(half2_of(v[i]), low);
+        if (SCALED) h = __hmul2(h, d);
+        r[i] = bits_of(h);
+    }
+}
+
+// Exponent field of the power of two that takes a number m >= 0 (its bits) to [2^14, 2^15), kept to powers whose
+// inverse (254 less the field) is normal too.
+__device__ __forceinline__ uint32_t q4_power(uint32_t m) { return (uint32_t)min(max(268 - (int)(m >> 23), 1), 253); }
+
 // One to eight tokens (or an expert's tokens, eight at a time), on mma.sync: lb_q4_gemv.cu.
 // codes: all matrices' rows, `rows` of them.
 int q4_gemv(const Q4Params &p, Q4Use use, int type, const uint8_t *codes, int64_t rows, int sms,

@@ -109,9 +109,6 @@ __device__ __forceinline__ void gm_tmem_st16(uint32_t taddr, const uint32_t *r) 
         "r"(r[8]), "r"(r[9]), "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
-__device__ __forceinline__ uint32_t bits_of(__half2 h) { return *reinterpret_cast<const uint32_t *>(&h); }
-__device__ __forceinline__ __half2 half2_of(uint32_t v) { return *reinterpret_cast<const __half2 *>(&v); }
-
 // A group of four warps' registers per thread.  640 threads start with 96 (61440); with fp32 tensors 256 have 144 then,
 // 256 have 80 and 128 have 32 (61440), and in the end all 96 again.  The others take theirs back only after the
 // 256 have given theirs up: a CTA without work would otherwise have nothing left for warps that still wait
@@ -141,26 +138,6 @@ __device__ __forceinline__ void gm_ld_wait(uint32_t (&r)[16]) {
                    "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15])
                  :
                  : "memory");
-}
-
-// Eight codes of a word less the zero, times the scale: pairs (0, 4), (1, 5), (2, 6), (3, 7) of fp16.  The codes
-// go under the exponent of 1024, at the last place or (times 16) four above it.
-// low: 1024 + z twice, high: -(64 + z) twice.
-template <bool SCALED>
-__device__ __forceinline__ void expand_f16(uint32_t w, __half2 low, __half2 high, __half2 d, uint32_t *r) {
-    const __half2 sixteenth = half2_of(0x2C002C00u);
-    const uint32_t s = w >> 8;
-    uint32_t v[4];
-    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(v[0]) : "r"(w));
-    asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(v[1]) : "r"(w));
-    asm("lop3.b32 %0, %1, 0x000F000F, 0x64006400, 0xEA;" : "=r"(v[2]) : "r"(s));
-    asm("lop3.b32 %0, %1, 0x00F000F0, 0x64006400, 0xEA;" : "=r"(v[3]) : "r"(s));
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        __half2 h = i & 1 ? __hfma2(half2_of(v[i]), sixteenth, high) : __hsub2(half2_of(v[i]), low);
-        if (SCALED) h = __hmul2(h, d);
-        r[i] = bits_of(h);
-    }
 }
 
 __device__ __forceinline__ void gm_store(float *p, float v) { *p = v; }
@@ -884,10 +861,9 @@ __global__ void __launch_bounds__(kRowThreads)
     if ((tid & 31) == 0) most[tid >> 5] = m;
     __syncthreads();
     m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
-    // 2^(14 - e) for m in [2^e, 2^(e + 1)), kept to powers whose inverse is normal too
-    const int e = min(max(268 - (int)(__float_as_uint(m) >> 23), 1), 253);
-    const float up = __uint_as_float((uint32_t)e << 23);
-    if (tid == 0) row_scale[row] = __uint_as_float((uint32_t)(254 - e) << 23);
+    const uint32_t e = q4_power(__float_as_uint(m));
+    const float up = __uint_as_float(e << 23);
+    if (tid == 0) row_scale[row] = __uint_as_float((254 - e) << 23);
     auto put = [&](int u, const float (&v)[8]) {
         uint32_t hi[4], lo[4];
 #pragma unroll

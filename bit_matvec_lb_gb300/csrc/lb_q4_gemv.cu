@@ -1,9 +1,9 @@
 // lb_q4_gemv.cu -- products of 4-bit weights with group scales for a few tokens.
 //
 // Mathematics.  y[t][n] = sum over groups g of d[n][g] * sum_{k in g} (c[n][k] - z[n][g]) x[t][k].  The
-// inner sums run on mma.sync m16n8k16 (bf16 operands, binary32 sums): 16 weight rows times 8 tokens.
-// c - z is a whole number of at most eight bits, exact in bf16; a bf16 x is its own operand, an fp32 x is cut into
-// three bf16 parts, which together are all its 24 bits, so the products are exact.  The scale acts
+// inner sums run on mma.sync m16n8k16 (fp16 operands, binary32 sums): 16 weight rows times 8 tokens.
+// c - z is a whole number, exact in fp16; a token's slice of x is scaled by a power of two into fp16's range, where a
+// bf16 x has all its bits and an fp32 one takes two parts (22 bits).  The scale d acts
 // on a group's sum in binary32: a fused multiply-add per group, row and token.
 //
 // Work: units of 128 rows (of a token piece), each split along K over a cluster of up to eight CTAs; a cluster
@@ -11,14 +11,15 @@
 // One warp copies blocks of 128 rows x 512 columns (32 KB, tensor copies, with their scales and zeros) into a
 // ring; the first ones start before the previous kernel in the stream has ended.  Eight warps take 16 rows
 // each (experts' up products: 8 gate and the same 8 up rows): ldmatrix hands a lane whole words of eight
-// consecutive columns of its row, which are four operand registers after a shift, a logic
-// operation that puts the codes under the exponent of 128, and a subtraction of 128 + z.  The eight
+// consecutive columns of its row, which are four operand registers after logic operations that put the codes
+// under the exponent of 1024 and a subtraction of 1024 + z (the upper codes of a byte: times 1/16, less 64 + z).  The eight
 // columns of a word enter as pairs (0, 4), (1, 5), (2, 6), (3, 7); x is laid out in shared memory in that
 // order, so a 16-byte read is the other operand of two steps.  A warp sends its sums to the CTA of the
 // cluster that is to finish its rows, and that CTA adds them up, in the order of the ranks, after its next unit.
 //
-// What bounds it: HBM.  Per 512 weights a warp issues about 30 instructions, 0.6 of what the SM has at
-// the rate the weights come in.
+// What bounds it: HBM.  Per 512 weights a warp issues about 25 instructions, half of what the SM has at the rate
+// the weights come in; 128 columns are in flight at a time, on four accumulators, since the products' latency would
+// otherwise set the pace (one accumulator: 190 cycles for 512 weights).
 #include "lb_q4.cuh"
 
 #include <algorithm>
@@ -48,38 +49,17 @@ struct MvLaunch {
     int tiles;     // of 128 rows
 };
 
-__device__ __forceinline__ void ldmatrix4(uint32_t (&r)[4], uint32_t addr) {
+// (volatile: stays behind the wait for its stage)
+__device__ __forceinline__ void ldmatrix4(uint32_t *r, uint32_t addr) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0,%1,%2,%3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
-                 : "r"(addr)
-                 : "memory");
+                 : "r"(addr));
 }
-__device__ __forceinline__ void mma_bf16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
-                                         uint32_t b0, uint32_t b1) {
-    asm volatile(
-        "mma.sync.aligned.m16n8k16.row.col.f32.bf16.bf16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, "
-        "{%0,%1,%2,%3};"
+__device__ __forceinline__ void mma_f16_16x8x16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                                uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
-}
-// Eight codes of a word less the zero: pairs (0, 4), (1, 5), (2, 6), (3, 7) of bf16.  bias: 128 + z twice.
-__device__ __forceinline__ void expand_bf16(uint32_t w, uint32_t bias, uint32_t (&r)[4]) {
-#pragma unroll
-    for (int i = 0; i < 4; i++) {
-        const uint32_t s = i ? w >> (4 * i) : w;
-        uint32_t v;
-        asm("lop3.b32 %0, %1, 0x000F000F, 0x43004300, 0xEA;" : "=r"(v) : "r"(s));  // (s & m) | 128
-        const __nv_bfloat162 h = __hsub2(*reinterpret_cast<__nv_bfloat162 *>(&v),
-                                         *reinterpret_cast<const __nv_bfloat162 *>(&bias));
-        r[i] = *reinterpret_cast<const uint32_t *>(&h);
-    }
-}
-// The high halves of two binary32 numbers: their first eight bits, cut off.
-__device__ __forceinline__ uint32_t high_halves(float a, float b) {
-    return prmt(__float_as_uint(a), __float_as_uint(b), 0x7632);
-}
-__device__ __forceinline__ float rest_of(float v) {
-    return v - __uint_as_float(__float_as_uint(v) & 0xFFFF0000u);
 }
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int bytes) {
     if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
@@ -118,7 +98,7 @@ __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
 __device__ __forceinline__ void store_y(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_y(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
-// T: the type of x (dense, up; h is fp32) and of a dense y; PARTS: bf16 parts of an x.
+// T: the type of x (dense, up; h is fp32) and of a dense y; PARTS: fp16 parts of an x.
 template <Q4Use USE, typename T, int PARTS, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kMvThreads, 2)
     q4_gemv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Q4Params p,
@@ -132,6 +112,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
     __shared__ __align__(16) uint8_t zs[ZEROS ? kMvMaxStages : 1][kMvRows][kPer];
     __shared__ __align__(16) float sums[2][8][16][kMvTokens];    // [rank, own warp][row][column]
     __shared__ int row_of[kMvTokens];
+    __shared__ uint32_t most[kMvTokens];                         // of a token's slice of x
     __shared__ uint16_t s_first[kExperts];                       // pieces before an expert's
     __shared__ int s_part[kMvThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -214,7 +195,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
     };
     // This cluster's units.
     const int64_t units = (int64_t)pieces * l.tiles, clusters = gridDim.x / l.split, c = blockIdx.x / l.split;
-    const int64_t u_begin = units * c / clusters, u_end = units * (c + 1) / clusters;
+    const int u_begin = (int)(units * c / clusters), u_end = (int)(units * (c + 1) / clusters);
     constexpr int kTileRows = USE == kQ4Up ? kMvRows / 2 : kMvRows;
 
     if (warp == kMvWarps) {
@@ -224,9 +205,9 @@ __global__ void __launch_bounds__(kMvThreads, 2)
         bool ok = true;
         int at_piece = -1;
         Piece q{0, 0, 0};
-        for (int64_t u = u_begin; u < u_end && ok; u++) {
-            const int piece = (int)(u / l.tiles);
-            const int64_t n0 = (u - (int64_t)piece * l.tiles) * kTileRows;
+        for (int u = u_begin; u < u_end && ok; u++) {
+            const int piece = u / l.tiles;
+            const int64_t n0 = (int64_t)(u - piece * l.tiles) * kTileRows;
             if (piece != at_piece) q = piece_of(piece), at_piece = piece;
             const int64_t matrix = (int64_t)q.expert * (USE == kQ4Up ? 2 * p.N : p.N);
             const int64_t last = matrix + (USE == kQ4Up ? 2 * p.N : p.N);
@@ -298,6 +279,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
         uint32_t phase = 0;
         bool ok = true;
         int at_piece = -1, cols = 0, planes = 1;
+        float back[2] = {0.f, 0.f};
         Piece q{0, 0, 0};
         // The parts of few tokens lie in one operand's eight columns, of more in an operand each.
         auto packed = [](const Piece &a) { return a.tokens * PARTS <= kMvTokens; };
@@ -319,9 +301,10 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                 }
             }
             const int parts = packed(q_done) ? PARTS : 1;
-            const int per_warp = USE == kQ4Up ? 8 : 16, rows = own * per_warp;
-            for (int i = tid; i < rows * q_done.tokens; i += 32 * kMvWarps) {
-                const int tk = i / rows, r = i % rows, w = r / per_warp, rr = r % per_warp;
+            constexpr int per_warp = USE == kQ4Up ? 8 : 16;
+            const int shift = (USE == kQ4Up ? 6 : 7) - (31 - __clz(l.split));   // rows: a power of two
+            for (int i = tid; i < q_done.tokens << shift; i += 32 * kMvWarps) {
+                const int tk = i >> shift, r = i & ((1 << shift) - 1), w = r / per_warp, rr = r % per_warp;
                 const int64_t row_n = n_done + (rank * own + w) * per_warp + rr;
                 float v[2] = {0.f, 0.f};
 #pragma unroll
@@ -343,95 +326,144 @@ __global__ void __launch_bounds__(kMvThreads, 2)
             }
         };
         int n = 0;
-        for (int64_t u = u_begin; u < u_end; u++, n++) {
-            const int piece = (int)(u / l.tiles);
+        for (int u = u_begin; u < u_end; u++, n++) {
+            const int piece = u / l.tiles;
             if (piece != at_piece) {
                 // x of the slice: operand row (packed: token * PARTS + part, else part * tokens + token), columns in
                 // the order of the codes' pairs, zeros behind K
                 q = piece_of(piece), at_piece = piece;
                 named_sync(1, 32 * kMvWarps);   // the last piece's x is done with
-                if (USE != kQ4Dense) {
-                    if (tid < q.tokens) row_of[tid] = p.order[q.t0 + tid];
-                    named_sync(1, 32 * kMvWarps);
-                }
+                if (tid < kMvTokens) most[tid] = 0;
+                if (USE != kQ4Dense && tid < q.tokens) row_of[tid] = p.order[q.t0 + tid];
+                named_sync(1, 32 * kMvWarps);
                 const bool pack = packed(q);
                 cols = pack ? q.tokens * PARTS : q.tokens, planes = pack ? 1 : PARTS;
-                const int each = blocks * (kMvBlock / 8);
-                for (int i = tid; i < q.tokens * each; i += 32 * kMvWarps) {
-                    const int tk = i / each, at = i % each;
-                    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
-                    int64_t from = q.t0 + tk;
-                    bool in = 8 * at < columns;
+                const uint32_t each = (uint32_t)blocks * (kMvBlock / 8), all = q.tokens * each;
+                auto load = [&](uint32_t tk, uint32_t at, float (&v)[8]) {
+#pragma unroll
+                    for (int j = 0; j < 8; j++) v[j] = 0.f;
+                    int64_t from = q.t0 + (int)tk;
+                    if (8 * (int)at >= columns) return;
                     if (USE != kQ4Dense) {
                         const int pair = row_of[tk];
-                        in = in && pair >= 0 && pair < p.T;
+                        if (pair < 0 || pair >= p.T) return;
                         if (USE == kQ4Up) from = pair / p.k;
                     }
-                    if (in) load8(static_cast<const X *>(p.x) + from * p.x_stride + k0 + 8 * at, v);
+                    load8(static_cast<const X *>(p.x) + from * p.x_stride + k0 + 8 * at, v);
+                };
+                // the largest of each token's slice ...
+#pragma unroll 4
+                for (uint32_t i = tid; i < all; i += 32 * kMvWarps) {
+                    float v[8], m = 0.f;
+                    load(i / each, i % each, v);
+#pragma unroll
+                    for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
+                    // (32 neighbours are one token's: a block has 64)
+                    const uint32_t most_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
+                    if (lane == 0) atomicMax(&most[i / each], most_bits);
+                }
+                named_sync(1, 32 * kMvWarps);
+                // ... comes to lie in [2^14, 2^15)
+#pragma unroll 4
+                for (uint32_t i = tid; i < all; i += 32 * kMvWarps) {
+                    const uint32_t tk = i / each, at = i % each;
+                    float v[8];
+                    load(tk, at, v);
+                    const float up = __uint_as_float(q4_power(most[tk]) << 23);
+                    uint32_t w[PARTS][4];
+#pragma unroll
+                    for (int j = 0; j < 4; j++) {
+                        const float a = v[j] * up, c2 = v[j + 4] * up;
+                        const __half2 h = __floats2half2_rn(a, c2);
+                        w[0][j] = bits_of(h);
+                        if (PARTS == 2)
+                            w[PARTS - 1][j] = bits_of(__floats2half2_rn(a - __low2float(h), c2 - __high2float(h)));
+                    }
 #pragma unroll
                     for (int part = 0; part < PARTS; part++) {
-                        const int to = pack ? tk * PARTS + part : part * q.tokens + tk;
+                        const uint32_t to = pack ? tk * PARTS + part : part * q.tokens + tk;
                         *reinterpret_cast<uint4 *>(xs + to * x_pitch + 16 * at) =
-                            make_uint4(high_halves(v[0], v[4]), high_halves(v[1], v[5]), high_halves(v[2], v[6]),
-                                       high_halves(v[3], v[7]));
-#pragma unroll
-                        for (int j = 0; j < 8; j++) v[j] = rest_of(v[j]);
+                            make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
                     }
                 }
                 named_sync(1, 32 * kMvWarps);
+                // what takes the scaling back from this lane's two columns
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    const int col = 2 * t + i, tk = pack ? col / PARTS : col;
+                    back[i] = tk < q.tokens ? __uint_as_float((254u - q4_power(most[tk])) << 23) : 0.f;
+                }
             }
             const uint8_t *xrow = xs + g * x_pitch + 16 * t;
             const int plane = q.tokens * x_pitch;
             const bool have = g < cols;
-            float total[4] = {0.f, 0.f, 0.f, 0.f}, sum[4] = {0.f, 0.f, 0.f, 0.f};
+            float total[4] = {0.f, 0.f, 0.f, 0.f};
             for (int b = 0; b < blocks && ok; b++) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
                     if (lane == 0) atomicOr(p.error, 1);
                     ok = false;
                     break;
                 }
-                const int chunks = min(kMvBlock, columns - b * kMvBlock) / 32;   // of 32 columns
-#pragma unroll
+                const int chunks = min(kMvBlock, columns - b * kMvBlock) / 32;   // of 32 columns (K is a multiple)
+                // 128 columns at a time; where K ends inside, x is zero and a group behind K is left out
+#pragma unroll 2
                 for (int j = 0; j < kMvBlock / 128; j++) {
                     if (4 * j >= chunks) break;
+                    uint32_t w[2][4];   // the lane's two rows of chunks 0 and 1, then of 2 and 3
 #pragma unroll
-                    for (int h = 0; h < 2; h++) {
-                        if (4 * j + 2 * h >= chunks) break;
-                        uint32_t w[4];   // the lane's two rows of chunk 2h, then of chunk 2h + 1
-                        ldmatrix4(w, at_row + stage * kMvStage + j * kMvBox +
-                                         (((uint32_t)(2 * h) + (lane >> 4)) ^ turn) * 16);
+                    for (int h = 0; h < 2; h++)
+                        ldmatrix4(w[h], at_row + stage * kMvStage + j * kMvBox +
+                                            (((uint32_t)(2 * h) + (lane >> 4)) ^ turn) * 16);
+                    uint4 x[PARTS][4];
 #pragma unroll
-                        for (int e = 0; e < 2; e++) {
-                            const int chunk = 4 * j + 2 * h + e;
-                            if (chunk >= chunks) break;   // (K is a multiple of 32)
-                            constexpr int kEach = GROUP / 32;
-                            uint32_t bias[2] = {0x43084308u, 0x43084308u};
-                            if (ZEROS) {
-                                bias[0] = 0x43004300u | zs[ZEROS ? stage : 0][row0][chunk / kEach] * 0x10001u;
-                                bias[1] = 0x43004300u | zs[ZEROS ? stage : 0][row1][chunk / kEach] * 0x10001u;
-                            }
-                            uint32_t a[2][4];
-                            expand_bf16(w[2 * e], bias[0], a[0]);
-                            expand_bf16(w[2 * e + 1], bias[1], a[1]);
-                            const uint8_t *xc = xrow + (b * (kMvBlock / 32) + chunk) * 64;
+                    for (int k = 0; k < PARTS; k++)
 #pragma unroll
-                            for (int k = 0; k < PARTS; k++) {
-                                if (k >= planes) break;
-                                uint4 x = make_uint4(0, 0, 0, 0);
-                                if (have) x = *reinterpret_cast<const uint4 *>(xc + k * plane);
-                                mma_bf16(sum, a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
-                                mma_bf16(sum, a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
-                            }
-                            if ((chunk + 1) % kEach == 0) {
-                                const float d0 = f16_bits_to_float(ds[stage][row0][chunk / kEach]);
-                                const float d1 = f16_bits_to_float(ds[stage][row1][chunk / kEach]);
-                                total[0] = fmaf(d0, sum[0], total[0]);
-                                total[1] = fmaf(d0, sum[1], total[1]);
-                                total[2] = fmaf(d1, sum[2], total[2]);
-                                total[3] = fmaf(d1, sum[3], total[3]);
-                                sum[0] = sum[1] = sum[2] = sum[3] = 0.f;
-                            }
+                        for (int e = 0; e < 4; e++) {
+                            x[k][e] = make_uint4(0, 0, 0, 0);
+                            if (have && k < planes)
+                                x[k][e] = *reinterpret_cast<const uint4 *>(
+                                    xrow + k * plane + (b * (kMvBlock / 32) + 4 * j + e) * 64);
                         }
+                    constexpr int kGroups = 128 / GROUP, kEach = GROUP / 32;   // groups of 128 columns, chunks of a group
+                    float sum[kGroups < 4 ? 4 : kGroups][4];
+#pragma unroll
+                    for (int i = 0; i < (kGroups < 4 ? 4 : kGroups); i++)
+                        sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
+#pragma unroll
+                    for (int e = 0; e < 4; e++) {
+                        const int gi = j * kGroups + e / kEach;
+                        __half2 low[2], high[2];
+#pragma unroll
+                        for (int r = 0; r < 2; r++) {
+                            const uint32_t z = ZEROS ? zs[ZEROS ? stage : 0][r ? row1 : row0][gi] : 8u;
+                            low[r] = half2_of(0x64006400u + z * 0x10001u);
+                            high[r] = half2_of(0xD400D400u + z * 0x00100010u);
+                        }
+                        uint32_t a[2][4];
+                        const __half2 none = half2_of(0);
+                        expand_f16<false>(w[e >> 1][2 * (e & 1)], low[0], high[0], none, a[0]);
+                        expand_f16<false>(w[e >> 1][2 * (e & 1) + 1], low[1], high[1], none, a[1]);
+#pragma unroll
+                        for (int k = 0; k < PARTS; k++) {
+                            if (k > 0 && planes == 1) break;
+                            mma_f16_16x8x16(sum[e], a[0][0], a[1][0], a[0][1], a[1][1], x[k][e].x, x[k][e].y);
+                            mma_f16_16x8x16(sum[e], a[0][2], a[1][2], a[0][3], a[1][3], x[k][e].z, x[k][e].w);
+                        }
+                    }
+#pragma unroll
+                    for (int i = 0; i < kGroups; i++) {
+                        if (4 * j + i * kEach >= chunks) break;
+                        const int gi = j * kGroups + i;
+                        const float d0 = f16_bits_to_float(ds[stage][row0][gi]);
+                        const float d1 = f16_bits_to_float(ds[stage][row1][gi]);
+#pragma unroll
+                        for (int e = i * kEach + 1; e < (i + 1) * kEach; e++)
+#pragma unroll
+                            for (int c2 = 0; c2 < 4; c2++) sum[i * kEach][c2] += sum[e][c2];
+                        total[0] = fmaf(d0, sum[i * kEach][0], total[0]);
+                        total[1] = fmaf(d0, sum[i * kEach][1], total[1]);
+                        total[2] = fmaf(d1, sum[i * kEach][2], total[2]);
+                        total[3] = fmaf(d1, sum[i * kEach][3], total[3]);
                     }
                 }
                 __syncwarp();
@@ -443,12 +475,12 @@ __global__ void __launch_bounds__(kMvThreads, 2)
             named_sync(1, 32 * kMvWarps);
             // rows g and g + 8, columns 2t and 2t + 1, to the CTA that finishes them
             const uint32_t to = send_to + (n & 1) * (uint32_t)(sizeof(sums) / 2);
-            store_in(to, total[0], total[1]);
-            store_in(to + 8 * kMvTokens * 4, total[2], total[3]);
+            store_in(to, total[0] * back[0], total[1] * back[1]);
+            store_in(to + 8 * kMvTokens * 4, total[2] * back[0], total[3] * back[1]);
             __syncwarp();
             if (lane < 2) arrive_in(tell[n & 1]);
             q_done = q;
-            n_done = (u - (int64_t)piece * l.tiles) * kTileRows;
+            n_done = (int64_t)(u - piece * l.tiles) * kTileRows;
         }
         if (n > 0) finish(n - 1);
     }
@@ -564,14 +596,14 @@ int q4_gemv(const Q4Params &p, Q4Use use, int type, const uint8_t *codes, int64_
             cudaStream_t st) {
     const bool f32 = type == LB_OUT_F32;
     if (use == kQ4Dense)
-        return f32 ? dispatch_gemv<kQ4Dense, float, 3>(p, codes, rows, sms, st)
+        return f32 ? dispatch_gemv<kQ4Dense, float, 2>(p, codes, rows, sms, st)
                    : dispatch_gemv<kQ4Dense, __nv_bfloat16, 1>(p, codes, rows, sms, st);
     if (use == kQ4Up)
-        return f32 ? dispatch_gemv<kQ4Up, float, 3>(p, codes, rows, sms, st)
+        return f32 ? dispatch_gemv<kQ4Up, float, 2>(p, codes, rows, sms, st)
                    : dispatch_gemv<kQ4Up, __nv_bfloat16, 1>(p, codes, rows, sms, st);
-    // h in two parts: 16 bits, 2^-8 of a bf16 output's rounding
-    return f32 ? dispatch_gemv<kQ4Down, float, 3>(p, codes, rows, sms, st)
-               : dispatch_gemv<kQ4Down, float, 2>(p, codes, rows, sms, st);
+    // (with bf16 tensors h is rounded to 11 bits, an eighth of an output's rounding)
+    return f32 ? dispatch_gemv<kQ4Down, float, 2>(p, codes, rows, sms, st)
+               : dispatch_gemv<kQ4Down, float, 1>(p, codes, rows, sms, st);
 }
 
 }  // namespace lb

@@ -32,11 +32,11 @@ def half_step(dtype):
 
 
 def product(x, w, dtype, tokens=None):
-    """(exact y, bound of an output's error).  For up to eight tokens every product is exact and what
-    is left is binary32 addition, cut on the tensor cores: per group 8 steps (24 with three parts) that
-    lose below 2^-22 of its magnitudes each, then at most 1024 groups in up to eight chains, 2^-24 each
+    """(exact y, bound of an output's error).  For up to eight tokens c - z is exact, x too (fp32: to 22
+    bits), and what is left is binary32 addition, cut on the tensor cores: per group 8 steps (16 with two parts)
+    that lose below 2^-22 of its magnitudes each, then at most 1024 groups in up to eight chains, 2^-24 each
     of all of it: below 1e-5 of the sum of magnitudes.  More bf16 tokens: weights rounded to 11 bits,
-    2^-11 of the magnitudes; fp32: x to 22 bits, sums cut as above.  A row of more tokens is scaled so that its
+    2^-11 of the magnitudes; fp32: as few tokens.  A row of x is scaled so that its
     largest value lies below 2^15, and fp16's last place is 2^-24 (half of it is lost): 2^-39 of that value."""
     xd = x.double()
     y, mag = xd @ w.t(), xd.abs() @ w.abs().t()
