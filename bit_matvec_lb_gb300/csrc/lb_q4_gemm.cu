@@ -173,20 +173,16 @@ __device__ __forceinline__ void gm_commit_multicast(uint64_t *b, uint16_t mask) 
         : "memory");
 }
 
-// On to the next scales and zeros of a warp that takes every other step of 64 columns.
+// On to the next scales and zeros of a warp that takes every other unit of 128 columns.
 template <int GROUP>
 __device__ __forceinline__ void q4_rotate(uint4 &d, uint2 &z) {
-    if (GROUP == 32) {
+    if (GROUP == 64) {
         d.x = d.z, d.y = d.w;
         z.x = z.y;
-    } else if (GROUP == 64) {
+    } else if (GROUP == 128) {
         d.x = d.y, d.y = d.z, d.z = d.w;
         z.x = __funnelshift_r(z.x, z.y, 16), z.y >>= 16;
-    } else {
-        d.x = __funnelshift_r(d.x, d.y, 16), d.y = __funnelshift_r(d.y, d.z, 16);
-        d.z = __funnelshift_r(d.z, d.w, 16), d.w >>= 16;
-        z.x = __funnelshift_r(z.x, z.y, 8), z.y >>= 8;
-    }
+    }   // (32: a block of eight groups has one unit of the warp's)
 }
 
 // A place in a ring of N stages, and the parity of its present phase.
@@ -227,14 +223,15 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     __shared__ int s_part[32];
     __shared__ __align__(16) float col_scale[2][kTokens];   // of an item and the next one
     __shared__ __align__(16) int col_row[2][kTokens];
-    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    // (from the warp's first lane: what is made of it stays in the uniform registers that the operations take)
+    const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int rank = blockIdx.x % l.split;            // along K
     const int cluster = l.split * l.share;
 
     if (tid == 0) {
         // a stage is full when its four warps of weights and the copies of x are there
         for (int i = 0; i < kGmStages; i++) mbar_init(&bar.full[i], 5), mbar_init(&bar.empty[i], l.share);
-        for (int i = 0; i < kGmCStages; i++) mbar_init(&bar.c_full[i], 1), mbar_init(&bar.c_empty[i], kGmExpandWarps);
+        for (int i = 0; i < kGmCStages; i++) mbar_init(&bar.c_full[i], 1), mbar_init(&bar.c_empty[i], 4);
         for (int i = 0; i < 2; i++) mbar_init(&bar.d_full[i], 1), mbar_init(&bar.d_empty[i], kGmOutWarps);
         mbar_init(&bar.done, 1);
         fence_mbar_init();
@@ -287,7 +284,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     else __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
-    const uint32_t tmem = s_tmem;
+    const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
     const int side = l.tiles / l.share;
     const int items = pieces * side;   // of a cluster
     const int each = gridDim.x / cluster, begin = blockIdx.x / cluster;
@@ -513,24 +510,24 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             named_sync(2, kGmThreads);
         }
     } else if (warp < kGmOutWarps + kGmExpandWarps) {
-        // =================== weights: a thread per row, every other step ===================
+        // =================== weights: a thread per row, every other unit of two steps ===================
         if constexpr (F32) gm_fewer_registers<80>();
         const int quarter = warp & 3, half = (warp - kGmOutWarps) >> 2;
         const uint32_t to = tmem + kGmABase + ((uint32_t)(quarter * 32) << 16);
-        constexpr int kBlock = 8 * GROUP / kGmStep;   // steps of eight groups, whose scales are held
+        constexpr int kBlock = 8 * GROUP / 128;   // units of eight groups, whose scales are held
         // the lane's row of a stage of codes, under the 64-byte swizzle
         const int at = USE == kQ4Up ? (lane & 16) * 4 + quarter * 16 + (lane & 15) : quarter * 32 + lane;
         const uint32_t from = smem_u32(smem) + kGmStages * kGmB + at * 64, swizzle = (at >> 1) & 3;
         GmRing<kGmStages> ring;
         GmRing<kGmCStages> code;
-        uint32_t turn = 0;   // this CTA's steps so far
+        const int units = (steps + 1) / 2;
+        uint32_t turn = 0;   // this CTA's units so far
         // Scales and zeros of eight groups are asked for before the eight before them are used, an item's first ones
         // during the item before it.
-        const int s_begin = k0 / kGmStep, first_block = s_begin / kBlock;       // (s_begin is even)
-        const int end_block = (s_begin + steps + kBlock - 1) / kBlock;
+        const int u_begin = k0 / 128, end_block = (u_begin + units + kBlock - 1) / kBlock;
         uint4 d_next = make_uint4(0, 0, 0, 0);
         uint2 z_next = make_uint2(0, 0);
-        int held = -1, next = 0, asked = -1;   // the item of d_next, the next block, the item that `at` is for
+        int held = -1, next = 0, asked = -1;   // the item of d_next, the next block, the item that at_row is for
         int64_t at_row = 0;
         auto ask = [&](int i, int block) {
             if (i >= items) return;
@@ -540,99 +537,93 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 at_row = (in ? row : 0) * p.pitch;
                 asked = i;
             }
+            held = i;
+            if (block >= end_block) return;   // (nothing of the item is this warp's)
             if (!F32) d_next = reinterpret_cast<const uint4 *>(p.scales + at_row)[block];
             if (ZEROS) z_next = reinterpret_cast<const uint2 *>(p.zeros + at_row)[block];
-            held = i;
         };
         for (int i = begin; i < items; i += each) {
-            const int parity = (half ^ turn) & 1;   // of the steps that are this warp's
-            if (held != i) ask(i, first_block);
-            next = first_block + 1;
+            const uint32_t parity = (half ^ turn) & 1;   // of the units that are this warp's
+            next = (u_begin + (int)parity) / kBlock;
+            if (held != i) ask(i, next);
+            next++;
             GmRing<kGmStages> at_step = ring;
-            at_step.next(parity);
-            // the block of eight groups that is held: step `sj` of it is next
+            GmRing<kGmCStages> at_code = code;
+            at_step.next(2 * parity), at_code.next(parity);
+            // the block of eight groups that is held: unit `uj` of it is next
             uint4 d8 = make_uint4(0, 0, 0, 0);
             uint2 z8 = make_uint2(0, 0);
-            int sj = kBlock;
-            uint4 c[2];
-            bool there = false;
-            auto load = [&]() {
+            int uj = kBlock;
+#pragma unroll 1
+            for (int u = parity; u < units; u += 2) {
+                if (uj >= kBlock) {
+                    d8 = d_next, z8 = z_next;
+                    uj = (u_begin + u) % kBlock;
+                    if (next < end_block) ask(i, next++);
+                    else ask(i + each, (u_begin + (int)((half ^ (turn + units)) & 1)) / kBlock);
+                    // (a slice of K may begin inside a block)
+                    for (int skip = uj / 2; skip > 0; skip--) q4_rotate<GROUP>(d8, z8);
+                }
+                const bool odd = uj & 1;
+                wait(bar.c_full[at_code.i], at_code.phase);
+                uint4 c[4];
 #pragma unroll
-                for (int h = 0; h < 2; h++)
+                for (int h = 0; h < 4; h++)
                     asm volatile("ld.shared.v4.u32 {%0,%1,%2,%3}, [%4];"
                                  : "=r"(c[h].x), "=r"(c[h].y), "=r"(c[h].z), "=r"(c[h].w)
-                                 : "r"(from + code.i * kGmC + ((2 * parity + h) ^ swizzle) * 16)
+                                 : "r"(from + at_code.i * kGmC + (h ^ swizzle) * 16)
                                  : "memory");
-            };
-#pragma unroll 1
-            for (int s = parity; s < steps; s += 2) {
-                if (sj >= kBlock) {
-                    d8 = d_next, z8 = z_next;
-                    sj = (s_begin + s) % kBlock;
-                    if (next < end_block) ask(i, next++);
-                    else ask(i + each, first_block);
-                    // (a slice of K may begin inside a block)
-                    for (int skip = sj / 2; skip > 0; skip--) q4_rotate<GROUP>(d8, z8);
-                }
-                // the scales (and zeros) of the step's two halves
-                uint32_t d[2], z[2] = {8, 8};
+                // the scales (and zeros) of the unit's four chunks of 32 columns
+                uint32_t d[4], z[4] = {8, 8, 8, 8};
                 if (GROUP == 32) {
-                    const uint32_t w = parity ? d8.y : d8.x, v = parity ? z8.x >> 16 : z8.x;
-                    d[0] = w & 0xffff, d[1] = w >> 16;
-                    if (ZEROS) z[0] = v & 0xff, z[1] = v >> 8 & 0xff;
+                    const uint32_t w0 = odd ? d8.z : d8.x, w1 = odd ? d8.w : d8.y, v = odd ? z8.y : z8.x;
+                    d[0] = w0 & 0xffff, d[1] = w0 >> 16, d[2] = w1 & 0xffff, d[3] = w1 >> 16;
+                    if (ZEROS) z[0] = v & 0xff, z[1] = v >> 8 & 0xff, z[2] = v >> 16 & 0xff, z[3] = v >> 24;
                 } else if (GROUP == 64) {
-                    d[0] = d[1] = parity ? d8.x >> 16 : d8.x & 0xffff;
-                    if (ZEROS) z[0] = z[1] = (parity ? z8.x >> 8 : z8.x) & 0xff;
+                    const uint32_t w = odd ? d8.y : d8.x, v = odd ? z8.x >> 16 : z8.x;
+                    d[0] = d[1] = w & 0xffff, d[2] = d[3] = w >> 16;
+                    if (ZEROS) z[0] = z[1] = v & 0xff, z[2] = z[3] = v >> 8 & 0xff;
                 } else {
-                    d[0] = d[1] = d8.x & 0xffff;
-                    if (ZEROS) z[0] = z[1] = z8.x & 0xff;
+                    d[0] = d[1] = d[2] = d[3] = odd ? d8.x >> 16 : d8.x & 0xffff;
+                    if (ZEROS) z[0] = z[1] = z[2] = z[3] = (odd ? z8.x >> 8 : z8.x) & 0xff;
                 }
                 q4_rotate<GROUP>(d8, z8);
-                sj += 2;
-                if (!there) {
-                    wait(bar.c_full[code.i], code.phase);
-                    load();
-                }
-                wait(bar.empty[at_step.i], at_step.phase ^ 1);
-                tc_fence_after();
+                uj += 2;
 #pragma unroll
-                for (int h = 0; h < 2; h++) {
-                    const __half2 low = half2_of(0x64006400u + z[h] * 0x10001u);   // 1024 + z
-                    // -(64 + z), whose last place is 2^-4
-                    const __half2 high = half2_of(0xD400D400u + z[h] * 0x00100010u);
-                    const __half2 scale = half2_of(d[h] * 0x10001u);
-                    uint32_t v[16];
-                    if (s * kGmStep + 32 * h < columns) {
-                        expand_f16<!F32>(c[h].x, low, high, scale, v);
-                        expand_f16<!F32>(c[h].y, low, high, scale, v + 4);
-                        expand_f16<!F32>(c[h].z, low, high, scale, v + 8);
-                        expand_f16<!F32>(c[h].w, low, high, scale, v + 12);
-                    } else {
+                for (int s = 0; s < 2; s++) {
+                    if (2 * u + s >= steps) break;
+                    uint32_t v[32];
 #pragma unroll
-                        for (int e = 0; e < 16; e++) v[e] = 0;
+                    for (int h = 0; h < 2; h++) {
+                        const int q = 2 * s + h;
+                        const __half2 low = half2_of(0x64006400u + z[q] * 0x10001u);   // 1024 + z
+                        // -(64 + z), whose last place is 2^-4
+                        const __half2 high = half2_of(0xD400D400u + z[q] * 0x00100010u);
+                        const __half2 scale = half2_of(d[q] * 0x10001u);
+                        expand_f16<!F32>(c[q].x, low, high, scale, v + 16 * h);
+                        expand_f16<!F32>(c[q].y, low, high, scale, v + 16 * h + 4);
+                        expand_f16<!F32>(c[q].z, low, high, scale, v + 16 * h + 8);
+                        expand_f16<!F32>(c[q].w, low, high, scale, v + 16 * h + 12);
                     }
-                    gm_tmem_st16(to + at_step.i * 32 + 16 * h, v);
+                    if ((2 * u + s) * kGmStep + 32 >= columns)   // K ends after half a step
+#pragma unroll
+                        for (int e = 16; e < 32; e++) v[e] = 0;
+                    wait(bar.empty[at_step.i], at_step.phase ^ 1);
+                    tc_fence_after();
+                    gm_tmem_st16(to + at_step.i * 32, v);
+                    gm_tmem_st16(to + at_step.i * 32 + 16, v + 16);
+                    if (s == 0 && lane == 0) mbar_arrive(&bar.c_empty[at_code.i]);   // (all lanes have theirs: wait)
+                    asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
+                    tc_fence_before();
+                    __syncwarp();
+                    if (lane == 0) mbar_arrive(&bar.full[at_step.i]);
+                    at_step.next();
                 }
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.c_empty[code.i]);
-                code.next();
-                // the next step's codes, if they have come, while the weights are on their way
-                there = s + 2 < steps && __all_sync(0xffffffffu, mbar_try_wait(&bar.c_full[code.i], code.phase));
-                if (there) load();
-                asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory");
-                tc_fence_before();
-                __syncwarp();
-                if (lane == 0) mbar_arrive(&bar.full[at_step.i]);
-                at_step.next(2);
+                at_step.next(2), at_code.next(2);
             }
-            // (an odd number of steps leaves half a stage of codes that one half of the warps has nothing of)
-            if ((steps & 1) && parity) {
-                wait(bar.c_full[code.i], code.phase);
-                if (lane == 0) mbar_arrive(&bar.c_empty[code.i]);
-                code.next();
-            }
-            turn += steps;
+            turn += units;
             ring.skip(steps);
+            code.skip(units);
         }
         __syncwarp();
         if constexpr (F32) {

@@ -61,6 +61,13 @@ __device__ __forceinline__ void mma_f16_16x8x16(float (&d)[4], uint32_t a0, uint
         : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
         : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
 }
+// The same onto nothing.
+__device__ __forceinline__ void mma_f16_begin(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3,
+                                              uint32_t b0, uint32_t b1) {
+    asm("mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%10,%10,%10,%10};"
+        : "=f"(d[0]), "=f"(d[1]), "=f"(d[2]), "=f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1), "f"(0.f));
+}
 __device__ __forceinline__ void copy_async(uint32_t dst, const void *src, int bytes) {
     if (bytes == 16) asm volatile("cp.async.cg.shared.global [%0], [%1], 16;" ::"r"(dst), "l"(src) : "memory");
     else if (bytes == 8) asm volatile("cp.async.ca.shared.global [%0], [%1], 8;" ::"r"(dst), "l"(src) : "memory");
@@ -88,9 +95,6 @@ __device__ __forceinline__ bool mv_try_wait_cluster(uint64_t *bar, uint32_t pari
         : "memory");
     return ok != 0;
 }
-__device__ __forceinline__ void mv_cluster_sync() {
-    asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
-}
 // cp.async's of this thread so far arrive once on bar when they have landed (counted in the barrier's number).
 __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -111,8 +115,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
     __shared__ __align__(16) uint16_t ds[kMvMaxStages][kMvRows][kPer];
     __shared__ __align__(16) uint8_t zs[ZEROS ? kMvMaxStages : 1][kMvRows][kPer];
     __shared__ __align__(16) float sums[2][8][16][kMvTokens];    // [rank, own warp][row][column]
-    __shared__ int row_of[kMvTokens];
-    __shared__ uint32_t most[kMvTokens];                         // of a token's slice of x
+    __shared__ int row_of[2][kMvTokens];
     __shared__ uint16_t s_first[kExperts];                       // pieces before an expert's
     __shared__ int s_part[kMvThreads / 32];
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -120,7 +123,9 @@ __global__ void __launch_bounds__(kMvThreads, 2)
     const int k0 = rank * slice, columns = min(p.K - k0, slice);
     const int blocks = max((columns + kMvBlock - 1) / kMvBlock, 0);   // (the last CTAs along K may have none)
     const int x_pitch = 2 * slice + 64;
-    uint8_t *ring = smem, *xs = smem + l.stages * kMvStage;
+    uint8_t *ring = smem;
+    float *back = reinterpret_cast<float *>(ring + l.stages * kMvStage);   // takes scaling back: [256 columns][operand column]
+    uint8_t *xs = reinterpret_cast<uint8_t *>(back + 2 * l.blocks * kMvTokens);
 
     pdl_launch_dependents();
     if (tid == 0) {
@@ -170,13 +175,15 @@ __global__ void __launch_bounds__(kMvThreads, 2)
             before += n[i];
         }
     }
-    if (l.split > 1) mv_cluster_sync();   // (everybody's barriers are there)
-    else __syncthreads();
+    // (everybody's barriers are there before anybody's sums are sent: waited for then)
+    if (l.split > 1) asm volatile("barrier.cluster.arrive.release;" ::: "memory");
+    __syncthreads();
     struct Piece {
-        int expert, t0, tokens;
+        int expert, t0, tokens, slot;   // slot: of row_of
     };
     auto piece_of = [&](int i) {
         Piece q;
+        q.slot = 0;
         if constexpr (USE == kQ4Dense) {
             q.expert = 0, q.t0 = i * l.tokens;
             q.tokens = (int)min((int64_t)l.tokens, p.T - q.t0);
@@ -204,7 +211,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
         uint32_t phase = 0;
         bool ok = true;
         int at_piece = -1;
-        Piece q{0, 0, 0};
+        Piece q{0, 0, 0, 0};
         for (int u = u_begin; u < u_end && ok; u++) {
             const int piece = u / l.tiles;
             const int64_t n0 = (int64_t)(u - piece * l.tiles) * kTileRows;
@@ -263,6 +270,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
             mbar_wait(&full[stage], phase);
         }
         if (USE == kQ4Dense) pdl_wait();
+        if (l.split > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     } else {
         // =================== products ===================
         if (USE == kQ4Dense) pdl_wait();
@@ -279,13 +287,29 @@ __global__ void __launch_bounds__(kMvThreads, 2)
         uint32_t phase = 0;
         bool ok = true;
         int at_piece = -1, cols = 0, planes = 1;
-        float back[2] = {0.f, 0.f};
-        Piece q{0, 0, 0};
+        Piece q{0, 0, 0, 0};
         // The parts of few tokens lie in one operand's eight columns, of more in an operand each.
         auto packed = [](const Piece &a) { return a.tokens * PARTS <= kMvTokens; };
         // What a finished unit leaves to be done after the next one's products.
-        Piece q_done{0, 0, 0};
+        Piece q_done{0, 0, 0, 0};
         int64_t n_done = 0;
+        // a finished sum of row `row_n` of the matrix (up: gate and up rows')
+        auto store = [&](const Piece &a, int64_t row_n, int tk, float v0, float v1) {
+            if (row_n >= p.N) return;
+            if (USE == kQ4Dense) {
+                store_y(static_cast<T *>(p.y) + (a.t0 + tk) * p.y_stride + row_n, v0);
+            } else if (USE == kQ4Up) {
+                static_cast<float *>(p.y)[(int64_t)(a.t0 + tk) * p.y_stride + row_n] = v0 / (1.f + expf(-v0)) * v1;
+            } else {
+                const int pair = row_of[a.slot][tk];
+                if (pair >= 0 && pair < p.T) static_cast<float *>(p.y)[(int64_t)pair * p.y_stride + row_n] = v0;
+            }
+        };
+        // a lane's two rows' sums
+        auto put = [&](const Piece &a, int64_t row_n, int tk, float v0, float v1) {
+            store(a, row_n, tk, v0, v1);
+            if (USE != kQ4Up) store(a, row_n + 8, tk, v1, 0.f);
+        };
         // the sums of unit number n (of this cluster's), added up over the ranks and stored
         auto finish = [&](int n) {
             if (ok) {
@@ -312,17 +336,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                     for (int k = 0; k < parts; k++)
                         for (int s = 0; s < l.split; s++)
                             v[h] += sums[n & 1][s * own + w][rr + 8 * h][tk * parts + k];
-                if (row_n >= p.N) continue;
-                if (USE == kQ4Dense) {
-                    store_y(static_cast<T *>(p.y) + (q_done.t0 + tk) * p.y_stride + row_n, v[0]);
-                } else if (USE == kQ4Up) {
-                    static_cast<float *>(p.y)[(int64_t)(q_done.t0 + tk) * p.y_stride + row_n] =
-                        v[0] / (1.f + expf(-v[0])) * v[1];
-                } else {
-                    const int pair = p.order[q_done.t0 + tk];
-                    if (pair >= 0 && pair < p.T)
-                        static_cast<float *>(p.y)[(int64_t)pair * p.y_stride + row_n] = v[0];
-                }
+                store(q_done, row_n, tk, v[0], v[1]);
             }
         };
         int n = 0;
@@ -331,72 +345,68 @@ __global__ void __launch_bounds__(kMvThreads, 2)
             if (piece != at_piece) {
                 // x of the slice: operand row (packed: token * PARTS + part, else part * tokens + token), columns in
                 // the order of the codes' pairs, zeros behind K
-                q = piece_of(piece), at_piece = piece;
+                const int slot = q.slot ^ 1;   // (the last piece's rows may still be asked for)
+                q = piece_of(piece), at_piece = piece, q.slot = slot;
                 named_sync(1, 32 * kMvWarps);   // the last piece's x is done with
-                if (tid < kMvTokens) most[tid] = 0;
-                if (USE != kQ4Dense && tid < q.tokens) row_of[tid] = p.order[q.t0 + tid];
+                if (USE != kQ4Dense && tid < q.tokens) row_of[slot][tid] = p.order[q.t0 + tid];
                 named_sync(1, 32 * kMvWarps);
                 const bool pack = packed(q);
                 cols = pack ? q.tokens * PARTS : q.tokens, planes = pack ? 1 : PARTS;
-                const uint32_t each = (uint32_t)blocks * (kMvBlock / 8), all = q.tokens * each;
-                auto load = [&](uint32_t tk, uint32_t at, float (&v)[8]) {
+                // 64 threads take a block of a token, eight columns each, four tokens at a time; a warp's 256 columns
+                // are scaled so that the largest comes to lie in [2^14, 2^15).  Four blocks are asked for together.
+                const int each = max(blocks, 0), all = (q.tokens + 3) / 4 * each;
+                for (int c0 = 0; c0 < all; c0 += 4) {
+                    float v[4][8];
+                    bool in[4];
+                    int tok[4], blk[4];
 #pragma unroll
-                    for (int j = 0; j < 8; j++) v[j] = 0.f;
-                    int64_t from = q.t0 + (int)tk;
-                    if (8 * (int)at >= columns) return;
-                    if (USE != kQ4Dense) {
-                        const int pair = row_of[tk];
-                        if (pair < 0 || pair >= p.T) return;
-                        if (USE == kQ4Up) from = pair / p.k;
+                    for (int k = 0; k < 4; k++) {
+                        const int c2 = c0 + k, i = c2 / each;
+                        blk[k] = c2 - i * each, tok[k] = 4 * i + (tid >> 6);
+                        const int at = blk[k] * kMvBlock + (tid & 63) * 8;
+                        in[k] = c2 < all && tok[k] < q.tokens && at < columns;
+                        int64_t from = q.t0 + tok[k];
+                        if (USE != kQ4Dense) {
+                            const int pair = in[k] ? row_of[slot][tok[k]] : -1;
+                            in[k] = pair >= 0 && pair < p.T;
+                            if (USE == kQ4Up) from = pair / p.k;
+                        }
+                        load8(static_cast<const X *>(p.x) + (in[k] ? from * p.x_stride + k0 + at : 0), v[k]);
                     }
-                    load8(static_cast<const X *>(p.x) + from * p.x_stride + k0 + 8 * at, v);
-                };
-                // the largest of each token's slice ...
-#pragma unroll 4
-                for (uint32_t i = tid; i < all; i += 32 * kMvWarps) {
-                    float v[8], m = 0.f;
-                    load(i / each, i % each, v);
 #pragma unroll
-                    for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
-                    // (32 neighbours are one token's: a block has 64)
-                    const uint32_t most_bits = __reduce_max_sync(0xffffffffu, __float_as_uint(m));
-                    if (lane == 0) atomicMax(&most[i / each], most_bits);
+                    for (int k = 0; k < 4; k++) {
+                        if (c0 + k >= all || tok[k] >= q.tokens) break;
+                        float m = 0.f;
+#pragma unroll
+                        for (int j = 0; j < 8; j++) {
+                            v[k][j] = in[k] ? v[k][j] : 0.f;
+                            m = fmaxf(m, fabsf(v[k][j]));
+                        }
+                        const uint32_t e = q4_power(__reduce_max_sync(0xffffffffu, __float_as_uint(m)));
+                        const float up = __uint_as_float(e << 23);
+                        uint32_t w[PARTS][4];
+#pragma unroll
+                        for (int j = 0; j < 4; j++) {
+                            const float a = v[k][j] * up, c2 = v[k][j + 4] * up;
+                            const __half2 h = __floats2half2_rn(a, c2);
+                            w[0][j] = bits_of(h);
+                            if (PARTS == 2)
+                                w[PARTS - 1][j] = bits_of(__floats2half2_rn(a - __low2float(h), c2 - __high2float(h)));
+                        }
+#pragma unroll
+                        for (int part = 0; part < PARTS; part++) {
+                            const int to = pack ? tok[k] * PARTS + part : part * q.tokens + tok[k];
+                            *reinterpret_cast<uint4 *>(xs + to * x_pitch + blk[k] * (2 * kMvBlock) + 16 * (tid & 63)) =
+                                make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
+                            const int col = pack ? to : tok[k];
+                            if (lane == 0) back[(blk[k] * 2 + ((tid >> 5) & 1)) * kMvTokens + col] = __uint_as_float((254u - e) << 23);
+                        }
+                    }
                 }
                 named_sync(1, 32 * kMvWarps);
-                // ... comes to lie in [2^14, 2^15)
-#pragma unroll 4
-                for (uint32_t i = tid; i < all; i += 32 * kMvWarps) {
-                    const uint32_t tk = i / each, at = i % each;
-                    float v[8];
-                    load(tk, at, v);
-                    const float up = __uint_as_float(q4_power(most[tk]) << 23);
-                    uint32_t w[PARTS][4];
-#pragma unroll
-                    for (int j = 0; j < 4; j++) {
-                        const float a = v[j] * up, c2 = v[j + 4] * up;
-                        const __half2 h = __floats2half2_rn(a, c2);
-                        w[0][j] = bits_of(h);
-                        if (PARTS == 2)
-                            w[PARTS - 1][j] = bits_of(__floats2half2_rn(a - __low2float(h), c2 - __high2float(h)));
-                    }
-#pragma unroll
-                    for (int part = 0; part < PARTS; part++) {
-                        const uint32_t to = pack ? tk * PARTS + part : part * q.tokens + tk;
-                        *reinterpret_cast<uint4 *>(xs + to * x_pitch + 16 * at) =
-                            make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
-                    }
-                }
-                named_sync(1, 32 * kMvWarps);
-                // what takes the scaling back from this lane's two columns
-#pragma unroll
-                for (int i = 0; i < 2; i++) {
-                    const int col = 2 * t + i, tk = pack ? col / PARTS : col;
-                    back[i] = tk < q.tokens ? __uint_as_float((254u - q4_power(most[tk])) << 23) : 0.f;
-                }
             }
-            const uint8_t *xrow = xs + g * x_pitch + 16 * t;
+            const uint8_t *xrow = xs + min(g, cols - 1) * x_pitch + 16 * t;   // (columns without a token repeat one)
             const int plane = q.tokens * x_pitch;
-            const bool have = g < cols;
             float total[4] = {0.f, 0.f, 0.f, 0.f};
             for (int b = 0; b < blocks && ok; b++) {
                 if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
@@ -414,21 +424,9 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                     for (int h = 0; h < 2; h++)
                         ldmatrix4(w[h], at_row + stage * kMvStage + j * kMvBox +
                                             (((uint32_t)(2 * h) + (lane >> 4)) ^ turn) * 16);
-                    uint4 x[PARTS][4];
-#pragma unroll
-                    for (int k = 0; k < PARTS; k++)
-#pragma unroll
-                        for (int e = 0; e < 4; e++) {
-                            x[k][e] = make_uint4(0, 0, 0, 0);
-                            if (have && k < planes)
-                                x[k][e] = *reinterpret_cast<const uint4 *>(
-                                    xrow + k * plane + (b * (kMvBlock / 32) + 4 * j + e) * 64);
-                        }
+                    const uint8_t *xc = xrow + (b * (kMvBlock / 32) + 4 * j) * 64;
                     constexpr int kGroups = 128 / GROUP, kEach = GROUP / 32;   // groups of 128 columns, chunks of a group
-                    float sum[kGroups < 4 ? 4 : kGroups][4];
-#pragma unroll
-                    for (int i = 0; i < (kGroups < 4 ? 4 : kGroups); i++)
-                        sum[i][0] = sum[i][1] = sum[i][2] = sum[i][3] = 0.f;
+                    float sum[4][4];   // of each chunk; a group of four chunks takes two
 #pragma unroll
                     for (int e = 0; e < 4; e++) {
                         const int gi = j * kGroups + e / kEach;
@@ -443,49 +441,72 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                         const __half2 none = half2_of(0);
                         expand_f16<false>(w[e >> 1][2 * (e & 1)], low[0], high[0], none, a[0]);
                         expand_f16<false>(w[e >> 1][2 * (e & 1) + 1], low[1], high[1], none, a[1]);
-#pragma unroll
-                        for (int k = 0; k < PARTS; k++) {
-                            if (k > 0 && planes == 1) break;
-                            mma_f16_16x8x16(sum[e], a[0][0], a[1][0], a[0][1], a[1][1], x[k][e].x, x[k][e].y);
-                            mma_f16_16x8x16(sum[e], a[0][2], a[1][2], a[0][3], a[1][3], x[k][e].z, x[k][e].w);
+                        const int at = kEach == 4 ? e & 1 : e;
+                        const uint4 x = *reinterpret_cast<const uint4 *>(xc + e * 64);
+                        if (at == e) mma_f16_begin(sum[at], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                        else mma_f16_16x8x16(sum[at], a[0][0], a[1][0], a[0][1], a[1][1], x.x, x.y);
+                        mma_f16_16x8x16(sum[at], a[0][2], a[1][2], a[0][3], a[1][3], x.z, x.w);
+                        if (PARTS == 2 && planes == 2) {
+                            const uint4 rest = *reinterpret_cast<const uint4 *>(xc + plane + e * 64);
+                            mma_f16_16x8x16(sum[at], a[0][0], a[1][0], a[0][1], a[1][1], rest.x, rest.y);
+                            mma_f16_16x8x16(sum[at], a[0][2], a[1][2], a[0][3], a[1][3], rest.z, rest.w);
                         }
                     }
+                    float part[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
                     for (int i = 0; i < kGroups; i++) {
                         if (4 * j + i * kEach >= chunks) break;
-                        const int gi = j * kGroups + i;
+                        const int gi = j * kGroups + i, at = i * (kEach == 4 ? 1 : kEach);
                         const float d0 = f16_bits_to_float(ds[stage][row0][gi]);
                         const float d1 = f16_bits_to_float(ds[stage][row1][gi]);
+                        if (kEach > 1)
 #pragma unroll
-                        for (int e = i * kEach + 1; e < (i + 1) * kEach; e++)
-#pragma unroll
-                            for (int c2 = 0; c2 < 4; c2++) sum[i * kEach][c2] += sum[e][c2];
-                        total[0] = fmaf(d0, sum[i * kEach][0], total[0]);
-                        total[1] = fmaf(d0, sum[i * kEach][1], total[1]);
-                        total[2] = fmaf(d1, sum[i * kEach][2], total[2]);
-                        total[3] = fmaf(d1, sum[i * kEach][3], total[3]);
+                            for (int c2 = 0; c2 < 4; c2++) sum[at][c2] += sum[at + 1][c2];
+                        part[0] = fmaf(d0, sum[at][0], part[0]), part[1] = fmaf(d0, sum[at][1], part[1]);
+                        part[2] = fmaf(d1, sum[at][2], part[2]), part[3] = fmaf(d1, sum[at][3], part[3]);
                     }
+                    const float2 f = *reinterpret_cast<const float2 *>(back + (2 * b + (j >> 1)) * kMvTokens + 2 * t);
+                    total[0] = fmaf(part[0], f.x, total[0]), total[1] = fmaf(part[1], f.y, total[1]);
+                    total[2] = fmaf(part[2], f.x, total[2]), total[3] = fmaf(part[3], f.y, total[3]);
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[stage]);
                 if (++stage == l.stages) stage = 0, phase ^= 1;
             }
+            const int64_t n0 = (int64_t)(u - piece * l.tiles) * kTileRows;
+            if (l.split == 1) {
+                // alone: out of the registers, nobody waits for anybody
+                const bool pack = packed(q);
+#pragma unroll
+                for (int i = 0; i < 2; i++) {
+                    if (PARTS == 2 && pack && i == 1) break;
+                    const int tk = PARTS == 2 && pack ? t : 2 * t + i;
+                    if (tk >= q.tokens) continue;
+                    const float v0 = PARTS == 2 && pack ? total[0] + total[1] : total[i];
+                    const float v1 = PARTS == 2 && pack ? total[2] + total[3] : total[2 + i];
+                    put(q, n0 + row0, tk, v0, v1);
+                }
+                continue;
+            }
             if (n > 0) finish(n - 1);
+            else asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
             // (a CTA that has sent has done with the unit before the last one: its sums' place may be written to)
             named_sync(1, 32 * kMvWarps);
             // rows g and g + 8, columns 2t and 2t + 1, to the CTA that finishes them
             const uint32_t to = send_to + (n & 1) * (uint32_t)(sizeof(sums) / 2);
-            store_in(to, total[0] * back[0], total[1] * back[1]);
-            store_in(to + 8 * kMvTokens * 4, total[2] * back[0], total[3] * back[1]);
+            store_in(to, total[0], total[1]);
+            store_in(to + 8 * kMvTokens * 4, total[2], total[3]);
             __syncwarp();
             if (lane < 2) arrive_in(tell[n & 1]);
             q_done = q;
-            n_done = (int64_t)(u - piece * l.tiles) * kTileRows;
+            n_done = n0;
         }
-        if (n > 0) finish(n - 1);
+        if (l.split > 1) {
+            if (n > 0) finish(n - 1);
+            else asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+        }
     }
-    __syncwarp();
-    if (l.split > 1) mv_cluster_sync();   // nobody's sums come after a CTA has gone
+    // (a CTA has all sums that are sent to it when its last unit is finished: it may go)
 }
 
 // How a call of given sizes is cut up.
@@ -495,7 +516,7 @@ struct MvPlan {
     size_t smem = 0;
 };
 
-// The split whose longest run of blocks is the shortest; of equal ones the smallest.  `fixed`: static shared memory.
+// The split whose longest run is the shortest; of equal ones the smallest.  `fixed`: static shared memory.
 static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces, int K, int parts, size_t fixed, int sms) {
     const int blocks = (K + kMvBlock - 1) / kMvBlock;
     MvPlan best;
@@ -505,14 +526,14 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
         l.blocks = (blocks + split - 1) / split;
         l.split = split, l.tiles = tiles;
         // Tokens: eight, or as many as their parts' slices fit beside two stages.
-        const size_t pitch = 2 * (size_t)l.blocks * kMvBlock + 64;
+        const size_t pitch = 2 * (size_t)l.blocks * kMvBlock + 64, scales = 2 * (size_t)l.blocks * kMvTokens * 4;
         l.tokens = (int)std::min<int64_t>(T, kMvTokens);
-        const size_t most = kMvShared - fixed - 2 * kMvStage;
+        const size_t most = kMvShared - fixed - 2 * kMvStage - scales;
         if (parts * l.tokens * pitch > most && split < kMvMaxSplit) continue;
         while (parts * l.tokens * pitch > most && l.tokens > 1) l.tokens--;
         // Three stages, or two where two CTAs fit an SM then (or three do not fit at all).
         l.stages = 3;
-        size_t smem = l.stages * kMvStage + parts * l.tokens * pitch;
+        size_t smem = l.stages * kMvStage + scales + parts * l.tokens * pitch;
         if (smem + fixed > kMvShared || (smem + fixed > kMvShared / 2 && smem + fixed - kMvStage <= kMvShared / 2))
             l.stages = 2, smem -= kMvStage;
         int per_sm;
@@ -533,7 +554,10 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
         if (held < 1) continue;
         const int64_t units = (pieces ? pieces : (T + l.tokens - 1) / l.tokens) * tiles;
         const int64_t clusters = std::min<int64_t>(units, held);
-        const int64_t time = (units + clusters - 1) / clusters * l.blocks;
+        // in fifths of a block's time for one CTA on an SM: two take 10 for both, one 7; a unit takes 2 by itself, 6 with
+        // sums that go through the cluster
+        const int64_t time = (units + clusters - 1) / clusters *
+                             (l.blocks * (clusters * split > sms ? 10 : 7) + (split > 1 ? 6 : 2));
         if (!best.clusters || time < best_time) best.l = l, best.clusters = clusters, best.smem = smem, best_time = time;
     }
     return best;
