@@ -6,10 +6,10 @@
 // bf16 x has all its bits and an fp32 one takes two parts (22 bits).  The scale d acts
 // on a group's sum in binary32: a fused multiply-add per group, row and token.
 //
-// Work: units of 128 rows (of a token piece), each split along K over a cluster of up to eight CTAs; a cluster
+// Work: units of 256 rows (of a token piece), each split along K over a cluster of up to eight CTAs; a cluster
 // takes an equal run of units, so x is laid out once (experts: once per piece) and weights keep coming across the units' borders.
-// One warp copies blocks of 128 rows x 512 columns (32 KB, tensor copies, with their scales and zeros) into a
-// ring; the first ones start before the previous kernel in the stream has ended.  Eight warps take 16 rows
+// One CTA per SM.  One warp copies blocks of 256 rows x 256 columns (32 KB, tensor copies, with their scales and zeros)
+// into a ring; the first ones start before the previous kernel in the stream has ended.  16 warps take 16 rows
 // each (experts' up products: 8 gate and the same 8 up rows): ldmatrix hands a lane whole words of eight
 // consecutive columns of its row, which are four operand registers after logic operations that put the codes
 // under the exponent of 1024 and a subtraction of 1024 + z (the upper codes of a byte: times 1/16, less 64 + z).  The eight
@@ -30,16 +30,16 @@
 
 namespace lb {
 
-constexpr int kMvRows = 128;                     // of a CTA
-constexpr int kMvBlock = 512;                    // columns of a ring stage
+constexpr int kMvRows = 256;                     // of a unit
+constexpr int kMvBlock = 256;                    // columns of a ring stage
 constexpr int kMvBox = kMvRows * 64;             // bytes of a copy: 128 columns
 constexpr int kMvStage = kMvRows * kMvBlock / 2;
-constexpr int kMvWarps = 8;
+constexpr int kMvWarps = 16;
 constexpr int kMvThreads = 32 * (kMvWarps + 1);
 constexpr int kMvTokens = 8;
 constexpr int kMvMaxSplit = 8;
-constexpr int kMvMaxStages = 3;
-constexpr size_t kMvShared = 226 * 1024;         // shared memory of an SM's CTAs, static and dynamic
+constexpr int kMvMaxStages = 5;
+constexpr size_t kMvShared = 226 * 1024;         // shared memory of a CTA, static and dynamic
 
 struct MvLaunch {
     int blocks;    // blocks of K of a CTA
@@ -104,7 +104,7 @@ __device__ __forceinline__ void store_y(__nv_bfloat16 *p, float v) { *p = __floa
 
 // T: the type of x (dense, up; h is fp32) and of a dense y; PARTS: fp16 parts of an x.
 template <Q4Use USE, typename T, int PARTS, int GROUP, bool ZEROS>
-__global__ void __launch_bounds__(kMvThreads, 2)
+__global__ void __launch_bounds__(kMvThreads, 1)
     q4_gemv_kernel(const __grid_constant__ CUtensorMap map, const __grid_constant__ Q4Params p,
                    const __grid_constant__ MvLaunch l) {
     using X = typename std::conditional<USE == kQ4Down, float, T>::type;
@@ -113,8 +113,8 @@ __global__ void __launch_bounds__(kMvThreads, 2)
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ uint64_t full[kMvMaxStages], empty[kMvMaxStages], sums_full[2];
     __shared__ __align__(16) uint16_t ds[kMvMaxStages][kMvRows][kPer];
-    __shared__ __align__(16) uint8_t zs[ZEROS ? kMvMaxStages : 1][kMvRows][kPer];
-    __shared__ __align__(16) float sums[2][8][16][kMvTokens];    // [rank, own warp][row][column]
+    __shared__ __align__(16) uint8_t zs[ZEROS ? kMvMaxStages : 1][kMvRows][kPer < 4 ? 4 : kPer];
+    __shared__ __align__(16) float sums[2][kMvWarps][16][kMvTokens];   // [rank, own warp][row][column]
     __shared__ int row_of[2][kMvTokens];
     __shared__ uint16_t s_first[kExperts];                       // pieces before an expert's
     __shared__ int s_part[kMvThreads / 32];
@@ -125,14 +125,14 @@ __global__ void __launch_bounds__(kMvThreads, 2)
     const int x_pitch = 2 * slice + 64;
     uint8_t *ring = smem;
     float *back = reinterpret_cast<float *>(ring + l.stages * kMvStage);   // takes scaling back: [256 columns][operand column]
-    uint8_t *xs = reinterpret_cast<uint8_t *>(back + 2 * l.blocks * kMvTokens);
+    uint8_t *xs = reinterpret_cast<uint8_t *>(back + l.blocks * kMvTokens);
 
     pdl_launch_dependents();
     if (tid == 0) {
         // a stage is full when the copies of codes and the 32 lanes' copies of scales have landed
         for (int i = 0; i < kMvMaxStages; i++) mbar_init(&full[i], 33), mbar_init(&empty[i], kMvWarps);
-        // sums of 16 groups of 8 rows come to a CTA, whatever the split
-        mbar_init(&sums_full[0], 16), mbar_init(&sums_full[1], 16);
+        // sums of 32 groups of 8 rows come to a CTA, whatever the split
+        mbar_init(&sums_full[0], kMvRows / 8), mbar_init(&sums_full[1], kMvRows / 8);
         fence_mbar_init();
     }
     // Pieces of at most l.tokens tokens (of one expert).
@@ -237,7 +237,8 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                     }
                 }
                 __syncwarp();
-                // (a row's entries reach to a multiple of eight, a block's may be four)
+                // (a row's entries reach to a multiple of eight; copies have four bytes at least, so where a block has two
+                // zeros, the next or last block's come along)
                 const int first = k0 / GROUP + b * kPer;
 #pragma unroll
                 for (int j = 0; j < kMvRows / 32; j++) {
@@ -245,17 +246,10 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                     const int64_t row = r < kMvRows / 2 ? matrix + n0 + r : upper + r - kMvRows / 2;
                     if (row >= last) continue;   // the products of rows behind the matrix go nowhere
                     const int64_t from = row * p.pitch + first;
-                    if constexpr (kPer == 4) {
-                        copy_async(smem_u32(&ds[stage][r][0]), p.scales + from, 8);
-                        if (ZEROS) copy_async(smem_u32(&zs[ZEROS ? stage : 0][r][0]), p.zeros + from, 4);
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < kPer; e += 8) {
-                            if (first + e >= p.pitch) break;
-                            copy_async(smem_u32(&ds[stage][r][e]), p.scales + from + e, 16);
-                            if (ZEROS) copy_async(smem_u32(&zs[ZEROS ? stage : 0][r][e]), p.zeros + from + e, 8);
-                        }
-                    }
+                    copy_async(smem_u32(&ds[stage][r][0]), p.scales + from, 2 * kPer);
+                    if (ZEROS)
+                        copy_async(smem_u32(&zs[ZEROS ? stage : 0][r][0]), p.zeros + (kPer == 2 ? from & ~3 : from),
+                                   kPer < 4 ? 4 : kPer);
                 }
                 copies_arrive(bar);
                 if (++stage == l.stages) stage = 0, phase ^= 1;
@@ -276,8 +270,8 @@ __global__ void __launch_bounds__(kMvThreads, 2)
         if (USE == kQ4Dense) pdl_wait();
         const int g = lane >> 2, t = lane & 3;
         // the row this lane points ldmatrix at, and the two rows of its sums, in the tile
-        const int row = USE == kQ4Up ? warp * 8 + (lane & 7) + (lane & 8) * 8 : warp * 16 + (lane & 15);
-        const int row0 = USE == kQ4Up ? warp * 8 + g : warp * 16 + g, row1 = USE == kQ4Up ? row0 + 64 : row0 + 8;
+        const int row = USE == kQ4Up ? warp * 8 + (lane & 7) + (lane & 8) * (kMvRows / 16) : warp * 16 + (lane & 15);
+        const int row0 = USE == kQ4Up ? warp * 8 + g : warp * 16 + g, row1 = USE == kQ4Up ? row0 + kMvRows / 2 : row0 + 8;
         const uint32_t at_row = smem_u32(ring) + row * 64, turn = (row >> 1) & 3;
         const int own = kMvWarps / l.split;              // warps whose rows a CTA finishes
         const uint32_t owner = warp / own;
@@ -326,7 +320,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
             }
             const int parts = packed(q_done) ? PARTS : 1;
             constexpr int per_warp = USE == kQ4Up ? 8 : 16;
-            const int shift = (USE == kQ4Up ? 6 : 7) - (31 - __clz(l.split));   // rows: a power of two
+            const int shift = (USE == kQ4Up ? 7 : 8) - (31 - __clz(l.split));   // rows: a power of two
             for (int i = tid; i < q_done.tokens << shift; i += 32 * kMvWarps) {
                 const int tk = i >> shift, r = i & ((1 << shift) - 1), w = r / per_warp, rr = r % per_warp;
                 const int64_t row_n = n_done + (rank * own + w) * per_warp + rr;
@@ -352,19 +346,19 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                 named_sync(1, 32 * kMvWarps);
                 const bool pack = packed(q);
                 cols = pack ? q.tokens * PARTS : q.tokens, planes = pack ? 1 : PARTS;
-                // 64 threads take a block of a token, eight columns each, four tokens at a time; a warp's 256 columns
-                // are scaled so that the largest comes to lie in [2^14, 2^15).  Four blocks are asked for together.
-                const int each = max(blocks, 0), all = (q.tokens + 3) / 4 * each;
-                for (int c0 = 0; c0 < all; c0 += 4) {
+                // A warp takes a block of a token, eight columns a lane, scaled so that the largest comes to lie in [2^14,
+                // 2^15).  Four blocks are asked for together.
+                const int each = max(blocks, 0), all = q.tokens * each;
+                for (int c0 = warp; c0 < all; c0 += 4 * kMvWarps) {
                     float v[4][8];
                     bool in[4];
                     int tok[4], blk[4];
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        const int c2 = c0 + k, i = c2 / each;
-                        blk[k] = c2 - i * each, tok[k] = 4 * i + (tid >> 6);
-                        const int at = blk[k] * kMvBlock + (tid & 63) * 8;
-                        in[k] = c2 < all && tok[k] < q.tokens && at < columns;
+                        const int c2 = c0 + k * kMvWarps;
+                        tok[k] = c2 / each, blk[k] = c2 - tok[k] * each;
+                        const int at = blk[k] * kMvBlock + lane * 8;
+                        in[k] = c2 < all && at < columns;
                         int64_t from = q.t0 + tok[k];
                         if (USE != kQ4Dense) {
                             const int pair = in[k] ? row_of[slot][tok[k]] : -1;
@@ -375,7 +369,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                     }
 #pragma unroll
                     for (int k = 0; k < 4; k++) {
-                        if (c0 + k >= all || tok[k] >= q.tokens) break;
+                        if (c0 + k * kMvWarps >= all) break;
                         float m = 0.f;
 #pragma unroll
                         for (int j = 0; j < 8; j++) {
@@ -396,10 +390,10 @@ __global__ void __launch_bounds__(kMvThreads, 2)
 #pragma unroll
                         for (int part = 0; part < PARTS; part++) {
                             const int to = pack ? tok[k] * PARTS + part : part * q.tokens + tok[k];
-                            *reinterpret_cast<uint4 *>(xs + to * x_pitch + blk[k] * (2 * kMvBlock) + 16 * (tid & 63)) =
+                            *reinterpret_cast<uint4 *>(xs + to * x_pitch + blk[k] * (2 * kMvBlock) + 16 * lane) =
                                 make_uint4(w[part][0], w[part][1], w[part][2], w[part][3]);
                             const int col = pack ? to : tok[k];
-                            if (lane == 0) back[(blk[k] * 2 + ((tid >> 5) & 1)) * kMvTokens + col] = __uint_as_float((254u - e) << 23);
+                            if (lane == 0) back[blk[k] * kMvTokens + col] = __uint_as_float((254u - e) << 23);
                         }
                     }
                 }
@@ -415,8 +409,9 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                     break;
                 }
                 const int chunks = min(kMvBlock, columns - b * kMvBlock) / 32;   // of 32 columns (K is a multiple)
+                const int z_at = kPer == 2 ? (k0 / GROUP + b * kPer) & 2 : 0;
                 // 128 columns at a time; where K ends inside, x is zero and a group behind K is left out
-#pragma unroll 2
+#pragma unroll
                 for (int j = 0; j < kMvBlock / 128; j++) {
                     if (4 * j >= chunks) break;
                     uint32_t w[2][4];   // the lane's two rows of chunks 0 and 1, then of 2 and 3
@@ -433,7 +428,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                         __half2 low[2], high[2];
 #pragma unroll
                         for (int r = 0; r < 2; r++) {
-                            const uint32_t z = ZEROS ? zs[ZEROS ? stage : 0][r ? row1 : row0][gi] : 8u;
+                            const uint32_t z = ZEROS ? zs[ZEROS ? stage : 0][r ? row1 : row0][gi + z_at] : 8u;
                             low[r] = half2_of(0x64006400u + z * 0x10001u);
                             high[r] = half2_of(0xD400D400u + z * 0x00100010u);
                         }
@@ -465,7 +460,7 @@ __global__ void __launch_bounds__(kMvThreads, 2)
                         part[0] = fmaf(d0, sum[at][0], part[0]), part[1] = fmaf(d0, sum[at][1], part[1]);
                         part[2] = fmaf(d1, sum[at][2], part[2]), part[3] = fmaf(d1, sum[at][3], part[3]);
                     }
-                    const float2 f = *reinterpret_cast<const float2 *>(back + (2 * b + (j >> 1)) * kMvTokens + 2 * t);
+                    const float2 f = *reinterpret_cast<const float2 *>(back + b * kMvTokens + 2 * t);
                     total[0] = fmaf(part[0], f.x, total[0]), total[1] = fmaf(part[1], f.y, total[1]);
                     total[2] = fmaf(part[2], f.x, total[2]), total[3] = fmaf(part[3], f.y, total[3]);
                 }
@@ -526,16 +521,14 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
         l.blocks = (blocks + split - 1) / split;
         l.split = split, l.tiles = tiles;
         // Tokens: eight, or as many as their parts' slices fit beside two stages.
-        const size_t pitch = 2 * (size_t)l.blocks * kMvBlock + 64, scales = 2 * (size_t)l.blocks * kMvTokens * 4;
+        const size_t pitch = 2 * (size_t)l.blocks * kMvBlock + 64, scales = (size_t)l.blocks * kMvTokens * 4;
         l.tokens = (int)std::min<int64_t>(T, kMvTokens);
         const size_t most = kMvShared - fixed - 2 * kMvStage - scales;
         if (parts * l.tokens * pitch > most && split < kMvMaxSplit) continue;
         while (parts * l.tokens * pitch > most && l.tokens > 1) l.tokens--;
-        // Three stages, or two where two CTAs fit an SM then (or three do not fit at all).
-        l.stages = 3;
-        size_t smem = l.stages * kMvStage + scales + parts * l.tokens * pitch;
-        if (smem + fixed > kMvShared || (smem + fixed > kMvShared / 2 && smem + fixed - kMvStage <= kMvShared / 2))
-            l.stages = 2, smem -= kMvStage;
+        // As many stages as fit.
+        size_t smem = 2 * kMvStage + scales + parts * l.tokens * pitch;
+        for (l.stages = 2; l.stages < kMvMaxStages && smem + kMvStage + fixed <= kMvShared; l.stages++) smem += kMvStage;
         int per_sm;
         if (prepare_kernel(kernel, kMvThreads, smem, &per_sm)) continue;
         int held = sms * per_sm;
@@ -554,10 +547,8 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
         if (held < 1) continue;
         const int64_t units = (pieces ? pieces : (T + l.tokens - 1) / l.tokens) * tiles;
         const int64_t clusters = std::min<int64_t>(units, held);
-        // in fifths of a block's time for one CTA on an SM: two take 10 for both, one 7; a unit takes 2 by itself, 6 with
-        // sums that go through the cluster
-        const int64_t time = (units + clusters - 1) / clusters *
-                             (l.blocks * (clusters * split > sms ? 10 : 7) + (split > 1 ? 6 : 2));
+        // in blocks: a unit takes one by itself, two with sums that go through the cluster
+        const int64_t time = (units + clusters - 1) / clusters * (l.blocks + (split > 1 ? 2 : 1));
         if (!best.clusters || time < best_time) best.l = l, best.clusters = clusters, best.smem = smem, best_time = time;
     }
     return best;
