@@ -14,8 +14,9 @@
 // More tokens take a second kernel: the first leaves each CTA's counts per expert, the second adds
 // up the counts of the CTAs before its own and places its tokens by the same masks.
 //
-// What bounds it: latency.  One token is the launch, one load and k rounds of two warp reductions;
-// many are the rounds' latency over the warps an SM holds.
+// What bounds it: instructions.  A token of 256 experts takes about 700 of a warp.  Each lane keeps its best two keys, so a
+// round of the selection is two warp reductions and a few operations of the lane that loses its best; all of its
+// keys are looked through again only when that happens to it a second time.
 #include "lb_kv4.cuh"
 
 #include <cfloat>
@@ -25,6 +26,7 @@ namespace lb {
 constexpr int kRouteTile = 64;         // tokens whose marks fit a mask
 constexpr int kRouteMaxCtas = 256;     // of the first kernel: bounds what the second adds up
 constexpr int kPlaceThreads = 512;
+constexpr int kPlaceSums = 4096;        // partial counts: as many as fit
 
 struct RouteParams {
     const void *logits;
@@ -35,7 +37,10 @@ struct RouteParams {
     float *weights;
     uint16_t *counts;  // [CTA][pitch]
     int T, E, k, sigmoid, groups, keep, best, renormalize, tile, pitch;
+    int per, inverse;  // experts of a group, and 2^20 / per
     float scale;
+    // e / per: inverse is at most 1 (of 2^20 / per) too large, e below 2^10, so the quotient's error is below 1 / per
+    __device__ __forceinline__ int group_of(int e) const { return min((uint32_t)(e * inverse) >> 20, 31u); }
 };
 
 __device__ __forceinline__ float route_load(const float *p) { return *p; }
@@ -72,16 +77,13 @@ __device__ __forceinline__ void warp_best(double &v, int &i) {
     }
 }
 
-__device__ __forceinline__ float exp_of(float v) { return expf(v); }
-__device__ __forceinline__ double exp_of(double v) { return exp(v); }
-// x - m and what its rounding left out.
+// exp(x - m), with what the difference's rounding left out.
 __device__ __forceinline__ float exp_difference(float x, float m) {
     const float t = x - m, back = x - t;
     const float rest = (x - (t + back)) + (back - m);
     const float s = expf(t);
     return t < -100.f ? s : fmaf(s, rest, s);  // (infinite differences leave no rest)
 }
-__device__ __forceinline__ double exp_difference(double x, double m) { return exp(x - m); }
 
 struct Chosen {
     int id;        // lane j's expert, -1 without
@@ -89,18 +91,18 @@ struct Chosen {
     float sum;     // softmax: sum of exp(x - max)
 };
 
-// The k experts of a token, one per lane.  x: the lane's logits (-inf: not to be chosen), m their
-// warp's maximum.
-template <int EL, typename R>
-__device__ __forceinline__ Chosen choose(const RouteParams &p, const float (&x)[EL], float m, R *keys,
-                                         int lane) {
+// The k experts of a token, one per lane.  x: the lane's logits (-inf: not to be chosen), b: their biases, m: the warp's
+// largest logit.
+template <int EL>
+__device__ __forceinline__ Chosen choose(const RouteParams &p, const float (&x)[EL], const float (&b)[EL], float m,
+                                         float *keys, int lane) {
     const bool plain = !p.bias && p.best == 1;
-    constexpr bool kFloat = sizeof(R) == 4;
+    const float none = -INFINITY;
     Chosen c{-1, false, 0.f};
-    R key[EL], tol = 0;
+    float key[EL], tol = 0.f;
     if (plain) {
 #pragma unroll
-        for (int i = 0; i < EL; i++) key[i] = (R)x[i] + (R)0;  // -0 and 0 are the same number
+        for (int i = 0; i < EL; i++) key[i] = x[i] + 0.f;  // -0 and 0 are the same number
         if (!p.sigmoid && !p.renormalize) {
             float s = 0.f;
 #pragma unroll
@@ -108,96 +110,188 @@ __device__ __forceinline__ Chosen choose(const RouteParams &p, const float (&x)[
             c.sum = warp_add(s);
         }
     } else {
-        R bias[EL], s = 0;
-        float most = 0.f;
+        float s = 0.f, most = 0.f;
 #pragma unroll
         for (int i = 0; i < EL; i++) {
             const bool in = x[i] > -INFINITY;
-            bias[i] = in && p.bias ? (R)p.bias[lane + 32 * i] : (R)0;
-            most = fmaxf(most, fabsf((float)bias[i]));
-            key[i] = !in ? (R)0
-                     : p.sigmoid ? (R)1 / ((R)1 + exp_of(-(R)x[i]))
-                                 : exp_difference((R)x[i], (R)m);
-            s += key[i];
+            most = fmaxf(most, in ? fabsf(b[i]) : 0.f);
+            if (p.sigmoid) key[i] = __fdividef(1.f, 1.f + __expf(-x[i]));
+            else key[i] = in ? exp_difference(x[i], m) : 0.f, s += key[i];
         }
+        float by = 1.f;
         if (!p.sigmoid) {
             s = warp_add(s);
-            c.sum = (float)s;
+            c.sum = s;
+            by = __fdividef(1.f, s);
         }
-        const R one = p.sigmoid ? (R)1 : s;
 #pragma unroll
-        for (int i = 0; i < EL; i++)
-            key[i] = x[i] > -INFINITY ? key[i] / one + bias[i] + (R)0 : -(R)INFINITY;
-        // exp to 2 units in the last place, a sum, a quotient and a sum: well below 2^-21 of the largest score
-        if (kFloat)
-            tol = (p.sigmoid ? 0x1p-21f : 0x1p-20f / (float)one) + 0x1p-22f * warp_max(most) + 1e-37f;
+        for (int i = 0; i < EL; i++) key[i] = x[i] > -INFINITY ? key[i] * by + b[i] + 0.f : none;
+        // A sigmoid: exp to 2 + 1.2 |x| units of its last place changes it by s (1 - s) times that, a unit at most; a
+        // sum, a reciprocal and a sum: below 2^-21.  A softmax: exp to two units, a sum of up to 1024 scores in 32
+        // chains, a reciprocal, a product and a sum: below 2^-18 of the largest score.
+        tol = (p.sigmoid ? 0x1p-21f : 0x1p-18f * by) + 0x1p-22f * warp_max(most) + 1e-37f;
     }
     if (p.groups > 1) {
         // lanes [g * part, (g + 1) * part) look through group g
-        const int per = p.E / p.groups, part = 32 >> (32 - __clz(p.groups - 1));
+        const int per = p.per, part = 32 >> (32 - __clz(p.groups - 1));
         const int g = lane / part;
 #pragma unroll
         for (int i = 0; i < EL; i++)
             if (lane + 32 * i < p.E) keys[lane + 32 * i] = key[i];
         __syncwarp();
-        R first = -(R)INFINITY, second = -(R)INFINITY;
+        float first = none, second = none;
         if (g < p.groups)
+#pragma unroll 4
             for (int e = lane % part; e < per; e += part) {
-                const R v = keys[g * per + e];
-                if (v > first) second = first, first = v;
-                else if (v > second) second = v;
+                const float v = keys[g * per + e], low = first < v ? first : v;
+                first = first < v ? v : first;
+                second = second < low ? low : second;
             }
         __syncwarp();
         for (int o = 1; o < part; o <<= 1) {
-            const R a = __shfl_xor_sync(0xffffffffu, first, o), b = __shfl_xor_sync(0xffffffffu, second, o);
-            const R low = first < a ? first : a;
+            const float a = __shfl_xor_sync(0xffffffffu, first, o), d = __shfl_xor_sync(0xffffffffu, second, o);
+            const float low = first < a ? first : a;
             first = first < a ? a : first;
-            second = second < b ? b : second;
+            second = second < d ? d : second;
             second = second < low ? low : second;
         }
-        R value = p.best == 2 && second > -(R)INFINITY ? first + second + (R)0 : first;
+        const float value = p.best == 2 && second > none ? first + second + 0.f : first;
         uint32_t kept = 0;
-        R last = 0;
+        float last = 0.f;
         for (int j = 0; j <= p.keep; j++) {
-            R v = g < p.groups && !(kept >> g & 1) ? value : -(R)INFINITY;
+            float v = g < p.groups && !(kept >> g & 1) ? value : none;
             int at = g;
             warp_best(v, at);
-            if (v == -(R)INFINITY) break;
+            if (v == none) break;
             if (j == p.keep) {
-                if (kFloat && !plain && last - v <= 4 * tol) c.close = true;
+                if (!plain && last - v <= 4 * tol) c.close = true;
                 break;
             }
             kept |= 1u << at;
             last = v;
         }
-#pragma unroll
-        for (int i = 0; i < EL; i++)
-            if (!(kept >> min((lane + 32 * i) / per, 31) & 1)) key[i] = -(R)INFINITY;
-    }
-    R last = 0;
-    for (int j = 0; j <= p.k; j++) {
-        R v = key[0];
+        // (a lane's experts lie 32 apart)
         int at = lane;
 #pragma unroll
-        for (int i = 1; i < EL; i++)
-            if (key[i] > v) v = key[i], at = lane + 32 * i;
-        if (j == p.k && (!kFloat || plain)) break;
+        for (int i = 0; i < EL; i++, at += 32)
+            if (!(kept >> p.group_of(at) & 1)) key[i] = none;
+    }
+    // the lane's best two of those not taken
+    uint32_t taken = 0;
+    float v1, v2;
+    int i1, i2;
+    auto look = [&]() {
+        v1 = v2 = none, i1 = i2 = lane;
+#pragma unroll
+        for (int i = 0; i < EL; i++) {
+            const float v = taken >> i & 1 ? none : key[i];
+            if (v > v1) v2 = v1, i2 = i1, v1 = v, i1 = lane + 32 * i;
+            else if (v > v2) v2 = v, i2 = lane + 32 * i;
+        }
+    };
+    look();
+    bool second = true;   // v2 is known
+    float last = 0.f;
+#pragma unroll 1
+    for (int j = 0; j <= p.k; j++) {
+        if (j == p.k && plain) break;
+        float v = v1;
+        int at = i1;
         warp_best(v, at);
-        if (v == -(R)INFINITY) break;
-        if (kFloat && !plain && j && last - v <= 2 * tol) c.close = true;
+        if (v == none) break;
+        if (!plain && j && last - v <= 2 * tol) c.close = true;
         if (j == p.k) break;
         last = v;
         if (lane == j) c.id = at;
-#pragma unroll
-        for (int i = 0; i < EL; i++)
-            if (at == lane + 32 * i) key[i] = -(R)INFINITY;
+        bool again = false;
+        if (at == i1 && v1 > none) {
+            taken |= 1u << (at >> 5);
+            again = !second;
+            v1 = v2, i1 = i2, second = false;
+        }
+        if (__any_sync(0xffffffffu, again)) {
+            if (again) look(), second = true;
+            __syncwarp();
+        }
     }
     return c;
 }
-template <int EL>
-__device__ __noinline__ Chosen choose_again(const RouteParams &p, const float (&x)[EL], float m,
-                                            double *keys, int lane) {
-    return choose<EL, double>(p, x, m, keys, lane);
+// The same with binary64 keys, in shared memory: few tokens come here, but a kernel lasts as long as its last one, so four
+// keys' chains of operations run side by side (one at a time: 40 us for a token of 256).
+template <typename T>
+__device__ __noinline__ int choose_again(const RouteParams &p, const T *row, float m, double *keys, int lane) {
+    const double none = -(double)INFINITY;
+    double s = 0;
+#pragma unroll 1
+    for (int e0 = lane; e0 < p.E; e0 += 128) {
+        float x[4], b[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int e = e0 + 32 * i;
+            x[i] = e < p.E ? fminf(route_load(row + e), FLT_MAX) : 0.f;
+            b[i] = e < p.E && p.bias ? p.bias[e] : 0.f;
+            if (e < p.E && isnan(route_load(row + e))) x[i] = -INFINITY;
+        }
+        double v[4];
+#pragma unroll
+        for (int i = 0; i < 4; i++) v[i] = exp(p.sigmoid ? -(double)x[i] : (double)x[i] - m);
+#pragma unroll
+        for (int i = 0; i < 4; i++) {
+            const int e = e0 + 32 * i;
+            const bool in = e < p.E && x[i] > -INFINITY && b[i] > -INFINITY;
+            if (p.sigmoid) v[i] = 1 / (1 + v[i]) + b[i] + 0.0;
+            else if (in) s += v[i];
+            if (e < p.E) keys[e] = in ? v[i] : none;
+        }
+    }
+    if (!p.sigmoid) {
+        s = warp_add(s);
+#pragma unroll 4
+        for (int e = lane; e < p.E; e += 32)
+            if (keys[e] > none) keys[e] = keys[e] / s + (p.bias ? p.bias[e] : 0.f) + 0.0;
+    }
+    __syncwarp();
+    const int per = p.per;
+    if (p.groups > 1) {   // a lane per group
+        uint32_t kept = 0;
+        double first = none, second = none;
+#pragma unroll 1
+        for (int e = 0; e < per && lane < p.groups; e++) {
+            const double v = keys[lane * per + e];
+            if (v > first) second = first, first = v;
+            else if (v > second) second = v;
+        }
+        double value = p.best == 2 && second > none ? first + second : first;
+#pragma unroll 1
+        for (int j = 0; j < p.keep; j++) {
+            double v = value;
+            int at = lane;
+            warp_best(v, at);
+            if (v == none) break;
+            kept |= 1u << at;
+            if (lane == at) value = none;
+        }
+        for (int e = lane; e < p.E; e += 32)
+            if (!(kept >> p.group_of(e) & 1)) keys[e] = none;
+        __syncwarp();
+    }
+    int id = -1;
+#pragma unroll 1
+    for (int j = 0; j < p.k; j++) {
+        double v = none;
+        int at = lane;
+#pragma unroll 4
+        for (int e = lane; e < p.E; e += 32) {
+            const double w = keys[e];
+            if (w > v) v = w, at = e;
+        }
+        warp_best(v, at);
+        if (v == none) break;
+        if (lane == j) id = at;
+        if (lane == (at & 31)) keys[at] = none;
+        __syncwarp();
+    }
+    return id;
 }
 
 // Weight of the expert whose logit is x, one per lane (in: the lane has one).
@@ -264,7 +358,7 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const __grid_constant__ 
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     uint64_t *mark = route_smem;
     int32_t *count = reinterpret_cast<int32_t *>(route_smem);
-    double *keys = reinterpret_cast<double *>(route_smem + p.E) + (p.groups > 1 ? warp * p.E : 0);
+    double *keys = reinterpret_cast<double *>(route_smem + p.E) + (p.bias || p.best == 2 || p.groups > 1 ? warp * p.E : 0);
     pdl_launch_dependents();
     for (int e = tid; e < p.E; e += THREADS) mark[e] = 0;
     __syncthreads();
@@ -279,18 +373,21 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const __grid_constant__ 
             float w = 0.f;
             if (t < live) {
                 const T *row = static_cast<const T *>(p.logits) + t * p.stride;
-                float x[EL], m = -INFINITY;
+                float x[EL], b[EL], m = -INFINITY;
 #pragma unroll
                 for (int i = 0; i < EL; i++) {
                     const int e = lane + 32 * i;
-                    x[i] = e < p.E ? fminf(route_load(row + e), FLT_MAX) : -INFINITY;
-                    if (e < p.E && isnan(route_load(row + e))) x[i] = -INFINITY;
-                    if (p.bias && e < p.E && !(p.bias[e] > -INFINITY)) x[i] = -INFINITY;
+                    x[i] = e < p.E ? route_load(row + e) : -INFINITY;
+                    b[i] = p.bias && e < p.E ? p.bias[e] : 0.f;
+                }
+#pragma unroll
+                for (int i = 0; i < EL; i++) {
+                    x[i] = x[i] > -INFINITY && b[i] > -INFINITY ? fminf(x[i], FLT_MAX) : -INFINITY;   // (NaN is not)
                     m = fmaxf(m, x[i]);
                 }
                 m = warp_max(m);
-                Chosen c = choose<EL, float>(p, x, m, reinterpret_cast<float *>(keys), lane);
-                if (c.close) c.id = choose_again<EL>(p, x, m, keys, lane).id;
+                Chosen c = choose<EL>(p, x, b, m, reinterpret_cast<float *>(keys), lane);
+                if (c.close) c.id = choose_again(p, row, m, keys, lane);
                 id = c.id;
                 const float xj = id >= 0 ? fminf(route_load(row + id), FLT_MAX) : 0.f;
                 w = weight_of(p, xj, id >= 0, m, c.sum);
@@ -333,28 +430,40 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const __grid_constant__ 
 __global__ void __launch_bounds__(kPlaceThreads) place_kernel(const __grid_constant__ RouteParams p) {
     __shared__ int32_t before[LB_ROUTE_MAX_EXPERTS], start[LB_ROUTE_MAX_EXPERTS], part[kPlaceThreads / 32];
     __shared__ uint64_t mark[LB_ROUTE_MAX_EXPERTS];
+    __shared__ __align__(16) uint32_t sums[2][kPlaceSums];   // of all CTAs, of those before this one: [threads' share][expert]
     const int tid = threadIdx.x;
     pdl_launch_dependents();
-    for (int e = tid; e < LB_ROUTE_MAX_EXPERTS; e += kPlaceThreads) before[e] = start[e] = 0;
-    __syncthreads();
     pdl_wait();
-    // a thread adds up two experts' counts over every `parts`-th CTA
-    const int words = p.pitch / 2, parts = kPlaceThreads / words;
-    const uint32_t *counts = reinterpret_cast<const uint32_t *>(p.counts);
+    // a thread adds up eight experts' counts over every `parts`-th CTA
+    const int words = p.pitch / 8, parts = min(kPlaceThreads / words, kPlaceSums / p.pitch);
     const int w = tid % words, q = tid / words;
     if (q < parts) {
-        uint32_t all[2] = {0, 0}, mine[2] = {0, 0};
-#pragma unroll 8
+        uint32_t all[8] = {0, 0, 0, 0, 0, 0, 0, 0}, mine[8] = {0, 0, 0, 0, 0, 0, 0, 0};
+        const uint4 *counts = reinterpret_cast<const uint4 *>(p.counts) + w;
+#pragma unroll 4
         for (int c = q; c < (int)gridDim.x; c += parts) {
-            const uint32_t v = counts[c * words + w];
-            all[0] += v & 0xffff, all[1] += v >> 16;
-            if (c < (int)blockIdx.x) mine[0] += v & 0xffff, mine[1] += v >> 16;
+            const uint4 v = counts[c * words];
+            const uint32_t a[4] = {v.x, v.y, v.z, v.w};
+            const bool early = c < (int)blockIdx.x;
+#pragma unroll
+            for (int i = 0; i < 4; i++) {
+                all[2 * i] += a[i] & 0xffff, all[2 * i + 1] += a[i] >> 16;
+                if (early) mine[2 * i] += a[i] & 0xffff, mine[2 * i + 1] += a[i] >> 16;
+            }
         }
 #pragma unroll
         for (int i = 0; i < 2; i++) {
-            atomicAdd(start + 2 * w + i, (int)all[i]);
-            atomicAdd(before + 2 * w + i, (int)mine[i]);
+            const uint32_t *from = i ? mine : all;
+            uint4 *to = reinterpret_cast<uint4 *>(&sums[i][q * p.pitch + 8 * w]);
+            to[0] = make_uint4(from[0], from[1], from[2], from[3]);
+            to[1] = make_uint4(from[4], from[5], from[6], from[7]);
         }
+    }
+    __syncthreads();
+    for (int e = tid; e < p.E; e += kPlaceThreads) {
+        uint32_t all = 0, mine = 0;
+        for (int i = 0; i < parts; i++) all += sums[0][i * p.pitch + e], mine += sums[1][i * p.pitch + e];
+        start[e] = (int)all, before[e] = (int)mine;
     }
     __syncthreads();
     const int total = scan_experts<kPlaceThreads>(start, p.E, part);
@@ -391,8 +500,9 @@ static int route_tile(int64_t T) {
 
 template <typename T, int EL, int THREADS>
 static int launch_route(RouteParams p, cudaStream_t st) {
-    const size_t smem = (size_t)p.E * 8 * (1 + (p.groups > 1 ? THREADS / 32 : 0));
+    const size_t smem = (size_t)p.E * 8 * (1 + (p.groups > 1 || p.best == 2 || p.bias ? THREADS / 32 : 0));
     int per_sm;
+    if (THREADS > 256 && p.T <= 8) return launch_route<T, EL, 256>(p, st);   // (a warp per token does)
     if (p.T <= kRouteTile) {
         p.tile = kRouteTile;
         auto kernel = route_kernel<T, EL, THREADS, true>;
@@ -451,6 +561,7 @@ LB_EXPORT int lb_route(const void *logits, int type, int64_t stride, int64_t T, 
     p.counts = static_cast<uint16_t *>(workspace);
     p.T = (int)T, p.E = E, p.k = k, p.sigmoid = r.scoring == LB_ROUTE_SIGMOID;
     p.groups = r.groups, p.keep = r.keep_groups, p.best = r.group_best;
+    p.per = E / r.groups, p.inverse = (1 << 20) / p.per + 1;
     p.renormalize = r.renormalize != 0, p.scale = r.scale, p.pitch = (E + 7) / 8 * 8;
     cudaStream_t st = as_stream(stream);
     return type == LB_OUT_F32 ? dispatch_route<float>(p, st) : dispatch_route<__nv_bfloat16>(p, st);
