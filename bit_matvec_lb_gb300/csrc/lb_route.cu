@@ -67,14 +67,22 @@ __device__ __forceinline__ void warp_best(float &v, int &i) {
     v = __uint_as_float(m & 0x80000000u ? m & 0x7fffffffu : ~m);
     i = (int)__reduce_min_sync(0xffffffffu, u == m && v != -INFINITY ? (uint32_t)i : 0x7fffffffu);
 }
-__device__ __forceinline__ void warp_best(double &v, int &i) {
-    if (v == -INFINITY) i = 0x7fffffff;
-#pragma unroll
-    for (int o = 16; o; o >>= 1) {
-        const double w = __shfl_xor_sync(0xffffffffu, v, o);
-        const int j = __shfl_xor_sync(0xffffffffu, i, o);
-        if (w > v || (w == v && j < i)) v = w, i = j;
-    }
+// Binary64 numbers (none NaN or -0) as whole ones of the same order, 0 for none: the FP64 units take 64 times as long to
+// compare them.
+__device__ __forceinline__ uint64_t order_of(double v) {
+    const uint64_t b = (uint64_t)__double_as_longlong(v);
+    return b >> 63 ? ~b : b | 1ull << 63;
+}
+__device__ __forceinline__ double number_of(uint64_t u) {
+    return __longlong_as_double((long long)(u >> 63 ? u & ~(1ull << 63) : ~u));
+}
+// The largest of the lanes' and, of equal ones, the lowest index.
+__device__ __forceinline__ void warp_best(uint64_t &u, int &i) {
+    const uint32_t hi = __reduce_max_sync(0xffffffffu, (uint32_t)(u >> 32));
+    const uint32_t lo = __reduce_max_sync(0xffffffffu, (uint32_t)(u >> 32) == hi ? (uint32_t)u : 0u);
+    const uint64_t best = (uint64_t)hi << 32 | lo;
+    i = (int)__reduce_min_sync(0xffffffffu, u == best && u ? (uint32_t)i : 0x7fffffffu);
+    u = best;
 }
 
 // exp(x - m), with what the difference's rounding left out.
@@ -91,14 +99,49 @@ struct Chosen {
     float sum;     // softmax: sum of exp(x - max)
 };
 
+// Binary64 key of expert e.
+template <typename T>
+__device__ __forceinline__ double exact_key(const RouteParams &p, const T *row, int e, float m, double sum) {
+    const float x = fminf(route_load(row + e), FLT_MAX);
+    const double v = exp(p.sigmoid ? -(double)x : (double)x - m);
+    return (p.sigmoid ? 1 / (1 + v) : v / sum) + (p.bias ? p.bias[e] : 0.f) + 0.0;
+}
+// The first k of n <= 32 experts by their binary64 keys, a lane each.
+template <typename T>
+__device__ __noinline__ int order_again(const RouteParams &p, const T *row, float m, const int *list, int n, int lane) {
+    double sum = 0;
+    if (!p.sigmoid) {
+#pragma unroll 4
+        for (int e = lane; e < p.E; e += 32) {
+            const float x = route_load(row + e), b = p.bias ? p.bias[e] : 0.f;
+            if (x > -INFINITY && b > -INFINITY) sum += exp((double)fminf(x, FLT_MAX) - m);
+        }
+        sum = warp_add(sum);
+    }
+    const int e = list[lane < n ? lane : 0];
+    uint64_t key = lane < n ? order_of(exact_key(p, row, e, m, sum)) : 0;
+    int id = -1;
+#pragma unroll 1
+    for (int j = 0; j < p.k; j++) {
+        uint64_t v = key;
+        int at = e;
+        warp_best(v, at);
+        if (!v) break;
+        if (lane == j) id = at;
+        if (lane < n && e == at) key = 0;
+    }
+    return id;
+}
+
 // The k experts of a token, one per lane.  x: the lane's logits (-inf: not to be chosen), b: their biases, m: the warp's
 // largest logit.
-template <int EL>
-__device__ __forceinline__ Chosen choose(const RouteParams &p, const float (&x)[EL], const float (&b)[EL], float m,
+template <int EL, typename T>
+__device__ __forceinline__ Chosen choose(const RouteParams &p, const T *row, const float (&x)[EL], const float (&b)[EL], float m,
                                          float *keys, int lane) {
     const bool plain = !p.bias && p.best == 1;
     const float none = -INFINITY;
     Chosen c{-1, false, 0.f};
+    bool groups = false;   // two groups lie too close together
     float key[EL], tol = 0.f;
     if (plain) {
 #pragma unroll
@@ -164,7 +207,7 @@ __device__ __forceinline__ Chosen choose(const RouteParams &p, const float (&x)[
             warp_best(v, at);
             if (v == none) break;
             if (j == p.keep) {
-                if (!plain && last - v <= 4 * tol) c.close = true;
+                if (!plain && last - v <= 4 * tol) c.close = groups = true;
                 break;
             }
             kept |= 1u << at;
@@ -214,13 +257,29 @@ __device__ __forceinline__ Chosen choose(const RouteParams &p, const float (&x)[
             __syncwarp();
         }
     }
+    if (c.close && !groups) {
+        // Whatever lies below the last one's key by twice the error is not among the first k: only the others, mostly k
+        // and one more, are looked at again.
+        int *list = reinterpret_cast<int *>(keys), n = 0;
+        __syncwarp();
+#pragma unroll
+        for (int i = 0; i < EL; i++) {
+            const bool in = key[i] > none && key[i] >= last - 2 * tol;
+            const uint32_t all = __ballot_sync(0xffffffffu, in);
+            if (in) list[n + __popc(all & ((1u << lane) - 1))] = lane + 32 * i;
+            n += __popc(all);
+        }
+        __syncwarp();
+        if (n <= 32) c.id = order_again(p, row, m, list, n, lane), c.close = false;
+        __syncwarp();
+    }
     return c;
 }
 // The same with binary64 keys, in shared memory: few tokens come here, but a kernel lasts as long as its last one, so four
-// keys' chains of operations run side by side (one at a time: 40 us for a token of 256).
+// keys' chains of operations run side by side and are then compared as whole numbers (one at a time and as they
+// are: 40 us for a token of 256).
 template <typename T>
-__device__ __noinline__ int choose_again(const RouteParams &p, const T *row, float m, double *keys, int lane) {
-    const double none = -(double)INFINITY;
+__device__ __noinline__ int choose_again(const RouteParams &p, const T *row, float m, uint64_t *keys, int lane) {
     double s = 0;
 #pragma unroll 1
     for (int e0 = lane; e0 < p.E; e0 += 128) {
@@ -228,9 +287,9 @@ __device__ __noinline__ int choose_again(const RouteParams &p, const T *row, flo
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const int e = e0 + 32 * i;
-            x[i] = e < p.E ? fminf(route_load(row + e), FLT_MAX) : 0.f;
+            const float v = e < p.E ? route_load(row + e) : -INFINITY;
+            x[i] = v > -INFINITY ? fminf(v, FLT_MAX) : -INFINITY;   // (NaN is not)
             b[i] = e < p.E && p.bias ? p.bias[e] : 0.f;
-            if (e < p.E && isnan(route_load(row + e))) x[i] = -INFINITY;
         }
         double v[4];
 #pragma unroll
@@ -238,57 +297,57 @@ __device__ __noinline__ int choose_again(const RouteParams &p, const T *row, flo
 #pragma unroll
         for (int i = 0; i < 4; i++) {
             const int e = e0 + 32 * i;
-            const bool in = e < p.E && x[i] > -INFINITY && b[i] > -INFINITY;
+            const bool in = x[i] > -INFINITY && b[i] > -INFINITY;
             if (p.sigmoid) v[i] = 1 / (1 + v[i]) + b[i] + 0.0;
             else if (in) s += v[i];
-            if (e < p.E) keys[e] = in ? v[i] : none;
+            if (e < p.E) keys[e] = in ? order_of(v[i]) : 0;
         }
     }
     if (!p.sigmoid) {
         s = warp_add(s);
 #pragma unroll 4
         for (int e = lane; e < p.E; e += 32)
-            if (keys[e] > none) keys[e] = keys[e] / s + (p.bias ? p.bias[e] : 0.f) + 0.0;
+            if (keys[e]) keys[e] = order_of(number_of(keys[e]) / s + (p.bias ? p.bias[e] : 0.f) + 0.0);
     }
     __syncwarp();
-    const int per = p.per;
     if (p.groups > 1) {   // a lane per group
-        uint32_t kept = 0;
-        double first = none, second = none;
-#pragma unroll 1
-        for (int e = 0; e < per && lane < p.groups; e++) {
-            const double v = keys[lane * per + e];
-            if (v > first) second = first, first = v;
-            else if (v > second) second = v;
+        uint64_t first = 0, second = 0;
+#pragma unroll 4
+        for (int e = 0; e < p.per; e++) {
+            const uint64_t v = lane < p.groups ? keys[lane * p.per + e] : 0;
+            const uint64_t low = v < first ? v : first;
+            first = v < first ? first : v;
+            second = low < second ? second : low;
         }
-        double value = p.best == 2 && second > none ? first + second : first;
+        uint64_t value = p.best == 2 && second ? order_of(number_of(first) + number_of(second) + 0.0) : first;
+        uint32_t kept = 0;
 #pragma unroll 1
         for (int j = 0; j < p.keep; j++) {
-            double v = value;
+            uint64_t v = value;
             int at = lane;
             warp_best(v, at);
-            if (v == none) break;
+            if (!v) break;
             kept |= 1u << at;
-            if (lane == at) value = none;
+            if (lane == at) value = 0;
         }
         for (int e = lane; e < p.E; e += 32)
-            if (!(kept >> p.group_of(e) & 1)) keys[e] = none;
+            if (!(kept >> p.group_of(e) & 1)) keys[e] = 0;
         __syncwarp();
     }
     int id = -1;
 #pragma unroll 1
     for (int j = 0; j < p.k; j++) {
-        double v = none;
+        uint64_t v = 0;
         int at = lane;
 #pragma unroll 4
         for (int e = lane; e < p.E; e += 32) {
-            const double w = keys[e];
+            const uint64_t w = keys[e];
             if (w > v) v = w, at = e;
         }
         warp_best(v, at);
-        if (v == none) break;
+        if (!v) break;
         if (lane == j) id = at;
-        if (lane == (at & 31)) keys[at] = none;
+        if (lane == (at & 31)) keys[at] = 0;
         __syncwarp();
     }
     return id;
@@ -303,9 +362,11 @@ __device__ __forceinline__ float weight_of(const RouteParams &p, float x, bool i
     }
     // the largest chosen logit's power of e goes out of all of them, so their sum is never 0
     const float top = warp_max(in ? x : -INFINITY);
-    if (p.sigmoid) {
-        const float low = fminf(top, 0.f);
-        s = x < 0.f ? exp_difference(x, low) / (1.f + expf(x)) : 1.f / (1.f + expf(-x));
+    if (p.sigmoid && top > -40.f) {
+        const float e = expf(-fabsf(x));
+        s = (x < 0.f ? e : 1.f) / (1.f + e);
+    } else if (p.sigmoid) {
+        s = exp_difference(x, top);   // (1 + e^x is 1 in binary32)
     } else {
         s = exp_difference(x, top);
     }
@@ -385,9 +446,9 @@ __global__ void __launch_bounds__(THREADS) route_kernel(const __grid_constant__ 
                     x[i] = x[i] > -INFINITY && b[i] > -INFINITY ? fminf(x[i], FLT_MAX) : -INFINITY;   // (NaN is not)
                     m = fmaxf(m, x[i]);
                 }
-                m = warp_max(m);
-                Chosen c = choose<EL>(p, x, b, m, reinterpret_cast<float *>(keys), lane);
-                if (c.close) c.id = choose_again(p, row, m, keys, lane);
+                if (!p.sigmoid) m = warp_max(m);
+                Chosen c = choose<EL, T>(p, row, x, b, m, reinterpret_cast<float *>(keys), lane);
+                if (c.close) c.id = choose_again(p, row, m, reinterpret_cast<uint64_t *>(keys), lane);
                 id = c.id;
                 const float xj = id >= 0 ? fminf(route_load(row + id), FLT_MAX) : 0.f;
                 w = weight_of(p, xj, id >= 0, m, c.sum);
