@@ -147,7 +147,7 @@ LB_EXPORT int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uin
     const RowsAt r = rows_at(static_cast<uint8_t *>(workspace), M, K, type);
     if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, M, (int)K, nullptr, nullptr, 1, parts_of(type), r.to, r.scale, st))
         return e;
-    return q4_gemm(p, {r.to, r.scale, M}, kQ4Dense, type, codes, N, di.sms, st);
+    return q4_gemm_dense(p, {r.to, r.scale, M}, type, codes, N, di.sms, st);
 }
 
 LB_EXPORT size_t lb_experts_q4_workspace_bytes(int64_t T, int E, int k, int64_t hidden, int64_t ffn,
@@ -207,10 +207,10 @@ LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T
         if (int e = q4_rows(x, type == LB_OUT_F32, x_stride, pairs, (int)hidden, expert_start + E, order, k, parts, xr.to,
                             xr.scale, st))
             return e;
-        if (int e = q4_gemm(up, {xr.to, xr.scale, pairs}, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
+        if (int e = q4_gemm_experts(up, {xr.to, xr.scale, pairs}, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
         if (int e = q4_rows(h, true, ffn, pairs, (int)ffn, expert_start + E, nullptr, 1, parts, hr.to, hr.scale, st))
             return e;
-        if (int e = q4_gemm(down, {hr.to, hr.scale, pairs}, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
+        if (int e = q4_gemm_experts(down, {hr.to, hr.scale, pairs}, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
     }
     const int64_t blocks = (T * (hidden / 4) + kCombineThreads - 1) / kCombineThreads;
     if (blocks > 0x7fffffff) return LB_ERR_SHAPE;

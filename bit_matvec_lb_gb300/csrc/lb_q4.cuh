@@ -59,7 +59,7 @@ __device__ __forceinline__ uint32_t q4_power(uint32_t m) { return (uint32_t)min(
 int q4_gemv(const Q4Params &p, Q4Use use, int type, const uint8_t *codes, int64_t rows, int sms,
             cudaStream_t st);
 
-// More tokens, on tcgen05: lb_q4_gemm.cu.  r is what q4_rows left: rows of K fp16 numbers (and with
+// More tokens, on tcgen05: lb_q4_gemm.cuh.  r is what q4_rows left: rows of K fp16 numbers (and with
 // fp32 tensors, behind all of them, their second parts), each scaled by a power of two that row_scale
 // takes back.
 struct Q4Rows {
@@ -67,8 +67,10 @@ struct Q4Rows {
     const float *row_scale;
     int64_t rows;        // of a part
 };
-int q4_gemm(const Q4Params &p, const Q4Rows &r, Q4Use use, int type, const uint8_t *codes, int64_t rows,
-            int sms, cudaStream_t st);
+int q4_gemm_dense(const Q4Params &p, const Q4Rows &r, int type, const uint8_t *codes, int64_t rows, int sms,
+                  cudaStream_t st);
+int q4_gemm_experts(const Q4Params &p, const Q4Rows &r, Q4Use use, int type, const uint8_t *codes, int64_t rows,
+                    int sms, cudaStream_t st);
 // rows [n][K] of x (fp32 if f32 else bf16), x_stride apart -> fp16 parts and row_scale.  n_opt: NULL, or where
 // the number of rows that are there lies.  order: NULL, or the n pairs, whose rows of x are pair / k.
 int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt,
