@@ -38,6 +38,7 @@ constexpr int kMvWarps = 16;
 constexpr int kMvThreads = 32 * (kMvWarps + 1);
 constexpr int kMvTokens = 8;
 constexpr int kMvMaxSplit = 8;
+constexpr int kMvSums = 21;                      // most of split * ceil(kMvWarps / split)
 constexpr int kMvMaxStages = 5;
 constexpr size_t kMvShared = 226 * 1024;         // shared memory of a CTA, static and dynamic
 
@@ -102,6 +103,9 @@ __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
 __device__ __forceinline__ void store_y(float *p, float v) { *p = v; }
 __device__ __forceinline__ void store_y(__nv_bfloat16 *p, float v) { *p = __float2bfloat16_rn(v); }
 
+// The first of the warps whose rows the CTA of a rank finishes (warp w's is w * split / kMvWarps).
+__device__ __forceinline__ int first_warp(int rank, int split) { return (kMvWarps * rank + split - 1) / split; }
+
 // T: the type of x (dense, up; h is fp32) and of a dense y; PARTS: fp16 parts of an x.
 template <Q4Use USE, typename T, int PARTS, int GROUP, bool ZEROS>
 __global__ void __launch_bounds__(kMvThreads, 1)
@@ -114,7 +118,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
     __shared__ uint64_t full[kMvMaxStages], empty[kMvMaxStages], sums_full[2];
     __shared__ __align__(16) uint16_t ds[kMvMaxStages][kMvRows][kPer];
     __shared__ __align__(16) uint8_t zs[ZEROS ? kMvMaxStages : 1][kMvRows][kPer < 4 ? 4 : kPer];
-    __shared__ __align__(16) float sums[2][kMvWarps][16][kMvTokens];   // [rank, own warp][row][column]
+    __shared__ __align__(16) float sums[2][kMvSums][16][kMvTokens];   // [rank, own warp][row][column]
     __shared__ int row_of[2][kMvTokens];
     __shared__ uint16_t s_first[kExperts];                       // pieces before an expert's
     __shared__ int s_part[kMvThreads / 32];
@@ -131,8 +135,9 @@ __global__ void __launch_bounds__(kMvThreads, 1)
     if (tid == 0) {
         // a stage is full when the copies of codes and the 32 lanes' copies of scales have landed
         for (int i = 0; i < kMvMaxStages; i++) mbar_init(&full[i], 33), mbar_init(&empty[i], kMvWarps);
-        // sums of 32 groups of 8 rows come to a CTA, whatever the split
-        mbar_init(&sums_full[0], kMvRows / 8), mbar_init(&sums_full[1], kMvRows / 8);
+        // from every CTA come the sums of the warps whose rows are finished here, in two halves
+        const int arrivals = 2 * l.split * (first_warp(rank + 1, l.split) - first_warp(rank, l.split));
+        mbar_init(&sums_full[0], arrivals), mbar_init(&sums_full[1], arrivals);
         fence_mbar_init();
     }
     // Pieces of at most l.tokens tokens (of one expert).
@@ -273,9 +278,10 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         const int row = USE == kQ4Up ? warp * 8 + (lane & 7) + (lane & 8) * (kMvRows / 16) : warp * 16 + (lane & 15);
         const int row0 = USE == kQ4Up ? warp * 8 + g : warp * 16 + g, row1 = USE == kQ4Up ? row0 + kMvRows / 2 : row0 + 8;
         const uint32_t at_row = smem_u32(ring) + row * 64, turn = (row >> 1) & 3;
-        const int own = kMvWarps / l.split;              // warps whose rows a CTA finishes
-        const uint32_t owner = warp / own;
-        const uint32_t send_to = address_in(&sums[0][rank * own + warp % own][g][2 * t], owner);
+        const int pitch = (kMvWarps + l.split - 1) / l.split;   // of a rank's sums
+        const int first_own = first_warp(rank, l.split), own = first_warp(rank + 1, l.split) - first_own;
+        const uint32_t owner = warp * l.split / kMvWarps;
+        const uint32_t send_to = address_in(&sums[0][rank * pitch + warp - first_warp(owner, l.split)][g][2 * t], owner);
         const uint32_t tell[2] = {address_in(&sums_full[0], owner), address_in(&sums_full[1], owner)};
         int stage = 0;
         uint32_t phase = 0;
@@ -320,16 +326,16 @@ __global__ void __launch_bounds__(kMvThreads, 1)
             }
             const int parts = packed(q_done) ? PARTS : 1;
             constexpr int per_warp = USE == kQ4Up ? 8 : 16;
-            const int shift = (USE == kQ4Up ? 7 : 8) - (31 - __clz(l.split));   // rows: a power of two
-            for (int i = tid; i < q_done.tokens << shift; i += 32 * kMvWarps) {
-                const int tk = i >> shift, r = i & ((1 << shift) - 1), w = r / per_warp, rr = r % per_warp;
-                const int64_t row_n = n_done + (rank * own + w) * per_warp + rr;
+            const uint32_t rows = own * per_warp;
+            for (uint32_t i = tid; i < q_done.tokens * rows; i += 32 * kMvWarps) {
+                const int tk = i / rows, r = i - tk * rows, w = r / per_warp, rr = r % per_warp;
+                const int64_t row_n = n_done + (first_own + w) * per_warp + rr;
                 float v[2] = {0.f, 0.f};
 #pragma unroll
                 for (int h = 0; h < (USE == kQ4Up ? 2 : 1); h++)
                     for (int k = 0; k < parts; k++)
                         for (int s = 0; s < l.split; s++)
-                            v[h] += sums[n & 1][s * own + w][rr + 8 * h][tk * parts + k];
+                            v[h] += sums[n & 1][s * pitch + w][rr + 8 * h][tk * parts + k];
                 store(q_done, row_n, tk, v[0], v[1]);
             }
         };
@@ -516,7 +522,7 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
     const int blocks = (K + kMvBlock - 1) / kMvBlock;
     MvPlan best;
     int64_t best_time = 0;
-    for (int split = 1; split <= kMvMaxSplit; split *= 2) {
+    for (int split = 1; split <= kMvMaxSplit; split++) {
         MvLaunch l{};
         l.blocks = (blocks + split - 1) / split;
         l.split = split, l.tiles = tiles;
@@ -547,8 +553,8 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
         if (held < 1) continue;
         const int64_t units = (pieces ? pieces : (T + l.tokens - 1) / l.tokens) * tiles;
         const int64_t clusters = std::min<int64_t>(units, held);
-        // in blocks: a unit takes one by itself, two with sums that go through the cluster
-        const int64_t time = (units + clusters - 1) / clusters * (l.blocks + (split > 1 ? 2 : 1));
+        // in halves of a block's: a unit takes one by itself, three with sums that go through the cluster
+        const int64_t time = (units + clusters - 1) / clusters * (2 * l.blocks + (split > 1 ? 3 : 1));
         if (!best.clusters || time < best_time) best.l = l, best.clusters = clusters, best.smem = smem, best_time = time;
     }
     return best;
