@@ -12,37 +12,38 @@ namespace lb {
 
 constexpr int kCombineThreads = 256;
 
-// Four columns of a token per thread.
+// Eight columns of a token per thread.  (The experts' outputs in fp16, scaled for every 32 rows, make this 7 us shorter for
+// 32768 of 2048 and the product that leaves them 50 us longer.)
 template <typename T>
 __global__ void __launch_bounds__(kCombineThreads)
     experts_combine_kernel(const float *part, const int32_t *ids, const float *weights, T *y,
                            int64_t y_stride, int64_t tokens, int k, int columns) {
     pdl_launch_dependents();
     pdl_wait();
-    const int quads = columns / 4;
+    const int eights = columns / 8;
     const int64_t i = blockIdx.x * (int64_t)kCombineThreads + threadIdx.x;
-    if (i >= tokens * quads) return;
-    const int64_t t = i / quads;
-    const int c = (int)(i % quads) * 4;
-    float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+    if (i >= tokens * eights) return;
+    const int64_t t = i / eights;
+    const int c = (int)(i - t * eights) * 8;
+    float v[8] = {0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f, 0.f};
 #pragma unroll 4
     for (int j = 0; j < k; j++) {
-        if (ids[t * k + j] < 0) continue;
-        const float w = weights[t * k + j];
-        const float4 a = *reinterpret_cast<const float4 *>(part + (t * k + j) * columns + c);
-        v.x = fmaf(w, a.x, v.x), v.y = fmaf(w, a.y, v.y);
-        v.z = fmaf(w, a.z, v.z), v.w = fmaf(w, a.w, v.w);
+        const int64_t pair = t * k + j;
+        if (ids[pair] < 0) continue;
+        const float w = weights[pair];
+        float a[8];
+        load8(part + pair * columns + c, a);
+#pragma unroll
+        for (int e = 0; e < 8; e++) v[e] = fmaf(w, a[e], v[e]);
     }
     T *to = y + t * y_stride + c;
-    if constexpr (sizeof(T) == 4) {
-        if ((reinterpret_cast<uintptr_t>(to) & 15) == 0) *reinterpret_cast<float4 *>(to) = v;
-        else to[0] = v.x, to[1] = v.y, to[2] = v.z, to[3] = v.w;
+    if ((reinterpret_cast<uintptr_t>(to) & 15) == 0) {
+        store8(to, v);
     } else {
-        if ((reinterpret_cast<uintptr_t>(to) & 7) == 0) {
-            *reinterpret_cast<uint2 *>(to) = make_uint2(bf16_pair(v.x, v.y), bf16_pair(v.z, v.w));
-        } else {
-            to[0] = __float2bfloat16_rn(v.x), to[1] = __float2bfloat16_rn(v.y);
-            to[2] = __float2bfloat16_rn(v.z), to[3] = __float2bfloat16_rn(v.w);
+#pragma unroll
+        for (int e = 0; e < 8; e++) {
+            if constexpr (sizeof(T) == 4) to[e] = v[e];
+            else to[e] = __float2bfloat16_rn(v[e]);
         }
     }
 }
@@ -212,11 +213,12 @@ LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T
             return e;
         if (int e = q4_gemm_experts(down, {hr.to, hr.scale, pairs}, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
     }
-    const int64_t blocks = (T * (hidden / 4) + kCombineThreads - 1) / kCombineThreads;
+    const int64_t blocks = (T * (hidden / 8) + kCombineThreads - 1) / kCombineThreads;
     if (blocks > 0x7fffffff) return LB_ERR_SHAPE;
+    const dim3 grid((unsigned)blocks), block(kCombineThreads);
     if (type == LB_OUT_F32)
-        return launch_pdl(experts_combine_kernel<float>, dim3((unsigned)blocks), dim3(kCombineThreads), 0, st,
-                          part, ids, weights, static_cast<float *>(y), y_stride, T, k, (int)hidden);
-    return launch_pdl(experts_combine_kernel<__nv_bfloat16>, dim3((unsigned)blocks), dim3(kCombineThreads), 0,
-                      st, part, ids, weights, static_cast<__nv_bfloat16 *>(y), y_stride, T, k, (int)hidden);
+        return launch_pdl(experts_combine_kernel<float>, grid, block, 0, st, part, ids, weights, static_cast<float *>(y),
+                          y_stride, T, k, (int)hidden);
+    return launch_pdl(experts_combine_kernel<__nv_bfloat16>, grid, block, 0, st, part, ids, weights,
+                      static_cast<__nv_bfloat16 *>(y), y_stride, T, k, (int)hidden);
 }

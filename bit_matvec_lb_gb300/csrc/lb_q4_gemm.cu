@@ -9,50 +9,92 @@ namespace lb {
 // four-row gathering copies of the tensors' own rows take four times as long as the products): scaled so that the largest lies in [2^14, 2^15), in fp16 (one part, or two
 // that hold 22 bits), each eight columns in the order 0 4 1 5 2 6 3 7.
 // ------------------------------------------------------------------------------------------
-constexpr int kRowThreads = 128;
-constexpr int kRowHold = 4;   // groups of eight columns that a thread keeps between its two passes
+constexpr int kRowThreads = 256;
+constexpr int kRowHold = 8;        // groups of eight columns that a thread keeps between its two passes
+// Rows from which a warp takes a row, instead of four: many rows keep the memory busy by themselves and need no
+// barrier (32768 x 2048: 53 -> 35 us), few are sooner done by more threads (64 x 4096: 4.2 against 5.5).
+constexpr int kRowsMany = 2048;
 
-template <typename X, int PARTS>
+template <typename X>
+struct RawEight;   // eight numbers as they lie in memory
+template <>
+struct RawEight<float> {
+    float4 a, b;
+    __device__ __forceinline__ void load(const float *p) {
+        a = *reinterpret_cast<const float4 *>(p), b = *reinterpret_cast<const float4 *>(p + 4);
+    }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        v[0] = a.x, v[1] = a.y, v[2] = a.z, v[3] = a.w, v[4] = b.x, v[5] = b.y, v[6] = b.z, v[7] = b.w;
+    }
+};
+template <>
+struct RawEight<__nv_bfloat16> {
+    uint4 a;
+    __device__ __forceinline__ void load(const __nv_bfloat16 *p) { a = *reinterpret_cast<const uint4 *>(p); }
+    __device__ __forceinline__ void get(float (&v)[8]) const {
+        const uint32_t w[4] = {a.x, a.y, a.z, a.w};
+#pragma unroll
+        for (int i = 0; i < 4; i++)
+            v[2 * i] = __uint_as_float(w[i] << 16), v[2 * i + 1] = __uint_as_float(w[i] & 0xFFFF0000u);
+    }
+};
+
+// PER: threads of a row.
+template <typename X, int PARTS, int PER>
 __global__ void __launch_bounds__(kRowThreads)
     q4_rows_kernel(const X *x, int64_t x_stride, int64_t n, int K, const int32_t *n_opt,
                    const int32_t *order, int k, uint16_t *to, float *row_scale) {
     __shared__ float most[kRowThreads / 32];
-    const int tid = threadIdx.x;
+    const int tid = threadIdx.x % PER;
     pdl_launch_dependents();
     pdl_wait();
-    const int64_t row = blockIdx.x;
-    if (n_opt && row >= min(max(*n_opt, 0), (int)n)) return;
-    int64_t from = row;
-    if (order) {
+    const int64_t row = blockIdx.x * (int64_t)(kRowThreads / PER) + threadIdx.x / PER;
+    const int64_t end = n_opt ? min(max(*n_opt, 0), (int)n) : n;
+    int64_t from = row < end ? row : -1;
+    if (order && from >= 0) {
         const int pair = order[row];
         from = pair >= 0 && pair < n ? pair / k : -1;
     }
     const X *src = x + max(from, (int64_t)0) * x_stride;
     const int units = K / 8;
-    float held[kRowHold][8], m = 0.f;
-#pragma unroll
-    for (int h = 0; h < kRowHold; h++) {
-        const int u = tid + h * kRowThreads;
-        if (u >= units) break;
-        load8(src + 8 * u, held[h]);
-#pragma unroll
-        for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(held[h][j]));
-    }
-    for (int u = tid + kRowHold * kRowThreads; u < units; u += kRowThreads) {
+    RawEight<X> held[kRowHold];
+    float m = 0.f;
+    auto look = [&](const RawEight<X> &r) {
         float v[8];
-        load8(src + 8 * u, v);
+        r.get(v);
 #pragma unroll
         for (int j = 0; j < 8; j++) m = fmaxf(m, fabsf(v[j]));
+    };
+    if (from >= 0) {
+#pragma unroll
+        for (int h = 0; h < kRowHold; h++)
+            if (tid + h * PER < units) held[h].load(src + 8 * (tid + h * PER));
+#pragma unroll
+        for (int h = 0; h < kRowHold; h++)
+            if (tid + h * PER < units) look(held[h]);
+        for (int u = tid + kRowHold * PER; u < units; u += PER) {
+            RawEight<X> r;
+            r.load(src + 8 * u);
+            look(r);
+        }
     }
 #pragma unroll
     for (int o = 16; o; o >>= 1) m = fmaxf(m, __shfl_xor_sync(0xffffffffu, m, o));
-    if ((tid & 31) == 0) most[tid >> 5] = m;
-    __syncthreads();
-    m = fmaxf(fmaxf(most[0], most[1]), fmaxf(most[2], most[3]));
+    if (PER > 32) {
+        if ((threadIdx.x & 31) == 0) most[threadIdx.x >> 5] = m;
+        __syncthreads();
+        const float *mine = most + threadIdx.x / PER * (PER / 32);
+        m = mine[0];
+#pragma unroll
+        for (int w = 1; w < PER / 32; w++) m = fmaxf(m, mine[w]);
+    }
+    if (row >= end) return;
     const uint32_t e = q4_power(__float_as_uint(m));
     const float up = __uint_as_float(e << 23);
     if (tid == 0) row_scale[row] = __uint_as_float((254 - e) << 23);
-    auto put = [&](int u, const float (&v)[8]) {
+    auto put = [&](int u, const RawEight<X> &r) {
+        float v[8];
+        r.get(v);
         uint32_t hi[4], lo[4];
 #pragma unroll
         for (int j = 0; j < 4; j++) {
@@ -66,29 +108,32 @@ __global__ void __launch_bounds__(kRowThreads)
         if (PARTS == 2) *reinterpret_cast<uint4 *>(dst + n * K) = make_uint4(lo[0], lo[1], lo[2], lo[3]);
     };
 #pragma unroll
-    for (int h = 0; h < kRowHold; h++) {
-        const int u = tid + h * kRowThreads;
-        if (u >= units) break;
-        put(u, held[h]);
+    for (int h = 0; h < kRowHold; h++)
+        if (tid + h * PER < units) put(tid + h * PER, held[h]);
+    for (int u = tid + kRowHold * PER; u < units; u += PER) {
+        RawEight<X> r;
+        r.load(src + 8 * u);
+        put(u, r);
     }
-    for (int u = tid + kRowHold * kRowThreads; u < units; u += kRowThreads) {
-        float v[8];
-        load8(src + 8 * u, v);
-        put(u, v);
-    }
+}
+
+template <typename X, int PARTS>
+static int launch_rows(const X *x, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, const int32_t *order, int k,
+                       uint16_t *to, float *row_scale, cudaStream_t st) {
+    const int per = n >= kRowsMany ? 32 : 128, rows = kRowThreads / per;
+    auto kernel = per == 32 ? q4_rows_kernel<X, PARTS, 32> : q4_rows_kernel<X, PARTS, 128>;
+    return launch_pdl(kernel, dim3((unsigned)((n + rows - 1) / rows)), dim3(kRowThreads), 0, st, x, x_stride, n, K, n_opt,
+                      order, k, to, row_scale);
 }
 
 int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const int32_t *n_opt,
             const int32_t *order, int k, int parts, uint16_t *to, float *row_scale, cudaStream_t st) {
-    const dim3 grid((unsigned)n), block(kRowThreads);
-    if (f32) {
-        auto kernel = parts == 2 ? q4_rows_kernel<float, 2> : q4_rows_kernel<float, 1>;
-        return launch_pdl(kernel, grid, block, 0, st, static_cast<const float *>(x), x_stride, n, K, n_opt, order,
-                          k, to, row_scale);
-    }
-    return launch_pdl(q4_rows_kernel<__nv_bfloat16, 1>, grid, block, 0, st,
-                      static_cast<const __nv_bfloat16 *>(x), x_stride, n, K, n_opt, order, k, to,
-                      row_scale);
+    if (!f32)
+        return launch_rows<__nv_bfloat16, 1>(static_cast<const __nv_bfloat16 *>(x), x_stride, n, K, n_opt, order, k, to,
+                                             row_scale, st);
+    const float *v = static_cast<const float *>(x);
+    return parts == 2 ? launch_rows<float, 2>(v, x_stride, n, K, n_opt, order, k, to, row_scale, st)
+                      : launch_rows<float, 1>(v, x_stride, n, K, n_opt, order, k, to, row_scale, st);
 }
 
 int q4_gemm_dense(const Q4Params &p, const Q4Rows &r, int type, const uint8_t *codes, int64_t rows, int sms,

@@ -391,7 +391,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             float *park = reinterpret_cast<float *>(smem) + c0 * kGmRows + quarter * 32 + lane;   // [column][128]
             // 16 columns from c (of this warp's) on
             auto emit = [&](int c, const float (&v)[16]) {
-                if (l.split > 1) {
+                if (USE == kQ4Dense && l.split > 1) {
 #pragma unroll
                     for (int j = 0; j < 16; j++)
                         if (c + j < mine) park[(c + j) * kGmRows] = v[j];
@@ -786,37 +786,29 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     }
     __syncthreads();
     tc_fence_after();
-    if (l.split > 1) {
-        // one item per cluster: its parts' sums, a share of the columns per CTA, a warp per column
-        gm_cluster_sync();
-        if (begin < items) {
-            const GmItem it = item_of(begin);
-            const float *park = reinterpret_cast<const float *>(smem);
-            for (int c = rank + l.split * warp; c < it.tokens; c += l.split * kGmWarps) {
-                const float scale = col_scale[0][c];
-                const int to = col_row[0][c];
+    if constexpr (USE == kQ4Dense) {
+        if (l.split > 1) {
+            // one item per cluster: its parts' sums, a share of the columns per CTA, a warp per column
+            gm_cluster_sync();
+            if (begin < items) {
+                const GmItem it = item_of(begin);
+                const float *park = reinterpret_cast<const float *>(smem);
+                for (int c = rank + l.split * warp; c < it.tokens; c += l.split * kGmWarps) {
+                    const float scale = col_scale[0][c];
+                    T *y = static_cast<T *>(p.y) + col_row[0][c] * p.y_stride;
 #pragma unroll
-                for (int j = 0; j < 4; j++) {
-                    const int at = j * 32 + lane;
-                    float v = 0.f;
-                    for (int q = 0; q < l.split; q++) v += gm_cluster_load(park + c * kGmRows + at, q);
-                    v *= scale;
-                    bool in;
-                    const int64_t row = row_of(it, at, in);
-                    if (USE == kQ4Up) {
-                        const float up = __shfl_xor_sync(0xffffffffu, v, 16);
-                        if (lane < 16 && in)
-                            static_cast<float *>(p.y)[to * p.y_stride + (row - it.expert * matrix_rows)] =
-                                v / (1.f + expf(-v)) * up;
-                    } else if (in) {
-                        if (USE == kQ4Dense) gm_store(static_cast<T *>(p.y) + to * p.y_stride + row, v);
-                        else if (to >= 0)
-                            static_cast<float *>(p.y)[to * p.y_stride + (row - it.expert * matrix_rows)] = v;
+                    for (int j = 0; j < 4; j++) {
+                        const int at = j * 32 + lane;
+                        float v = 0.f;
+                        for (int q = 0; q < l.split; q++) v += gm_cluster_load(park + c * kGmRows + at, q);
+                        bool in;
+                        const int64_t row = row_of(it, at, in);
+                        if (in) gm_store(y + row, v * scale);
                     }
                 }
             }
+            gm_cluster_sync();
         }
-        gm_cluster_sync();
     }
     if (l.share > 1) gm_cluster_sync();   // nobody's copies or arrivals come after a CTA has gone
     if (warp == kGmMmaWarp) tmem_dealloc(tmem, 512);

@@ -416,10 +416,10 @@ __global__ void __launch_bounds__(kMvThreads, 1)
                 }
                 const int chunks = min(kMvBlock, columns - b * kMvBlock) / 32;   // of 32 columns (K is a multiple)
                 const int z_at = kPer == 2 ? (k0 / GROUP + b * kPer) & 2 : 0;
-                // 128 columns at a time; where K ends inside, x is zero and a group behind K is left out
-#pragma unroll
-                for (int j = 0; j < kMvBlock / 128; j++) {
-                    if (4 * j >= chunks) break;
+                // 128 columns at a time; where K ends inside, x is zero and a group behind K is left out.  (Whole blocks
+                // without a branch, so that their parts' chains of operations run side by side.)
+                auto columns128 = [&](int j, auto whole) {
+                    constexpr bool all = decltype(whole)::value;
                     uint32_t w[2][4];   // the lane's two rows of chunks 0 and 1, then of 2 and 3
 #pragma unroll
                     for (int h = 0; h < 2; h++)
@@ -454,12 +454,21 @@ __global__ void __launch_bounds__(kMvThreads, 1)
                         }
                     }
                     float part[4] = {0.f, 0.f, 0.f, 0.f};
+                    // the two rows' scales of these 128 columns
+                    uint2 d_row[2] = {make_uint2(0, 0), make_uint2(0, 0)};
+#pragma unroll
+                    for (int r = 0; r < 2; r++) {
+                        const uint16_t *d = &ds[stage][r ? row1 : row0][j * kGroups];
+                        if (kGroups == 4) d_row[r] = *reinterpret_cast<const uint2 *>(d);
+                        else if (kGroups == 2) d_row[r].x = *reinterpret_cast<const uint32_t *>(d);
+                        else d_row[r].x = *d;
+                    }
+                    auto scale_of = [](const uint2 &d, int i) { return (uint16_t)((i & 2 ? d.y : d.x) >> (16 * (i & 1))); };
 #pragma unroll
                     for (int i = 0; i < kGroups; i++) {
-                        if (4 * j + i * kEach >= chunks) break;
-                        const int gi = j * kGroups + i, at = i * (kEach == 4 ? 1 : kEach);
-                        const float d0 = f16_bits_to_float(ds[stage][row0][gi]);
-                        const float d1 = f16_bits_to_float(ds[stage][row1][gi]);
+                        if (!all && 4 * j + i * kEach >= chunks) break;
+                        const int at = i * (kEach == 4 ? 1 : kEach);
+                        const float d0 = f16_bits_to_float(scale_of(d_row[0], i)), d1 = f16_bits_to_float(scale_of(d_row[1], i));
                         if (kEach > 1)
 #pragma unroll
                             for (int c2 = 0; c2 < 4; c2++) sum[at][c2] += sum[at + 1][c2];
@@ -469,6 +478,13 @@ __global__ void __launch_bounds__(kMvThreads, 1)
                     const float2 f = *reinterpret_cast<const float2 *>(back + b * kMvTokens + 2 * t);
                     total[0] = fmaf(part[0], f.x, total[0]), total[1] = fmaf(part[1], f.y, total[1]);
                     total[2] = fmaf(part[2], f.x, total[2]), total[3] = fmaf(part[3], f.y, total[3]);
+                };
+                if (chunks >= kMvBlock / 32) {
+#pragma unroll
+                    for (int j = 0; j < kMvBlock / 128; j++) columns128(j, std::true_type{});
+                } else {
+#pragma unroll 1
+                    for (int j = 0; 4 * j < chunks; j++) columns128(j, std::false_type{});
                 }
                 __syncwarp();
                 if (lane == 0) mbar_arrive(&empty[stage]);
