@@ -173,6 +173,8 @@ __device__ __forceinline__ Chosen choose(const RouteParams &p, const T *row, con
         // sum, a reciprocal and a sum: below 2^-21.  A softmax: exp to two units, a sum of up to 1024 scores in 32
         // chains, a reciprocal, a product and a sum: below 2^-18 of the largest score.
         tol = (p.sigmoid ? 0x1p-21f : 0x1p-18f * by) + 0x1p-22f * warp_max(most) + 1e-37f;
+        // biases so large that sums of two overflow, or infinite: all in binary64
+        if (!(tol < 0x1p100f)) c.close = groups = true;
     }
     if (p.groups > 1) {
         // lanes [g * part, (g + 1) * part) look through group g

@@ -168,3 +168,16 @@ def test_captured_and_replayed():
     want = moe_ref.route(host(x), 8, False)
     for a, b in zip((out[0], out[2], out[3]), (want[0], want[2], want[3])):
         assert np.array_equal(host(a), b)
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("groups,best", [(1, 1), (1, 2), (6, 1), (6, 2)])
+def test_huge_biases(sigmoid, groups, best):
+    """Infinite ones, and ones of which two add up to more than binary32 holds; the ordinary experts among them keep
+    their order.  (No two groups' values are within a binary64 rounding of each other.)"""
+    x = np.random.default_rng(8).normal(0, 2, (70, 48)).astype(np.float32)
+    for at, size in ((5, np.inf), (30, 3.1e38), (31, 3.3e38), (5, 3.2e38), (5, -3.2e38)):
+        b = np.linspace(-0.1, 0.1, 48).astype(np.float32)
+        b[at] = size
+        b[17], b[44] = 2.9e38, -3e38
+        run(x, 8, sigmoid, b, groups=groups, keep=min(2, groups), best=best)
