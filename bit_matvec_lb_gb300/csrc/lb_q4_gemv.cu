@@ -47,7 +47,7 @@ struct MvLaunch {
     int stages;
     int tokens;    // most tokens of a piece
     int split;     // CTAs along K, a cluster
-    int tiles;     // of 128 rows
+    int tiles;     // of kMvRows rows (up: of half as many pairs)
 };
 
 // (volatile: stays behind the wait for its stage)
@@ -534,7 +534,7 @@ struct MvPlan {
 };
 
 // The split whose longest run is the shortest; of equal ones the smallest.  `fixed`: static shared memory.
-static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces, int K, int parts, size_t fixed, int sms) {
+static MvPlan plan_gemv(const void *kernel, int64_t tokens, int tiles, int64_t pieces, int K, int parts, size_t fixed, int sms) {
     const int blocks = (K + kMvBlock - 1) / kMvBlock;
     MvPlan best;
     int64_t best_time = 0;
@@ -544,7 +544,7 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
         l.split = split, l.tiles = tiles;
         // Tokens: eight, or as many as their parts' slices fit beside two stages.
         const size_t pitch = 2 * (size_t)l.blocks * kMvBlock + 64, scales = (size_t)l.blocks * kMvTokens * 4;
-        l.tokens = (int)std::min<int64_t>(T, kMvTokens);
+        l.tokens = (int)tokens;
         const size_t most = kMvShared - fixed - 2 * kMvStage - scales;
         if (parts * l.tokens * pitch > most && split < kMvMaxSplit) continue;
         while (parts * l.tokens * pitch > most && l.tokens > 1) l.tokens--;
@@ -567,7 +567,7 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
             }
         }
         if (held < 1) continue;
-        const int64_t units = (pieces ? pieces : (T + l.tokens - 1) / l.tokens) * tiles;
+        const int64_t units = (pieces ? pieces : (tokens + l.tokens - 1) / l.tokens) * tiles;
         const int64_t clusters = std::min<int64_t>(units, held);
         // in halves of a block's: a unit takes one by itself, three with sums that go through the cluster
         const int64_t time = (units + clusters - 1) / clusters * (2 * l.blocks + (split > 1 ? 3 : 1));
@@ -579,15 +579,16 @@ static MvPlan plan_gemv(const void *kernel, int64_t T, int tiles, int64_t pieces
 template <Q4Use USE, typename T, int PARTS, int GROUP>
 static int launch_gemv(const Q4Params &p, const CUtensorMap &map, int64_t pieces, int sms, cudaStream_t st) {
     auto kernel = p.zeros ? q4_gemv_kernel<USE, T, PARTS, GROUP, true> : q4_gemv_kernel<USE, T, PARTS, GROUP, false>;
-    // (asking the driver for each split takes longer than the launch: remembered by sizes)
+    // (asking the driver for each split takes longer than the launch: remembered by what a plan depends on)
     static std::mutex mutex;
     static std::map<std::tuple<int, bool, int64_t, int64_t, int64_t, int>, MvPlan> known;
     int dev = 0;
     cudaGetDevice(&dev);
+    const int64_t tokens = std::min<int64_t>(p.T, kMvTokens);
     MvPlan plan;
-    {
+    try {
         std::lock_guard<std::mutex> lock(mutex);
-        MvPlan &at = known[std::make_tuple(dev, p.zeros != nullptr, p.T, pieces, p.N, p.K)];
+        MvPlan &at = known[std::make_tuple(dev, p.zeros != nullptr, tokens, pieces, p.N, p.K)];
         if (!at.clusters) {
             constexpr int kTileRows = USE == kQ4Up ? kMvRows / 2 : kMvRows;
             cudaFuncAttributes fa{};
@@ -596,10 +597,12 @@ static int launch_gemv(const Q4Params &p, const CUtensorMap &map, int64_t pieces
                 record_cuda_error(e);
                 return LB_ERR_LAUNCH;
             }
-            at = plan_gemv((const void *)kernel, p.T, (int)((p.N + kTileRows - 1) / kTileRows), pieces, p.K, PARTS,
+            at = plan_gemv((const void *)kernel, tokens, (int)((p.N + kTileRows - 1) / kTileRows), pieces, p.K, PARTS,
                            fa.sharedSizeBytes + 1024, sms);
         }
         plan = at;
+    } catch (...) {   // (no memory on the host: nothing may be thrown through a C entry)
+        return LB_ERR_LAUNCH;
     }
     if (!plan.clusters) return LB_ERR_LAUNCH;
     cudaLaunchConfig_t cfg = {};
