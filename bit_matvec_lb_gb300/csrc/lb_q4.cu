@@ -90,9 +90,13 @@ static RowsAt rows_at(uint8_t *at, int64_t n, int64_t K, int type) {
             reinterpret_cast<float *>(at + align256((size_t)n * K * 2 * parts_of(type)))};
 }
 
-// Pairs per expert from which the experts' products run on tcgen05: below, most of its tiles would be empty
-// columns.
-constexpr int kManyPairs = 8;
+// Pairs per expert from which the experts' products run on tcgen05, whose time hardly grows with them; the other kernel
+// takes pieces of eight tokens, so its time grows with every one that begins.  64 experts of 2048 x 1024, eight per
+// token, 6, 12 and 16 pairs each: fp32 114, 150 and 181 us against tcgen05's 160, 168 and 170; bf16 87, 113 and 135
+// against 107, 109 and 110.  Eight of 4096 x 8192, two per token, 8, 12 and 16: fp32 202, 238 and 306 against 220, 242
+// and 246; bf16 182, 203 and 266 against 163, 177 and 178.  32 of 1024 x 512, four per token, 12 and 16: fp32 37 and 47
+// against 43 and 45; bf16 31 and 37 against 35 and 35.
+constexpr int many_pairs(int type) { return type == LB_OUT_F32 ? 13 : 10; }
 
 struct ExpertsAt {
     size_t x, h, h_rows, part, bytes;
@@ -199,7 +203,7 @@ LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T
     up.start = expert_start, up.order = order, up.E = E, up.k = k;
     Q4Params down = product_of(down_scales, down_zeros_opt, group, h, ffn, part, hidden, pairs, hidden, ffn);
     down.start = expert_start, down.order = order, down.E = E, down.k = k;
-    if (pairs < (int64_t)kManyPairs * E) {
+    if (pairs < (int64_t)many_pairs(type) * E) {
         if (int e = q4_gemv(up, kQ4Up, type, up_codes, E * 2 * ffn, di.sms, st)) return e;
         if (int e = q4_gemv(down, kQ4Down, type, down_codes, E * hidden, di.sms, st)) return e;
     } else {

@@ -5,14 +5,17 @@
 namespace lb {
 
 // ------------------------------------------------------------------------------------------
-// Rows of x for the tensor cores (with an order, row i is that of pair order[i], zeros where there is none;
-// four-row gathering copies of the tensors' own rows take four times as long as the products): scaled so that the largest lies in [2^14, 2^15), in fp16 (one part, or two
-// that hold 22 bits), each eight columns in the order 0 4 1 5 2 6 3 7.
+// Rows of x for the tensor cores (with an order, row i is that of pair order[i], zeros where there is none): scaled so
+// that the largest lies in [2^14, 2^15), in fp16 (one part, or two that hold 22 bits), each eight columns in the order
+// 0 4 1 5 2 6 3 7.  Bound by memory.
 // ------------------------------------------------------------------------------------------
 constexpr int kRowThreads = 256;
 constexpr int kRowHold = 8;        // groups of eight columns that a thread keeps between its two passes
-// Rows from which a warp takes a row, instead of four: many rows keep the memory busy by themselves and need no
-// barrier (32768 x 2048: 53 -> 35 us), few are sooner done by more threads (64 x 4096: 4.2 against 5.5).
+// A warp takes a row, instead of four, where there are so many rows and a warp's registers hold a row: many rows keep the
+// memory busy by themselves and need no barrier, few or longer ones are sooner done by more threads.  With a product of
+// 128 weight rows behind them, a warp against four: 32768 x 1024 fp32 73 against 122 us, bf16 37 against 64;
+// 2048 x 1024 15.1 against 18.6 and 14.4 against 16.4; 512 x 1024 14.5 both and 14.4 against 13.9; 32768 x 4096
+// 290 against 263 and 136 against 134; 64 x 4096 16.5 against 14.5 and 14.5 against 12.4.
 constexpr int kRowsMany = 2048;
 
 template <typename X>
@@ -120,7 +123,7 @@ __global__ void __launch_bounds__(kRowThreads)
 template <typename X, int PARTS>
 static int launch_rows(const X *x, int64_t x_stride, int64_t n, int K, const int32_t *n_opt, const int32_t *order, int k,
                        uint16_t *to, float *row_scale, cudaStream_t st) {
-    const int per = n >= kRowsMany ? 32 : 128, rows = kRowThreads / per;
+    const int per = n >= kRowsMany && K <= 32 * 8 * kRowHold ? 32 : 128, rows = kRowThreads / per;
     auto kernel = per == 32 ? q4_rows_kernel<X, PARTS, 32> : q4_rows_kernel<X, PARTS, 128>;
     return launch_pdl(kernel, dim3((unsigned)((n + rows - 1) / rows)), dim3(kRowThreads), 0, st, x, x_stride, n, K, n_opt,
                       order, k, to, row_scale);
