@@ -2,8 +2,9 @@
 // tokens, and the experts' feed-forward blocks.
 //
 // Experts: the gate and up rows are one product that ends in h = silu(gate) * up, kept in binary32 at
-// the pairs' places by expert; the down rows' product leaves an output row per pair; a last kernel adds
-// each token's up in the order of its places (no atomics, so the same inputs give the same bits).
+// the pairs' places by expert; the down rows' product leaves an output row per pair, in binary32; a last kernel adds
+// each token's up in the order of its places (no atomics, so the same inputs give the same bits).  Few pairs per expert:
+// three kernels (lb_q4_gemv.cu twice); many: five, with rows for the tensor cores laid out before each product.
 #include "lb_q4.cuh"
 
 #include <algorithm>
@@ -12,8 +13,9 @@ namespace lb {
 
 constexpr int kCombineThreads = 256;
 
-// Eight columns of a token per thread.  (The experts' outputs in fp16, scaled for every 32 rows, make this 7 us shorter for
-// 32768 of 2048 and the product that leaves them 50 us longer.)
+// y[t] = sum over j of weights[t][j] * part[t k + j].  Bound by memory: k numbers of 4 bytes in for one out.  Eight columns
+// of a token per thread.  (The experts' outputs in fp16, scaled for every 32 rows, make this 7 us shorter for 32768 of
+// 2048 and the product that leaves them 50 us longer.)
 template <typename T>
 __global__ void __launch_bounds__(kCombineThreads)
     experts_combine_kernel(const float *part, const int32_t *ids, const float *weights, T *y,

@@ -556,10 +556,11 @@ int lb_logits_adjust(const void *logits, int type, int64_t stride, void *out, in
  *       y_stride elements apart.  y may not overlap x.
  *   workspace : at least lb_gemm_q4_workspace_bytes(M, N, K, type) bytes, 16-byte aligned, owned by the
  *       caller, not used by another call that may run at the same time; it needs no initialization.
- * Up to eight tokens every product c - z times x is exact (an fp32 x enters as three bf16 parts), a
- * group's products are added up on the tensor cores and its scale acts on the sum in binary32.  For
- * more tokens, with bf16 tensors, weights round to 11 bits; with fp32 ones they, and x, enter as two fp16 parts
- * (22 bits of a row of x below its largest value, and 2^-38 of that).  Sums are held in binary32.
+ * Sums are held in binary32; c - z is exact.  A number of x enters with all of its bits if tensors are bf16, with 22
+ * (two fp16 parts) if they are fp32, and loses at most 2^-39 of the largest of its 256 columns (up to eight tokens) or
+ * of its row (more) where it is far smaller than that.  With bf16 tensors and more than eight tokens a weight
+ * d * (c - z) rounds to 11 bits, beyond 65504 to infinity; otherwise a scale acts on its group's sum in binary32.
+ * A token with a NaN or an infinite number gets nothing finite in its row of y; other rows do not change.
  * 1 <= N <= 2^23; group <= K <= LB_Q4_MAX_K; 0 <= M <= 2^20 (0: nothing is done); x and its stride in
  * bytes 16-byte aligned, y aligned to its elements; strides >= K and N, below 2^31. */
 int lb_gemv_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros_opt, int group,
@@ -574,7 +575,7 @@ int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zero
  * the largest finite number):
  *   score  s_e = exp(x_e) / sum of exp(x)  (LB_ROUTE_SOFTMAX)  or  1 / (1 + exp(-x_e))  (LB_ROUTE_SIGMOID)
  *   key    x_e if there is no bias and group_best is 1 (the logits' own order), else the binary64
- *          number s_e + bias_e (bias 0 without one)
+ *          number s_e + bias_e (bias 0 without one; +inf allowed)
  *   An expert whose logit or bias is NaN or -inf is never chosen and adds nothing to a sum.
  *   With groups > 1, group g holds the experts [g E / groups, (g + 1) E / groups); its value is the sum
  *   of its group_best (1 or 2; fewer if fewer can be chosen) largest keys, and only the experts of the
@@ -619,8 +620,9 @@ int lb_route(const void *logits, int type, int64_t stride, int64_t T, int E, int
  *          pairs are those of order and expert_start (not falling, at most T * k; entries of order outside
  *          [0, T * k) are passed over).  The sum over j runs from 0 on.
  *   workspace : lb_experts_q4_workspace_bytes(T, E, k, hidden, ffn, type) bytes, 16-byte aligned, as above.
- * Precision as in lb_gemv_q4 / lb_gemm_q4; h and the experts' outputs are kept to at least two bf16 parts (16
- * bits) with bf16 tensors, in binary32 with fp32 ones.
+ * Precision as in lb_gemv_q4 / lb_gemm_q4 (weights may round to 11 bits with bf16 tensors, whatever the number of
+ * tokens).  h enters the down rows' products with 11 bits where tensors are bf16 and with 22 where they are fp32, below
+ * its largest value as x does; the experts' outputs are binary32.
  * 0 <= T (0: nothing is done), T * k <= 2^24; 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= LB_ROUTE_MAX_CHOSEN; hidden and
  * ffn multiples of group, at most LB_Q4_MAX_K; alignment as in lb_gemv_q4, 4-byte for the routing's. */
 size_t lb_experts_q4_workspace_bytes(int64_t T, int E, int k, int64_t hidden, int64_t ffn, int type);
