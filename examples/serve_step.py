@@ -1,7 +1,7 @@
 #!/usr/bin/env python3
 """Continuous batching on the low-bit library: a small random-weight decoder served step by step.
 
-    python examples/serve_step.py [--steps N]
+    python examples/serve_step.py [--steps N] [--experts]
 
 Every step takes whatever tokens the requests bring -- a prompt, a chunk of one, or the token just
 chosen -- and runs
@@ -9,7 +9,9 @@ chosen -- and runs
     per layer: lb_quantize_q8_0, lb_gemv/gemm_q2_0_g64_grouped (q|k|v), lb_kv4_append, lb_attn_kv4,
                and the output, gate|up and down projections
     lb_gemv_bf16, lb_logits_adjust         head, penalties, biases and a grammar's mask
-on fp32 activations.  Norms, rotary positions and the choice of the token are plain torch.
+on fp32 activations.  With --experts the feed-forward blocks are experts on 4-bit weights: lb_gemv/gemm_q4 (gate
+logits), lb_route and lb_experts_q4 in place of the two projections.  Norms, rotary positions and the choice of the
+token are plain torch.
 """
 import argparse
 import os
@@ -27,6 +29,7 @@ import synth
 
 HIDDEN, HEADS, KV_HEADS, DIM, FFN, LAYERS, VOCAB = 512, 8, 2, 64, 1024, 2, 1000
 PAGE, PAGES = 16, 256
+EXPERTS, CHOSEN, EXPERT_FFN, GROUP = 16, 2, 512, 64
 
 
 class Matrix:
@@ -38,6 +41,46 @@ class Matrix:
         self.bits = torch.empty(N * K // 4, dtype=torch.uint8, device="cuda")
         self.scales = torch.empty(N * lb.scale_stride(K, 64), dtype=torch.int16, device="cuda")
         lb.lb_repack_q2_0_g64(blocks, N, K, self.bits, self.scales)
+
+
+def matrix4(count, N, K, seed):
+    """count matrices [N][K] of random 4-bit codes with group scales and zeros."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(seed)
+    S = lb.scale_stride(K, GROUP)
+    return (torch.randint(0, 256, (count, N, K // 2), generator=g, device="cuda", dtype=torch.uint8),
+            ((0.5 + torch.rand(count, N, S, generator=g, device="cuda")) / (5 * K ** 0.5)).half(),
+            torch.randint(6, 10, (count, N, S), generator=g, device="cuda", dtype=torch.uint8))
+
+
+class Experts:
+    """A feed-forward layer of EXPERTS gated blocks, CHOSEN of them for each token."""
+
+    def __init__(self, seed):
+        self.gate = matrix4(1, EXPERTS, HIDDEN, seed)
+        self.up = matrix4(EXPERTS, 2 * EXPERT_FFN, HIDDEN, seed + 1)
+        self.down = matrix4(EXPERTS, HIDDEN, EXPERT_FFN, seed + 2)
+
+    def __call__(self, x):
+        """x [T][HIDDEN] fp32 -> the experts' weighted sum."""
+        T, i32, f32 = len(x), dict(dtype=torch.int32, device="cuda"), dict(dtype=torch.float32, device="cuda")
+
+        def scratch(n):
+            return torch.empty(n, dtype=torch.uint8, device="cuda")
+
+        x = x.contiguous()
+        logits = torch.empty((T, EXPERTS), **f32)
+        lb.lb_gemm_q4(*self.gate, GROUP, x, lb.OUT_F32, HIDDEN, logits, EXPERTS, T, EXPERTS, HIDDEN,
+                      scratch(lb.lb_gemm_q4_workspace_bytes(T, EXPERTS, HIDDEN, lb.OUT_F32)))
+        ids, weights = torch.empty((T, CHOSEN), **i32), torch.empty((T, CHOSEN), **f32)
+        start, order = torch.empty(EXPERTS + 1, **i32), torch.empty(T * CHOSEN, **i32)
+        lb.lb_route(logits, lb.OUT_F32, EXPERTS, T, EXPERTS, CHOSEN, lb.ROUTE_SOFTMAX, ids, weights, start, order,
+                    scratch(lb.lb_route_workspace_bytes(T, EXPERTS)))
+        y = torch.empty_like(x)
+        lb.lb_experts_q4(x, lb.OUT_F32, HIDDEN, T, EXPERTS, CHOSEN, HIDDEN, EXPERT_FFN, GROUP, self.up, self.down, ids,
+                         weights, start, order, y, HIDDEN,
+                         scratch(lb.lb_experts_q4_workspace_bytes(T, EXPERTS, CHOSEN, HIDDEN, EXPERT_FFN, lb.OUT_F32)))
+        return y
 
 
 def project(x, mats):
@@ -68,7 +111,7 @@ def rotate(x, position):
 
 
 class Server:
-    def __init__(self, requests, grammar=None, seed=0):
+    def __init__(self, requests, grammar=None, seed=0, experts=False):
         g = torch.Generator(device="cuda")
         g.manual_seed(seed)
         self.R = requests
@@ -81,7 +124,7 @@ class Server:
                                          Matrix(KV_HEADS * DIM, HIDDEN, s + 2)],
                                     out=[Matrix(HIDDEN, HEADS * DIM, s + 3)],
                                     up=[Matrix(FFN, HIDDEN, s + 4), Matrix(FFN, HIDDEN, s + 5)],
-                                    down=[Matrix(HIDDEN, FFN, s + 6)],
+                                    down=[Matrix(HIDDEN, FFN, s + 6)], experts=Experts(s + 7) if experts else None,
                                     cache=torch.empty(lb.kv4_cache_bytes(PAGES, KV_HEADS, PAGE, DIM),
                                                       dtype=torch.uint8, device="cuda")))
         i32 = dict(dtype=torch.int32, device="cuda")
@@ -119,8 +162,11 @@ class Server:
             lb.lb_attn_kv4(q, lb.OUT_F32, HEADS * DIM, layer["cache"], PAGES, PAGE, HEADS, KV_HEADS, DIM, self.table,
                            PAGES, q_start, kv_len, R, T, most, DIM ** -0.5, True, 0, a, HEADS * DIM, None, ws)
             x = x + project(a.flatten(1), layer["out"])[0]
-            gate, up = project(norm(x), layer["up"])
-            x = x + project(torch.nn.functional.silu(gate) * up, layer["down"])[0]
+            if layer["experts"]:
+                x = x + layer["experts"](norm(x))
+            else:
+                gate, up = project(norm(x), layer["up"])
+                x = x + project(torch.nn.functional.silu(gate) * up, layer["down"])[0]
         last = norm(x[(q_start[1:] - 1).clamp(min=0).long()])
         logits = torch.empty((R, VOCAB), dtype=torch.float32, device="cuda")
         lb.lb_gemv_bf16(self.head, last, logits, VOCAB, HIDDEN, R)
@@ -176,10 +222,12 @@ def grammar_of(allowed):
 def main():
     ap = argparse.ArgumentParser()
     ap.add_argument("--steps", type=int, default=12)
-    steps = ap.parse_args().steps
+    ap.add_argument("--experts", action="store_true")
+    args = ap.parse_args()
+    steps = args.steps
     rng = np.random.default_rng(0)
     prompts = [rng.integers(0, VOCAB, n).tolist() for n in (70, 3, 33)]
-    server = Server(len(prompts), grammar=grammar_of(range(0, VOCAB, 2)))
+    server = Server(len(prompts), grammar=grammar_of(range(0, VOCAB, 2)), experts=args.experts)
     for prompt, answer in zip(prompts, server.generate(prompts, steps)):
         print(f"{len(prompt)} prompt tokens -> {answer}")
     assert lb.lb_device_status() == 0
