@@ -139,12 +139,32 @@ int q4_rows(const void *x, bool f32, int64_t x_stride, int64_t n, int K, const i
                       : launch_rows<float, 1>(v, x_stride, n, K, n_opt, order, k, to, row_scale, st);
 }
 
+// About the clocks that a call takes with items of so many tokens: rounds of items, each so many clocks a step, and what
+// one accumulator cannot hide behind the next item's products, or sums of a cluster cost.
+static int64_t gemm_clocks(const Q4Params &p, int tokens, int sms) {
+    const int64_t tiles = (p.N + kGmRows - 1) / kGmRows, pieces = (p.T + tokens - 1) / tokens;
+    int64_t steps = (p.K + kGmStep - 1) / kGmStep, rounds = 1, sums = 0;
+    if (tiles * pieces * 2 <= sms) {
+        const int64_t split = std::min<int64_t>({sms / (tiles * pieces), kGmMaxSplit, std::max<int64_t>(steps / 4, 1)});
+        steps = (steps + split - 1) / split;
+        sums = split > 1 ? 5000 : 0;
+    } else {
+        const int64_t clusters = sms / kGmShare;
+        rounds = (pieces * ((tiles + kGmShare - 1) / kGmShare) + clusters - 1) / clusters;
+    }
+    return rounds * (tokens == 128 ? 450 * steps : tokens == 176 ? 490 * steps : 520 * steps + 8000) + sums;
+}
+
 int q4_gemm_dense(const Q4Params &p, const Q4Rows &r, int type, const uint8_t *codes, int64_t rows, int sms,
                   cudaStream_t st) {
     if (type == LB_OUT_F32) return dispatch_gemm<kQ4Dense, float, 128>(p, r, codes, rows, sms, st);
-    // 256 tokens and one accumulator, or 128 and two in turn: the first expands weights half as often, the second
-    // hides what happens behind the last product, which a short K does not.
-    if (p.K >= kGmLongK) return dispatch_gemm<kQ4Dense, __nv_bfloat16, 256>(p, r, codes, rows, sms, st);
+    // Items of 256 tokens and one accumulator, or of 176 or 128 and two in turn: large ones expand weights less often, two
+    // accumulators hide what happens behind the last product, and items come in rounds.  us with 128, 176 and 256: 4096 x
+    // 12288 x 4096 310, 256, 250; 2048 x 4096 with K = 2816 51, 43, 41, with 768 23, 21, 21; 500 x 4096 with K = 2048 16.6,
+    // 17.9, 22.6.
+    const int64_t t128 = gemm_clocks(p, 128, sms), t176 = gemm_clocks(p, 176, sms), t256 = gemm_clocks(p, 256, sms);
+    if (t256 < t128 && t256 < t176) return dispatch_gemm<kQ4Dense, __nv_bfloat16, 256>(p, r, codes, rows, sms, st);
+    if (t176 < t128) return dispatch_gemm<kQ4Dense, __nv_bfloat16, 176>(p, r, codes, rows, sms, st);
     return dispatch_gemm<kQ4Dense, __nv_bfloat16, 128>(p, r, codes, rows, sms, st);
 }
 

@@ -42,19 +42,19 @@ constexpr int kGmWarps = kGmMmaWarp + 2;   // (whole groups of four)
 constexpr int kGmThreads = 32 * kGmWarps;
 constexpr int kGmOutThreads = 32 * kGmOutWarps;
 constexpr int kGmC = kGmRows * 64;       // bytes of a stage of codes: two steps
-constexpr int kGmABase = 256;            // expanded weights, 32 columns of tensor memory a stage, lie behind the accumulators
 
 constexpr int kGmMaxSplit = 8;           // a portable cluster
 constexpr int kGmShare = 2;
-// bf16 tensors, columns from which items of 256 tokens and one accumulator are ahead of 128 tokens and two (K = 4096:
-// 255 against 316 us for 4096 x 12288).
-constexpr int kGmLongK = 2048;
 // What depends on the tokens of an item (with two parts: of each).
 template <int TOKENS, int PARTS>
 struct GmShape {
     static constexpr int kB = TOKENS * 128 * PARTS;                // bytes of a stage of x
-    static constexpr int kStages = kB == 32768 ? 5 : 8;            // of x and of expanded weights
+    static constexpr int kBuffers = TOKENS > 176 ? 1 : 2;          // accumulators
+    static constexpr int kABase = kBuffers * TOKENS;               // expanded weights lie behind them, 32 columns a stage
+    static constexpr int kStages = kB > 16384 ? 5 : 8;             // of x and of expanded weights
     static constexpr int kCStages = kB == 32768 ? 6 : 10;          // of codes
+    static_assert(kABase + 32 * kStages <= 512, "tensor memory");
+    static_assert(TOKENS % 16 == 0, "pieces are multiples of 16");
     static constexpr int kSmem = kStages * kB + kCStages * kGmC;
 };
 constexpr int kGmMaxStages = 8, kGmMaxCStages = 10;
@@ -228,11 +228,11 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                    const __grid_constant__ GmLaunch l) {
     constexpr bool F32 = sizeof(T) == 4;
     constexpr int kTokens = TOKENS;
-    constexpr int kBuffers = 256 / TOKENS;       // accumulators
     constexpr int kParts = F32 ? 2 : 1;
-    constexpr int kCols = kTokens / 2;           // of an output warp
+    constexpr int kCols = (kTokens / 2 + 15) / 16 * 16;   // of an output warp, at most
     using Shape = GmShape<TOKENS, kParts>;
     constexpr int kGmStages = Shape::kStages, kGmB = Shape::kB, kGmCStages = Shape::kCStages;
+    constexpr int kBuffers = Shape::kBuffers, kGmABase = Shape::kABase;
     extern __shared__ __align__(1024) uint8_t smem[];
     __shared__ GmBars bar;
     __shared__ uint32_t s_tmem;
@@ -363,20 +363,20 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     if (warp < kGmOutWarps) {
         // =================== sums out: a lane per weight row ===================
         if constexpr (F32) gm_more_registers<144>();
-        const int quarter = warp & 3, c0 = (warp >> 2) * kCols;
-        const uint32_t at_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
+        const int quarter = warp & 3;
         uint32_t turn = 0;   // accumulators taken so far
         // scale and output row of an item's column tid
         float scale = 0.f;
         int to = 0;
+        GmItem ahead{0, 0, 0, 0};
         auto ask = [&](int i) {
             if (i >= items) return;
-            const GmItem it = item_of(i);
-            if (tid >= it.tokens) return;
-            scale = r.row_scale[it.t0 + tid];
-            to = it.t0 + tid;
+            ahead = item_of(i);
+            if (tid >= ahead.tokens) return;
+            scale = r.row_scale[ahead.t0 + tid];
+            to = ahead.t0 + tid;
             if (USE == kQ4Down) {
-                const int pair = p.order[it.t0 + tid];
+                const int pair = p.order[ahead.t0 + tid];
                 to = pair >= 0 && pair < p.T ? pair : -1;
             }
         };
@@ -390,11 +390,14 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         tell();
 #pragma unroll 1
         for (int i = begin; i < items; i += each) {
-            const GmItem it = item_of(i);
+            const GmItem it = ahead;
             ask(i + each);
             bool in;
             const int64_t row = row_of(it, quarter * 32 + lane, in);
-            const int mine = min(max(it.tokens - c0, 0), kCols);   // columns of this warp
+            // half of the columns each, in sixteens
+            const int half = (it.tokens + 31) / 32 * 16, c0 = warp < 4 ? 0 : half;
+            const int mine = warp < 4 ? min(it.tokens, half) : it.tokens - min(it.tokens, half);
+            const uint32_t at_lane = tmem + ((uint32_t)(quarter * 32) << 16) + c0;
             float *park = reinterpret_cast<float *>(smem) + c0 * kGmRows + quarter * 32 + lane;   // [column][128]
             // 16 columns from c (of this warp's) on
             auto emit = [&](int c, const float (&v)[16]) {
