@@ -21,10 +21,11 @@
 // with neighbouring tiles of the same tokens form a cluster and copy half of x each, to both: every SM on its
 // own would ask the L2 for 64 bytes a cycle.
 //
-// What bounds it: with many tokens the products (4096 x 12288 x 4096 bf16: 240 us, the tensor pipe busy for 77 % of
-// them); with few per item the expansion of weights, about 280 clocks a step of 64 columns, and the hand-overs between
-// warps, about 300 (49 tokens for each of 128 experts: issue slots 55 %, DRAM 33 %); in fp32 the products' issue and a
-// drain per group, about 1000 clocks a step (509 x 6912 x 2560: 44 us).
+// What bounds it: with many tokens the products (4096 x 12288 x 4096 bf16: 238 us, the tensor pipe busy for 77 % of
+// them); with few per item, at 480 clocks a step of 64 columns, issue slots (55 %) and latency: the warps that expand
+// weights are busy for 300, the one that issues products for 300, the one that copies x for 370 (49 tokens for each of
+// 128 experts, DRAM 33 %); in fp32 the products' issue and a drain per group, about 1000 clocks a step (509 x 6912 x
+// 2560: 45 us).
 #pragma once
 #include "lb_q4.cuh"
 #include "lb_tc.cuh"
