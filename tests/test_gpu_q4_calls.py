@@ -145,3 +145,14 @@ def test_no_tokens(dtype):
     ws = torch.empty(lb.lb_experts_q4_workspace_bytes(0, 8, 2, 256, 192, TYPES[dtype]), dtype=torch.uint8, device="cuda")
     lb.lb_experts_q4(x, TYPES[dtype], 256, 0, 8, 2, 256, 192, group, up, down, ids, w, start, order, y, 256, ws)
     assert bool((y == 7.0).all())
+
+
+@pytest.mark.parametrize("dtype", TYPES)
+@pytest.mark.parametrize("T,N,K,group,zeros", [
+    (500, 4096, 2048, 64, True), (2047, 4096, 768, 32, False), (1001, 4095, 4096, 128, True),
+    (1000, 4096, 4064, 32, True)])
+def test_items_of_every_size(dtype, T, N, K, group, zeros):
+    """Calls large enough for whole rounds of items: with bf16 tensors of 128, 176 and 256 tokens."""
+    g = generator(T + K)
+    x = torch.randn(T, K, generator=g, device="cuda").to(dtype)
+    check(x, one(g, N, K, group, zeros), N, K, group)
