@@ -149,8 +149,7 @@ static int64_t gemm_clocks(const Q4Params &p, int tokens, int sms) {
         steps = (steps + split - 1) / split;
         sums = split > 1 ? 5000 : 0;
     } else {
-        const int64_t clusters = sms / kGmShare;
-        rounds = (pieces * ((tiles + kGmShare - 1) / kGmShare) + clusters - 1) / clusters;
+        rounds = (pieces * tiles + sms - 1) / sms;
     }
     return rounds * (tokens == 128 ? 450 * steps : tokens == 176 ? 490 * steps : 520 * steps + 8000) + sums;
 }
@@ -160,8 +159,8 @@ int q4_gemm_dense(const Q4Params &p, const Q4Rows &r, int type, const uint8_t *c
     if (type == LB_OUT_F32) return dispatch_gemm<kQ4Dense, float, 128>(p, r, codes, rows, sms, st);
     // Items of 256 tokens and one accumulator, or of 176 or 128 and two in turn: large ones expand weights less often, two
     // accumulators hide what happens behind the last product, and items come in rounds.  us with 128, 176 and 256: 4096 x
-    // 12288 x 4096 310, 256, 250; 2048 x 4096 with K = 2816 51, 43, 41, with 768 23, 21, 21; 500 x 4096 with K = 2048 16.6,
-    // 17.9, 22.6.
+    // 12288 x 4096 309, 264, 255; 2048 x 4096 with K = 2816 49, 43, 40, with 768 21, 20, 21; 500 x 4096 with K = 2048 16.4,
+    // 16.5, 22.6.
     const int64_t t128 = gemm_clocks(p, 128, sms), t176 = gemm_clocks(p, 176, sms), t256 = gemm_clocks(p, 256, sms);
     if (t256 < t128 && t256 < t176) return dispatch_gemm<kQ4Dense, __nv_bfloat16, 256>(p, r, codes, rows, sms, st);
     if (t176 < t128) return dispatch_gemm<kQ4Dense, __nv_bfloat16, 176>(p, r, codes, rows, sms, st);

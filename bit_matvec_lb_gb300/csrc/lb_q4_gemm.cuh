@@ -16,10 +16,9 @@
 //
 // One CTA per SM, 20 warps (one has nothing to do): eight that take the sums out (a quarter of the lanes times half of
 // the columns each), eight that expand weights, one that has codes copied in (tensor copies, 128 rows x 128
-// columns), one that has x copied in (tensor copies of 64 rows x 64 columns), one that issues the tensor-core operations.  Calls with few tiles are
-// split along K over a cluster; the parts are added up through distributed shared memory.  In others two CTAs
-// with neighbouring tiles of the same tokens form a cluster and copy half of x each, to both: every SM on its
-// own would ask the L2 for 64 bytes a cycle.
+// columns), one that has x copied in (tensor copies of half of an item's tokens x 64 columns), one that issues the tensor-core
+// operations.  Each CTA copies what it multiplies into its own shared memory.  Calls with few tiles are split along K over
+// a cluster; the parts are added up through distributed shared memory.
 //
 // What bounds it: with many tokens the products (4096 x 12288 x 4096 bf16: 238 us, the tensor pipe busy for 77 % of
 // them); with few per item, at 480 clocks a step of 64 columns, issue slots (55 %) and latency: the warps that expand
@@ -45,7 +44,6 @@ constexpr int kGmOutThreads = 32 * kGmOutWarps;
 constexpr int kGmC = kGmRows * 64;       // bytes of a stage of codes: two steps
 
 constexpr int kGmMaxSplit = 8;           // a portable cluster
-constexpr int kGmShare = 2;
 // What depends on the tokens of an item (with two parts: of each).  Of tensor memory's 512 columns two accumulators of 176
 // tokens leave as many as five stages of weights take; 256 tokens leave room for one accumulator, whose way out then is
 // not hidden (a third of the time of experts' products with 205 tokens a piece, 12 % with K = 4096).
@@ -65,11 +63,10 @@ constexpr int kGmMaxStages = 8, kGmMaxCStages = 10;
 struct GmLaunch {
     int steps;        // of K, of a CTA
     int split;        // CTAs along K, a cluster
-    int share;        // CTAs that take the same tokens times tiles side by side, a cluster (split 1 then)
     int box;          // tokens of a copy
     int pairs;        // two rows of a bf16 y may be stored as one word
     int tokens;       // of an item, at most (dense)
-    int tiles;        // of weight rows, a multiple of share (the last ones may lie behind the matrix)
+    int tiles;        // of weight rows
 };
 
 struct GmBars {
@@ -172,25 +169,6 @@ __device__ __forceinline__ void gm_cluster_sync() {
     asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
 }
 
-// 2-D tensor copy into the same place of every CTA of the cluster that mask names, counted on each one's own
-// barrier at b's place.
-__device__ __forceinline__ void gm_load_multicast(void *dst, const CUtensorMap *map, int x, int y, uint64_t *b,
-                                                  uint16_t mask) {
-    asm volatile(
-        "cp.async.bulk.tensor.2d.shared::cluster.global.mbarrier::complete_tx::bytes.multicast::cluster [%0], [%1, "
-        "{%2, %3}], [%4], %5;" ::"r"(smem_u32(dst)),
-        "l"(reinterpret_cast<uint64_t>(map)), "r"(x), "r"(y), "r"(smem_u32(b)), "h"(mask)
-        : "memory");
-}
-// Arrive once on `b` of every CTA that mask names when the products issued so far have completed.
-__device__ __forceinline__ void gm_commit_multicast(uint64_t *b, uint16_t mask) {
-    asm volatile(
-        "tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.multicast::cluster.b64 [%0], %1;" ::"r"(
-            smem_u32(b)),
-        "h"(mask)
-        : "memory");
-}
-
 // On to the next scales and zeros of a warp that takes every other unit of 128 columns.
 template <int GROUP>
 __device__ __forceinline__ void q4_rotate(uint4 &d, uint2 &z) {
@@ -247,11 +225,10 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     // (from the warp's first lane: what is made of it stays in the uniform registers that the operations take)
     const int tid = threadIdx.x, lane = tid & 31, warp = __shfl_sync(0xffffffffu, tid >> 5, 0);
     const int rank = blockIdx.x % l.split;            // along K
-    const int cluster = l.split * l.share;
 
     if (tid == 0) {
         // a stage is full when its four warps of weights and the copies of x are there
-        for (int i = 0; i < kGmStages; i++) mbar_init(&bar.full[i], 5), mbar_init(&bar.empty[i], l.share);
+        for (int i = 0; i < kGmStages; i++) mbar_init(&bar.full[i], 5), mbar_init(&bar.empty[i], 1);
         for (int i = 0; i < kGmCStages; i++) mbar_init(&bar.c_full[i], 1), mbar_init(&bar.c_empty[i], 4);
         for (int i = 0; i < 2; i++) mbar_init(&bar.d_full[i], 1), mbar_init(&bar.d_empty[i], kGmOutWarps);
         mbar_init(&bar.done, 1);
@@ -301,18 +278,16 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     // it: neither waits for the other's columns.
     if (warp == kGmMmaWarp) tmem_alloc(&s_tmem, 512);
     tc_fence_before();
-    if (l.share > 1) gm_cluster_sync();   // (everybody's barriers are there)
-    else __syncthreads();
+    __syncthreads();
     tc_fence_after();
     pdl_launch_dependents();
     const uint32_t tmem = __shfl_sync(0xffffffffu, s_tmem, 0);
-    const int side = l.tiles / l.share;
-    const int items = pieces * side;   // of a cluster
-    const int each = gridDim.x / cluster, begin = blockIdx.x / cluster;
+    const int items = pieces * l.tiles;
+    const int each = gridDim.x / l.split, begin = blockIdx.x / l.split;
     auto item_of = [&](int i) {
         GmItem it;
-        const int piece = i / side;
-        it.tile = (i - piece * side) * l.share + blockIdx.x % l.share;
+        const int piece = i / l.tiles;
+        it.tile = i - piece * l.tiles;
         if constexpr (USE == kQ4Dense) {
             it.expert = 0;
             it.t0 = piece * l.tokens;
@@ -709,7 +684,6 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             const GmItem it = item_of(i);
             const int boxes = (it.tokens + l.box - 1) / l.box;
             const uint32_t bytes = (uint32_t)(kParts * boxes * l.box * 128);
-            const int side = l.share > 1 ? blockIdx.x % l.share : 0;
 #pragma unroll 1
             for (int s = 0; s < steps; s++) {
                 wait(bar.empty[ring.i], ring.phase ^ 1);
@@ -718,14 +692,12 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                     uint64_t *b = &bar.full[ring.i];
                     mbar_arrive_expect_tx(b, bytes);
                     const int byte = (k0 + s * kGmStep) * 2;
-                    // the CTAs that share the tokens copy every share-th box to all of them
-                    for (int box = side; box < boxes; box += l.share) {
+                    for (int box = 0; box < boxes; box++) {
 #pragma unroll
                         for (int part = 0; part < kParts; part++) {
                             uint8_t *to = smem + ring.i * kGmB + part * (kGmB / 2) + box * l.box * 128;
                             const int row = part * (int)r.rows + it.t0 + box * l.box;
-                            if (l.share > 1) gm_load_multicast(to, &x_map, byte, row, b, (uint16_t)((1 << l.share) - 1));
-                            else tma_load_2d(to, &x_map, byte, row, b);
+                            tma_load_2d(to, &x_map, byte, row, b);
                         }
                     }
                 }
@@ -734,12 +706,11 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 used = min(used + 1, kGmStages);
             }
         }
-        // (the other CTA's arrivals have to have come, too, before this one may exit)
+        // no copy may still be landing when the CTA exits
         for (int n = 0; n < used; n++) {
             if (ring.i == 0) ring.i = kGmStages, ring.phase ^= 1;
             ring.i--;
             wait(bar.full[ring.i], ring.phase);
-            wait(bar.empty[ring.i], ring.phase);
         }
     } else if (warp == kGmMmaWarp) {
         // =================== tensor-core operations ===================
@@ -758,8 +729,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                 if constexpr (!F32) {
                     if (gm_elect()) {
                         gm_mma4(at_d, a, b, idesc, s > 0);
-                        if (l.share > 1) gm_commit_multicast(&bar.empty[ring.i], (uint16_t)((1 << l.share) - 1));
-                        else mma_commit(&bar.empty[ring.i]);
+                        mma_commit(&bar.empty[ring.i]);
                     }
                 } else {
                     constexpr int kTurns = GROUP == 32 ? 2 : 1;   // accumulators of a step
@@ -785,10 +755,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                         if (GROUP < 128 || s % 2 == 1) taken++;
                         __syncwarp();
                     }
-                    if (gm_elect()) {
-                        if (l.share > 1) gm_commit_multicast(&bar.empty[ring.i], (uint16_t)((1 << l.share) - 1));
-                        else mma_commit(&bar.empty[ring.i]);
-                    }
+                    if (gm_elect()) mma_commit(&bar.empty[ring.i]);
                 }
                 __syncwarp();
                 ring.next();
@@ -836,7 +803,6 @@ __global__ void __launch_bounds__(kGmThreads, 1)
             gm_cluster_sync();
         }
     }
-    if (l.share > 1) gm_cluster_sync();   // nobody's copies or arrivals come after a CTA has gone
     if (warp == kGmMmaWarp) tmem_dealloc(tmem, 512);
 }
 
@@ -853,8 +819,8 @@ static int launch_gemm(const CUtensorMap &code_map, const CUtensorMap &x_map, co
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
     attr[0].val.programmaticStreamSerializationAllowed = 1;
     attr[1].id = cudaLaunchAttributeClusterDimension;
-    attr[1].val.clusterDim.x = (unsigned)(l.split * l.share), attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
-    cfg.attrs = attr, cfg.numAttrs = l.split * l.share > 1 ? 2 : 1;
+    attr[1].val.clusterDim.x = (unsigned)l.split, attr[1].val.clusterDim.y = attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr, cfg.numAttrs = l.split > 1 ? 2 : 1;
     const cudaError_t e = cudaLaunchKernelEx(&cfg, kernel, code_map, x_map, p, r, l);
     if (e == cudaSuccess) return LB_OK;
     record_cuda_error(e);
@@ -870,9 +836,9 @@ static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *code
     l.tokens = (int)((p.T + pieces - 1) / pieces + 15) / 16 * 16;
     l.tiles = (int)tiles;
     const int steps = (p.K + kGmStep - 1) / kGmStep;
-    l.split = 1, l.steps = steps, l.share = 1;
+    l.split = 1, l.steps = steps;
     l.pairs = p.N % 2 == 0 && p.y_stride % 2 == 0 && aligned_to(p.y, 4);
-    l.box = p.T <= 16 ? 16 : p.T <= 32 ? 32 : TOKENS / 2;   // (two, one from each CTA that shares them)
+    l.box = p.T <= 16 ? 16 : p.T <= 32 ? 32 : TOKENS / 2;   // (small items need one of the two)
     int64_t items = tiles * pieces;
     if (USE != kQ4Dense) items = tiles * std::min(p.T, std::min((int64_t)p.E, p.T) + p.T / TOKENS);
     if (USE == kQ4Dense && items * 2 <= sms) {
@@ -882,13 +848,7 @@ static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *code
         l.steps = (l.steps + 1) / 2 * 2;
         l.split = (steps + l.steps - 1) / l.steps;
     }
-    if (l.split == 1 && tiles > 1) {
-        l.share = kGmShare;
-        l.tiles = (int)((tiles + l.share - 1) / l.share * l.share);
-        items = items / tiles * (l.tiles / l.share);   // a cluster's
-    }
-    const int64_t most = l.split > 1 ? items : sms / l.share;
-    const unsigned grid = (unsigned)(std::min(items, most) * l.split * l.share);
+    const unsigned grid = (unsigned)(l.split > 1 ? items * l.split : std::min<int64_t>(items, sms));
     CUtensorMap codes_map, x_map;
     if (int e = encode_rows_map(&codes_map, codes, (uint64_t)p.K / 2, (uint64_t)code_rows, 64, kGmRows / 2, 64)) return e;
     if (int e = encode_rows_map(&x_map, r.x, (uint64_t)p.K * 2, (uint64_t)r.rows * (sizeof(T) == 4 ? 2 : 1), 128,

@@ -7,8 +7,8 @@ int q4_gemm_experts(const Q4Params &p, const Q4Rows &r, Q4Use use, int type, con
                     int sms, cudaStream_t st) {
     const bool f32 = type == LB_OUT_F32;
     // Pieces of 176 tokens expand weights less often, ones of 128 have more stages in flight: 32 experts of 2048 x 1024, 50,
-    // 87, 137 and 375 tokens each: 80, 80, 98 and 191 us against 76, 87, 107 and 211 (256 and one accumulator: 80, 91, 105
-    // and 209).
+    // 87, 137 and 375 tokens each: 76.0, 78, 93 and 194 us against 75.7, 84, 103 and 207 (256 and one accumulator: 76.0, 82,
+    // 93 and 189).
     const bool wide = p.T > 64 * (int64_t)p.E;
     if (use == kQ4Up)
         return f32    ? dispatch_gemm<kQ4Up, float, 128>(p, r, codes, rows, sms, st)
