@@ -19,6 +19,7 @@
 // keys are looked through again only when that happens to it a second time.
 #include "lb_kv4.cuh"
 
+#include <algorithm>
 #include <cfloat>
 
 namespace lb {
@@ -594,8 +595,9 @@ LB_EXPORT size_t lb_route_workspace_bytes(int64_t T, int E) {
     using namespace lb;
     if (T < 0 || T > (1 << 20) || E < 1 || E > LB_ROUTE_MAX_EXPERTS) return 0;
     if (T <= kRouteTile) return 16;
-    const int64_t tile = route_tile(T);
-    return (size_t)((T + tile - 1) / tile) * ((E + 7) / 8 * 8) * 2;
+    // (counts of as many CTAs as T, or any smaller number of tokens, can take: fewer where tiles have grown)
+    const int64_t ctas = std::min<int64_t>((T + kRouteTile - 1) / kRouteTile, kRouteMaxCtas);
+    return (size_t)ctas * ((E + 7) / 8 * 8) * 2;
 }
 
 LB_EXPORT int lb_route(const void *logits, int type, int64_t stride, int64_t T, int E, int k,

@@ -588,7 +588,7 @@ int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zero
  * Tokens from *live_opt on (NULL: none; below 0 counts as 0) get ids -1 and weights 0, and their logits are not read.
  *   logits : [T][E] fp32 (type LB_OUT_F32) or bf16 (LB_OUT_BF16), rows `stride` elements apart.
  *   ids : [T][k] int32.  weights : [T][k] fp32.  expert_start : [E + 1] int32.  order : [T * k] int32.
- *   workspace : lb_route_workspace_bytes(T, E) bytes, 16-byte aligned, as above.
+ *   workspace : lb_route_workspace_bytes(T, E) bytes (never fewer for more tokens), 16-byte aligned, as above.
  * Scores are computed in binary32, and in binary64 where two keys lie too close together for that;
  * exp(x - max) of experts more than 100 below the row's largest logit counts as 0 in the weights.
  * 0 <= T <= 2^20 (at 0 only expert_start is written); 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= min(E,
