@@ -306,8 +306,8 @@ def lb_device_status(stream=None) -> int:
 
 
 def lb_test_inject_wait_timeout(wait_us: int):
-    """Test hook: the next streaming GEMV call starves its first CTA, whose bounded wait then
-    gives up after wait_us microseconds (reported by lb_device_status as LB_ERR_DEVICE)."""
+    """Test hook: the next streaming GEMV call or 4-bit product starves its first CTA, whose bounded
+    wait then gives up after wait_us microseconds (reported by lb_device_status as LB_ERR_DEVICE)."""
     _check("lb_test_inject_wait_timeout", load().lb_test_inject_wait_timeout(int(wait_us)))
 
 

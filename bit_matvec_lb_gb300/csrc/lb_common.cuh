@@ -44,7 +44,7 @@ int encode_rows_map(CUtensorMap *map, const void *base, uint64_t row_bytes, uint
                     uint32_t box_bytes, uint32_t box_rows, int swizzle_bytes = 0);
 
 // Test hook: the wait limit in microseconds set by lb_test_inject_wait_timeout (then cleared),
-// or 0.  A streaming GEMV launch that takes a non-zero value makes CTA 0 copy no weights, so
+// or 0.  A streaming GEMV's or a 4-bit product's launch that takes a non-zero value makes CTA 0 copy no weights, so
 // that CTA's consumers give up after that many microseconds and report through the error word.
 int take_injected_wait_fault();
 

@@ -50,6 +50,7 @@ struct MvLaunch {
     int tokens;    // most tokens of a piece
     int split;     // CTAs along K, a cluster
     int tiles;     // of kMvRows rows (up: of half as many pairs)
+    int fault;     // test hook: the first CTA with a unit copies no weights and waits so many microseconds for them
 };
 
 // (volatile: stays behind the wait for its stage)
@@ -98,6 +99,10 @@ __device__ __forceinline__ bool mv_try_wait_cluster(uint64_t *bar, uint32_t pari
         : "memory");
     return ok != 0;
 }
+// (apart, so that what the test hook needs takes no registers beside the products)
+__device__ __noinline__ static bool mv_wait_weights(uint64_t *bar, uint32_t parity, const int *fault) {
+    return mbar_wait_slow(bar, parity, *fault ? (uint64_t)*fault * 1000u : 2000000000ull);
+}
 // cp.async's of this thread so far arrive once on bar when they have landed (counted in the barrier's number).
 __device__ __forceinline__ void copies_arrive(uint64_t *bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(bar)) : "memory");
@@ -123,7 +128,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
     __shared__ __align__(16) float sums[2][kMvSums][16][kMvTokens];   // [rank, own warp][row][column]
     __shared__ int row_of[2][kMvTokens];
     __shared__ uint16_t s_first[kExperts];                       // pieces before an expert's
-    __shared__ int s_part[kMvThreads / 32];
+    __shared__ int s_part[kMvThreads / 32], s_fault;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = l.blocks * kMvBlock, rank = blockIdx.x % l.split;
     const int k0 = rank * slice, columns = min(p.K - k0, slice);
@@ -219,6 +224,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         bool ok = true;
         int at_piece = -1;
         Piece q{0, 0, 0, 0};
+        if (l.fault && rank == 0 && u_begin == 0) ok = false;
         for (int u = u_begin; u < u_end && ok; u++) {
             const int piece = u / l.tiles;
             const int64_t n0 = (int64_t)(u - piece * l.tiles) * kTileRows;
@@ -274,6 +280,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         if (l.split > 1) asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
     } else {
         // =================== products ===================
+        if (tid == 0) s_fault = rank == 0 && u_begin == 0 ? l.fault : 0;   // (read behind the first barrier below)
         if (USE == kQ4Dense) pdl_wait();
         const int g = lane >> 2, t = lane & 3;
         // the row this lane points ldmatrix at, and the two rows of its sums, in the tile
@@ -287,7 +294,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         const uint32_t tell[2] = {address_in(&sums_full[0], owner), address_in(&sums_full[1], owner)};
         int stage = 0;
         uint32_t phase = 0;
-        bool ok = true;
+        bool ok = true, heard = true;   // no wait for weights, none for sums has run out
         int at_piece = -1, cols = 0, planes = 1;
         Piece q{0, 0, 0, 0};
         // The parts of few tokens lie in one operand's eight columns, of more in an operand each.
@@ -314,7 +321,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         };
         // the sums of unit number n (of this cluster's), added up over the ranks and stored
         auto finish = [&](int n) {
-            if (ok) {
+            if (heard) {
                 const uint64_t t_0 = global_ns();
                 bool there = mv_try_wait_cluster(&sums_full[n & 1], (uint32_t)(n >> 1) & 1u);
                 for (uint32_t i = 1; !there; i++) {
@@ -323,7 +330,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
                 }
                 if (!__all_sync(0xffffffffu, there)) {
                     if (lane == 0) atomicOr(p.error, 1);
-                    ok = false;
+                    heard = false;
                 }
             }
             const int parts = packed(q_done) ? PARTS : 1;
@@ -411,7 +418,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
             const int plane = q.tokens * x_pitch;
             float total[4] = {0.f, 0.f, 0.f, 0.f};
             for (int b = 0; b < blocks && ok; b++) {
-                if (!__all_sync(0xffffffffu, mbar_wait(&full[stage], phase))) {
+                if (!__all_sync(0xffffffffu, mbar_try_wait(&full[stage], phase) || mv_wait_weights(&full[stage], phase, &s_fault))) {
                     if (lane == 0) atomicOr(p.error, 1);
                     ok = false;
                     break;
@@ -523,9 +530,13 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         if (l.split > 1) {
             if (n > 0) finish(n - 1);
             else asm volatile("barrier.cluster.wait.acquire;" ::: "memory");
+            // A CTA may go when nobody writes to it any more.  One whose waits for sums succeeded has by now all that are sent
+            // to it (one without weights sends what it has; each sum arrives once, even from a CTA that gave its wait up and
+            // ran ahead).  One that gave such a wait up does not know: it stays until every thread of the cluster has got
+            // here or gone.  (All of them always waiting for each other: 13.4 us for 13.0, 5 x 4096 x 12288.)
+            if (!heard) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
         }
     }
-    // (a CTA has all sums that are sent to it when its last unit is finished: it may go)
 }
 
 // How a call of given sizes is cut up.
@@ -607,6 +618,7 @@ static int launch_gemv(const Q4Params &p, const CUtensorMap &map, int64_t pieces
         return LB_ERR_LAUNCH;
     }
     if (!plan.clusters) return LB_ERR_LAUNCH;
+    plan.l.fault = take_injected_wait_fault();
     cudaLaunchConfig_t cfg = {};
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;

@@ -898,7 +898,7 @@ inline int dispatch_stream(StreamParams &p, int B, bool aux, int sms, cudaStream
             case 8: return launch_tc_gemv<F, 8>(p, sms, st);
         }
     }
-    p.fault = take_injected_wait_fault();  // only the streaming kernels honor the test hook
+    p.fault = take_injected_wait_fault();  // (of the kernels here only the streaming ones honor the test hook)
     switch (B) {
         case 1: return launch_stream<F, 1>(p, aux, sms, st);
         case 2: return launch_stream<F, 2>(p, aux, sms, st);
