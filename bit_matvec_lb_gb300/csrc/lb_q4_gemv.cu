@@ -129,6 +129,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
     __shared__ int row_of[2][kMvTokens];
     __shared__ uint16_t s_first[kExperts];                       // pieces before an expert's
     __shared__ int s_part[kMvThreads / 32], s_fault;
+    __shared__ volatile int s_lost;                              // a wait for sums has run out
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int slice = l.blocks * kMvBlock, rank = blockIdx.x % l.split;
     const int k0 = rank * slice, columns = min(p.K - k0, slice);
@@ -140,6 +141,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
 
     pdl_launch_dependents();
     if (tid == 0) {
+        s_lost = 0;
         // a stage is full when the copies of codes and the 32 lanes' copies of scales have landed
         for (int i = 0; i < kMvMaxStages; i++) mbar_init(&full[i], 33), mbar_init(&empty[i], kMvWarps);
         // from every CTA come the sums of the warps whose rows are finished here, in two halves
@@ -294,7 +296,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         const uint32_t tell[2] = {address_in(&sums_full[0], owner), address_in(&sums_full[1], owner)};
         int stage = 0;
         uint32_t phase = 0;
-        bool ok = true, heard = true;   // no wait for weights, none for sums has run out
+        bool ok = true;   // no wait for weights has run out
         int at_piece = -1, cols = 0, planes = 1;
         Piece q{0, 0, 0, 0};
         // The parts of few tokens lie in one operand's eight columns, of more in an operand each.
@@ -321,7 +323,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         };
         // the sums of unit number n (of this cluster's), added up over the ranks and stored
         auto finish = [&](int n) {
-            if (heard) {
+            if (!s_lost) {
                 const uint64_t t_0 = global_ns();
                 bool there = mv_try_wait_cluster(&sums_full[n & 1], (uint32_t)(n >> 1) & 1u);
                 for (uint32_t i = 1; !there; i++) {
@@ -329,8 +331,8 @@ __global__ void __launch_bounds__(kMvThreads, 1)
                     if ((i & 15u) == 0 && global_ns() - t_0 > 2000000000ull) break;
                 }
                 if (!__all_sync(0xffffffffu, there)) {
-                    if (lane == 0) atomicOr(p.error, 1);
-                    heard = false;
+                    if (lane == 0) atomicOr(p.error, 1), s_lost = 1;
+                    __syncwarp();
                 }
             }
             const int parts = packed(q_done) ? PARTS : 1;
@@ -534,7 +536,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
             // to it (one without weights sends what it has; each sum arrives once, even from a CTA that gave its wait up and
             // ran ahead).  One that gave such a wait up does not know: it stays until every thread of the cluster has got
             // here or gone.  (All of them always waiting for each other: 13.4 us for 13.0, 5 x 4096 x 12288.)
-            if (!heard) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
+            if (s_lost) asm volatile("barrier.cluster.arrive.release;\n\tbarrier.cluster.wait.acquire;" ::: "memory");
         }
     }
 }
