@@ -343,14 +343,14 @@ __global__ void __launch_bounds__(kTcThreads, 1) attn_prompt_kernel(const AttnPa
     it.r = s_r, it.b = s_b, it.h = s_h, it.begin = s_begin;
     it.set(p);
 
-    // Bounded: about 2 s (2000 tries of up to a millisecond), after the first that ran out a few tries.
-    int tries = 2000;
+    // Bounded: about 2 s, after the first that ran out 0.1 ms.
+    int tries = kWaitTries;
     auto wait = [&](uint64_t &b, uint32_t parity) {
         int i = 0;
         while (!mbar_try_wait_hint(&b, parity & 1, 1000000u) && i < tries) i++;
         if (i >= tries) {
             *p.error = 1;
-            tries = 4;
+            tries = wait_tries(100);
         }
         __syncwarp();
     };

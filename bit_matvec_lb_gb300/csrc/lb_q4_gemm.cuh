@@ -67,6 +67,7 @@ struct GmLaunch {
     int pairs;        // two rows of a bf16 y may be stored as one word
     int tokens;       // of an item, at most (dense)
     int tiles;        // of weight rows
+    int fault;        // test hook: CTA 0 copies no codes and waits so many microseconds for the first ones
 };
 
 struct GmBars {
@@ -324,15 +325,16 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     const int columns = min(p.K - k0, l.steps * kGmStep);
     const int steps = (columns + kGmStep - 1) / kGmStep;
 
-    // Bounded: about 2 s (2000 tries of up to a millisecond), after the first that ran out a few tries.
-    int tries = 2000;
+    // Bounded: about 2 s, after the first that ran out 0.1 ms.
+    const bool starve = l.fault && blockIdx.x == 0;
+    int tries = kWaitTries;
     auto wait = [&](uint64_t &b, uint32_t parity) {
         if (!mbar_try_wait(&b, parity & 1)) {
             int i = 0;
             while (!mbar_try_wait_hint(&b, parity & 1, 1000000u) && i < tries) i++;
             if (i >= tries) {
                 *p.error = 1;
-                tries = 4;
+                tries = wait_tries(100);
             }
         }
         __syncwarp();
@@ -527,6 +529,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
     } else if (warp < kGmOutWarps + kGmExpandWarps) {
         // =================== weights: a thread per row, every other unit of two steps ===================
         if constexpr (F32) gm_fewer_registers<80>();
+        if (starve) tries = wait_tries(l.fault);
         const int quarter = warp & 3, half = (warp - kGmOutWarps) >> 2;
         const uint32_t to = tmem + kGmABase + ((uint32_t)(quarter * 32) << 16);
         constexpr int kBlock = 8 * GROUP / 128;   // units of eight groups, whose scales are held
@@ -651,7 +654,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
         // =================== codes: two copies of 64 rows x 128 columns a stage ===================
         GmRing<kGmCStages> code;
         int used = 0;
-        for (int i = begin; i < items; i += each) {
+        for (int i = begin; i < items && !starve; i += each) {
             const GmItem it = item_of(i);
             const int64_t first = it.expert * matrix_rows + it.tile * (int64_t)(USE == kQ4Up ? kGmRows / 2 : kGmRows);
             const int64_t second = USE == kQ4Up ? first + p.N : first + kGmRows / 2;
@@ -848,6 +851,7 @@ static int dispatch_gemm(const Q4Params &p, const Q4Rows &r, const uint8_t *code
         l.steps = (l.steps + 1) / 2 * 2;
         l.split = (steps + l.steps - 1) / l.steps;
     }
+    l.fault = take_injected_wait_fault();
     const unsigned grid = (unsigned)(l.split > 1 ? items * l.split : std::min<int64_t>(items, sms));
     CUtensorMap codes_map, x_map;
     if (int e = encode_rows_map(&codes_map, codes, (uint64_t)p.K / 2, (uint64_t)code_rows, 64, kGmRows / 2, 64)) return e;

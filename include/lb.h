@@ -79,8 +79,8 @@ int lb_device_status(void *stream);
  * grouped) that runs on the streaming or lane-per-row kernel (1-2 tokens, or 3-8 tokens outside
  * the tensor-core kernel's shapes) makes its first CTA copy no weights, so that CTA's bounded
  * wait gives up after `wait_us` microseconds instead of about 2 s: the call then leaves part of
- * y unwritten and lb_device_status() reports LB_ERR_DEVICE.  So does the next 4-bit product of up to eight tokens
- * (or of an expert's), whichever comes first, with the first CTA that has work (parts of y are then wrong).  Nothing faults, traps or hangs.
+ * y unwritten and lb_device_status() reports LB_ERR_DEVICE.  So does the next product kernel of lb_gemv_q4, lb_gemm_q4
+ * or lb_experts_q4, whichever comes first, with the first CTA that has work (parts of y are then wrong).  Nothing faults, traps or hangs.
  * One-shot, process-wide.  1 <= wait_us <= 10^6, else LB_ERR_SHAPE.  Not for production use. */
 int lb_test_inject_wait_timeout(int wait_us);
 

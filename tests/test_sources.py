@@ -16,3 +16,16 @@ def test_a_copy_goes_into_one_cta():
             text = re.sub(r'"\s*\n?\s*"', "", f.read())   # strings that go on are one
         found = re.findall(r"cp\.(?:reduce\.)?async\.bulk[^;\"]*multicast[^;\"]*", text)
         assert not found, (os.path.basename(path), found)
+
+
+def test_counted_waits_last_as_long_as_the_others():
+    """A try's time hint is a most, not a length: waits that count tries take their number from the one place that
+    knows how long a try is."""
+    counted = 0
+    for path in glob.glob(os.path.join(CSRC, "*.cu*")):
+        with open(path) as f:
+            text = f.read()
+        for first in re.findall(r"\bint tries = ([^;]*);", text):
+            assert first == "kWaitTries", os.path.basename(path)
+            counted += 1
+    assert counted == 2
