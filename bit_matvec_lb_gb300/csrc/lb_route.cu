@@ -363,13 +363,14 @@ __device__ __forceinline__ float weight_of(const RouteParams &p, float x, bool i
         s = p.sigmoid ? 1.f / (1.f + expf(-x)) : exp_difference(x, m) / sum;
         return in ? s * p.scale : 0.f;
     }
-    // the largest chosen logit's power of e goes out of all of them, so their sum is never 0
+    // the largest chosen logit's power of e goes out of all of them, so their sum is never 0 and only a weight that is itself
+    // below binary32's normal numbers has fewer bits; sigmoids from a logit above 0 on are 1/2 at least as they are
     const float top = warp_max(in ? x : -INFINITY);
-    if (p.sigmoid && top > -40.f) {
+    if (p.sigmoid && top > 0.f) {
         const float e = expf(-fabsf(x));
         s = (x < 0.f ? e : 1.f) / (1.f + e);
     } else if (p.sigmoid) {
-        s = exp_difference(x, top);   // (1 + e^x is 1 in binary32)
+        s = exp_difference(x, top) / (1.f + expf(x));
     } else {
         s = exp_difference(x, top);
     }

@@ -591,7 +591,8 @@ int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zero
  *   ids : [T][k] int32.  weights : [T][k] fp32.  expert_start : [E + 1] int32.  order : [T * k] int32.
  *   workspace : lb_route_workspace_bytes(T, E) bytes (never fewer for more tokens), 16-byte aligned, as above.
  * Scores are computed in binary32, and in binary64 where two keys lie too close together for that;
- * exp(x - max) of experts more than 100 below the row's largest logit counts as 0 in the weights.
+ * exp(x - max) of experts more than 100 below the row's largest logit counts as 0 in the weights; a weight below 2^-126
+ * (before the scale) may lose bits or be 0.
  * 0 <= T <= 2^20 (at 0 only expert_start is written); 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= min(E,
  * LB_ROUTE_MAX_CHOSEN); groups <= 32 divides E; 1 <= keep_groups <= groups; stride >= E; pointers aligned to
  * their elements. */

@@ -1,9 +1,11 @@
 """Routing calls that stand apart from ordinary ones."""
-import torch
+import numpy as np
 import pytest
+import torch
 
 import bit_matvec_lb_gb300 as lb
 from gpu_util import guarded
+from test_gpu_route import run
 
 pytestmark = pytest.mark.gpu
 
@@ -33,3 +35,19 @@ def test_one_workspace_for_every_batch():
         got, want = softmax_route(torch.randn(T, E, generator=g, device="cuda"), k, ws)
         for i in (0, 2, 3):
             assert torch.equal(got[i].long(), want[i])
+
+
+@pytest.mark.parametrize("sigmoid", [False, True])
+@pytest.mark.parametrize("top", [3.0, 0.5, 0.0, -0.5, -5.0, -20.0, -39.0, -39.99, -40.0, -41.0, -87.0, -100.0])
+def test_weights_of_logits_far_apart(sigmoid, top):
+    """Renormalized weights keep their bits down to the type's smallest normal number, wherever the logits lie: at -39
+    and -100 the second one's is e^-61, far above that, although e^-100 itself is far below."""
+    x = top - np.array([[0, 1, 61, 30, 80, 86, 86.9], [0, 45.5, 0.25, 60, 70, 87, 95]], np.float32)
+    ids, w = run(x, 7, sigmoid, scale=2.5)
+    if top <= -10 or not sigmoid:   # the weights' ratios are the powers of e there
+        want = np.exp(x.astype(np.float64) - x[:, :1])
+        got = np.take_along_axis(w, np.argsort(ids, 1), 1)
+        normal = want > 2e-38
+        # (two weights, each within 48 half steps; 1 + e^x adds below 5e-5 at -10)
+        assert np.all(np.abs(got / got[:, :1] / want - 1)[normal] < 1e-5 + np.exp(top) * sigmoid)
+    run(np.repeat(x, 40, 0), 7, sigmoid, np.zeros(7, np.float32), scale=1.0)
