@@ -82,15 +82,20 @@ struct KernelPrep {
     int threads = 0;
     int blocks_per_sm = 0;
 };
-static std::unordered_map<const void *, KernelPrep> g_prep;
+// (the shared-memory limit is an attribute of a kernel on one device)
+static std::unordered_map<const void *, KernelPrep> g_prep[kMaxDevices];
 static std::mutex g_prep_mutex;
 
 int prepare_kernel(const void *kernel, int threads, size_t smem, int *blocks_per_sm) {
+    int dev = 0;
+    if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
+        cudaGetLastError();
+        return LB_ERR_ARCH;
+    }
     std::lock_guard<std::mutex> lock(g_prep_mutex);
-    KernelPrep &p = g_prep[kernel];
+    KernelPrep &p = g_prep[dev][kernel];
     if (!p.attr_set) {
-        int dev = 0, optin = 0;
-        cudaGetDevice(&dev);
+        int optin = 0;
         cudaDeviceGetAttribute(&optin, cudaDevAttrMaxSharedMemoryPerBlockOptin, dev);
         // The dynamic limit plus the kernel's static shared memory may not exceed the opt-in
         // maximum.

@@ -29,8 +29,8 @@ int current_device_info(DeviceInfo *out);  // LB_OK or LB_ERR_ARCH
 // bounded wait set it; lb_device_status() reads and clears it.
 int *device_error_word();
 
-// Per-kernel launch preparation, cached: raise the dynamic shared-memory limit once and
-// remember the occupancy for the last shared-memory size used.  LB_OK, LB_ERR_SHAPE when the
+// Per-kernel launch preparation on the current device, cached per device: raise the dynamic shared-memory
+// limit once and remember the occupancy for the last shared-memory size used.  LB_OK, LB_ERR_SHAPE when the
 // requested shared memory cannot be resident, or LB_ERR_LAUNCH.
 int prepare_kernel(const void *kernel, int threads, size_t smem, int *blocks_per_sm);
 
