@@ -86,7 +86,7 @@ struct KernelPrep {
 static std::unordered_map<const void *, KernelPrep> g_prep[kMaxDevices];
 static std::mutex g_prep_mutex;
 
-int prepare_kernel(const void *kernel, int threads, size_t smem, int *blocks_per_sm) {
+static int prepare_on_device(const void *kernel, int threads, size_t smem, int *blocks_per_sm) {
     int dev = 0;
     if (cudaGetDevice(&dev) != cudaSuccess || dev < 0 || dev >= kMaxDevices) {
         cudaGetLastError();
@@ -124,6 +124,14 @@ int prepare_kernel(const void *kernel, int threads, size_t smem, int *blocks_per
     }
     *blocks_per_sm = p.blocks_per_sm;
     return p.blocks_per_sm >= 1 ? LB_OK : LB_ERR_SHAPE;
+}
+
+int prepare_kernel(const void *kernel, int threads, size_t smem, int *blocks_per_sm) {
+    try {
+        return prepare_on_device(kernel, threads, smem, blocks_per_sm);
+    } catch (...) {   // (no memory on the host: nothing may be thrown through a C entry)
+        return LB_ERR_LAUNCH;
+    }
 }
 
 static PFN_cuTensorMapEncodeTiled_v12000 g_encode_tiled = nullptr;

@@ -11,9 +11,19 @@ from bit_matvec_lb_gb300 import build
 
 RUNTIME = r"""
 #include <cuda_runtime.h>
+#include <cstdlib>
 #include <map>
+#include <new>
 #include <utility>
 static int device = 0;
+static bool no_memory = false;
+void *operator new(size_t n) {
+    void *p = no_memory ? nullptr : std::malloc(n);
+    if (!p) throw std::bad_alloc();
+    return p;
+}
+void operator delete(void *p) noexcept { std::free(p); }
+void operator delete(void *p, size_t) noexcept { std::free(p); }
 static std::map<std::pair<int, const void *>, int> limit;   // dynamic shared memory, 48 KB unless it was raised
 extern "C" {
 cudaError_t cudaGetDevice(int *d) { *d = device; return cudaSuccess; }
@@ -49,6 +59,14 @@ void __cudaRegisterFunction(void **, const char *, char *, const char *, int, vo
 char __cudaInitModule(void **) { return 0; }
 }
 namespace lb { int prepare_kernel(const void *kernel, int threads, size_t smem, int *blocks_per_sm); }
+extern "C" __attribute__((visibility("default"))) int prepare_without_memory(const void *kernel) {
+    int per_sm = 0;
+    device = 0;
+    no_memory = true;
+    const int status = lb::prepare_kernel(kernel, 256, 1024, &per_sm);   // (an exception would end the process)
+    no_memory = false;
+    return status;
+}
 extern "C" __attribute__((visibility("default"))) int prepare_on(int dev, const void *kernel, size_t smem) {
     int per_sm = 0;
     device = dev;
@@ -61,16 +79,20 @@ extern "C" __attribute__((visibility("default"))) int prepare_on(int dev, const 
 
 
 @pytest.fixture(scope="module")
-def prepare_on(tmp_path_factory):
+def runtime(tmp_path_factory):
     lb.load()   # (the objects are there and up to date)
     at = tmp_path_factory.mktemp("devices")
     (at / "runtime.cpp").write_text(RUNTIME)
     cuda = os.path.dirname(os.path.dirname(os.path.realpath(build._nvcc())))
     subprocess.run(["g++", "-shared", "-fPIC", "-O1", "-I", os.path.join(cuda, "include"), str(at / "runtime.cpp"),
                     os.path.join(build.BUILD, "lb_capi.o"), "-Wl,-Bsymbolic", "-o", str(at / "devices.so")], check=True)
-    fn = ctypes.CDLL(str(at / "devices.so")).prepare_on
-    fn.argtypes = [ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t]
-    return fn
+    return ctypes.CDLL(str(at / "devices.so"))
+
+
+@pytest.fixture(scope="module")
+def prepare_on(runtime):
+    runtime.prepare_on.argtypes = [ctypes.c_int, ctypes.c_void_p, ctypes.c_size_t]
+    return runtime.prepare_on
 
 
 def test_shared_memory_limit_of_every_device(prepare_on):
@@ -82,3 +104,10 @@ def test_shared_memory_limit_of_every_device(prepare_on):
 
 def test_a_device_beyond_the_last(prepare_on):
     assert prepare_on(64, 0x3000, 1024) == -5
+
+
+def test_no_memory_on_the_host(runtime):
+    """An error, not an exception through a C entry; the next call finds its way."""
+    runtime.prepare_without_memory.argtypes = [ctypes.c_void_p]
+    assert runtime.prepare_without_memory(0x4000) == -6
+    assert runtime.prepare_on(0, 0x4000, 1024) == 0
