@@ -747,7 +747,8 @@ LB_EXPORT int lb_attn_kv4(const void *q, int type, int64_t q_stride, const uint8
                           float *lse_opt, void *workspace, size_t workspace_bytes, void *stream) {
     using namespace lb;
     const int64_t lim = int64_t(1) << 31;
-    if (!q || !cache || !block_table || !q_start || !kv_len || !out || !workspace) return LB_ERR_NULL;
+    if (!cache || !block_table || !q_start || !kv_len || !workspace || (T != 0 && (!q || !out)))
+        return LB_ERR_NULL;
     if ((type != LB_OUT_F32 && type != LB_OUT_BF16) ||
         !kv4_shape_ok(pages, page_size, kv_heads, head_dim) || heads < kv_heads ||
         heads % kv_heads || heads / kv_heads > 64 || R < 1 || R > LB_KV_MAX_REQUESTS || T < 0 ||

@@ -324,7 +324,7 @@ LB_EXPORT int lb_kv4_append(const void *k, const void *v, int type, int64_t k_st
                             int64_t pages, int page_size, int kv_heads, int head_dim,
                             void *stream) {
     using namespace lb;
-    if (!k || !v || !slot || !cache) return LB_ERR_NULL;
+    if (!cache || (T != 0 && (!k || !v || !slot))) return LB_ERR_NULL;
     if (!kv4_shape_ok(pages, page_size, kv_heads, head_dim) || T < 0 || T >= (int64_t(1) << 31) ||
         (type != LB_OUT_F32 && type != LB_OUT_BF16) || k_stride < (int64_t)kv_heads * head_dim ||
         v_stride < (int64_t)kv_heads * head_dim)
@@ -344,7 +344,7 @@ LB_EXPORT int lb_dequantize_kv4(const uint8_t *cache, int64_t pages, int page_si
                                 int head_dim, const int64_t *slot, int64_t T, int out_format,
                                 void *k, void *v, void *stream) {
     using namespace lb;
-    if (!k || !v || !slot || !cache) return LB_ERR_NULL;
+    if (!cache || (T != 0 && (!k || !v || !slot))) return LB_ERR_NULL;
     if (!kv4_shape_ok(pages, page_size, kv_heads, head_dim) || T < 0 || T >= (int64_t(1) << 31) ||
         (out_format != LB_OUT_F32 && out_format != LB_OUT_BF16))
         return LB_ERR_SHAPE;

@@ -54,7 +54,7 @@ __global__ void __launch_bounds__(kCombineThreads)
 static int check_product(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros, int group,
                          const void *x, int type, int64_t x_stride, const void *y, int64_t y_stride,
                          int64_t M, int64_t N, int64_t K) {
-    if (!codes || !scales || !x || !y) return LB_ERR_NULL;
+    if (!codes || !scales || (M != 0 && (!x || !y))) return LB_ERR_NULL;   // (no tokens: empty tensors lie nowhere)
     if (!q4_group_ok(group) || !q4_type_ok(type) || M < 0 || M > (1 << 20) || N < 1 || N > (1 << 23) ||
         K < group || K > LB_Q4_MAX_K || K % group != 0 || x_stride < K || y_stride < N ||
         x_stride > 0x7fffffff || y_stride > 0x7fffffff)
@@ -175,8 +175,8 @@ LB_EXPORT int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T
                             const int32_t *expert_start, const int32_t *order, void *y, int64_t y_stride,
                             void *workspace, size_t workspace_bytes, void *stream) {
     using namespace lb;
-    if (!x || !up_codes || !up_scales || !down_codes || !down_scales || !ids || !weights ||
-        !expert_start || !order || !y || !workspace)
+    if (!up_codes || !up_scales || !down_codes || !down_scales || !expert_start || !workspace ||
+        (T != 0 && (!x || !ids || !weights || !order || !y)))
         return LB_ERR_NULL;
     if (!q4_group_ok(group) || hidden % group != 0 || ffn % group != 0 || x_stride < hidden ||
         y_stride < hidden || x_stride > 0x7fffffff || y_stride > 0x7fffffff)

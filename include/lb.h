@@ -449,7 +449,7 @@ int lb_kv_plan(const int32_t *past, const int32_t *fresh, int64_t R, const int32
  *          one call have different slots.
  *   cache: LB_KV4_CACHE_BYTES(pages, kv_heads, page_size, head_dim) bytes.
  * Rows with NaN or infinite values store unspecified codes and scales of their own row.
- * 0 <= T < 2^31 (0: nothing is done); strides >= kv_heads * head_dim; k, v, cache and the strides
+ * 0 <= T < 2^31 (0: nothing is done; k, v and slot may be NULL); strides >= kv_heads * head_dim; k, v, cache and the strides
  * in bytes 16-byte aligned, slot 8-byte. */
 int lb_kv4_append(const void *k, const void *v, int type, int64_t k_stride, int64_t v_stride,
                   const int64_t *slot, int64_t T, uint8_t *cache, int64_t pages, int page_size,
@@ -457,7 +457,7 @@ int lb_kv4_append(const void *k, const void *v, int type, int64_t k_stride, int6
 
 /* Cache -> values: k[t][h][i] = d * (c - z) of slot[t]'s key row of head h, v likewise (the exact
  * binary32 product; out_format LB_OUT_BF16 rounds it to nearest even).  A token whose slot is not in
- * [0, pages * page_size) gives zeros.  k, v : [T][kv_heads][head_dim], 16-byte aligned. */
+ * [0, pages * page_size) gives zeros.  k, v : [T][kv_heads][head_dim], 16-byte aligned.  T = 0 as in lb_kv4_append. */
 int lb_dequantize_kv4(const uint8_t *cache, int64_t pages, int page_size, int kv_heads,
                       int head_dim, const int64_t *slot, int64_t T, int out_format, void *k,
                       void *v, void *stream);
@@ -490,7 +490,7 @@ int lb_dequantize_kv4(const uint8_t *cache, int64_t pages, int page_size, int kv
  * scale * 15 * d * max_i |q_i| (codes enter as fp16 subnormals there).  Scores are expected below
  * 2^20 in size: beyond, binary32 no longer tells close ones apart, and a row's values are unspecified.
  * heads % kv_heads == 0, heads / kv_heads <= 64; 1 <= R <= LB_KV_MAX_REQUESTS; 0 <= T (0: nothing
- * is done), T * heads / kv_heads < 2^31; 1 <= table_width, table_width * page_size <= 2^30; max_q >= 1; 0 < scale
+ * is done; q and out may be NULL), T * heads / kv_heads < 2^31; 1 <= table_width, table_width * page_size <= 2^30; max_q >= 1; 0 < scale
  * finite; window >= 0, and 0 without causal; 16-byte alignment of q, out, cache, workspace and the
  * two strides in bytes, 4-byte of the others. */
 size_t lb_attn_kv4_workspace_bytes(int heads, int kv_heads, int head_dim, int64_t max_q);
@@ -562,7 +562,7 @@ int lb_logits_adjust(const void *logits, int type, int64_t stride, void *out, in
  * of its row (more) where it is far smaller than that.  With bf16 tensors and more than eight tokens a weight
  * d * (c - z) rounds to 11 bits, beyond 65504 to infinity; otherwise a scale acts on its group's sum in binary32.
  * A token with a NaN or an infinite number gets nothing finite in its row of y; other rows do not change.
- * 1 <= N <= 2^23; group <= K <= LB_Q4_MAX_K; 0 <= M <= 2^20 (0: nothing is done); x and its stride in
+ * 1 <= N <= 2^23; group <= K <= LB_Q4_MAX_K; 0 <= M <= 2^20 (0: nothing is done; x and y may be NULL); x and its stride in
  * bytes 16-byte aligned, y aligned to its elements; strides >= K and N, below 2^31. */
 int lb_gemv_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zeros_opt, int group,
                const void *x, int type, int64_t x_stride, void *y, int64_t y_stride, int64_t N,
@@ -593,7 +593,7 @@ int lb_gemm_q4(const uint8_t *codes, const uint16_t *scales, const uint8_t *zero
  * Scores are computed in binary32, and in binary64 where two keys lie too close together for that;
  * exp(x - max) of experts more than 100 below the row's largest logit counts as 0 in the weights; a weight below 2^-126
  * (before the scale) may lose bits or be 0.
- * 0 <= T <= 2^20 (at 0 only expert_start is written); 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= min(E,
+ * 0 <= T <= 2^20 (at 0 only expert_start is written; logits, ids, weights and order may be NULL); 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= min(E,
  * LB_ROUTE_MAX_CHOSEN); groups <= 32 divides E; 1 <= keep_groups <= groups; stride >= E; pointers aligned to
  * their elements. */
 #define LB_ROUTE_SOFTMAX 0
@@ -625,7 +625,7 @@ int lb_route(const void *logits, int type, int64_t stride, int64_t T, int E, int
  * Precision as in lb_gemv_q4 / lb_gemm_q4 (weights may round to 11 bits with bf16 tensors, whatever the number of
  * tokens).  h enters the down rows' products with 11 bits where tensors are bf16 and with 22 where they are fp32, below
  * its largest value as x does; the experts' outputs are binary32.
- * 0 <= T (0: nothing is done), T * k <= 2^24; 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= LB_ROUTE_MAX_CHOSEN; hidden and
+ * 0 <= T (0: nothing is done; x, y, ids, weights and order may be NULL), T * k <= 2^24; 1 <= E <= LB_ROUTE_MAX_EXPERTS; 1 <= k <= LB_ROUTE_MAX_CHOSEN; hidden and
  * ffn multiples of group, at most LB_Q4_MAX_K; alignment as in lb_gemv_q4, 4-byte for the routing's. */
 size_t lb_experts_q4_workspace_bytes(int64_t T, int E, int k, int64_t hidden, int64_t ffn, int type);
 int lb_experts_q4(const void *x, int type, int64_t x_stride, int64_t T, int E, int k, int64_t hidden,
