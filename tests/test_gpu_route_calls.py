@@ -5,7 +5,7 @@ import torch
 
 import bit_matvec_lb_gb300 as lb
 from gpu_util import guarded
-from test_gpu_route import run
+from test_gpu_route import REL, run
 
 pytestmark = pytest.mark.gpu
 
@@ -51,3 +51,30 @@ def test_weights_of_logits_far_apart(sigmoid, top):
         # (two weights, each within 48 half steps; 1 + e^x adds below 5e-5 at -10)
         assert np.all(np.abs(got / got[:, :1] / want - 1)[normal] < 1e-5 + np.exp(top) * sigmoid)
     run(np.repeat(x, 40, 0), 7, sigmoid, np.zeros(7, np.float32), scale=1.0)
+
+
+@pytest.mark.parametrize("T,E,k", [(64, 64, 8), (65, 256, 8), (20011, 40, 4), (3000, 1000, 32)])
+def test_each_weight_at_its_place(T, E, k):
+    """Every weight against its own expert's 64-bit softmax, not only their sums; then the same in a graph that is
+    replayed with other logits."""
+    g = torch.Generator(device="cuda")
+    g.manual_seed(T)
+    x = torch.randn(T, E, generator=g, device="cuda")
+    ws = guarded(lb.lb_route_workspace_bytes(T, E), torch.uint8)
+
+    def check(got, want):
+        for i in (0, 2, 3):
+            assert torch.equal(got[i].long(), want[i])
+        assert bool(((got[1].double() - want[1]).abs() <= REL * want[1] + 1e-37).all())
+
+    got, want = softmax_route(x, k, ws)
+    check(got, want)
+    torch.cuda.synchronize()
+    graph = torch.cuda.CUDAGraph()
+    with torch.cuda.graph(graph):
+        lb.lb_route(x, lb.OUT_F32, E, T, E, k, lb.ROUTE_SOFTMAX, *got, ws)
+    x.copy_(torch.randn(T, E, generator=g, device="cuda"))
+    for t in got:
+        t.zero_()
+    graph.replay()
+    check(got, softmax_route(x, k, torch.empty_like(ws))[1])
