@@ -94,10 +94,10 @@ static RowsAt rows_at(uint8_t *at, int64_t n, int64_t K, int type) {
 
 // Pairs per expert from which the experts' products run on tcgen05, whose time hardly grows with them; the other kernel
 // takes pieces of eight tokens, so its time grows with every one that begins.  64 experts of 2048 x 1024, eight per
-// token, 6, 12 and 16 pairs each: fp32 114, 150 and 181 us against tcgen05's 160, 168 and 170; bf16 87, 113 and 135
-// against 107, 109 and 110.  Eight of 4096 x 8192, two per token, 8, 12 and 16: fp32 202, 238 and 306 against 220, 242
-// and 246; bf16 182, 203 and 266 against 163, 177 and 178.  32 of 1024 x 512, four per token, 12 and 16: fp32 37 and 47
-// against 43 and 45; bf16 31 and 37 against 35 and 35.
+// token, 6, 12 and 16 pairs each: fp32 113, 149 and 180 us against tcgen05's 141, 145 and 148; bf16 88, 113 and 133
+// against 98, 100 and 101.  Eight of 4096 x 8192, two per token, 8, 12 and 16: fp32 203, 238 and 308 against 195, 215
+// and 219; bf16 183, 203 and 265 against 150, 162 and 163.  32 of 1024 x 512, four per token, 12 and 16: fp32 37 and 45
+// against 37 and 37; bf16 31 and 37 against 31 and 31.
 constexpr int many_pairs(int type) { return type == LB_OUT_F32 ? 13 : 10; }
 
 struct ExpertsAt {

@@ -20,11 +20,10 @@
 // operations.  Each CTA copies what it multiplies into its own shared memory.  Calls with few tiles are split along K over
 // a cluster; the parts are added up through distributed shared memory.
 //
-// What bounds it: with many tokens the products (4096 x 12288 x 4096 bf16: 238 us, the tensor pipe busy for 77 % of
-// them); with few per item, at 480 clocks a step of 64 columns, issue slots (55 %) and latency: the warps that expand
-// weights are busy for 300, the one that issues products for 300, the one that copies x for 370 (49 tokens for each of
-// 128 experts, DRAM 33 %); in fp32 the products' issue and a drain per group, about 1000 clocks a step (509 x 6912 x
-// 2560: 45 us).
+// What bounds it: with many tokens the products (4096 x 12288 x 4096 bf16: 235 us, the tensor pipe busy for 78 % of
+// them); with few per item, at 460 clocks a step of 64 columns, issue slots (56 %) and latency: the warps that expand
+// weights are busy for 300 of them, the one that issues products for 300 (49 tokens for each of 128 experts, DRAM 35 %);
+// in fp32 the products' issue and a drain per group, about 900 clocks a step (509 x 6912 x 2560: 38 us).
 #pragma once
 #include "lb_q4.cuh"
 #include "lb_tc.cuh"
@@ -409,7 +408,7 @@ __global__ void __launch_bounds__(kGmThreads, 1)
                         if (j < mine_left) *h = silu * up;
                     }
                 } else if constexpr (USE == kQ4Down) {
-                    // (rows of a full sixteen go out without a question each: 4096 tokens' experts 477 -> 466 us)
+                    // (rows of a full sixteen go out without a question each: 4096 tokens' experts in a graph 469 -> 464 us)
                     int at[16], all = 0;
 #pragma unroll
                     for (int j = 0; j < 4; j++) {

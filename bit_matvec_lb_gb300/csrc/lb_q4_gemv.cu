@@ -18,10 +18,10 @@
 // cluster that is to finish its rows, and that CTA adds them up, in the order of the ranks, after its next unit.
 //
 // What bounds it: in the steady state the issue slots (a warp issues about 60 instructions for 512 weights with two-part x,
-// 52 to 58 % of the slots over a call), before HBM (21 to 31 %); in short calls the fixed parts: about 3000 clocks to the
+// 51 to 59 % of the slots over a call), before HBM (20 to 31 %); in short calls the fixed parts: about 3000 clocks to the
 // first product and 2000 to 4000 for x.  128 columns are in flight at a time, on four accumulators, since the products'
 // latency would otherwise set the pace (one accumulator: 190 cycles for 512 weights).  1 x 12288 x 4096 fp32 in groups
-// of 32: 12.7 us, 5 x 4096 x 12288 bf16: 12.9; 43 tokens' eight of 64 experts of 2048 x 1024, fp32: 95 with their sum.
+// of 32: 12.7 us, 5 x 4096 x 12288 bf16: 13.0; 43 tokens' eight of 64 experts of 2048 x 1024, fp32: 94 to 100 with their sum.
 #include "lb_q4.cuh"
 
 #include <algorithm>

@@ -14,7 +14,8 @@
 // More tokens take a second kernel: the first leaves each CTA's counts per expert, the second adds
 // up the counts of the CTAs before its own and places its tokens by the same masks.
 //
-// What bounds it: instructions.  A token of 256 experts takes about 700 of a warp.  Each lane keeps its best two keys, so a
+// What bounds it: instructions.  A token of 256 experts takes about 1500 of a warp (counted over 8191 with sigmoid
+// scores, a bias and eight groups).  Each lane keeps its best two keys, so a
 // round of the selection is two warp reductions and a few operations of the lane that loses its best; all of its
 // keys are looked through again only when that happens to it a second time.
 #include "lb_kv4.cuh"
