@@ -323,7 +323,7 @@ __global__ void __launch_bounds__(kMvThreads, 1)
         };
         // the sums of unit number n (of this cluster's), added up over the ranks and stored
         auto finish = [&](int n) {
-            if (!s_lost) {
+            if (!__any_sync(0xffffffffu, s_lost)) {   // (the whole warp waits, or none of it)
                 const uint64_t t_0 = global_ns();
                 bool there = mv_try_wait_cluster(&sums_full[n & 1], (uint32_t)(n >> 1) & 1u);
                 for (uint32_t i = 1; !there; i++) {
